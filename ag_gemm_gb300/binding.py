@@ -32,6 +32,11 @@ TILE_CONFIGS = {"auto": 0, "single": 1}
 INTERLEAVES = {"auto": 0, "lockstep": 1, "skewed": 2, "rank_major": 3, "skewed_pairs": 4}
 RS_ALGOS = {"direct": 0, "ring": 1}
 TAIL_SPLITS = {"auto": 0, "off": 1, "on": 2}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "wavelength": 2, "parts": 3}
+FO_ROPE_MAX_DIM = 256
+FO_NORM_MAX_H = 32768
+FO_FP8_BLOCK = 128
 
 # Every symbol include/flashoverlap.h declares.
 EXPORTED = [
@@ -41,6 +46,8 @@ EXPORTED = [
     "fo_plan_last_launches", "fo_status_string", "fo_version", "fo_gemm_rs_noalloc", "fo_plan_task_order",
     "fo_gemm_ar", "fo_trace_query", "fo_plan_last_split_tiles", "fo_check_device_pointers",
     "fo_gemm_a2a", "fo_all_to_all_copy", "fo_attn_rs", "fo_attention", "fo_gemm_partials_sharded",
+    "fo_rmsnorm", "fo_rmsnorm_bwd", "fo_rmsnorm_bwd_workspace", "fo_quant_fp8", "fo_gemm_fp8",
+    "fo_gemm_fp8_workspace", "fo_ops_workspace_init", "fo_ops_status_query", "fo_rope_init", "fo_rope",
 ]
 
 
@@ -63,6 +70,22 @@ class PlanDesc(ctypes.Structure):
         ("trace", c_int32), ("inject_delay_us", c_int32), ("tail_split", c_int32),
         ("reserved", c_int32 * 1),
     ]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("R", c_int32), ("H", c_int32), ("dtype", c_int32), ("w_dtype", c_int32), ("eps", ctypes.c_float),
+                ("w_offset", ctypes.c_float), ("reserved", c_int32 * 2)]
+
+
+class GemmFp8Desc(ctypes.Structure):
+    _fields_ = [("R", c_int32), ("out_dtype", c_int32), ("N", c_int64), ("K", c_int64), ("reserved", c_int32 * 4)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("R", "head_dim", "rot_dim", "heads_q", "heads_k", "heads_v", "layout", "dtype",
+                                       "scaling", "reserved")]
+    _fields_ += [(n, ctypes.c_double) for n in ("base", "stretch", "trained", "slow", "fast")]
+    _fields_ += [("turns", c_uint64 * (FO_ROPE_MAX_DIM // 2)), ("factor", ctypes.c_float), ("ready", c_int32)]
 
 
 _lib = None
@@ -107,6 +130,17 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "fo_plan_last_launches": ([P], c_int32),
         "fo_plan_last_split_tiles": ([P], c_int32),
         "fo_check_device_pointers": ([c_int32, PP, P], c_int32),
+        "fo_rmsnorm": ([POINTER(NormDesc), c_int64, PP, PP, P, PP, PP, PP, PP, PP, P], c_int32),
+        "fo_rmsnorm_bwd": ([POINTER(NormDesc), c_int64, PP, PP, PP, P, PP, PP, P, P, P], c_int32),
+        "fo_rmsnorm_bwd_workspace": ([POINTER(NormDesc), c_int64, POINTER(c_size_t)], c_int32),
+        "fo_quant_fp8": ([c_int32, c_int64, c_int64, c_int32, c_int32, PP, PP, PP, PP, PP, P], c_int32),
+        "fo_gemm_fp8": ([POINTER(GemmFp8Desc), c_int64, PP, PP, PP, PP, PP, P, P], c_int32),
+        "fo_gemm_fp8_workspace": ([POINTER(GemmFp8Desc), c_int64, POINTER(c_size_t)], c_int32),
+        "fo_ops_workspace_init": ([P, c_size_t, P], c_int32),
+        "fo_ops_status_query": ([P, P, POINTER(c_int32)], c_int32),
+        "fo_rope_init": ([POINTER(RopeDesc)], c_int32),
+        "fo_rope": ([POINTER(RopeDesc), c_int64, P, c_int32, PP, PP, PP, POINTER(c_int64), PP, PP, PP,
+                     POINTER(c_int64), c_int32, P], c_int32),
         "fo_status_string": ([c_int32], ctypes.c_char_p),
         "fo_version": ([], c_int32),
     }
@@ -359,6 +393,205 @@ def trace_summary(stamps):
     end = max(r[6] for r in stamps)
     return {"span_ns": end - start, "mma_end_ns": mma_end - start, "transfers_end_ns": xfer_end - start,
             "exposed_tail_ns": max(0, xfer_end - mma_end)}
+
+
+# ---- operators between the residual stream and the attention
+
+_TORCH_DTYPES = None
+
+
+def _types():
+    """DTYPES code -> the torch types that may stand for it (8-bit values: e4m3 or raw bytes)."""
+    global _TORCH_DTYPES
+    if _TORCH_DTYPES is None:
+        import torch
+        _TORCH_DTYPES = {0: (torch.bfloat16,), 1: (torch.float32,), "q": (torch.float8_e4m3fn, torch.uint8)}
+    return _TORCH_DTYPES
+
+
+def _checked(x, n: int, types, what: str) -> int:
+    """The address of x: a dense CUDA tensor of n values of one of `types`, or a raw address."""
+    if isinstance(x, int):
+        return x
+    if x.dtype not in types:
+        raise ValueError(f"{what}: {x.dtype} given, {' or '.join(map(str, types))} expected")
+    if x.numel() != n:
+        raise ValueError(f"{what}: {x.numel()} values given, {n} expected")
+    return _ptr(x)
+
+
+def _checked_array(xs, R: int, n: int, types, what: str):
+    if xs is None:
+        return None
+    if len(xs) != R:
+        raise ValueError(f"{what}: {len(xs)} tensors given, one for each of {R} ranks expected")
+    return (c_void_p * R)(*[_checked(x, n, types, what) for x in xs])
+
+
+def fo_norm_desc(H: int, *, R: int = 1, dtype="bf16", w_dtype=None, eps: float = 1e-6, w_offset: float = 0.0) -> NormDesc:
+    """Description of an RMSNorm of H columns over R shards of rows (the weight has the rows' dtype unless w_dtype
+    says otherwise)."""
+    d = NormDesc()
+    d.R, d.H, d.eps, d.w_offset = R, H, eps, w_offset
+    d.dtype, d.w_dtype = DTYPES[dtype], DTYPES[dtype if w_dtype is None else w_dtype]
+    return d
+
+
+def fo_rmsnorm(desc: NormDesc, rows: int, x, residual, weight, h=None, y=None, q=None, scale=None, rstd=None,
+               stream=None) -> None:
+    """x, residual, h, y [rows, H], q [rows, H] in 8 bits, scale [rows, ceil(H/128)], rstd [rows]: one tensor for each
+    shard; all but x and weight may be None (see the header for what is computed)."""
+    R, H, t = desc.R, desc.H, _types()
+    n, types = rows * H, t[desc.dtype]
+    groups = rows * -(-H // FO_FP8_BLOCK)
+    _check(load().fo_rmsnorm(desc, rows, _checked_array(x, R, n, types, "x"),
+                             _checked_array(residual, R, n, types, "residual"),
+                             _checked(weight, H, t[desc.w_dtype], "weight"), _checked_array(h, R, n, types, "h"),
+                             _checked_array(y, R, n, types, "y"), _checked_array(q, R, n, t["q"], "q"),
+                             _checked_array(scale, R, groups, t[1], "scale"),
+                             _checked_array(rstd, R, rows, t[1], "rstd"), _stream(stream)), "fo_rmsnorm")
+
+
+def fo_rmsnorm_bwd_workspace(desc: NormDesc, rows: int) -> int:
+    n = c_size_t()
+    _check(load().fo_rmsnorm_bwd_workspace(desc, rows, ctypes.byref(n)), "fo_rmsnorm_bwd_workspace")
+    return n.value
+
+
+def fo_rmsnorm_bwd(desc: NormDesc, rows: int, dy, dh, h, weight, rstd, dx, dweight=None, ws=None, stream=None) -> None:
+    """dy, dh (may be None), h, dx [rows, H] and rstd [rows]: one tensor for each shard; dweight [H] fp32 or None."""
+    R, H, t = desc.R, desc.H, _types()
+    n, types = rows * H, t[desc.dtype]
+    if ws is not None and not isinstance(ws, int) and ws.numel() * ws.element_size() < fo_rmsnorm_bwd_workspace(desc, rows):
+        raise ValueError("fo_rmsnorm_bwd: the workspace is smaller than fo_rmsnorm_bwd_workspace says")
+    _check(load().fo_rmsnorm_bwd(desc, rows, _checked_array(dy, R, n, types, "dy"),
+                                 _checked_array(dh, R, n, types, "dh"), _checked_array(h, R, n, types, "h"),
+                                 _checked(weight, H, t[desc.w_dtype], "weight"),
+                                 _checked_array(rstd, R, rows, t[1], "rstd"), _checked_array(dx, R, n, types, "dx"),
+                                 None if dweight is None else _checked(dweight, H, t[1], "dweight"), _ptr(ws),
+                                 _stream(stream)), "fo_rmsnorm_bwd")
+
+
+def fo_quant_fp8(rows: int, cols: int, x, q, scale, qt=None, scale_t=None, *, block_rows: int = 1, dtype=None,
+                 stream=None) -> None:
+    """x [rows, cols] -> q in 8 bits and scale (one tensor for each rank); block_rows 1: scales of 1 x 128 values,
+    128: of 128 x 128, with the transposed copy qt [cols, rows] and scale_t if given. The dtype is x's own unless
+    x holds raw addresses."""
+    t = _types()
+    if dtype is None:
+        dtype = "bf16" if x[0].dtype in t[0] else "f32"
+    R, code = len(x), DTYPES[dtype]
+    up, across = (-(-rows // block_rows) if block_rows > 0 else 0), -(-cols // FO_FP8_BLOCK)
+    _check(load().fo_quant_fp8(R, rows, cols, code, block_rows, _checked_array(x, R, rows * cols, t[code], "x"),
+                               _checked_array(q, R, rows * cols, t["q"], "q"),
+                               _checked_array(scale, R, up * across, t[1], "scale"),
+                               _checked_array(qt, R, rows * cols, t["q"], "qt"),
+                               _checked_array(scale_t, R, up * across, t[1], "scale_t"), _stream(stream)),
+           "fo_quant_fp8")
+
+
+def fo_gemm_fp8_desc(N: int, K: int, *, R: int = 1, out_dtype="bf16") -> GemmFp8Desc:
+    d = GemmFp8Desc()
+    d.R, d.N, d.K, d.out_dtype = R, N, K, DTYPES[out_dtype]
+    return d
+
+
+def fo_gemm_fp8_workspace(desc: GemmFp8Desc, M: int) -> int:
+    n = c_size_t()
+    _check(load().fo_gemm_fp8_workspace(desc, M, ctypes.byref(n)), "fo_gemm_fp8_workspace")
+    return n.value
+
+
+def fo_gemm_fp8(desc: GemmFp8Desc, M: int, A, sA, W, sW, Y, ws, stream=None) -> None:
+    """Y_r [M, N] = (A_r scaled by sA_r) (W_r scaled by sW_r)^T: A [M, K] and W [N, K] in 8 bits, sA [M, ceil(K/128)],
+    sW [ceil(N/128), ceil(K/128)]; one tensor for each rank."""
+    R, N, K, t = desc.R, desc.N, desc.K, _types()
+    k = -(-K // FO_FP8_BLOCK)
+    _check(load().fo_gemm_fp8(desc, M, _checked_array(A, R, M * K, t["q"], "A"),
+                              _checked_array(sA, R, M * k, t[1], "sA"), _checked_array(W, R, N * K, t["q"], "W"),
+                              _checked_array(sW, R, -(-N // FO_FP8_BLOCK) * k, t[1], "sW"),
+                              _checked_array(Y, R, M * N, t[desc.out_dtype], "Y"), _ptr(ws), _stream(stream)),
+           "fo_gemm_fp8")
+
+
+def fo_ops_workspace_init(ws, stream=None) -> None:
+    _check(load().fo_ops_workspace_init(_ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "fo_ops_workspace_init")
+
+
+def fo_ops_status_query(ws, stream=None):
+    """Returns (status code, info) without raising, like fo_status_query."""
+    info = (c_int32 * 4)()
+    code = load().fo_ops_status_query(_ptr(ws), _stream(stream), info)
+    return code, list(info)
+
+
+def fo_rope_desc(head_dim: int, heads_q: int, heads_k: int = 0, heads_v: int = 0, *, R: int = 1, rot_dim=None,
+                 layout="half", dtype="bf16", base: float = 10000.0, scaling="none", stretch: float = 1.0,
+                 trained: float = 0.0, slow: float = 0.0, fast: float = 0.0) -> RopeDesc:
+    """Description of the rotary positions of heads_q + heads_k heads a rank, heads_v more copied (fo_rope_init
+    checks it and fills in the pairs' frequencies)."""
+    d = RopeDesc()
+    d.R, d.head_dim, d.rot_dim = R, head_dim, head_dim if rot_dim is None else rot_dim
+    d.heads_q, d.heads_k, d.heads_v = heads_q, heads_k, heads_v
+    d.layout, d.dtype, d.scaling = ROPE_LAYOUTS[layout], DTYPES[dtype], ROPE_SCALINGS[scaling]
+    d.base, d.stretch, d.trained, d.slow, d.fast = base, stretch, trained, slow, fast
+    _check(load().fo_rope_init(d), "fo_rope_init")
+    return d
+
+
+def _row_array(xs, R: int, rows: int, width: int, types, what: str):
+    """Addresses and the common row stride of R matrices [rows, width] whose rows are dense (parts of packed rows
+    among them)."""
+    if len(xs) != R:
+        raise ValueError(f"{what}: {len(xs)} tensors given, one for each of {R} ranks expected")
+    ld, at = None, []
+    for x in xs:
+        if isinstance(x, int):
+            at.append(x)
+            continue
+        if x.dtype not in types:
+            raise ValueError(f"{what}: {x.dtype} given, {' or '.join(map(str, types))} expected")
+        if x.dim() != 2 or x.shape[0] != rows or x.shape[1] != width or (width > 1 and rows > 0 and x.stride(1) != 1):
+            raise ValueError(f"{what}: {rows} rows of {width} dense values expected, {tuple(x.shape)} given")
+        stride = x.stride(0) if rows > 1 else width
+        if ld is not None and stride != ld:
+            raise ValueError(f"{what}: every rank's rows need the same stride")
+        if not x.is_cuda and not x.is_pinned():
+            raise ValueError("tensors passed to libflashoverlap must be CUDA tensors (or pinned host memory)")
+        ld = stride
+        at.append(x.data_ptr())
+    return (c_void_p * R)(*at), width if ld is None else ld
+
+
+def fo_rope(desc: RopeDesc, rows: int, positions, q_in, k_in, v_in, q_out, k_out, v_out, *, inverse: bool = False,
+            stream=None) -> None:
+    """Turn Q and K by their positions ([rows] int32 or int64, None: 0, 1, ...) and copy V; one matrix [rows, heads *
+    head_dim] for each rank, whose rows may be parts of packed ones; k_*, v_* are not looked at without heads of
+    their kind. inverse: turn back (the gradient)."""
+    types = _types()[desc.dtype]
+    D, R = desc.head_dim, desc.R
+    ins, outs, ld_in, ld_out = [], [], (c_int64 * 3)(), (c_int64 * 3)()
+    for j, (heads, i, o, what) in enumerate(((desc.heads_q, q_in, q_out, "Q"), (desc.heads_k, k_in, k_out, "K"),
+                                             (desc.heads_v, v_in, v_out, "V"))):
+        if heads == 0:
+            ins.append(None)
+            outs.append(None)
+            continue
+        a, ld_in[j] = _row_array(i, R, rows, heads * D, types, what)
+        b, ld_out[j] = _row_array(o, R, rows, heads * D, types, what)
+        ins.append(a)
+        outs.append(b)
+    at, size = 0, 8
+    if positions is not None and not isinstance(positions, int):
+        size = positions.element_size()
+        if positions.is_floating_point() or size not in (4, 8):
+            raise ValueError(f"positions: int32 or int64 expected, {positions.dtype} given")
+        at = _checked(positions, rows, (positions.dtype,), "positions")
+    elif positions is not None:
+        at = positions
+    _check(load().fo_rope(desc, rows, at, size, *ins, ld_in, *outs, ld_out, 1 if inverse else 0, _stream(stream)),
+           "fo_rope")
 
 
 def fo_plan_last_launches(plan: Plan) -> int:

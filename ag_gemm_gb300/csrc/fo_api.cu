@@ -611,6 +611,13 @@ fo_status fo_internal_rs_params_nocache(fo_plan_t p, const void* const* X, const
 }
 
 fo_status fo_internal_check_ptrs(int R, const void* const* a) { return check_ptrs(R, a); }
+fo_status fo_internal_device_sms(int* sms) {
+  DevInfo di;
+  if (fo_status st = device_info(&di)) return st;
+  if (!di.sm103) return FO_ERR_UNSUPPORTED;
+  *sms = di.sms;
+  return FO_OK;
+}
 fo_status fo_internal_check_device_ptrs(int R, const void* const* a, fo_stream_t stream) {
   return check_device_ptrs(R, a, (cudaStream_t)stream);
 }

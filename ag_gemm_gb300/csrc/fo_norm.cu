@@ -1,0 +1,420 @@
+// RMSNorm with the residual's addition, its output in 16/32 bits, in 8 bits
+// with one scale for 128 columns, or both; and its gradient.
+#include <string.h>
+
+#include "fo_ops.h"
+
+namespace fo_ops {
+namespace {
+
+struct NormParams {
+  const void* x[kMaxR];
+  const void* res[kMaxR];
+  void* h[kMaxR];
+  void* y[kMaxR];
+  uint8_t* q[kMaxR];
+  float* scale[kMaxR];
+  float* rstd[kMaxR];
+  const void* w;
+  int64_t rows, total;   // rows of a shard, rows of all shards
+  int32_t H, groups;
+  float eps, w_offset;
+  bool has_res, has_h, has_y, has_q, has_rstd, w_f32;
+};
+
+// Where a thread's values lie. A warp's chunk c is 32 * E columns: with
+// 16-byte alignment each lane holds E = 16 / sizeof(T) neighbouring ones (one
+// wide access), else four that are 32 apart (each access still covers whole
+// sectors). Either way a group of 128 columns belongs to one warp, or to one
+// half of it, so its maximum never leaves the warp.
+template <typename T, bool WIDE>
+struct Chunk {
+  static constexpr int E = WIDE ? Vec16<T>::N : 4;
+  static constexpr int COLS = 32 * E;
+  static constexpr int GROUP_LANES = WIDE ? 128 / E : 32;
+  static __device__ __forceinline__ int col(int chunk, int lane, int j) {
+    return chunk * COLS + (WIDE ? lane * E + j : lane + 32 * j);
+  }
+  static __device__ __forceinline__ void load(const T* p, int chunk, int lane, int H, float (&f)[E]) {
+    if constexpr (WIDE) {
+      const int c = col(chunk, lane, 0);
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (c < H) u = *reinterpret_cast<const uint4*>(p + c);
+      Vec16<T>::unpack(u, f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int c = col(chunk, lane, j);
+        f[j] = c < H ? to_f(p[c]) : 0.f;
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, int chunk, int lane, int H, const float (&f)[E]) {
+    if constexpr (WIDE) {
+      const int c = col(chunk, lane, 0);
+      if (c < H) *reinterpret_cast<uint4*>(p + c) = Vec16<T>::pack(f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int c = col(chunk, lane, j);
+        if (c < H) from_f(f[j], p[c]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void store_e4m3(uint8_t* p, int chunk, int lane, int H, const float (&f)[E]) {
+    if constexpr (WIDE) {
+      const int c = col(chunk, lane, 0);
+      if (c < H) {
+        if constexpr (E == 8)
+          *reinterpret_cast<uint2*>(p + c) = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+        else
+          *reinterpret_cast<uint32_t*>(p + c) = e4m3x4(f[0], f[1], f[2], f[3]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int c = col(chunk, lane, j);
+        if (c < H) p[c] = (uint8_t)e4m3x2(f[j], 0.f);
+      }
+    }
+  }
+  // The weight's values of the chunk (dtype its own, read value by value).
+  static __device__ __forceinline__ void load_w(const void* w, bool f32, float offset, int chunk, int lane, int H,
+                                                float (&f)[E]) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const int c = col(chunk, lane, j);
+      f[j] = c >= H ? 0.f
+                    : offset + (f32 ? static_cast<const float*>(w)[c]
+                                    : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c]));
+    }
+  }
+};
+
+// Sum over the block's NW warps, the same in every thread. `smem`: NW floats.
+template <int NW>
+__device__ __forceinline__ float block_sum(float v, float* smem) {
+  v = warp_sum(v);
+  if constexpr (NW == 1) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) smem[warp] = v;
+  __syncthreads();
+  v = warp_sum(lane < NW ? smem[lane] : 0.f);
+  __syncthreads();
+  return v;
+}
+
+template <typename T, bool WIDE, int NW, int C>
+__global__ void __launch_bounds__(NW * 32) rmsnorm_kernel(const __grid_constant__ NormParams p) {
+  using K = Chunk<T, WIDE>;
+  __shared__ float smem[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t row = blockIdx.x; row < p.total; row += gridDim.x) {
+    const int r = (int)(row / p.rows);
+    const int64_t at = row - r * p.rows;
+    const int64_t off = at * p.H;
+    float s[C][K::E];
+    float sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int chunk = c * NW + warp;
+      K::load(static_cast<const T*>(p.x[r]) + off, chunk, lane, p.H, s[c]);
+      if (p.has_res) {
+        float t[K::E];
+        K::load(static_cast<const T*>(p.res[r]) + off, chunk, lane, p.H, t);
+#pragma unroll
+        for (int j = 0; j < K::E; ++j) s[c][j] += t[j];
+      }
+      if (p.has_h) K::store(static_cast<T*>(p.h[r]) + off, chunk, lane, p.H, s[c]);
+#pragma unroll
+      for (int j = 0; j < K::E; ++j) sum = fmaf(s[c][j], s[c][j], sum);
+    }
+    const float rstd = 1.f / sqrtf(block_sum<NW>(sum, smem) / (float)p.H + p.eps);
+    if (p.has_rstd && threadIdx.x == 0) p.rstd[r][at] = rstd;
+    if (!p.has_y && !p.has_q) continue;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int chunk = c * NW + warp;
+      float w[K::E];
+      K::load_w(p.w, p.w_f32, p.w_offset, chunk, lane, p.H, w);
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < K::E; ++j) {
+        s[c][j] = s[c][j] * rstd * w[j];
+        amax = max_nan(amax, fabsf(s[c][j]));
+      }
+      if (p.has_y) K::store(static_cast<T*>(p.y[r]) + off, chunk, lane, p.H, s[c]);
+      if (p.has_q) {
+        const float scale = scale_of(lanes_max<K::GROUP_LANES>(amax));
+        const float inv = 1.f / scale;
+#pragma unroll
+        for (int j = 0; j < K::E; ++j) s[c][j] *= inv;
+        K::store_e4m3(p.q[r] + off, chunk, lane, p.H, s[c]);
+        const int group = K::col(chunk, lane, 0) / FO_FP8_BLOCK;
+        if (lane % K::GROUP_LANES == 0 && group < p.groups) p.scale[r][at * p.groups + group] = scale;
+      }
+    }
+  }
+}
+
+struct NormBwdParams {
+  const void* dy[kMaxR];
+  const void* dh[kMaxR];
+  const void* h[kMaxR];
+  const float* rstd[kMaxR];
+  void* dx[kMaxR];
+  const void* w;
+  float* part;   // [gridDim.x][H] partial sums of dweight
+  int64_t rows, total;
+  int32_t H;
+  float w_offset;
+  bool has_dh, has_dw, w_f32;
+};
+
+// A block takes every gridDim.x-th row and keeps its columns' share of the
+// weight's gradient in registers.
+template <typename T, bool WIDE, int NW, int C>
+__global__ void __launch_bounds__(NW * 32) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+  using K = Chunk<T, WIDE>;
+  __shared__ float smem[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float dw[C][K::E];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < K::E; ++j) dw[c][j] = 0.f;
+  for (int64_t row = blockIdx.x; row < p.total; row += gridDim.x) {
+    const int r = (int)(row / p.rows);
+    const int64_t at = row - r * p.rows;
+    const int64_t off = at * p.H;
+    const float rstd = p.rstd[r][at];
+    float h[C][K::E], u[C][K::E];
+    float sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int chunk = c * NW + warp;
+      float w[K::E];
+      K::load(static_cast<const T*>(p.dy[r]) + off, chunk, lane, p.H, u[c]);
+      K::load(static_cast<const T*>(p.h[r]) + off, chunk, lane, p.H, h[c]);
+      K::load_w(p.w, p.w_f32, p.w_offset, chunk, lane, p.H, w);
+#pragma unroll
+      for (int j = 0; j < K::E; ++j) {
+        dw[c][j] = fmaf(u[c][j] * rstd, h[c][j], dw[c][j]);
+        u[c][j] *= w[j];
+        sum = fmaf(u[c][j], h[c][j], sum);
+      }
+    }
+    const float k = block_sum<NW>(sum, smem) / (float)p.H * rstd * rstd * rstd;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int chunk = c * NW + warp;
+      float d[K::E];
+#pragma unroll
+      for (int j = 0; j < K::E; ++j) d[j] = rstd * u[c][j] - h[c][j] * k;
+      if (p.has_dh) {
+        float t[K::E];
+        K::load(static_cast<const T*>(p.dh[r]) + off, chunk, lane, p.H, t);
+#pragma unroll
+        for (int j = 0; j < K::E; ++j) d[j] += t[j];
+      }
+      K::store(static_cast<T*>(p.dx[r]) + off, chunk, lane, p.H, d);
+    }
+  }
+  if (p.has_dw) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int j = 0; j < K::E; ++j) {
+        const int col = K::col(c * NW + warp, lane, j);
+        if (col < p.H) p.part[(int64_t)blockIdx.x * p.H + col] = dw[c][j];
+      }
+  }
+}
+
+// dweight[c] = sum of the blocks' partial sums, in block order.
+__global__ void __launch_bounds__(256) dweight_kernel(const float* part, int blocks, int H, float* dw) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= H) return;
+  float s = 0.f;
+  for (int b = 0; b < blocks; ++b) s += part[(int64_t)b * H + c];
+  dw[c] = s;
+}
+
+fo_status check_desc(const fo_norm_desc* d, int64_t rows) {
+  if (!d) return FO_ERR_INVALID_ARG;
+  if (d->R < 1 || d->R > kMaxR || d->reserved[0] || d->reserved[1]) return FO_ERR_INVALID_ARG;
+  if (d->H < 1 || d->H > FO_NORM_MAX_H || rows < 0 || rows > INT32_MAX) return FO_ERR_SHAPE;
+  if ((d->dtype != FO_BF16 && d->dtype != FO_F32) || (d->w_dtype != FO_BF16 && d->w_dtype != FO_F32))
+    return FO_ERR_DTYPE;
+  if (!(d->eps >= 0.f) || !(d->w_offset == d->w_offset)) return FO_ERR_INVALID_ARG;
+  return FO_OK;
+}
+
+size_t elem(int32_t dtype) { return dtype == FO_BF16 ? 2 : 4; }
+
+// Blocks of the backward pass: enough to fill the GPU, few enough that their
+// partial sums stay small.
+int bwd_blocks(int64_t total) { return (int)(total < 2 * FO_GB300_SMS ? total : 2 * FO_GB300_SMS); }
+
+// Calls f.template operator()<T, WIDE, NW, C>() with the fewest warps whose
+// chunks cover H: one chunk a lane while 8 warps suffice, then up to 32 warps
+// and up to 8 chunks.
+template <typename T, bool WIDE, typename F>
+fo_status by_width(int H, F&& f) {
+  const int n = (H + Chunk<T, WIDE>::COLS - 1) / Chunk<T, WIDE>::COLS;
+  if (n <= 1) return f.template operator()<T, WIDE, 1, 1>();
+  if (n <= 2) return f.template operator()<T, WIDE, 2, 1>();
+  if (n <= 4) return f.template operator()<T, WIDE, 4, 1>();
+  if (n <= 8) return f.template operator()<T, WIDE, 8, 1>();
+  if (n <= 16) return f.template operator()<T, WIDE, 8, 2>();
+  if (n <= 32) return f.template operator()<T, WIDE, 16, 2>();
+  if (n <= 64) return f.template operator()<T, WIDE, 16, 4>();
+  if (n <= 128) return f.template operator()<T, WIDE, 32, 4>();
+  if constexpr (Chunk<T, WIDE>::COLS * 128 < FO_NORM_MAX_H) return f.template operator()<T, WIDE, 32, 8>();
+  return FO_ERR_SHAPE;
+}
+template <typename F>
+fo_status by_type(int32_t dtype, bool wide, int H, F&& f) {
+  if (dtype == FO_BF16) return wide ? by_width<__nv_bfloat16, true>(H, f) : by_width<__nv_bfloat16, false>(H, f);
+  return wide ? by_width<float, true>(H, f) : by_width<float, false>(H, f);
+}
+
+struct LaunchFwd {
+  const NormParams& k;
+  cudaStream_t s;
+  int R;
+  template <typename T, bool WIDE, int NW, int C>
+  fo_status operator()() const {
+    const int grid = (int)(k.total < (1 << 30) ? k.total : (1 << 30));
+    rmsnorm_kernel<T, WIDE, NW, C><<<grid, NW * 32, 0, s>>>(k);
+    return launched("rmsnorm", R, k.rows, k.H, grid, NW * 32);
+  }
+};
+struct LaunchBwd {
+  const NormBwdParams& k;
+  cudaStream_t s;
+  int R, grid;
+  template <typename T, bool WIDE, int NW, int C>
+  fo_status operator()() const {
+    rmsnorm_bwd_kernel<T, WIDE, NW, C><<<grid, NW * 32, 0, s>>>(k);
+    return launched("rmsnorm_bwd", R, k.rows, k.H, grid, NW * 32);
+  }
+};
+
+}  // namespace
+}  // namespace fo_ops
+
+extern "C" fo_status fo_rmsnorm(const fo_norm_desc* d, int64_t rows, const void* const* x,
+                                const void* const* residual, const void* weight, void* const* h, void* const* y,
+                                void* const* q, float* const* scale, float* const* rstd, fo_stream_t stream) {
+  using namespace fo_ops;
+  fo_status st = check_desc(d, rows);
+  if (st) return st;
+  if (!weight || (!h && !y && !q && !rstd) || (!q != !scale)) return FO_ERR_INVALID_ARG;
+  if (rows == 0) return FO_OK;
+  const int R = d->R;
+  const size_t es = elem(d->dtype);
+  typedef const void* const* A;
+  if ((st = check_array(R, x, es)) || (residual && (st = check_array(R, residual, es))) ||
+      (h && (st = check_array(R, (A)h, es))) || (y && (st = check_array(R, (A)y, es))) ||
+      (q && ((st = check_array(R, (A)q, 1)) || (st = check_array(R, (A)scale, 4)))) ||
+      (rstd && (st = check_array(R, (A)rstd, 4))))
+    return st;
+  if (!aligned(weight, elem(d->w_dtype))) return FO_ERR_ALIGN;
+  int sms;
+  if ((st = device_sms(&sms))) return st;
+  PtrList l;
+  l.add(R, x), l.add(R, residual), l.add(R, (A)h), l.add(R, (A)y), l.add(R, (A)q), l.add(R, (A)scale);
+  l.add(R, (A)rstd), l.add(weight);
+  if ((st = check_device(l, stream))) return st;
+  NormParams k;
+  memset(&k, 0, sizeof(k));
+  for (int r = 0; r < R; ++r) {
+    k.x[r] = x[r];
+    k.res[r] = residual ? residual[r] : nullptr;
+    k.h[r] = h ? h[r] : nullptr;
+    k.y[r] = y ? y[r] : nullptr;
+    k.q[r] = q ? static_cast<uint8_t*>(q[r]) : nullptr;
+    k.scale[r] = scale ? scale[r] : nullptr;
+    k.rstd[r] = rstd ? rstd[r] : nullptr;
+  }
+  k.w = weight;
+  k.rows = rows;
+  k.total = rows * R;
+  k.H = d->H;
+  k.groups = (d->H + FO_FP8_BLOCK - 1) / FO_FP8_BLOCK;
+  k.eps = d->eps;
+  k.w_offset = d->w_offset;
+  k.has_res = residual, k.has_h = h, k.has_y = y, k.has_q = q, k.has_rstd = rstd;
+  k.w_f32 = d->w_dtype == FO_F32;
+  const bool wide = (d->H * es) % 16 == 0 && all_aligned(R, x, 16) && all_aligned(R, residual, 16) &&
+                    all_aligned(R, (A)h, 16) && all_aligned(R, (A)y, 16) && all_aligned(R, (A)q, 8);
+  return by_type(d->dtype, wide, d->H, LaunchFwd{k, (cudaStream_t)stream, R});
+}
+
+extern "C" fo_status fo_rmsnorm_bwd_workspace(const fo_norm_desc* d, int64_t rows, size_t* bytes) {
+  using namespace fo_ops;
+  const fo_status st = check_desc(d, rows);
+  if (st) return st;
+  if (!bytes) return FO_ERR_INVALID_ARG;
+  const size_t n = (size_t)bwd_blocks(rows * d->R) * (size_t)d->H * sizeof(float);
+  *bytes = n ? n : 16;
+  return FO_OK;
+}
+
+extern "C" fo_status fo_rmsnorm_bwd(const fo_norm_desc* d, int64_t rows, const void* const* dy,
+                                    const void* const* dh, const void* const* h, const void* weight,
+                                    const float* const* rstd, void* const* dx, float* dweight, void* ws,
+                                    fo_stream_t stream) {
+  using namespace fo_ops;
+  fo_status st = check_desc(d, rows);
+  if (st) return st;
+  if (!weight || (dweight && !ws)) return FO_ERR_INVALID_ARG;
+  const int R = d->R;
+  const size_t es = elem(d->dtype);
+  typedef const void* const* A;
+  if (rows > 0 && ((st = check_array(R, dy, es)) || (dh && (st = check_array(R, dh, es))) ||
+                   (st = check_array(R, h, es)) || (st = check_array(R, (A)rstd, 4)) ||
+                   (st = check_array(R, (A)dx, es))))
+    return st;
+  if (!aligned(weight, elem(d->w_dtype)) || !aligned(dweight, 4) || !aligned(ws, 16)) return FO_ERR_ALIGN;
+  int sms;
+  if ((st = device_sms(&sms))) return st;
+  PtrList l;
+  if (rows > 0) l.add(R, dy), l.add(R, dh), l.add(R, h), l.add(R, (A)rstd), l.add(R, (A)dx), l.add(weight);
+  l.add(dweight), l.add(ws);
+  if ((st = check_device(l, stream))) return st;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (rows == 0) {   // an empty sum
+    if (dweight && cudaMemsetAsync(dweight, 0, (size_t)d->H * 4, s) != cudaSuccess) {
+      cudaGetLastError();
+      return FO_ERR_CUDA;
+    }
+    return FO_OK;
+  }
+  NormBwdParams k;
+  memset(&k, 0, sizeof(k));
+  for (int r = 0; r < R; ++r) {
+    k.dy[r] = dy[r];
+    k.dh[r] = dh ? dh[r] : nullptr;
+    k.h[r] = h[r];
+    k.rstd[r] = rstd[r];
+    k.dx[r] = dx[r];
+  }
+  k.w = weight;
+  k.part = static_cast<float*>(ws);
+  k.rows = rows;
+  k.total = rows * R;
+  k.H = d->H;
+  k.w_offset = d->w_offset;
+  k.has_dh = dh, k.has_dw = dweight;
+  k.w_f32 = d->w_dtype == FO_F32;
+  const bool wide = (d->H * es) % 16 == 0 && all_aligned(R, dy, 16) && all_aligned(R, dh, 16) &&
+                    all_aligned(R, h, 16) && all_aligned(R, (A)dx, 16);
+  const int grid = bwd_blocks(k.total);
+  if ((st = by_type(d->dtype, wide, d->H, LaunchBwd{k, s, R, grid}))) return st;
+  if (!dweight) return FO_OK;
+  const int cols = (d->H + 255) / 256;
+  dweight_kernel<<<cols, 256, 0, s>>>(k.part, grid, d->H, dweight);
+  return launched("rmsnorm_dweight", R, grid, d->H, cols, 256);
+}

@@ -1,0 +1,135 @@
+// Host-side checks and device helpers shared by the operators between the
+// residual stream and the attention (norm, quantisation, 8-bit product,
+// rotary positions).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fo_internal.h"
+
+namespace fo_ops {
+
+constexpr int kMaxR = FO_MAX_R;
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// R non-null pointers of `align` bytes' alignment.
+inline fo_status check_array(int R, const void* const* a, size_t align) {
+  if (!a) return FO_ERR_INVALID_ARG;
+  for (int r = 0; r < R; ++r) {
+    if (!a[r]) return FO_ERR_INVALID_ARG;
+    if (!aligned(a[r], align)) return FO_ERR_ALIGN;
+  }
+  return FO_OK;
+}
+inline bool all_aligned(int R, const void* const* a, size_t align) {
+  if (a)
+    for (int r = 0; r < R; ++r)
+      if (!aligned(a[r], align)) return false;
+  return true;
+}
+
+// The device addresses of one call, gathered so that the driver is asked
+// about all of them in one go, after every other check.
+struct PtrList {
+  const void* p[16 * kMaxR];
+  int n = 0;
+  void add(const void* q) {
+    if (q) p[n++] = q;
+  }
+  void add(int R, const void* const* a) {
+    if (a)
+      for (int r = 0; r < R; ++r)
+        if (r == 0 || a[r] != a[r - 1]) add(a[r]);
+  }
+};
+
+// The SMs of the current device; FO_ERR_UNSUPPORTED when it is no sm_103.
+inline fo_status device_sms(int* sms) { return fo_internal_device_sms(sms); }
+// fo_check_device_pointers on the list.
+fo_status check_device(const PtrList& l, fo_stream_t stream);
+// After a launch: FO_OK or FO_ERR_CUDA, with FO_LOG's line.
+fo_status launched(const char* what, int R, int64_t rows, int64_t cols, int grid, int threads);
+
+// ------------------------------------------------------------- device side
+
+constexpr float kE4M3Top = 448.f;
+constexpr float kLeastScale = 1.17549435e-38f;   // 2^-126
+
+// Maximum that hands a NaN on (fmaxf drops it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+__device__ __forceinline__ float scale_of(float amax) { return max_nan(amax / kE4M3Top, kLeastScale); }
+
+// Two / four values in 8 bits, the first in the lowest byte. Rounded to
+// nearest even; beyond 448 (only by the quotient's rounding) held to 448.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f(float v, float& o) { o = v; }
+__device__ __forceinline__ void from_f(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
+
+// 16 bytes <-> the fp32 values they hold.
+template <typename T>
+struct Vec16;
+template <>
+struct Vec16<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
+    f[0] = __uint_as_float(u.x);
+    f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z);
+    f[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+template <>
+struct Vec16<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {   // over LANES neighbouring lanes
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+}  // namespace fo_ops

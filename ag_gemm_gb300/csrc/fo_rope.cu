@@ -1,0 +1,174 @@
+// Rotary positions on Q and K, V copied: packed rows to parted ones or back,
+// or in place.
+#include <math.h>
+#include <string.h>
+
+#include "fo_ops.h"
+
+namespace fo_ops {
+namespace {
+
+struct RopeParams {
+  const void* in[3][kMaxR];
+  void* out[3][kMaxR];
+  int64_t ld_in[3], ld_out[3];
+  const void* positions;
+  int64_t rows;
+  int32_t pos_bytes;
+  int32_t heads[3];
+  int32_t D, rot;
+  int32_t half;       // layout
+  float factor, sign;
+  uint64_t turns[FO_ROPE_MAX_DIM / 2];
+};
+
+// cos and sin (times the factor) of position * turns: the product modulo
+// 2^64 is the angle's fraction of a turn, exact but for the frequency's own
+// last bit; as a signed number it lies in [-1/2, 1/2).
+__device__ __forceinline__ float2 rotation(const RopeParams& p, int64_t pos, int pair) {
+  const int64_t frac = (int64_t)((uint64_t)pos * p.turns[pair]);
+  float s, c;
+  sincospif((float)frac * 1.08420217e-19f, &s, &c);   // 2^-63: half turns
+  return make_float2(c * p.factor, s * p.factor * p.sign);
+}
+
+__device__ __forceinline__ int64_t position_of(const RopeParams& p, int64_t t) {
+  if (!p.positions) return t;
+  return p.pos_bytes == 8 ? static_cast<const int64_t*>(p.positions)[t]
+                          : (int64_t)static_cast<const int32_t*>(p.positions)[t];
+}
+
+// One block for each row and rank: the angles once, then every pair.
+template <typename T>
+__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ float2 rot[FO_ROPE_MAX_DIM / 2];
+  const int64_t t = blockIdx.x;
+  const int r = blockIdx.y, pairs = p.rot / 2;
+  if (threadIdx.x < pairs) rot[threadIdx.x] = rotation(p, position_of(p, t), threadIdx.x);
+  __syncthreads();
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {
+    if (!p.heads[part]) continue;
+    const T* in = static_cast<const T*>(p.in[part][r]) + t * p.ld_in[part];
+    T* out = static_cast<T*>(p.out[part][r]) + t * p.ld_out[part];
+    const int per_head = part == 2 ? p.D : pairs + p.D - p.rot;
+    for (int i = threadIdx.x; i < p.heads[part] * per_head; i += 256) {
+      const int head = i / per_head, k = i - head * per_head;
+      const int at = head * p.D;
+      if (part == 2) {
+        out[at + k] = in[at + k];
+      } else if (k >= pairs) {
+        out[at + k + pairs] = in[at + k + pairs];
+      } else {
+        const int ia = at + (p.half ? k : 2 * k), ib = p.half ? ia + pairs : ia + 1;
+        const float a = to_f(in[ia]), b = to_f(in[ib]);
+        from_f(a * rot[k].x - b * rot[k].y, out[ia]);
+        from_f(b * rot[k].x + a * rot[k].y, out[ib]);
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace fo_ops
+
+extern "C" fo_status fo_rope_init(fo_rope_desc* d) {
+  if (!d) return FO_ERR_INVALID_ARG;
+  d->ready = 0;
+  if (d->R < 1 || d->R > FO_MAX_R || d->reserved) return FO_ERR_INVALID_ARG;
+  if (d->head_dim < 1 || d->head_dim > FO_ROPE_MAX_DIM || d->rot_dim < 2 || d->rot_dim % 2 ||
+      d->rot_dim > d->head_dim || d->heads_q < 1 || d->heads_k < 0 || d->heads_v < 0 || d->heads_q > 65536 ||
+      d->heads_k > 65536 || d->heads_v > 65536)
+    return FO_ERR_SHAPE;
+  if (d->dtype != FO_BF16 && d->dtype != FO_F32) return FO_ERR_DTYPE;
+  if (d->layout != FO_ROPE_HALF && d->layout != FO_ROPE_INTERLEAVED) return FO_ERR_INVALID_ARG;
+  if (d->scaling < FO_ROPE_SCALE_NONE || d->scaling > FO_ROPE_SCALE_PARTS) return FO_ERR_INVALID_ARG;
+  if (!(d->base > 1.0) || !isfinite(d->base)) return FO_ERR_INVALID_ARG;
+  const bool mixed = d->scaling == FO_ROPE_SCALE_WAVELENGTH || d->scaling == FO_ROPE_SCALE_PARTS;
+  if (d->scaling != FO_ROPE_SCALE_NONE && (!(d->stretch >= 1.0) || !isfinite(d->stretch))) return FO_ERR_INVALID_ARG;
+  if (mixed && (!(d->trained >= 1.0) || !isfinite(d->trained) || !(d->slow > 0.0) || !(d->fast > d->slow) ||
+                !isfinite(d->fast)))
+    return FO_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925286766559;
+  const int pairs = d->rot_dim / 2;
+  // PARTS: the (real) pair indices that make `fast` and `slow` turns.
+  double lo = 0.0, hi = 0.0;
+  if (d->scaling == FO_ROPE_SCALE_PARTS) {
+    lo = floor(d->rot_dim * log(d->trained / (two_pi * d->fast)) / (2.0 * log(d->base)));
+    hi = ceil(d->rot_dim * log(d->trained / (two_pi * d->slow)) / (2.0 * log(d->base)));
+    lo = fmax(lo, 0.0);
+    hi = fmin(hi, d->rot_dim - 1.0);
+  }
+  memset(d->turns, 0, sizeof(d->turns));
+  for (int i = 0; i < pairs; ++i) {
+    double f = pow(d->base, -2.0 * i / d->rot_dim);
+    if (d->scaling == FO_ROPE_SCALE_LINEAR) f /= d->stretch;
+    if (mixed) {
+      const double k = d->scaling == FO_ROPE_SCALE_WAVELENGTH
+                           ? (d->trained * f / two_pi - d->slow) / (d->fast - d->slow)
+                           : 1.0 - (i - lo) / fmax(hi - lo, 0.001);
+      const double kc = fmin(fmax(k, 0.0), 1.0);
+      f = kc * f + (1.0 - kc) * f / d->stretch;
+    }
+    d->turns[i] = (uint64_t)ldexp(f / two_pi, 64);   // below 2^62: f <= 1
+  }
+  d->factor = d->scaling == FO_ROPE_SCALE_PARTS ? (float)(0.1 * log(d->stretch) + 1.0) : 1.f;
+  d->ready = 1;
+  return FO_OK;
+}
+
+extern "C" fo_status fo_rope(const fo_rope_desc* d, int64_t rows, const void* positions, int32_t pos_bytes,
+                             const void* const* q_in, const void* const* k_in, const void* const* v_in,
+                             const int64_t ld_in[3], void* const* q_out, void* const* k_out, void* const* v_out,
+                             const int64_t ld_out[3], int32_t inverse, fo_stream_t stream) {
+  using namespace fo_ops;
+  if (!d || d->ready != 1 || !ld_in || !ld_out) return FO_ERR_INVALID_ARG;
+  if (d->R < 1 || d->R > kMaxR || d->rot_dim < 2 || d->rot_dim > d->head_dim || d->head_dim > FO_ROPE_MAX_DIM)
+    return FO_ERR_INVALID_ARG;
+  if ((inverse != 0 && inverse != 1) || (positions && pos_bytes != 4 && pos_bytes != 8)) return FO_ERR_INVALID_ARG;
+  if (rows < 0 || rows > INT32_MAX) return FO_ERR_SHAPE;
+  const int R = d->R;
+  const size_t es = d->dtype == FO_BF16 ? 2 : 4;
+  typedef const void* const* A;
+  const int32_t heads[3] = {d->heads_q, d->heads_k, d->heads_v};
+  const A in[3] = {q_in, k_in, v_in}, out[3] = {(A)q_out, (A)k_out, (A)v_out};
+  fo_status st;
+  for (int j = 0; j < 3; ++j) {
+    if (!heads[j]) continue;
+    if (ld_in[j] < (int64_t)heads[j] * d->head_dim || ld_out[j] < (int64_t)heads[j] * d->head_dim)
+      return FO_ERR_SHAPE;
+    if (rows && ((st = check_array(R, in[j], es)) || (st = check_array(R, out[j], es)))) return st;
+  }
+  if (positions && !aligned(positions, pos_bytes)) return FO_ERR_ALIGN;
+  if (rows == 0) return FO_OK;
+  int sms;
+  if ((st = device_sms(&sms))) return st;
+  PtrList l;
+  for (int j = 0; j < 3; ++j)
+    if (heads[j]) l.add(R, in[j]), l.add(R, out[j]);
+  l.add(positions);
+  if ((st = check_device(l, stream))) return st;
+  RopeParams k;
+  memset(&k, 0, sizeof(k));
+  for (int j = 0; j < 3; ++j) {
+    if (!heads[j]) continue;
+    k.heads[j] = heads[j];
+    k.ld_in[j] = ld_in[j];
+    k.ld_out[j] = ld_out[j];
+    for (int r = 0; r < R; ++r) k.in[j][r] = in[j][r], k.out[j][r] = const_cast<void*>(out[j][r]);
+  }
+  k.positions = positions;
+  k.pos_bytes = pos_bytes;
+  k.rows = rows;
+  k.D = d->head_dim;
+  k.rot = d->rot_dim;
+  k.half = d->layout == FO_ROPE_HALF;
+  k.factor = d->factor;
+  k.sign = inverse ? -1.f : 1.f;
+  memcpy(k.turns, d->turns, sizeof(k.turns));
+  const dim3 grid((unsigned)rows, R);
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (d->dtype == FO_BF16) rope_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(k);
+  else rope_kernel<float><<<grid, 256, 0, s>>>(k);
+  return launched("rope", R, rows, d->head_dim, (int)rows, 256);
+}

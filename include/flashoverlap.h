@@ -429,6 +429,181 @@ fo_status fo_status_query(fo_plan_t plan, void* ws, fo_stream_t stream, int32_t 
 fo_status fo_gemm_rs_noalloc(fo_plan_t plan, const void* const* X, const void* const* W,
                              void* const* Y, fo_stream_t stream);
 
+/* ---- operators between the residual stream and the attention ------------
+ *
+ * What a transformer layer runs round the projections and the attention
+ * above: the norm with the residual's addition, quantisation to 8 bits, the
+ * product of 8-bit matrices, and rotary positions. The norm's 8-bit output
+ * is the product's left operand; the product's packed Q|K|V rows are what
+ * fo_rope turns and parts into the attention's Q, K and V.
+ *
+ * Conventions on top of the file's: a call takes a description (`desc`, host
+ * memory, read during the call only), the row count and the pointers. As
+ * above, pointer arrays hold R device pointers; a pointer may repeat where
+ * ranks share an input. Pointers need the alignment of their element type
+ * (16 bytes where a call says so). Every entry point checks its arguments on
+ * the host first and launches nothing when it refuses; zero rows are FO_OK
+ * and launch nothing. 8-bit values are e4m3 (largest 448), rounded to
+ * nearest even; a scale is the number an 8-bit value is multiplied by,
+ *     scale = max(max |v| / 448, 2^-126)   over the scale's block of v,
+ * so a block of zeros has scale 2^-126 and zero values, and a block that
+ * holds a NaN or an infinity has a scale of the same kind and NaN values
+ * where the quotient is one. */
+
+#define FO_NORM_MAX_H 32768
+#define FO_ROPE_MAX_DIM 256       /* largest head dimension */
+#define FO_FP8_BLOCK 128          /* values (rows, columns) under one scale */
+
+typedef struct {
+  int32_t R;                  /* shards of the rows, 1..16 */
+  int32_t H;                  /* columns, 1..FO_NORM_MAX_H */
+  int32_t dtype;              /* FO_BF16 or FO_F32: x, residual, h, y, dy, dh, dx */
+  int32_t w_dtype;            /* FO_BF16 or FO_F32: weight */
+  float eps;                  /* >= 0 */
+  float w_offset;             /* the weight used is weight + w_offset (0 or 1 in practice) */
+  int32_t reserved[2];        /* must be zero */
+} fo_norm_desc;
+
+/* RMSNorm with the residual's addition. For each of the `rows` rows of every
+ * shard, in fp32:
+ *     s = x + residual         (residual NULL: s = x)
+ *     rstd = 1 / sqrt(mean(s^2) + eps)
+ *     n = s * rstd * (weight + w_offset)
+ * h (may be NULL) receives s and y (may be NULL) receives n, both rounded
+ * once to dtype; q and scale (both or neither) receive n in 8 bits with one
+ * scale for every 128 columns (scale: [rows x ceil(H/128)] fp32, the last
+ * group may be short); rstd (may be NULL) receives rstd [rows] fp32, which the
+ * backward pass takes. x, residual, h, y: [rows x H]; q: [rows x H] bytes.
+ * `weight` [H] is one pointer: a replicated parameter. h may be x or the
+ * residual itself (every element is read before it is written), so may y;
+ * other overlaps are not allowed. At least one of h, y, q and rstd is needed.
+ * One launch. */
+fo_status fo_rmsnorm(const fo_norm_desc* desc, int64_t rows, const void* const* x, const void* const* residual,
+                     const void* weight, void* const* h, void* const* y, void* const* q, float* const* scale,
+                     float* const* rstd, fo_stream_t stream);
+
+/* Its gradient. With u = dy * (weight + w_offset), per row:
+ *     dx = rstd * u - h * rstd^3 / H * sum(u * h)  (+ dh)
+ * where h is the forward's sum (x itself without a residual), rstd the
+ * forward's, and dh (may be NULL) the gradient that reaches h by the residual
+ * path; dx is the gradient of x and of the residual alike, rounded once. dx
+ * may be dy or dh. dweight ([H] fp32, may be NULL) receives the sum over every row
+ * of every shard of dy * h * rstd: the gradient of the replicated weight,
+ * after its all-reduce. An 8-bit forward output passes its gradient straight
+ * through. Sums run in fp32 in an order that the sizes alone fix, so results
+ * repeat bit for bit. `ws` (16-byte aligned): fo_rmsnorm_bwd_workspace bytes
+ * of scratch, no initialisation needed; NULL is allowed when dweight is NULL.
+ * Two launches (one without dweight). */
+fo_status fo_rmsnorm_bwd(const fo_norm_desc* desc, int64_t rows, const void* const* dy, const void* const* dh,
+                         const void* const* h, const void* weight, const float* const* rstd, void* const* dx,
+                         float* dweight, void* ws, fo_stream_t stream);
+fo_status fo_rmsnorm_bwd_workspace(const fo_norm_desc* desc, int64_t rows, size_t* bytes);
+
+/* Quantisation of R matrices x [rows x cols] (dtype FO_BF16 or FO_F32) to
+ * 8 bits. block_rows = 1: one scale for every 128 columns of a row (activations
+ * and upstream gradients), scale [rows x ceil(cols/128)]. block_rows = 128:
+ * one for every 128 x 128 block (weights), scale [ceil(rows/128) x
+ * ceil(cols/128)]; qt and scale_t (both or neither; block_rows = 128 only)
+ * also receive the transposed copy [cols x rows] and its scales, with which
+ * the product gives the gradient of its left operand. One launch. */
+fo_status fo_quant_fp8(int32_t R, int64_t rows, int64_t cols, int32_t dtype, int32_t block_rows,
+                       const void* const* x, void* const* q, float* const* scale, void* const* qt,
+                       float* const* scale_t, fo_stream_t stream);
+
+typedef struct {
+  int32_t R;                  /* products per call, 1..16 */
+  int32_t out_dtype;          /* FO_BF16 or FO_F32 */
+  int64_t N, K;               /* columns of Y; reduction, a multiple of 16 */
+  int32_t reserved[4];        /* must be zero */
+} fo_gemm_fp8_desc;
+
+/* Product of 8-bit matrices with a scale for each block of 128 of the
+ * reduction, for each r < R:
+ *   Y[m][n] = sum_b sA[m][b] sW[n/128][b] sum_{k in block b} A[m][k] W[n][k]
+ * A [M x K] e4m3 with sA [M x ceil(K/128)] (fo_rmsnorm's q and scale, or
+ * fo_quant_fp8 with block_rows = 1), W [N x K] e4m3 (the nn.Linear layout)
+ * with sW [ceil(N/128) x ceil(K/128)] (block_rows = 128), Y [M x N]. Products
+ * and sums in fp32, Y rounded once. The gradient of A's real values is the
+ * same call on dY in 8 bits and the transposed weight (qt, scale_t). A, W and
+ * Y are 16-byte aligned; K a multiple of 16 (FO_ERR_ALIGN). `ws`: a workspace
+ * of fo_gemm_fp8_workspace bytes for calls of up to M rows (16-byte aligned),
+ * zeroed once by fo_ops_workspace_init; one call per workspace may be in
+ * flight. A device wait that runs out is reported by fo_ops_status_query.
+ * Results repeat bit for bit. One launch. */
+fo_status fo_gemm_fp8(const fo_gemm_fp8_desc* desc, int64_t M, const void* const* A, const float* const* sA,
+                      const void* const* W, const float* const* sW, void* const* Y, void* ws, fo_stream_t stream);
+fo_status fo_gemm_fp8_workspace(const fo_gemm_fp8_desc* desc, int64_t M, size_t* bytes);
+
+/* Zero an operator's workspace, and read (and, after a failure, clear) its
+ * status word: like fo_workspace_init and fo_status_query. */
+fo_status fo_ops_workspace_init(void* ws, size_t bytes, fo_stream_t stream);
+fo_status fo_ops_status_query(void* ws, fo_stream_t stream, int32_t info[4]);
+
+/* Pairs of a rotated head: HALF couples element i with i + rot_dim/2,
+ * INTERLEAVED element 2i with 2i + 1. */
+typedef enum { FO_ROPE_HALF = 0, FO_ROPE_INTERLEAVED = 1 } fo_rope_layout;
+
+/* Scaling of the frequencies f_i = base^(-2i/rot_dim) for contexts `stretch`
+ * times as long as the trained one (`trained` tokens):
+ *   NONE        f_i
+ *   LINEAR      f_i / stretch
+ *   WAVELENGTH  k f_i + (1 - k) f_i / stretch, with k = (n_i - slow) /
+ *               (fast - slow) held to [0, 1] and n_i = trained f_i / 2 pi the
+ *               turns of pair i in the trained context
+ *   PARTS       the same mix with k falling linearly in i, from 1 at the last
+ *               whole pair index before `fast` turns to 0 at the first one
+ *               after `slow` turns; the rotated values are also multiplied by
+ *               0.1 ln(stretch) + 1 */
+typedef enum {
+  FO_ROPE_SCALE_NONE = 0,
+  FO_ROPE_SCALE_LINEAR = 1,
+  FO_ROPE_SCALE_WAVELENGTH = 2,
+  FO_ROPE_SCALE_PARTS = 3
+} fo_rope_scaling;
+
+typedef struct {
+  int32_t R;                  /* ranks, 1..16 (each its own heads, the same positions) */
+  int32_t head_dim;           /* 1..FO_ROPE_MAX_DIM */
+  int32_t rot_dim;            /* elements of a head that are rotated: even, 2..head_dim */
+  int32_t heads_q, heads_k;   /* heads of Q (>= 1) and K (>= 0) per rank, rotated */
+  int32_t heads_v;            /* heads of V (>= 0) per rank, copied */
+  int32_t layout;             /* fo_rope_layout */
+  int32_t dtype;              /* FO_BF16 or FO_F32 */
+  int32_t scaling;            /* fo_rope_scaling */
+  int32_t reserved;           /* must be zero */
+  double base;                /* > 1 */
+  double stretch;             /* >= 1 */
+  double trained, slow, fast; /* WAVELENGTH, PARTS: trained >= 1, 0 < slow < fast */
+  /* Filled by fo_rope_init: turns a position of each pair, as 64-bit fixed
+   * point fractions (so position x turns, modulo 2^64, is the angle without
+   * its whole turns and without rounding); the factor on the rotated values. */
+  uint64_t turns[FO_ROPE_MAX_DIM / 2];
+  float factor;
+  int32_t ready;
+} fo_rope_desc;
+
+/* Check the description and fill turns, factor and ready. Host only. */
+fo_status fo_rope_init(fo_rope_desc* desc);
+
+/* Rotary positions. For each rank, row t and head of Q and K, each pair
+ * (a, b) of the first rot_dim elements becomes
+ *     factor * (a cos - b sin, b cos + a sin),   angle = positions[t] * f_i,
+ * in fp32, rounded once; the head's other elements and V are copied. inverse =
+ * 1 turns back (the gradient: the factor stays, the angle changes its sign).
+ * Rows of q_in, k_in, v_in have ld_in[0..2] elements from one to the next
+ * (at least heads * head_dim), rows of the outputs ld_out[0..2]; head h of a
+ * row starts at h * head_dim. So the inputs may be the three parts of packed
+ * rows, and the outputs the attention's own Q, K and V, or the other way
+ * round. q_out = q_in (with the same row stride) works in place, likewise k
+ * and v; other overlaps are not allowed. k_in and k_out (v_in and v_out) may
+ * be NULL without heads of K (V). positions: `rows` numbers, int32 (pos_bytes
+ * 4) or int64 (pos_bytes 8), negative ones allowed, shared by every rank;
+ * NULL: row t is at position t. One launch. */
+fo_status fo_rope(const fo_rope_desc* desc, int64_t rows, const void* positions, int32_t pos_bytes,
+                  const void* const* q_in, const void* const* k_in, const void* const* v_in, const int64_t ld_in[3],
+                  void* const* q_out, void* const* k_out, void* const* v_out, const int64_t ld_out[3],
+                  int32_t inverse, fo_stream_t stream);
+
 /* ---- tracing ------------------------------------------------------------ */
 
 /* Timestamps (%globaltimer, ns) of the last fused-kernel launch that used

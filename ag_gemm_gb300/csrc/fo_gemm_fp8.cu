@@ -65,6 +65,15 @@ __device__ __forceinline__ void mma_fp8(uint32_t d_tmem, uint64_t adesc, uint64_
         : "memory");
 }
 
+// One arrival on an mbarrier of this cluster. Release at CTA scope: what it
+// guards, tensor memory that has been read into registers
+// (tcgen05.wait::ld), is no memory that a wider fence would order, and the
+// cluster-wide release waits for every outstanding store: with it each block
+// of the reduction took about four times as long.
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Packed fp32 pairs (each half rounded as the scalar instruction would).
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 pair_of(float a, float b) {
@@ -93,7 +102,7 @@ namespace wide {
 // 12 warps: 0 TMA producer, 1 MMAs (the pair's leader) and TMEM, 2-3 idle,
 // 4-11 accumulate: a warp's 32 rows (its TMEM lane quarter) x 128 columns,
 // 128 fp32 sums a thread. The registers come from the first warpgroup: 384 x
-// 168 at launch = 128 x 40 + 256 x 232.
+// 168 at launch = 128 x 56 + 256 x 224.
 constexpr int kThreads = 384;
 constexpr int kStages = 6;
 constexpr int kTile = 256;
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
   const uint32_t tmem = *tmem_slot;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {
       // -------------------------------------------------------- producer
       uint32_t it = 0, ph = 0;
@@ -267,9 +276,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
     }
   } else {
     // ---------------------------------------------------------- accumulate
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_col = ((uint32_t)(q * 32) << 16) + (uint32_t)half * 128u;
+    const uint32_t free0 = mapa_shared(tempty_bar(0), 0), free1 = mapa_shared(tempty_bar(1), 0);
     uint32_t it = 0;
     bool ok = true;
     for (int L = unit; L < total && ok; L += units) {
@@ -306,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
           if (c == 2) {   // the buffer has been read: the tensor core may fill it again
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(mapa_shared(tempty_bar(b), 0));
+            if (lane == 0) arrive_at(b ? free1 : free0);
           }
 #pragma unroll
           for (int j = 0; j < 32; ++j)

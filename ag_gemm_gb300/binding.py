@@ -187,10 +187,20 @@ def _ptr_array(xs: Optional[Sequence]):
     return arr
 
 
+_current_stream = None
+
+
 def _stream(s) -> int:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else 0
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            if not torch.cuda.is_available():
+                return 0
+            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            # The stream's address alone, where torch gives it: a Stream object for every call took 3 us.
+            _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -409,23 +419,43 @@ def _types():
     return _TORCH_DTYPES
 
 
-def _checked(x, n: int, types, what: str) -> int:
-    """The address of x: a dense CUDA tensor of n values of one of `types`, or a raw address."""
-    if isinstance(x, int):
-        return x
+def _refuse(x, n: int, types, what: str):
+    """Raise for what _address found wrong (all but the host memory that can be used after all)."""
     if x.dtype not in types:
         raise ValueError(f"{what}: {x.dtype} given, {' or '.join(map(str, types))} expected")
     if x.numel() != n:
         raise ValueError(f"{what}: {x.numel()} values given, {n} expected")
-    return _ptr(x)
+    _ptr(x)
 
 
-def _checked_array(xs, R: int, n: int, types, what: str):
+def _address(x, n: int, types, what: str) -> int:
+    """The address of x: a dense CUDA tensor of n values of one of `types`, or a raw address."""
+    if type(x) is int:
+        return x
+    if x.dtype not in types or x.numel() != n or not x.is_contiguous() or not x.is_cuda:
+        _refuse(x, n, types, what)
+    return x.data_ptr()
+
+
+# These calls are made once a layer on a few rows in serving, so their marshalling counts: about 0.5 us a tensor.
+_ARRAYS = [None] + [c_void_p * n for n in range(1, 17)]
+
+
+def _array_of(R: int):
+    return _ARRAYS[R] if 0 < R <= 16 else c_void_p * max(R, 0)
+
+
+def _addresses(xs, R: int, n: int, types, what: str):
     if xs is None:
         return None
     if len(xs) != R:
         raise ValueError(f"{what}: {len(xs)} tensors given, one for each of {R} ranks expected")
-    return (c_void_p * R)(*[_checked(x, n, types, what) for x in xs])
+    at, last = [], None
+    for x in xs:
+        if x is not last:
+            here, last = _address(x, n, types, what), x
+        at.append(here)
+    return _array_of(R)(*at)
 
 
 def fo_norm_desc(H: int, *, R: int = 1, dtype="bf16", w_dtype=None, eps: float = 1e-6, w_offset: float = 0.0) -> NormDesc:
@@ -444,12 +474,12 @@ def fo_rmsnorm(desc: NormDesc, rows: int, x, residual, weight, h=None, y=None, q
     R, H, t = desc.R, desc.H, _types()
     n, types = rows * H, t[desc.dtype]
     groups = rows * -(-H // FO_FP8_BLOCK)
-    _check(load().fo_rmsnorm(desc, rows, _checked_array(x, R, n, types, "x"),
-                             _checked_array(residual, R, n, types, "residual"),
-                             _checked(weight, H, t[desc.w_dtype], "weight"), _checked_array(h, R, n, types, "h"),
-                             _checked_array(y, R, n, types, "y"), _checked_array(q, R, n, t["q"], "q"),
-                             _checked_array(scale, R, groups, t[1], "scale"),
-                             _checked_array(rstd, R, rows, t[1], "rstd"), _stream(stream)), "fo_rmsnorm")
+    _check(load().fo_rmsnorm(desc, rows, _addresses(x, R, n, types, "x"),
+                             _addresses(residual, R, n, types, "residual"),
+                             _address(weight, H, t[desc.w_dtype], "weight"), _addresses(h, R, n, types, "h"),
+                             _addresses(y, R, n, types, "y"), _addresses(q, R, n, t["q"], "q"),
+                             _addresses(scale, R, groups, t[1], "scale"),
+                             _addresses(rstd, R, rows, t[1], "rstd"), _stream(stream)), "fo_rmsnorm")
 
 
 def fo_rmsnorm_bwd_workspace(desc: NormDesc, rows: int) -> int:
@@ -464,11 +494,11 @@ def fo_rmsnorm_bwd(desc: NormDesc, rows: int, dy, dh, h, weight, rstd, dx, dweig
     n, types = rows * H, t[desc.dtype]
     if ws is not None and not isinstance(ws, int) and ws.numel() * ws.element_size() < fo_rmsnorm_bwd_workspace(desc, rows):
         raise ValueError("fo_rmsnorm_bwd: the workspace is smaller than fo_rmsnorm_bwd_workspace says")
-    _check(load().fo_rmsnorm_bwd(desc, rows, _checked_array(dy, R, n, types, "dy"),
-                                 _checked_array(dh, R, n, types, "dh"), _checked_array(h, R, n, types, "h"),
-                                 _checked(weight, H, t[desc.w_dtype], "weight"),
-                                 _checked_array(rstd, R, rows, t[1], "rstd"), _checked_array(dx, R, n, types, "dx"),
-                                 None if dweight is None else _checked(dweight, H, t[1], "dweight"), _ptr(ws),
+    _check(load().fo_rmsnorm_bwd(desc, rows, _addresses(dy, R, n, types, "dy"),
+                                 _addresses(dh, R, n, types, "dh"), _addresses(h, R, n, types, "h"),
+                                 _address(weight, H, t[desc.w_dtype], "weight"),
+                                 _addresses(rstd, R, rows, t[1], "rstd"), _addresses(dx, R, n, types, "dx"),
+                                 None if dweight is None else _address(dweight, H, t[1], "dweight"), _ptr(ws),
                                  _stream(stream)), "fo_rmsnorm_bwd")
 
 
@@ -482,11 +512,11 @@ def fo_quant_fp8(rows: int, cols: int, x, q, scale, qt=None, scale_t=None, *, bl
         dtype = "bf16" if x[0].dtype in t[0] else "f32"
     R, code = len(x), DTYPES[dtype]
     up, across = (-(-rows // block_rows) if block_rows > 0 else 0), -(-cols // FO_FP8_BLOCK)
-    _check(load().fo_quant_fp8(R, rows, cols, code, block_rows, _checked_array(x, R, rows * cols, t[code], "x"),
-                               _checked_array(q, R, rows * cols, t["q"], "q"),
-                               _checked_array(scale, R, up * across, t[1], "scale"),
-                               _checked_array(qt, R, rows * cols, t["q"], "qt"),
-                               _checked_array(scale_t, R, up * across, t[1], "scale_t"), _stream(stream)),
+    _check(load().fo_quant_fp8(R, rows, cols, code, block_rows, _addresses(x, R, rows * cols, t[code], "x"),
+                               _addresses(q, R, rows * cols, t["q"], "q"),
+                               _addresses(scale, R, up * across, t[1], "scale"),
+                               _addresses(qt, R, rows * cols, t["q"], "qt"),
+                               _addresses(scale_t, R, up * across, t[1], "scale_t"), _stream(stream)),
            "fo_quant_fp8")
 
 
@@ -507,10 +537,10 @@ def fo_gemm_fp8(desc: GemmFp8Desc, M: int, A, sA, W, sW, Y, ws, stream=None) -> 
     sW [ceil(N/128), ceil(K/128)]; one tensor for each rank."""
     R, N, K, t = desc.R, desc.N, desc.K, _types()
     k = -(-K // FO_FP8_BLOCK)
-    _check(load().fo_gemm_fp8(desc, M, _checked_array(A, R, M * K, t["q"], "A"),
-                              _checked_array(sA, R, M * k, t[1], "sA"), _checked_array(W, R, N * K, t["q"], "W"),
-                              _checked_array(sW, R, -(-N // FO_FP8_BLOCK) * k, t[1], "sW"),
-                              _checked_array(Y, R, M * N, t[desc.out_dtype], "Y"), _ptr(ws), _stream(stream)),
+    _check(load().fo_gemm_fp8(desc, M, _addresses(A, R, M * K, t["q"], "A"),
+                              _addresses(sA, R, M * k, t[1], "sA"), _addresses(W, R, N * K, t["q"], "W"),
+                              _addresses(sW, R, -(-N // FO_FP8_BLOCK) * k, t[1], "sW"),
+                              _addresses(Y, R, M * N, t[desc.out_dtype], "Y"), _ptr(ws), _stream(stream)),
            "fo_gemm_fp8")
 
 
@@ -540,28 +570,33 @@ def fo_rope_desc(head_dim: int, heads_q: int, heads_k: int = 0, heads_v: int = 0
     return d
 
 
-def _row_array(xs, R: int, rows: int, width: int, types, what: str):
+def _rows_of(xs, R: int, rows: int, width: int, types, what: str):
     """Addresses and the common row stride of R matrices [rows, width] whose rows are dense (parts of packed rows
     among them)."""
     if len(xs) != R:
         raise ValueError(f"{what}: {len(xs)} tensors given, one for each of {R} ranks expected")
-    ld, at = None, []
+    ld, at, shape = None, [], (rows, width)
     for x in xs:
-        if isinstance(x, int):
+        if type(x) is int:
             at.append(x)
             continue
         if x.dtype not in types:
             raise ValueError(f"{what}: {x.dtype} given, {' or '.join(map(str, types))} expected")
-        if x.dim() != 2 or x.shape[0] != rows or x.shape[1] != width or (width > 1 and rows > 0 and x.stride(1) != 1):
+        if x.shape != shape:
             raise ValueError(f"{what}: {rows} rows of {width} dense values expected, {tuple(x.shape)} given")
-        stride = x.stride(0) if rows > 1 else width
-        if ld is not None and stride != ld:
-            raise ValueError(f"{what}: every rank's rows need the same stride")
+        up, across = x.stride()
+        if across != 1 and width > 1 and rows > 0:
+            raise ValueError(f"{what}: {rows} rows of {width} dense values expected, strides {up} and {across} given")
+        if rows <= 1:
+            up = width
+        if up != ld:
+            if ld is not None:
+                raise ValueError(f"{what}: every rank's rows need the same stride")
+            ld = up
         if not x.is_cuda and not x.is_pinned():
             raise ValueError("tensors passed to libflashoverlap must be CUDA tensors (or pinned host memory)")
-        ld = stride
         at.append(x.data_ptr())
-    return (c_void_p * R)(*at), width if ld is None else ld
+    return _array_of(R)(*at), width if ld is None else ld
 
 
 def fo_rope(desc: RopeDesc, rows: int, positions, q_in, k_in, v_in, q_out, k_out, v_out, *, inverse: bool = False,
@@ -578,8 +613,8 @@ def fo_rope(desc: RopeDesc, rows: int, positions, q_in, k_in, v_in, q_out, k_out
             ins.append(None)
             outs.append(None)
             continue
-        a, ld_in[j] = _row_array(i, R, rows, heads * D, types, what)
-        b, ld_out[j] = _row_array(o, R, rows, heads * D, types, what)
+        a, ld_in[j] = _rows_of(i, R, rows, heads * D, types, what)
+        b, ld_out[j] = _rows_of(o, R, rows, heads * D, types, what)
         ins.append(a)
         outs.append(b)
     at, size = 0, 8
@@ -587,7 +622,7 @@ def fo_rope(desc: RopeDesc, rows: int, positions, q_in, k_in, v_in, q_out, k_out
         size = positions.element_size()
         if positions.is_floating_point() or size not in (4, 8):
             raise ValueError(f"positions: int32 or int64 expected, {positions.dtype} given")
-        at = _checked(positions, rows, (positions.dtype,), "positions")
+        at = _address(positions, rows, (positions.dtype,), "positions")
     elif positions is not None:
         at = positions
     _check(load().fo_rope(desc, rows, at, size, *ins, ld_in, *outs, ld_out, 1 if inverse else 0, _stream(stream)),

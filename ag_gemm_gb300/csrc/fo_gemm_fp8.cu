@@ -10,7 +10,7 @@
 //
 // Two kernels share the work by size (choose() below says which):
 //   wide    256 x 256 tiles on CTA pairs, persistent: many rows, tensor-bound;
-//   narrow  128 weight rows x 16..128 rows of A on one CTA, the operands'
+//   narrow  128 weight rows x 16..64 rows of A on one CTA, the operands'
 //           roles swapped (the weight is the MMA's 128-row operand, so few
 //           rows of A cost few columns), the reduction split over a cluster:
 //           few rows, bound by the stream of weights.
@@ -32,13 +32,15 @@ constexpr int kBlockK = FO_FP8_BLOCK;         // reduction bytes a stage
 struct GemmParams {
   CUtensorMap tmA[kMaxR];   // A_r [M x K] bytes
   CUtensorMap tmW[kMaxR];   // W_r [N x K] bytes
+  CUtensorMap tmY[kMaxR];   // Y_r [M x N] (where its rows start on 16 bytes)
   const float* sA[kMaxR];
   const float* sW[kMaxR];
   void* Y[kMaxR];
   int32_t* status;
   int32_t R, M, N, kblocks, nblocks;   // nblocks: 128-row blocks of W
   int32_t tiles_m, tiles_n;
-  int32_t f32, vec;                    // vec: rows of Y start on 16 bytes
+  int32_t f32;
+  int32_t vec;                         // rows of Y start on 16 bytes
 };
 
 // kind::f8f6f4 instruction descriptor: D fp32 (bits 4-5 = 1), A and B e4m3
@@ -74,6 +76,43 @@ __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// 32 lanes x 16 consecutive columns (tmem_ld32's layout).
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(at));
+}
+
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one;
+}
+
+// mbar_wait without a look at the clock on the common path (the clock is
+// first read after 64 tries).
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 63u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t t = globaltimer();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitNs) {
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
 // Packed fp32 pairs (each half rounded as the scalar instruction would).
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 pair_of(float a, float b) {
@@ -103,12 +142,23 @@ namespace wide {
 // 4-11 accumulate: a warp's 32 rows (its TMEM lane quarter) x 128 columns,
 // 128 fp32 sums a thread. The registers come from the first warpgroup: 384 x
 // 168 at launch = 128 x 56 + 256 x 224.
+//
+// A block of the reduction is 512 cycles of the tensor core. Two buffers of
+// 256 columns leave 1024 from the start of a buffer's MMAs to its next ones,
+// so that commit, wake-up, reads and release have to fit in 512: the second
+// half of a buffer is loaded while the first is being added, and the buffer
+// is released before the last additions. A finished tile goes through shared
+// memory to TMA stores (rows stored straight from registers took 6000 cycles
+// a tile); scales are loaded a block ahead, across tiles too.
 constexpr int kThreads = 384;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kTile = 256;
 constexpr uint32_t kOperand = 128 * kBlockK;          // 16 KB: this CTA's 128 rows of A, or its half of W's 256
 constexpr uint32_t kStageBytes = 2 * kOperand;
-constexpr int kSmem = 1024 + kStages * (int)kStageBytes + 256;
+constexpr uint32_t kOutBuf = 32 * 128;                // a warp's piece of the output: 32 rows x 128 bytes
+constexpr uint32_t kOffOut = kStages * kStageBytes;
+constexpr uint32_t kOffBar = kOffOut + 16 * kOutBuf;
+constexpr int kSmem = 1024 + (int)kOffBar + 256;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 constexpr int kPanel = 8;   // row tiles that go through all column tiles together (their A stays in L2)
 
@@ -128,39 +178,73 @@ __device__ __forceinline__ Tile decode(const GemmParams& p, int L) {
   return t;
 }
 
+// 32 words a lane (a row of 128 bytes) into a 32 x 128 byte buffer, 16-byte
+// chunk j of row i at chunk j ^ (i % 8): the TMA's 128-byte swizzle, and free
+// of bank conflicts.
+__device__ __forceinline__ void stage_row(uint32_t buf, int lane, const uint32_t (&w)[32]) {
+  const uint32_t row = buf + (uint32_t)lane * 128u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((uint32_t)(j ^ (lane & 7)) << 4)),
+                 "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t staged_word(uint32_t buf, int row, int word) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];"
+               : "=r"(v)
+               : "r"(buf + (uint32_t)row * 128u + ((uint32_t)((word >> 2) ^ (row & 7)) << 4) + (uint32_t)(word & 3) * 4u)
+               : "memory");
+  return v;
+}
+
+// A warp's 32 rows x 128 columns at (m, n) of Y_r, through its two buffers.
 template <bool F32>
-__device__ __forceinline__ void store_row(const GemmParams& p, int r, int m, int n0, const f32x2 (&acc)[64]) {
-  if (m >= p.M || n0 >= p.N) return;
-  const int left = p.N - n0;
-  if constexpr (F32) {
-    float* y = static_cast<float*>(p.Y[r]) + (int64_t)m * p.N + n0;
+__device__ __forceinline__ void store_part(const GemmParams& p, int r, int m, int n, uint32_t bufs, int lane,
+                                           const f32x2 (&acc)[64]) {
+  if (m >= p.M || n >= p.N) return;
+  constexpr int kCols = F32 ? 32 : 64, kParts = 128 / kCols;   // columns in 128 bytes
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      float v[4];
-      halves(acc[2 * c], v[0], v[1]);
-      halves(acc[2 * c + 1], v[2], v[3]);
-      if (p.vec && 4 * c + 4 <= left) {
-        *reinterpret_cast<float4*>(y + 4 * c) = make_float4(v[0], v[1], v[2], v[3]);
+  for (int h = 0; h < kParts; ++h) {
+    const uint32_t buf = bufs + (uint32_t)(h & 1) * kOutBuf;
+    uint32_t w[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      float lo, hi;
+      if constexpr (F32) {
+        halves(acc[h * 16 + j / 2], lo, hi);
+        w[j] = __float_as_uint(j & 1 ? hi : lo);
       } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (4 * c + j < left) y[4 * c + j] = v[j];
+        halves(acc[h * 32 + j], lo, hi);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
       }
     }
-  } else {
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.Y[r]) + (int64_t)m * p.N + n0;
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) halves(acc[4 * c + j], v[2 * j], v[2 * j + 1]);
-      if (p.vec && 8 * c + 8 <= left) {
-        *reinterpret_cast<uint4*>(y + 8 * c) = Vec16<__nv_bfloat16>::pack(v);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (8 * c + j < left) y[8 * c + j] = __float2bfloat16_rn(v[j]);
+    if (lane == 0) bulk_wait_read<1>();   // the buffer's last store has read it
+    __syncwarp();
+    stage_row(buf, lane, w);
+    if (p.vec) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (n + h * kCols < p.N) tma_store_2d(&p.tmY[r], buf, n + h * kCols, m);   // clipped at Y's edges
+        bulk_commit();
       }
+    } else {   // rows of Y that no TMA store can start on: lanes along the columns
+      __syncwarp();
+      for (int i = 0; i < 32 && m + i < p.M; ++i) {
+        const uint32_t v = staged_word(buf, i, lane);
+        if constexpr (F32) {
+          const int c = n + h * 32 + lane;
+          if (c < p.N) static_cast<float*>(p.Y[r])[(int64_t)(m + i) * p.N + c] = __uint_as_float(v);
+        } else {
+          const int c = n + h * 64 + 2 * lane;
+          uint16_t* y = static_cast<uint16_t*>(p.Y[r]) + (int64_t)(m + i) * p.N + c;
+          if (c < p.N) y[0] = (uint16_t)v;
+          if (c + 1 < p.N) y[1] = (uint16_t)(v >> 16);
+        }
+      }
+      __syncwarp();
     }
   }
 }
@@ -171,9 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t sBar = base + kStages * kStageBytes;
-  auto full_bar = [&](int i) { return sBar + 8u * i; };
-  auto empty_bar = [&](int i) { return sBar + 8u * (kStages + i); };
+  const uint32_t sBar = base + kOffBar;
+  auto full_bar = [&](uint32_t i) { return sBar + 8u * i; };
+  auto empty_bar = [&](uint32_t i) { return sBar + 8u * (kStages + i); };
   auto tfull_bar = [&](uint32_t a) { return sBar + 8u * (2 * kStages + a); };
   auto tempty_bar = [&](uint32_t a) { return sBar + 8u * (2 * kStages + 2 + a); };
   const uint32_t done_bar = sBar + 8u * (2 * kStages + 4);
@@ -181,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + (slot - base));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + (slot - base) + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t prank = cluster_ctarank();
   const bool leader = prank == 0;
   const int unit = (int)(blockIdx.x >> 1), units = (int)(gridDim.x >> 1);
@@ -222,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
         const Tile t = decode(p, L);
         const int m0 = t.mt * kTile + (int)prank * 128, n0 = t.nt * kTile + (int)prank * 128;
         for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-          if (!mbar_wait(empty_bar(st), ph ^ 1u, abort_flag, kWaitNs)) {
+          if (!wait_bar(empty_bar(st), ph ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
@@ -244,87 +328,121 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
         while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
       }
       if (*abort_flag) record_error(p.status, FO_ERR_TIMEOUT, -1, -1, 0);
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
       // ------------------------------------------------------------ MMAs
-      uint32_t it = 0, ph = 0;
-      int st = 0;
-      bool ok = true;
+      // The whole warp runs the loop and one elected lane issues: descriptors
+      // and barrier addresses are then the same in every lane for the
+      // compiler too and stay in uniform registers, where the MMA wants them.
+      // (From a loop of one lane's own, each MMA took 85 cycles to issue.)
       constexpr uint32_t id = idesc_fp8(256, 256);
+      const uint64_t a0 = smem_desc_sw128(base, 16, 1024), w0 = smem_desc_sw128(base + kOperand, 16, 1024);
+      uint32_t st = 0, ph = 0, b = 0, bph = 1;
+      bool ok = true;
       for (int L = unit; L < total && ok; L += units) {
-        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-          const uint32_t a = it & 1u;
-          if (!mbar_wait(tempty_bar(a), ((it >> 1) & 1u) ^ 1u, abort_flag, kWaitNs) ||
-              !mbar_wait(full_bar(st), ph, abort_flag, kWaitNs)) {
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (!__all_sync(0xffffffffu,
+                          wait_bar(tempty_bar(b), bph, abort_flag) && wait_bar(full_bar(st), ph, abort_flag))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = base + st * kStageBytes;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_fp8<2>(tmem + a * 256u, smem_desc_sw128(sa + k * 32u, 16, 1024),
-                       smem_desc_sw128(sa + kOperand + k * 32u, 16, 1024), id, k > 0 ? 1u : 0u);
-          tc_commit_pair_multicast(empty_bar(st), 0x3);
-          tc_commit_pair_multicast(tfull_bar(a), 0x3);
+          if (elect_one()) {
+            const uint64_t da = a0 + st * (kStageBytes >> 4), dw = w0 + st * (kStageBytes >> 4);
+            const uint32_t d = tmem + b * 256u;
+            mma_fp8<2>(d, da, dw, id, 0);
+            mma_fp8<2>(d, da + 2, dw + 2, id, 1);   // 32 bytes further along the rows
+            mma_fp8<2>(d, da + 4, dw + 4, id, 1);
+            mma_fp8<2>(d, da + 6, dw + 6, id, 1);
+            tc_commit_pair_multicast(tfull_bar(b), 0x3);
+            tc_commit_pair_multicast(empty_bar(st), 0x3);
+          }
+          __syncwarp();
           if (++st == kStages) st = 0, ph ^= 1u;
+          b ^= 1u;
+          if (b == 0) bph ^= 1u;
         }
       }
       // Every issued MMA completes before TMEM is released.
-      tc_commit<2>(done_bar);
-      volatile int never = 0;
-      mbar_wait(done_bar, 0, &never, 100000000ull);
+      if (elect_one()) {
+        tc_commit<2>(done_bar);
+        volatile int never = 0;
+        mbar_wait(done_bar, 0, &never, 100000000ull);
+      }
+      __syncwarp();
     }
   } else {
     // ---------------------------------------------------------- accumulate
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    const int q = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t lane_col = ((uint32_t)(q * 32) << 16) + (uint32_t)half * 128u;
-    const uint32_t free0 = mapa_shared(tempty_bar(0), 0), free1 = mapa_shared(tempty_bar(1), 0);
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    const uint32_t at0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)h * 128u;
+    const uint32_t bufs = base + kOffOut + (uint32_t)(warp - 4) * 2 * kOutBuf;
+    const uint32_t free0 = mapa_shared(tempty_bar(0), 0);
     uint32_t it = 0;
     bool ok = true;
-    for (int L = unit; L < total && ok; L += units) {
+    // The scales of the row and of the columns' block, by block of the
+    // reduction; what lies outside reads the first ones and is not stored.
+    const float *sa = nullptr, *sw = nullptr;
+    auto scales_of = [&](int L) {
       const Tile t = decode(p, L);
-      const int m = t.mt * kTile + (int)prank * 128 + q * 32 + lane;
-      const int n0 = t.nt * kTile + half * 128, nb = n0 / 128;
-      // The row's and the columns' scales of a block are loaded a block ahead.
-      const bool in = m < p.M && nb < p.nblocks;
-      const float* sa = p.sA[t.r] + (int64_t)(in ? m : 0) * p.kblocks;
-      const float* sw = p.sW[t.r] + (int64_t)(in ? nb : 0) * p.kblocks;
-      float a_next = __ldg(sa), w_next = __ldg(sw);
+      const int m = t.mt * kTile + (int)prank * 128 + q * 32 + lane, nb = t.nt * 2 + h;
+      sa = p.sA[t.r] + (int64_t)(m < p.M ? m : 0) * p.kblocks;
+      sw = p.sW[t.r] + (int64_t)(nb < p.nblocks ? nb : 0) * p.kblocks;
+    };
+    float a_next = 0.f, w_next = 0.f;
+    if (unit < total) {
+      scales_of(unit);
+      a_next = __ldg(sa), w_next = __ldg(sw);
+    }
+    for (int L = unit; L < total && ok; L += units) {
       f32x2 acc[64];
 #pragma unroll
       for (int c = 0; c < 64; ++c) acc[c] = 0ull;
       for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
         const float s = a_next * w_next;
         const f32x2 s2 = pair_of(s, s);
-        if (kb + 1 < p.kblocks) a_next = __ldg(sa + kb + 1), w_next = __ldg(sw + kb + 1);
+        if (kb + 1 < p.kblocks) {
+          a_next = __ldg(sa + kb + 1), w_next = __ldg(sw + kb + 1);
+        } else if (L + units < total) {
+          scales_of(L + units);
+          a_next = __ldg(sa), w_next = __ldg(sw);
+        }
         const uint32_t b = it & 1u;
-        if (!mbar_wait(tfull_bar(b), (it >> 1) & 1u, abort_flag, kWaitNs)) {
+        if (!wait_bar(tfull_bar(b), (it >> 1) & 1u, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t at = tmem + lane_col + b * 256u;
+        const uint32_t at = at0 + b * 256u;
+        auto add = [&](int c, const uint32_t(&v)[32]) {
 #pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-          uint32_t v[2][32];
-          tmem_ld32(at + c * 32, v[0]);
-          tmem_ld32(at + c * 32 + 32, v[1]);
-          tmem_ld_wait();
-          reg_fence(v[0]);
-          reg_fence(v[1]);
-          if (c == 2) {   // the buffer has been read: the tensor core may fill it again
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(b ? free1 : free0);
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            acc[c * 16 + j] = fma2(pair_of(v[j >> 4][(2 * j) & 31], v[j >> 4][(2 * j + 1) & 31]), s2, acc[c * 16 + j]);
-        }
+          for (int j = 0; j < 16; ++j) acc[c * 16 + j] = fma2(pair_of(v[2 * j], v[2 * j + 1]), s2, acc[c * 16 + j]);
+        };
+        uint32_t v0[32], v1[32];
+        tmem_ld32(at, v0);
+        tmem_ld32(at + 32, v1);
+        tmem_ld_wait();
+        reg_fence(v0);
+        reg_fence(v1);
+        add(0, v0);
+        tmem_ld32(at + 64, v0);
+        add(1, v1);
+        tmem_ld32(at + 96, v1);
+        tmem_ld_wait();
+        reg_fence(v0);
+        reg_fence(v1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(free0 + b * 8u);   // read: the tensor core may fill it again
+        add(2, v0);
+        add(3, v1);
       }
-      if (ok) store_row<F32>(p, t.r, m, n0, acc);
+      if (ok) {
+        const Tile t = decode(p, L);
+        store_part<F32>(p, t.r, t.mt * kTile + (int)prank * 128 + q * 32, t.nt * kTile + h * 128, bufs, lane, acc);
+      }
     }
+    if (lane == 0) bulk_wait<0>();   // the stores are done with shared memory
+    __syncwarp();
   }
   tc_fence_before();
   __syncwarp();
@@ -346,25 +464,33 @@ namespace narrow {
 // thread: lane = weight row, register = row of A). Two CTAs fit on an SM.
 constexpr int kThreads = 192;
 constexpr uint32_t kWBytes = 128 * kBlockK;
+constexpr int kScaleBlocks = 32;   // blocks whose scales are in shared memory at a time
+constexpr int kMaxSplit = 8;       // CTAs that share a reduction (portable cluster size)
 
 template <int TN>
 struct Cfg {
   static constexpr uint32_t kXBytes = TN * kBlockK;
   static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
-  static constexpr int kStages = TN <= 32 ? 5 : TN <= 64 ? 4 : 3;
-  static constexpr int kBufs = TN <= 64 ? 4 : 2;                      // TMEM buffers of TN columns
+  static constexpr int kStages = TN <= 16 ? 5 : 4;
+  static constexpr int kBufs = 4;                                        // TMEM buffers of TN columns
   static constexpr uint32_t kCols = TN * kBufs < 64 ? 64 : TN * kBufs;   // allocated: a power of two
   static constexpr uint32_t kRing = kStages * kStageBytes;
+  static constexpr int kScaleLd = TN + 4;   // [block][row of A], padded to spread the banks
+  static constexpr uint32_t kScales = kScaleBlocks * kScaleLd * 4;
+  // Sums that the cluster's CTAs send: [sender][row of A][128]. Beside the
+  // ring where that still leaves room for two CTAs on an SM, else in its
+  // place once every CTA is done with its ring.
+  static constexpr bool kOwnSums = TN <= 32;
+  static constexpr uint32_t kSums = (TN + kMaxSplit - 1) * 512;
+  static constexpr uint32_t kOffBar = kRing;
+  static constexpr uint32_t kOffScale = kOffBar + 256;
+  static constexpr uint32_t kOffSums = kOwnSums ? kOffScale + kScales : 0;
+  static constexpr int kSmem = 1024 + (int)(kOffScale + kScales + (kOwnSums ? kSums : 0));
+  static_assert(kOwnSums || kSums <= kRing, "the sums fit into the ring");
 };
 
-// Beside the ring: barriers, and the scales of kScaleBlocks blocks of the
-// reduction at a time ([blocks][TN], the product of both; rows padded to
-// spread the banks).
-constexpr int kScaleBlocks = 32;
-template <int TN>
-constexpr int smem_bytes() {
-  return 1024 + (int)Cfg<TN>::kRing + 256 + kScaleBlocks * (TN + 4) * 4;
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <int TN>
 __global__ void __launch_bounds__(kThreads) gemm_fp8_narrow_kernel(const __grid_constant__ GemmParams p, int split) {
@@ -374,9 +500,9 @@ __global__ void __launch_bounds__(kThreads) gemm_fp8_narrow_kernel(const __grid_
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t sBar = base + C::kRing;
-  auto full_bar = [&](int i) { return sBar + 8u * i; };
-  auto empty_bar = [&](int i) { return sBar + 8u * (S + i); };
+  const uint32_t sBar = base + C::kOffBar;
+  auto full_bar = [&](uint32_t i) { return sBar + 8u * i; };
+  auto empty_bar = [&](uint32_t i) { return sBar + 8u * (S + i); };
   auto tfull_bar = [&](uint32_t a) { return sBar + 8u * (2 * S + a); };
   auto tempty_bar = [&](uint32_t a) { return sBar + 8u * (2 * S + NB + a); };
   const uint32_t done_bar = sBar + 8u * (2 * S + 2 * NB);
@@ -384,15 +510,17 @@ __global__ void __launch_bounds__(kThreads) gemm_fp8_narrow_kernel(const __grid_
   static_assert(8 * (2 * S + 2 * NB + 2) <= 256, "barriers");
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + (slot - base));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + (slot - base) + 4);
-  float* const sScale = reinterpret_cast<float*>(gbase + C::kRing + 256);
+  float* const sScale = reinterpret_cast<float*>(gbase + C::kOffScale);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   // blockIdx.x: share of the reduction (the cluster's rank), .y: block of 128
   // weight rows, .z: rank and tile of A's rows.
   const int part = (int)blockIdx.x, nb = (int)blockIdx.y;
   const int r = (int)blockIdx.z / p.tiles_m, m0 = ((int)blockIdx.z % p.tiles_m) * TN;
-  const int kb0 = (int)((int64_t)p.kblocks * part / split), kb1 = (int)((int64_t)p.kblocks * (part + 1) / split);
+  const int kb0 = p.kblocks * part / split, kb1 = p.kblocks * (part + 1) / split;
   const int blocks = kb1 - kb0;
+  const int rows = min(TN, p.M - m0);
+  const int share = (rows + split - 1) / split;   // rows of A that one CTA adds up and stores
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -417,181 +545,200 @@ __global__ void __launch_bounds__(kThreads) gemm_fp8_narrow_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // The cluster's CTAs have started once this barrier completes; sums may be
+  // sent into them from then on (or, in the ring's place, from its second use).
+  __syncwarp();
+  if (C::kOwnSums && split > 1) cluster_arrive();
 
-  float acc[TN];
+  f32x2 acc[TN / 2];
   if (warp == 0) {
-    if (lane == 0) {
-      // -------------------------------------------------------- producer
-      int i = 0;
-      for (; i < blocks; ++i) {
-        const int st = i % S;
-        if (!mbar_wait(empty_bar(st), ((uint32_t)(i / S) & 1u) ^ 1u, abort_flag, kWaitNs)) break;
+    // ------------------------------------------------------------ producer
+    uint32_t st = 0, ph = 1;
+    int i = 0;
+    for (; i < blocks; ++i) {
+      if (!__all_sync(0xffffffffu, wait_bar(empty_bar(st), ph, abort_flag))) break;
+      if (elect_one()) {
         mbar_arrive_expect_tx(full_bar(st), C::kStageBytes);
         const uint32_t sw = base + st * C::kStageBytes;
         tma_load_2d(sw, &p.tmW[r], full_bar(st), (kb0 + i) * kBlockK, nb * 128);
         tma_load_2d(sw + kWBytes, &p.tmA[r], full_bar(st), (kb0 + i) * kBlockK, m0);
       }
-      // Every load still in flight lands before the ring is used again.
-      volatile int never = 0;
-      for (int j = i > S ? i - S : 0; j < i; ++j)
-        mbar_wait(full_bar(j % S), (uint32_t)(j / S) & 1u, &never, 100000000ull);
+      __syncwarp();
+      if (++st == S) st = 0, ph ^= 1u;
     }
+    // Every load still in flight lands before the ring is used again.
+    volatile int never = 0;
+    for (int j = i > S ? i - S : 0; j < i; ++j)
+      mbar_wait(full_bar(j % S), (uint32_t)(j / S) & 1u, &never, 100000000ull);
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMAs
-      constexpr uint32_t id = idesc_fp8(128, TN);
-      for (int i = 0; i < blocks; ++i) {
-        const int st = i % S;
-        const uint32_t a = (uint32_t)i % NB;
-        if (!mbar_wait(tempty_bar(a), ((uint32_t)(i / NB) & 1u) ^ 1u, abort_flag, kWaitNs) ||
-            !mbar_wait(full_bar(st), (uint32_t)(i / S) & 1u, abort_flag, kWaitNs))
-          break;
-        tc_fence_after();
-        const uint32_t sw = base + st * C::kStageBytes;
+    // -------------------------------------------------------------- MMAs
+    // (The whole warp, one lane issuing: see the wide kernel.)
+    constexpr uint32_t id = idesc_fp8(128, TN);
+    const uint64_t w0 = smem_desc_sw128(base, 16, 1024), x0 = smem_desc_sw128(base + kWBytes, 16, 1024);
+    uint32_t st = 0, a = 0, ph = 0, aph = 1;
+    for (int i = 0; i < blocks; ++i) {
+      if (!__all_sync(0xffffffffu, wait_bar(tempty_bar(a), aph, abort_flag) && wait_bar(full_bar(st), ph, abort_flag)))
+        break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t dw = w0 + st * (C::kStageBytes >> 4), dx = x0 + st * (C::kStageBytes >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_fp8<1>(tmem + a * TN, smem_desc_sw128(sw + k * 32u, 16, 1024),
-                     smem_desc_sw128(sw + kWBytes + k * 32u, 16, 1024), id, k > 0 ? 1u : 0u);
-        tc_commit<1>(empty_bar(st));
+        for (int k = 0; k < 4; ++k) mma_fp8<1>(tmem + a * TN, dw + 2 * k, dx + 2 * k, id, k > 0 ? 1u : 0u);
         tc_commit<1>(tfull_bar(a));
+        tc_commit<1>(empty_bar(st));
       }
+      __syncwarp();
+      if (++st == S) st = 0, ph ^= 1u;
+      if (++a == NB) a = 0, aph ^= 1u;
+    }
+    if (elect_one()) {
       tc_commit<1>(done_bar);
       volatile int never = 0;
       mbar_wait(done_bar, 0, &never, 100000000ull);
     }
+    __syncwarp();
   } else {
     // ---------------------------------------------------------- accumulate
-    const int q = warp & 3, tid = threadIdx.x - 64;
+    const int q = warp & 3;
+    // Scales of blocks first .. first + 31: lane = block, so a warp reads 128
+    // neighbouring bytes of a row's scales.
     auto load_scales = [&](int first) {
-#pragma unroll 4
-      for (int i = tid; i < kScaleBlocks * TN; i += 128) {
-        const int c = i / kScaleBlocks, b = i % kScaleBlocks;   // neighbours: neighbouring blocks of a row
-        const int m = m0 + c, kb = kb0 + first + b;
-        if (m < p.M && kb < kb1)
-          sScale[b * (TN + 4) + c] = __ldg(p.sA[r] + (int64_t)m * p.kblocks + kb) *
-                                     __ldg(p.sW[r] + (int64_t)nb * p.kblocks + kb);
-        else
-          sScale[b * (TN + 4) + c] = 0.f;
-      }
+      const int kb = kb0 + first + lane;
+      const bool in = kb < kb1;
+      const float w = in ? __ldg(p.sW[r] + (int64_t)nb * p.kblocks + kb) : 0.f;
+      const float* sa = p.sA[r] + (int64_t)m0 * p.kblocks + kb;
+#pragma unroll
+      for (int c = warp - 2; c < TN; c += 4)
+        sScale[lane * C::kScaleLd + c] = in && c < rows ? w * __ldg(sa + (int64_t)c * p.kblocks) : 0.f;
       asm volatile("bar.sync 1, 128;" ::: "memory");
     };
 #pragma unroll
-    for (int c = 0; c < TN; ++c) acc[c] = 0.f;
+    for (int c = 0; c < TN / 2; ++c) acc[c] = 0ull;
+    int a = 0;
+    uint32_t aph = 0;
     for (int i = 0; i < blocks; ++i) {
-      if (i % kScaleBlocks == 0) {
+      const int at_scale = i % kScaleBlocks;
+      if (at_scale == 0) {
         if (i) asm volatile("bar.sync 1, 128;" ::: "memory");   // the last scales have been read
         load_scales(i);
       }
-      const uint32_t a = (uint32_t)i % NB;
       // (After a wait that ran out the loop goes on, for the barriers' sake:
       // the waits that follow return at once.)
-      mbar_wait(tfull_bar(a), (uint32_t)(i / NB) & 1u, abort_flag, kWaitNs);
+      wait_bar(tfull_bar(a), aph, abort_flag);
       tc_fence_after();
       const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + a * TN;
-      const float4* s4 = reinterpret_cast<const float4*>(sScale + (i % kScaleBlocks) * (TN + 4));
-      if constexpr (TN == 16) {
-        uint32_t v[16];
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-              "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-            : "r"(at));
+      const ulonglong2* s4 = reinterpret_cast<const ulonglong2*>(sScale + at_scale * C::kScaleLd);
+      constexpr int W = TN < 32 ? TN : 32;
+#pragma unroll
+      for (int c = 0; c < TN; c += W) {
+        uint32_t v[W];
+        if constexpr (TN == 16) tmem_ld16(at, v);
+        else tmem_ld32(at + c, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(v[j]));
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tempty_bar(a));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 s = s4[j];
-          acc[4 * j] = fmaf(__uint_as_float(v[4 * j]), s.x, acc[4 * j]);
-          acc[4 * j + 1] = fmaf(__uint_as_float(v[4 * j + 1]), s.y, acc[4 * j + 1]);
-          acc[4 * j + 2] = fmaf(__uint_as_float(v[4 * j + 2]), s.z, acc[4 * j + 2]);
-          acc[4 * j + 3] = fmaf(__uint_as_float(v[4 * j + 3]), s.w, acc[4 * j + 3]);
+        for (int j = 0; j < W; ++j) asm volatile("" : "+r"(v[j]));
+        if (c + W == TN) {   // the buffer has been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty_bar(a));
         }
-      } else {
 #pragma unroll
-        for (int c = 0; c < TN; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(at + c, v);
-          tmem_ld_wait();
-          reg_fence(v);
-          if (c + 32 == TN) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tempty_bar(a));
-          }
+        for (int j = 0; j < W / 4; ++j) {
+          const ulonglong2 s = s4[c / 4 + j];
+          acc[c / 2 + 2 * j] = fma2(pair_of(v[4 * j], v[4 * j + 1]), s.x, acc[c / 2 + 2 * j]);
+          acc[c / 2 + 2 * j + 1] = fma2(pair_of(v[4 * j + 2], v[4 * j + 3]), s.y, acc[c / 2 + 2 * j + 1]);
+        }
+      }
+      if (++a == NB) a = 0, aph ^= 1u;
+    }
+  }
+  if (!C::kOwnSums) {   // loads and MMAs are done, in every CTA of the cluster: the rings are free
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    __syncwarp();
+    if (split > 1) cluster_arrive();
+  }
+  __syncwarp();
+  if (split > 1) cluster_wait();
+  if (warp >= 2) {
+    // Each row's sums go to the CTA that stores it (this one without a
+    // split), 128 floats from a sender.
+    const uint32_t mine = base + C::kOffSums + (uint32_t)part * (uint32_t)share * 512u +
+                          (uint32_t)((warp & 3) * 32 + lane) * 4u;
+    int owner = 0, left = share;
+    uint32_t to = split > 1 ? mapa_shared(mine, 0) : mine;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 s = s4[c / 4 + j];
-            acc[c + 4 * j] = fmaf(__uint_as_float(v[4 * j]), s.x, acc[c + 4 * j]);
-            acc[c + 4 * j + 1] = fmaf(__uint_as_float(v[4 * j + 1]), s.y, acc[c + 4 * j + 1]);
-            acc[c + 4 * j + 2] = fmaf(__uint_as_float(v[4 * j + 2]), s.z, acc[c + 4 * j + 2]);
-            acc[c + 4 * j + 3] = fmaf(__uint_as_float(v[4 * j + 3]), s.w, acc[c + 4 * j + 3]);
-          }
+    for (int c = 0; c < TN; ++c) {
+      if (c < rows) {
+        float lo, hi;
+        halves(acc[c / 2], lo, hi);
+        const float v = c & 1 ? hi : lo;
+        if (split > 1) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+        else asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+        to += 512u;
+        if (--left == 0) {
+          left = share;
+          if (++owner < split) to = mapa_shared(mine, (uint32_t)owner);
         }
       }
     }
   }
   tc_fence_before();
-  __syncthreads();   // loads and MMAs are done: the ring is free
+  __syncwarp();
+  if (split > 1) cluster_sync_all();
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     __syncwarp();
     tmem_dealloc<1>(tmem, C::kCols);
   }
   if (threadIdx.x == 0 && *abort_flag) record_error(p.status, FO_ERR_TIMEOUT, -1, -1, 0);
-
-  // The sums of the cluster's CTAs meet in shared memory, [TN][128] each in
-  // the ring's place; every CTA adds and stores its share of A's rows, in
-  // the order of the reduction.
-  float* const sSum = reinterpret_cast<float*>(gbase);
-  static_assert(C::kRing >= TN * 128 * 4, "the sums fit into the ring");
-  if (warp >= 2) {
-    const int row = (warp & 3) * 32 + lane;
+  // This CTA's rows: the senders' sums added in the order of the reduction.
+  const float4* sums = reinterpret_cast<const float4*>(gbase + C::kOffSums);
+  const int n = nb * 128 + lane * 4;
+  for (int c = warp; c < share && part * share + c < rows; c += kThreads / 32) {
+    float4 v = sums[c * 32 + lane];
+    for (int k = 1; k < split; ++k) {
+      const float4 u = sums[(k * share + c) * 32 + lane];
+      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    const int64_t at = (int64_t)(m0 + part * share + c) * p.N + n;
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    if (p.f32) {
+      float* y = static_cast<float*>(p.Y[r]) + at;
+      if (p.vec && n + 4 <= p.N) {
+        *reinterpret_cast<float4*>(y) = v;
+      } else {
 #pragma unroll
-    for (int c = 0; c < TN; ++c) sSum[c * 128 + row] = acc[c];
-  }
-  __syncwarp();
-  if (split > 1) cluster_sync_all();
-  else __syncthreads();
-  const int rows = min(TN, p.M - m0);
-  const int c0 = rows * part / split, c1 = rows * (part + 1) / split;
-  for (int i = c0 * 128 + (int)threadIdx.x; i < c1 * 128; i += kThreads) {
-    const int c = i >> 7, n = nb * 128 + (i & 127);
-    float s = 0.f;
-    if (split > 1) {
-      for (int k = 0; k < split; ++k) {
-        float v;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(base + 4u * (uint32_t)i, k)) : "memory");
-        s += v;
+        for (int j = 0; j < 4; ++j)
+          if (n + j < p.N) y[j] = f[j];
       }
     } else {
-      s = sSum[i];
-    }
-    if (n < p.N) {
-      const int64_t at = (int64_t)(m0 + c) * p.N + n;
-      if (p.f32) static_cast<float*>(p.Y[r])[at] = s;
-      else static_cast<__nv_bfloat16*>(p.Y[r])[at] = __float2bfloat16_rn(s);
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.Y[r]) + at;
+      if (p.vec && n + 4 <= p.N) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(y) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j < p.N) y[j] = __float2bfloat16_rn(f[j]);
+      }
     }
   }
-  __syncwarp();
-  if (split > 1) cluster_sync_all();   // no CTA leaves while another reads its sums
 }
 
 template <int TN>
 cudaError_t launch(const GemmParams& k, int split, cudaStream_t s, int* grid_out) {
-  constexpr int smem = smem_bytes<TN>();
   auto kern = gemm_fp8_narrow_kernel<TN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<TN>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(split, k.nblocks, k.tiles_m * k.R);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = Cfg<TN>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
@@ -614,10 +761,15 @@ Choice choose(int R, int64_t M, int64_t N, int64_t kblocks) {
   Choice c;
   const int64_t pairs = R * ((M + 255) / 256) * ((N + 255) / 256);
   if (M > 128 && pairs >= 38) return {0, 1};
-  c.tn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  c.tn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
   const int64_t tiles = R * ((M + c.tn - 1) / c.tn) * ((N + 127) / 128);
+  int64_t best = INT64_MAX;
   c.split = 1;
-  while (c.split < 8 && tiles * c.split * 2 <= 2 * FO_GB300_SMS && kblocks >= 4 * c.split) c.split *= 2;
+  for (int64_t k = 1; k <= narrow::kMaxSplit && k <= kblocks; ++k) {
+    const int64_t n = (tiles * k + FO_GB300_SMS - 1) / FO_GB300_SMS;
+    const int64_t cost = n * ((kblocks + k - 1) / k) + 6 * ((n + 1) / 2) + (k > 1 ? 4 : 0);
+    if (cost < best) best = cost, c.split = (int)k;
+  }
   return c;
 }
 
@@ -632,9 +784,9 @@ fo_status check_desc(const fo_gemm_fp8_desc* d, int64_t M) {
   return FO_OK;
 }
 
-// [rows x cols] bytes, boxes of 128 columns x `box` rows; what lies outside
-// reads as zero.
-bool encode(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint32_t box) {
+// [rows x cols] values of `es` bytes, boxes of 128 bytes x `box` rows; what
+// lies outside reads as zero and is not written.
+bool encode(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint32_t box, int es = 1) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -645,10 +797,13 @@ bool encode(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint3
   }();
   if (!fn) return false;
   cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols};
-  cuuint32_t size[2] = {128, box};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, size, es,
+  cuuint64_t strides[1] = {cols * es};
+  cuuint32_t size[2] = {128u / es, box};
+  cuuint32_t each[2] = {1, 1};
+  const CUtensorMapDataType type = es == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  return fn(m, type, 2, const_cast<void*>(ptr), dims, strides, size, each,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -727,7 +882,11 @@ extern "C" fo_status fo_gemm_fp8(const fo_gemm_fp8_desc* d, int64_t M, const voi
   k.kblocks = (int32_t)((d->K + kBlockK - 1) / kBlockK);
   k.nblocks = (int32_t)((d->N + 127) / 128);
   const Choice c = choose(R, M, d->N, k.kblocks);
+  k.f32 = d->out_dtype == FO_F32;
+  const int es = k.f32 ? 4 : 2;
+  k.vec = (d->N * es) % 16 == 0;
   for (int r = 0; r < R; ++r) {
+    if (c.tn == 0 && k.vec && !encode(&k.tmY[r], Y[r], (uint64_t)d->N, (uint64_t)M, 32, es)) return FO_ERR_CUDA;
     if (r && A[r] == A[r - 1]) k.tmA[r] = k.tmA[r - 1];
     else if (!encode(&k.tmA[r], A[r], (uint64_t)d->K, (uint64_t)M, c.tn ? c.tn : 128)) return FO_ERR_CUDA;
     if (!encode(&k.tmW[r], W[r], (uint64_t)d->K, (uint64_t)d->N, 128)) return FO_ERR_CUDA;
@@ -739,8 +898,6 @@ extern "C" fo_status fo_gemm_fp8(const fo_gemm_fp8_desc* d, int64_t M, const voi
   k.R = R;
   k.M = (int32_t)M;
   k.N = (int32_t)d->N;
-  k.f32 = d->out_dtype == FO_F32;
-  k.vec = (d->N * (k.f32 ? 4 : 2)) % 16 == 0;
   const cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
   int grid = 0, threads = 0;
@@ -775,8 +932,7 @@ extern "C" fo_status fo_gemm_fp8(const fo_gemm_fp8_desc* d, int64_t M, const voi
     switch (c.tn) {
       case 16: e = narrow::launch<16>(k, c.split, s, &grid); break;
       case 32: e = narrow::launch<32>(k, c.split, s, &grid); break;
-      case 64: e = narrow::launch<64>(k, c.split, s, &grid); break;
-      default: e = narrow::launch<128>(k, c.split, s, &grid); break;
+      default: e = narrow::launch<64>(k, c.split, s, &grid); break;
     }
   }
   if (e != cudaSuccess) {

@@ -477,20 +477,11 @@ struct Cfg {
   static constexpr uint32_t kRing = kStages * kStageBytes;
   static constexpr int kScaleLd = TN + 4;   // [block][row of A], padded to spread the banks
   static constexpr uint32_t kScales = kScaleBlocks * kScaleLd * 4;
-  // Sums that the cluster's CTAs send: [sender][row of A][128]. Beside the
-  // ring where that still leaves room for two CTAs on an SM, else in its
-  // place once every CTA is done with its ring.
-  static constexpr bool kOwnSums = TN <= 32;
-  static constexpr uint32_t kSums = (TN + kMaxSplit - 1) * 512;
   static constexpr uint32_t kOffBar = kRing;
   static constexpr uint32_t kOffScale = kOffBar + 256;
-  static constexpr uint32_t kOffSums = kOwnSums ? kOffScale + kScales : 0;
-  static constexpr int kSmem = 1024 + (int)(kOffScale + kScales + (kOwnSums ? kSums : 0));
-  static_assert(kOwnSums || kSums <= kRing, "the sums fit into the ring");
+  static constexpr int kSmem = 1024 + (int)(kOffScale + kScales);
+  static_assert(TN * 128 * 4 <= kRing, "a CTA's sums fit in the ring's place");
 };
-
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <int TN>
 __global__ void __launch_bounds__(kThreads) gemm_fp8_narrow_kernel(const __grid_constant__ GemmParams p, int split) {
@@ -545,10 +536,7 @@ __global__ void __launch_bounds__(kThreads) gemm_fp8_narrow_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // The cluster's CTAs have started once this barrier completes; sums may be
-  // sent into them from then on (or, in the ring's place, from its second use).
   __syncwarp();
-  if (C::kOwnSums && split > 1) cluster_arrive();
 
   f32x2 acc[TN / 2];
   if (warp == 0) {
@@ -652,81 +640,69 @@ __global__ void __launch_bounds__(kThreads) gemm_fp8_narrow_kernel(const __grid_
       if (++a == NB) a = 0, aph ^= 1u;
     }
   }
-  if (!C::kOwnSums) {   // loads and MMAs are done, in every CTA of the cluster: the rings are free
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    __syncwarp();
-    if (split > 1) cluster_arrive();
-  }
-  __syncwarp();
-  if (split > 1) cluster_wait();
-  if (warp >= 2) {
-    // Each row's sums go to the CTA that stores it (this one without a
-    // split), 128 floats from a sender.
-    const uint32_t mine = base + C::kOffSums + (uint32_t)part * (uint32_t)share * 512u +
-                          (uint32_t)((warp & 3) * 32 + lane) * 4u;
-    int owner = 0, left = share;
-    uint32_t to = split > 1 ? mapa_shared(mine, 0) : mine;
-#pragma unroll
-    for (int c = 0; c < TN; ++c) {
-      if (c < rows) {
-        float lo, hi;
-        halves(acc[c / 2], lo, hi);
-        const float v = c & 1 ? hi : lo;
-        if (split > 1) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
-        else asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
-        to += 512u;
-        if (--left == 0) {
-          left = share;
-          if (++owner < split) to = mapa_shared(mine, (uint32_t)owner);
-        }
-      }
-    }
-  }
   tc_fence_before();
-  __syncwarp();
-  if (split > 1) cluster_sync_all();
-  else __syncthreads();
+  __syncthreads();   // loads and MMAs are done: the ring is free
   if (warp == 1) {
     tc_fence_after();
     __syncwarp();
     tmem_dealloc<1>(tmem, C::kCols);
   }
   if (threadIdx.x == 0 && *abort_flag) record_error(p.status, FO_ERR_TIMEOUT, -1, -1, 0);
-  // This CTA's rows: the senders' sums added in the order of the reduction.
-  const float4* sums = reinterpret_cast<const float4*>(gbase + C::kOffSums);
+  // The CTA's sums into its shared memory, [row of A][128 weight rows]; then
+  // every CTA of the cluster adds up its share of A's rows from all of them,
+  // in the order of the reduction, and stores them.
+  if (warp >= 2) {
+    float* mine = reinterpret_cast<float*>(gbase) + (warp & 3) * 32 + lane;
+#pragma unroll
+    for (int c = 0; c < TN; c += 2) halves(acc[c / 2], mine[c * 128], mine[c * 128 + 128]);
+  }
+  __syncwarp();
+  if (split > 1) cluster_sync_all();
+  else __syncthreads();
   const int n = nb * 128 + lane * 4;
-  for (int c = warp; c < share && part * share + c < rows; c += kThreads / 32) {
-    float4 v = sums[c * 32 + lane];
-    for (int k = 1; k < split; ++k) {
-      const float4 u = sums[(k * share + c) * 32 + lane];
-      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+  for (int j = warp; j < share && part * share + j < rows; j += kThreads / 32) {
+    const int c = part * share + j;
+    const uint32_t at = base + (uint32_t)(c * 128 + lane * 4) * 4u;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (split > 1) {
+#pragma unroll 4
+      for (int k = 0; k < split; ++k) {
+        float4 u;
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(u.x), "=f"(u.y), "=f"(u.z), "=f"(u.w)
+                     : "r"(mapa_shared(at, (uint32_t)k))
+                     : "memory");
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+      }
+    } else {
+      v = *reinterpret_cast<const float4*>(gbase + (c * 128 + lane * 4) * 4);
     }
-    const int64_t at = (int64_t)(m0 + part * share + c) * p.N + n;
+    const int64_t to = (int64_t)(m0 + c) * p.N + n;
     const float f[4] = {v.x, v.y, v.z, v.w};
     if (p.f32) {
-      float* y = static_cast<float*>(p.Y[r]) + at;
+      float* y = static_cast<float*>(p.Y[r]) + to;
       if (p.vec && n + 4 <= p.N) {
         *reinterpret_cast<float4*>(y) = v;
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (n + j < p.N) y[j] = f[j];
+        for (int i = 0; i < 4; ++i)
+          if (n + i < p.N) y[i] = f[i];
       }
     } else {
-      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.Y[r]) + at;
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.Y[r]) + to;
       if (p.vec && n + 4 <= p.N) {
         const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
         *reinterpret_cast<uint2*>(y) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (n + j < p.N) y[j] = __float2bfloat16_rn(f[j]);
+        for (int i = 0; i < 4; ++i)
+          if (n + i < p.N) y[i] = __float2bfloat16_rn(f[i]);
       }
     }
   }
+  __syncwarp();
+  if (split > 1) cluster_sync_all();   // no CTA leaves while another reads its sums
 }
 
 template <int TN>
@@ -756,21 +732,37 @@ struct Choice {
   int tn, split;   // tn 0: wide
 };
 
-// Which kernel, and how it is cut.
+// Which kernel, and how it is cut: the cheapest by a model of the time in ns,
+// fitted to GB300 runs (operands in L2):
+//   wide    5200 + waves of 76 tiles x (345 a block + 800)
+//   narrow  a start and an end, then per block of a CTA's share one time when
+//           it has the SM for itself and one when two share it; a split adds
+//           the cluster's barriers and sums.
+// Both sides, measured: 128 x 12288 x 4096 wide 16.5 us, narrow 20.8 us; 128 x
+// 4096 x 4096 wide 16.2 us, narrow 10.1 us (64 rows, split 4); 333 x 1000 x
+// 1744 wide 11.1 us, narrow 6.8 us (32 rows, no split; split 3: 7.7 us); 4 x
+// 12288 x 4096 8.9 us split in 3, 9.1 us whole; 1 x 4096 x 4096 5.5 us split in
+// 4, 9.1 us whole.
 Choice choose(int R, int64_t M, int64_t N, int64_t kblocks) {
-  Choice c;
-  const int64_t pairs = R * ((M + 255) / 256) * ((N + 255) / 256);
-  if (M > 128 && pairs >= 38) return {0, 1};
-  c.tn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-  const int64_t tiles = R * ((M + c.tn - 1) / c.tn) * ((N + 127) / 128);
-  int64_t best = INT64_MAX;
-  c.split = 1;
-  for (int64_t k = 1; k <= narrow::kMaxSplit && k <= kblocks; ++k) {
-    const int64_t n = (tiles * k + FO_GB300_SMS - 1) / FO_GB300_SMS;
-    const int64_t cost = n * ((kblocks + k - 1) / k) + 6 * ((n + 1) / 2) + (k > 1 ? 4 : 0);
-    if (cost < best) best = cost, c.split = (int)k;
+  const int64_t pairs = FO_GB300_SMS / 2, tiles_w = R * ((M + 255) / 256) * ((N + 255) / 256);
+  Choice best = {0, 1};
+  int64_t least = 5200 + (tiles_w + pairs - 1) / pairs * (kblocks * 345 + 800);
+  static const struct {
+    int tn, fixed, alone, shared;
+  } kNarrow[3] = {{16, 3300, 180, 400}, {32, 4350, 190, 320}, {64, 4900, 280, 520}};
+  for (const auto& v : kNarrow) {
+    if (v.tn > 16 && v.tn >= 2 * M) break;   // more than half of the columns would be empty
+    const int64_t tiles = R * ((M + v.tn - 1) / v.tn) * ((N + 127) / 128);
+    if (tiles > 64 * FO_GB300_SMS) continue;   // long past the point where wide wins
+    for (int64_t k = 1; k <= narrow::kMaxSplit && k <= kblocks; ++k) {
+      const int64_t full = tiles * k / (2 * FO_GB300_SMS), rest = tiles * k % (2 * FO_GB300_SMS);
+      const int64_t block = full * v.shared + (rest == 0 ? 0 : rest <= FO_GB300_SMS ? v.alone : v.shared);
+      const int64_t waves = full + (rest ? 1 : 0);
+      const int64_t cost = v.fixed + (waves - 1) * v.fixed / 2 + (k > 1 ? 1200 : 0) + (kblocks + k - 1) / k * block;
+      if (cost < least) least = cost, best = {v.tn, (int)k};
+    }
   }
-  return c;
+  return best;
 }
 
 fo_status check_desc(const fo_gemm_fp8_desc* d, int64_t M) {

@@ -78,15 +78,40 @@ struct Chunk {
       }
     }
   }
-  // The weight's values of the chunk (dtype its own, read value by value).
+  // The chunk's weights plus the offset (WIDE: in 16- or 8-byte pieces, for
+  // which the weight starts on 16 bytes; zero beyond H).
   static __device__ __forceinline__ void load_w(const void* w, bool f32, float offset, int chunk, int lane, int H,
                                                 float (&f)[E]) {
+    if constexpr (WIDE) {
+      const int c = col(chunk, lane, 0);
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const int c = col(chunk, lane, j);
-      f[j] = c >= H ? 0.f
-                    : offset + (f32 ? static_cast<const float*>(w)[c]
-                                    : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c]));
+      for (int j = 0; j < E; ++j) f[j] = 0.f;
+      if (c < H) {
+        if (f32) {
+#pragma unroll
+          for (int j = 0; j < E; j += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + j));
+            f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; j += 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + c + j));
+            f[j] = __uint_as_float(v.x << 16), f[j + 1] = __uint_as_float(v.x & 0xffff0000u);
+            f[j + 2] = __uint_as_float(v.y << 16), f[j + 3] = __uint_as_float(v.y & 0xffff0000u);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < E; ++j) f[j] += offset;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int c = col(chunk, lane, j);
+        f[j] = c >= H ? 0.f
+                      : offset + (f32 ? static_cast<const float*>(w)[c]
+                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c]));
+      }
     }
   }
 };
@@ -116,18 +141,24 @@ __global__ void __launch_bounds__(NW * 32) rmsnorm_kernel(const __grid_constant_
     float s[C][K::E];
     float sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int chunk = c * NW + warp;
-      K::load(static_cast<const T*>(p.x[r]) + off, chunk, lane, p.H, s[c]);
-      if (p.has_res) {
+    for (int c = 0; c < C; ++c) K::load(static_cast<const T*>(p.x[r]) + off, c * NW + warp, lane, p.H, s[c]);
+    if (p.has_res) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
         float t[K::E];
-        K::load(static_cast<const T*>(p.res[r]) + off, chunk, lane, p.H, t);
+        K::load(static_cast<const T*>(p.res[r]) + off, c * NW + warp, lane, p.H, t);
 #pragma unroll
         for (int j = 0; j < K::E; ++j) s[c][j] += t[j];
       }
-      if (p.has_h) K::store(static_cast<T*>(p.h[r]) + off, chunk, lane, p.H, s[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
 #pragma unroll
       for (int j = 0; j < K::E; ++j) sum = fmaf(s[c][j], s[c][j], sum);
+    }
+    if (p.has_h) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) K::store(static_cast<T*>(p.h[r]) + off, c * NW + warp, lane, p.H, s[c]);
     }
     const float rstd = 1.f / sqrtf(block_sum<NW>(sum, smem) / (float)p.H + p.eps);
     if (p.has_rstd && threadIdx.x == 0) p.rstd[r][at] = rstd;
@@ -171,73 +202,156 @@ struct NormBwdParams {
   bool has_dh, has_dw, w_f32;
 };
 
-// A block takes every gridDim.x-th row and keeps its columns' share of the
-// weight's gradient in registers.
-template <typename T, bool WIDE, int NW, int C>
-__global__ void __launch_bounds__(NW * 32) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+// A thread's raw values of one row's chunk: 16 bytes (WIDE) or E values.
+template <typename T, bool WIDE>
+struct Raw {
   using K = Chunk<T, WIDE>;
+  uint4 u;
+  float f[WIDE ? 1 : K::E];
+  __device__ __forceinline__ void load(const T* p, int chunk, int lane, int H) {
+    if constexpr (WIDE) {
+      const int c = K::col(chunk, lane, 0);
+      u = make_uint4(0, 0, 0, 0);
+      if (c < H) u = *reinterpret_cast<const uint4*>(p + c);
+    } else {
+      K::load(p, chunk, lane, H, f);
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[K::E]) const {
+    if constexpr (WIDE) {
+      Vec16<T>::unpack(u, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < K::E; ++j) v[j] = f[j];
+    }
+  }
+};
+
+// Blocks of the backward kernel on an SM: sixteen warps' worth.
+constexpr int bwd_per_sm(int nw) { return nw <= 16 ? 16 / nw : 1; }
+
+// A block takes every gridDim.x-th row and keeps its columns' share of the
+// weight's gradient in registers. What else it keeps goes by the registers
+// that a thread's part of a row takes: where it is 32 bytes or less, the
+// weights too, and the next row's values are loaded before this row's sum is
+// known, so that loads are in flight through the two barriers; beyond, with
+// up to 16 warps, this row's values; else nothing, and the second pass over
+// the row reads it again, from L2.
+template <typename T, bool WIDE, int NW, int C>
+__global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+  using K = Chunk<T, WIDE>;
+  constexpr int E = K::E;
+  constexpr bool kAhead = C * E * (WIDE ? (int)sizeof(T) : 4) <= 32, kHold = kAhead || NW <= 16;
   __shared__ float smem[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float dw[C][K::E];
+  float w[kAhead ? C : 1][E], dw[C][E];
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    if constexpr (kAhead) K::load_w(p.w, p.w_f32, p.w_offset, c * NW + warp, lane, p.H, w[c]);
 #pragma unroll
-    for (int j = 0; j < K::E; ++j) dw[c][j] = 0.f;
+    for (int j = 0; j < E; ++j) dw[c][j] = 0.f;
+  }
+  constexpr int CA = kAhead ? C : 1;
+  Raw<T, WIDE> dy_n[CA], h_n[CA], dh_n[CA];
+  float rstd_n = 0.f;
+  auto fetch = [&](int64_t row) {
+    const int r = (int)(row / p.rows);
+    const int64_t at = row - r * p.rows, off = at * p.H;
+    rstd_n = p.rstd[r][at];
+#pragma unroll
+    for (int c = 0; c < CA; ++c) {
+      dy_n[c].load(static_cast<const T*>(p.dy[r]) + off, c * NW + warp, lane, p.H);
+      h_n[c].load(static_cast<const T*>(p.h[r]) + off, c * NW + warp, lane, p.H);
+      if (p.has_dh) dh_n[c].load(static_cast<const T*>(p.dh[r]) + off, c * NW + warp, lane, p.H);
+    }
+  };
+  if (kAhead && blockIdx.x < p.total) fetch(blockIdx.x);
   for (int64_t row = blockIdx.x; row < p.total; row += gridDim.x) {
     const int r = (int)(row / p.rows);
-    const int64_t at = row - r * p.rows;
-    const int64_t off = at * p.H;
-    const float rstd = p.rstd[r][at];
-    float h[C][K::E], u[C][K::E];
+    const int64_t at = row - r * p.rows, off = at * p.H;
+    const T* const dy = static_cast<const T*>(p.dy[r]) + off;
+    const T* const hp = static_cast<const T*>(p.h[r]) + off;
+    const float rstd = kAhead ? rstd_n : p.rstd[r][at];
+    float h[kHold ? C : 1][E], u[kHold ? C : 1][E];
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int chunk = c * NW + warp;
-      float w[K::E];
-      K::load(static_cast<const T*>(p.dy[r]) + off, chunk, lane, p.H, u[c]);
-      K::load(static_cast<const T*>(p.h[r]) + off, chunk, lane, p.H, h[c]);
-      K::load_w(p.w, p.w_f32, p.w_offset, chunk, lane, p.H, w);
-#pragma unroll
-      for (int j = 0; j < K::E; ++j) {
-        dw[c][j] = fmaf(u[c][j] * rstd, h[c][j], dw[c][j]);
-        u[c][j] *= w[j];
-        sum = fmaf(u[c][j], h[c][j], sum);
+      float(&uc)[E] = u[kHold ? c : 0];
+      float(&hc)[E] = h[kHold ? c : 0];
+      if constexpr (kAhead) {
+        dy_n[c].values(uc);
+        h_n[c].values(hc);
+      } else {
+        K::load(dy, c * NW + warp, lane, p.H, uc);
+        K::load(hp, c * NW + warp, lane, p.H, hc);
+        K::load_w(p.w, p.w_f32, p.w_offset, c * NW + warp, lane, p.H, w[0]);
       }
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        dw[c][j] = fmaf(uc[j] * rstd, hc[j], dw[c][j]);
+        uc[j] *= w[kAhead ? c : 0][j];
+        sum = fmaf(uc[j], hc[j], sum);
+      }
+    }
+    Raw<T, WIDE> dh[CA];
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) dh[c] = dh_n[c];
+      if (row + gridDim.x < p.total) fetch(row + gridDim.x);
     }
     const float k = block_sum<NW>(sum, smem) / (float)p.H * rstd * rstd * rstd;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int chunk = c * NW + warp;
-      float d[K::E];
+      float(&uc)[E] = u[kHold ? c : 0];
+      float(&hc)[E] = h[kHold ? c : 0];
+      if constexpr (!kHold) {
+        K::load(dy, c * NW + warp, lane, p.H, uc);
+        K::load(hp, c * NW + warp, lane, p.H, hc);
+        K::load_w(p.w, p.w_f32, p.w_offset, c * NW + warp, lane, p.H, w[0]);
 #pragma unroll
-      for (int j = 0; j < K::E; ++j) d[j] = rstd * u[c][j] - h[c][j] * k;
-      if (p.has_dh) {
-        float t[K::E];
-        K::load(static_cast<const T*>(p.dh[r]) + off, chunk, lane, p.H, t);
-#pragma unroll
-        for (int j = 0; j < K::E; ++j) d[j] += t[j];
+        for (int j = 0; j < E; ++j) uc[j] *= w[0][j];
       }
-      K::store(static_cast<T*>(p.dx[r]) + off, chunk, lane, p.H, d);
+      float d[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) d[j] = rstd * uc[j] - hc[j] * k;
+      if (p.has_dh) {
+        float t[E];
+        if constexpr (kAhead) dh[c].values(t);
+        else K::load(static_cast<const T*>(p.dh[r]) + off, c * NW + warp, lane, p.H, t);
+#pragma unroll
+        for (int j = 0; j < E; ++j) d[j] += t[j];
+      }
+      K::store(static_cast<T*>(p.dx[r]) + off, c * NW + warp, lane, p.H, d);
     }
   }
   if (p.has_dw) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int j = 0; j < K::E; ++j) {
+      for (int j = 0; j < E; ++j) {
         const int col = K::col(c * NW + warp, lane, j);
         if (col < p.H) p.part[(int64_t)blockIdx.x * p.H + col] = dw[c][j];
       }
   }
 }
 
-// dweight[c] = sum of the blocks' partial sums, in block order.
+// dweight[c] = sum of the blocks' partial sums: a warp adds every eighth
+// block's for 32 columns, then the eight warps' sums are added in order.
 __global__ void __launch_bounds__(256) dweight_kernel(const float* part, int blocks, int H, float* dw) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= H) return;
+  __shared__ float smem[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  for (int b = 0; b < blocks; ++b) s += part[(int64_t)b * H + c];
-  dw[c] = s;
+  if (c < H) {
+#pragma unroll 8
+    for (int b = warp; b < blocks; b += 8) s += part[(int64_t)b * H + c];
+  }
+  smem[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < H) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += smem[k][lane];
+    dw[c] = s;
+  }
 }
 
 fo_status check_desc(const fo_norm_desc* d, int64_t rows) {
@@ -252,9 +366,13 @@ fo_status check_desc(const fo_norm_desc* d, int64_t rows) {
 
 size_t elem(int32_t dtype) { return dtype == FO_BF16 ? 2 : 4; }
 
-// Blocks of the backward pass: enough to fill the GPU, few enough that their
-// partial sums stay small.
-int bwd_blocks(int64_t total) { return (int)(total < 2 * FO_GB300_SMS ? total : 2 * FO_GB300_SMS); }
+// Warps of a block for rows of n chunks (by_width's choice).
+int warps_for(int n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 16 ? 8 : n <= 64 ? 16 : 32; }
+// Blocks of the backward pass (its partial sums are one row each).
+int bwd_blocks(int64_t total, int nw) {
+  const int most = bwd_per_sm(nw) * FO_GB300_SMS;
+  return (int)(total < most ? total : most);
+}
 
 // Calls f.template operator()<T, WIDE, NW, C>() with the fewest warps whose
 // chunks cover H: one chunk a lane while 8 warps suffice, then up to 32 warps
@@ -293,9 +411,11 @@ struct LaunchFwd {
 struct LaunchBwd {
   const NormBwdParams& k;
   cudaStream_t s;
-  int R, grid;
+  int R;
+  int* blocks;
   template <typename T, bool WIDE, int NW, int C>
   fo_status operator()() const {
+    const int grid = *blocks = bwd_blocks(k.total, NW);
     rmsnorm_bwd_kernel<T, WIDE, NW, C><<<grid, NW * 32, 0, s>>>(k);
     return launched("rmsnorm_bwd", R, k.rows, k.H, grid, NW * 32);
   }
@@ -347,7 +467,7 @@ extern "C" fo_status fo_rmsnorm(const fo_norm_desc* d, int64_t rows, const void*
   k.w_offset = d->w_offset;
   k.has_res = residual, k.has_h = h, k.has_y = y, k.has_q = q, k.has_rstd = rstd;
   k.w_f32 = d->w_dtype == FO_F32;
-  const bool wide = (d->H * es) % 16 == 0 && all_aligned(R, x, 16) && all_aligned(R, residual, 16) &&
+  const bool wide = (d->H * es) % 16 == 0 && aligned(weight, 16) && all_aligned(R, x, 16) && all_aligned(R, residual, 16) &&
                     all_aligned(R, (A)h, 16) && all_aligned(R, (A)y, 16) && all_aligned(R, (A)q, 8);
   return by_type(d->dtype, wide, d->H, LaunchFwd{k, (cudaStream_t)stream, R});
 }
@@ -357,7 +477,10 @@ extern "C" fo_status fo_rmsnorm_bwd_workspace(const fo_norm_desc* d, int64_t row
   const fo_status st = check_desc(d, rows);
   if (st) return st;
   if (!bytes) return FO_ERR_INVALID_ARG;
-  const size_t n = (size_t)bwd_blocks(rows * d->R) * (size_t)d->H * sizeof(float);
+  // With 16-byte alignment a chunk is wider and the warps are fewer, so the
+  // blocks are more: enough for either.
+  const int cols = d->dtype == FO_BF16 ? 256 : 128;
+  const size_t n = (size_t)bwd_blocks(rows * d->R, warps_for((d->H + cols - 1) / cols)) * (size_t)d->H * sizeof(float);
   *bytes = n ? n : 16;
   return FO_OK;
 }
@@ -409,12 +532,12 @@ extern "C" fo_status fo_rmsnorm_bwd(const fo_norm_desc* d, int64_t rows, const v
   k.w_offset = d->w_offset;
   k.has_dh = dh, k.has_dw = dweight;
   k.w_f32 = d->w_dtype == FO_F32;
-  const bool wide = (d->H * es) % 16 == 0 && all_aligned(R, dy, 16) && all_aligned(R, dh, 16) &&
+  const bool wide = (d->H * es) % 16 == 0 && aligned(weight, 16) && all_aligned(R, dy, 16) && all_aligned(R, dh, 16) &&
                     all_aligned(R, h, 16) && all_aligned(R, (A)dx, 16);
-  const int grid = bwd_blocks(k.total);
-  if ((st = by_type(d->dtype, wide, d->H, LaunchBwd{k, s, R, grid}))) return st;
+  int grid = 0;
+  if ((st = by_type(d->dtype, wide, d->H, LaunchBwd{k, s, R, &grid}))) return st;
   if (!dweight) return FO_OK;
-  const int cols = (d->H + 255) / 256;
+  const int cols = (d->H + 31) / 32;
   dweight_kernel<<<cols, 256, 0, s>>>(k.part, grid, d->H, dweight);
   return launched("rmsnorm_dweight", R, grid, d->H, cols, 256);
 }

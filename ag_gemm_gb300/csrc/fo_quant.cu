@@ -1,5 +1,6 @@
 // Quantisation to e4m3 with one scale for 128 values of a row, or for each
-// 128 x 128 block (with the transposed copy).
+// 128 x 128 block (with the transposed copy). Bandwidth-bound: each value is
+// read once, in 16-byte pieces, and written once (twice with the copy).
 #include <string.h>
 
 #include "fo_ops.h"
@@ -15,9 +16,11 @@ struct QuantParams {
   float* scale_t[kMaxR];
   int64_t rows, cols;
   int32_t groups, row_blocks;
+  int32_t pieces;   // quant_rows_wide_kernel: warp-wide pieces of a row
 };
 
-// One warp for each group of 128 values of a row.
+// One warp for each group of 128 values of a row (rows that do not start on
+// 16 bytes).
 template <typename T>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__ QuantParams p) {
   const int lane = threadIdx.x & 31, r = blockIdx.y;
@@ -44,7 +47,51 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
   }
 }
 
-// One block for each 128 x 128 block: warp w holds rows w, w + 8, ...
+// A warp takes kUnroll pieces of 32 lanes x 16 bytes at a time, all loads
+// first; a group's scale is the maximum over the 16 (bf16) or 32 lanes that
+// hold it. A piece never crosses a row (rows of whole groups are one long
+// row to this kernel).
+template <typename T>
+__global__ void __launch_bounds__(256) quant_rows_wide_kernel(const __grid_constant__ QuantParams p) {
+  constexpr int E = Vec16<T>::N, kCols = 32 * E, kUnroll = 4, kLanes = FO_FP8_BLOCK / E;
+  const int lane = threadIdx.x & 31, r = blockIdx.y;
+  const int64_t n = p.rows * p.pieces, step = (int64_t)gridDim.x * 8;
+  for (int64_t w = blockIdx.x * 8ll + (threadIdx.x >> 5); w < n; w += step * kUnroll) {
+    uint4 raw[kUnroll];
+    int64_t row[kUnroll];
+    int col[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int64_t u = w + i * step;
+      // (A 64-bit division costs as much as the rest of a piece.)
+      row[i] = p.rows == 1 ? 0 : n <= UINT32_MAX ? (int64_t)((uint32_t)u / (uint32_t)p.pieces) : u / p.pieces;
+      col[i] = (int)(u - row[i] * p.pieces) * kCols + lane * E;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (u < n && col[i] < p.cols)
+        raw[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.x[r]) + row[i] * p.cols + col[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      float v[E], amax = 0.f;
+      Vec16<T>::unpack(raw[i], v);
+#pragma unroll
+      for (int j = 0; j < E; ++j) amax = max_nan(amax, fabsf(v[j]));
+      const float scale = scale_of(lanes_max<kLanes>(amax)), inv = 1.f / scale;
+      if (w + i * step >= n || col[i] >= p.cols) continue;
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[j] *= inv;
+      uint8_t* q = p.q[r] + row[i] * p.cols + col[i];
+      if constexpr (E == 8)
+        *reinterpret_cast<uint2*>(q) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+      else
+        *reinterpret_cast<uint32_t*>(q) = e4m3x4(v[0], v[1], v[2], v[3]);
+      if (lane % kLanes == 0) p.scale[r][row[i] * p.groups + col[i] / FO_FP8_BLOCK] = scale;
+    }
+  }
+}
+
+// One block for each 128 x 128 block: warp w holds rows w, w + 8, ... (rows
+// that do not start on 16 bytes).
 template <typename T>
 __global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant__ QuantParams p) {
   __shared__ float smem[8];
@@ -86,6 +133,98 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant
     }
 }
 
+// Four words of four bytes each, transposed: byte j of word i becomes byte i
+// of word j.
+__device__ __forceinline__ void transpose4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  const uint32_t ab_lo = __byte_perm(a, b, 0x5140), ab_hi = __byte_perm(a, b, 0x7362);
+  const uint32_t cd_lo = __byte_perm(c, d, 0x5140), cd_hi = __byte_perm(c, d, 0x7362);
+  a = __byte_perm(ab_lo, cd_lo, 0x5410);
+  b = __byte_perm(ab_lo, cd_lo, 0x7632);
+  c = __byte_perm(ab_hi, cd_hi, 0x5410);
+  d = __byte_perm(ab_hi, cd_hi, 0x7632);
+}
+
+// One block for each 128 x 128 block, a thread for 8 neighbouring columns of
+// 8 neighbouring rows: the rows' loads are whole 256-byte (fp32: 512-byte)
+// runs, and the thread can transpose its 8 x 8 bytes by itself. The copy's
+// lines of 128 bytes are put together in shared memory, in 8-byte pieces
+// whose place is mixed with the column, so that neither the writes nor the
+// reads meet in a bank.
+template <typename T, bool COPY>
+__global__ void __launch_bounds__(256) quant_blocks_wide_kernel(const __grid_constant__ QuantParams p) {
+  constexpr int V = 8 / Vec16<T>::N;   // 16-byte loads for 8 values
+  __shared__ float smem[8];
+  __shared__ uint2 tile[COPY ? 128 * 16 : 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.z;
+  const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
+  const int rg = tid >> 4, cg = tid & 15;   // groups of 8 rows, of 8 columns
+  const int64_t row0 = r0 + rg * 8, col = c0 + cg * 8;
+  const bool in = col < p.cols;   // whole groups: the columns are a multiple of 8
+  uint4 raw[8][V];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      raw[i][k] = make_uint4(0, 0, 0, 0);
+      if (in && row0 + i < p.rows)
+        raw[i][k] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.x[r]) + (row0 + i) * p.cols + col) + k);
+    }
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      float v[Vec16<T>::N];
+      Vec16<T>::unpack(raw[i][k], v);
+#pragma unroll
+      for (int j = 0; j < Vec16<T>::N; ++j) amax = max_nan(amax, fabsf(v[j]));
+    }
+  amax = lanes_max<32>(amax);
+  if (lane == 0) smem[warp] = amax;
+  __syncthreads();
+  const float scale = scale_of(lanes_max<8>(smem[lane & 7])), inv = 1.f / scale;
+  uint32_t lo[8], hi[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v[8];
+    if constexpr (V == 1) {
+      Vec16<T>::unpack(raw[i][0], reinterpret_cast<float(&)[Vec16<T>::N]>(v));
+    } else {
+      Vec16<T>::unpack(raw[i][0], reinterpret_cast<float(&)[Vec16<T>::N]>(v[0]));
+      Vec16<T>::unpack(raw[i][V - 1], reinterpret_cast<float(&)[Vec16<T>::N]>(v[4]));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= inv;
+    lo[i] = e4m3x4(v[0], v[1], v[2], v[3]);
+    hi[i] = e4m3x4(v[4], v[5], v[6], v[7]);
+    if (in && row0 + i < p.rows) *reinterpret_cast<uint2*>(p.q[r] + (row0 + i) * p.cols + col) = make_uint2(lo[i], hi[i]);
+  }
+  if (tid == 0) {
+    p.scale[r][(int64_t)blockIdx.y * p.groups + blockIdx.x] = scale;
+    if (COPY) p.scale_t[r][(int64_t)blockIdx.x * p.row_blocks + blockIdx.y] = scale;
+  }
+  if constexpr (COPY) {
+    transpose4(lo[0], lo[1], lo[2], lo[3]);   // columns 0-3 of rows 0-3
+    transpose4(lo[4], lo[5], lo[6], lo[7]);   // of rows 4-7
+    transpose4(hi[0], hi[1], hi[2], hi[3]);   // columns 4-7
+    transpose4(hi[4], hi[5], hi[6], hi[7]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      tile[(cg * 8 + j) * 16 + (rg ^ cg)] = make_uint2(lo[j], lo[j + 4]);
+      tile[(cg * 8 + 4 + j) * 16 + (rg ^ cg)] = make_uint2(hi[j], hi[j + 4]);
+    }
+    __syncthreads();
+    // Sixteen threads store a line of the copy (the rows are a multiple of 8).
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = i * 16 + rg;
+      const int64_t row = r0 + cg * 8;
+      if (c0 + c < p.cols && row < p.rows)
+        *reinterpret_cast<uint2*>(p.qt[r] + (c0 + c) * p.rows + row) = tile[c * 16 + (cg ^ (c >> 3))];
+    }
+  }
+}
+
 }  // namespace
 }  // namespace fo_ops
 
@@ -96,7 +235,7 @@ extern "C" fo_status fo_quant_fp8(int32_t R, int64_t rows, int64_t cols, int32_t
   if (R < 1 || R > kMaxR || (block_rows != 1 && block_rows != FO_FP8_BLOCK)) return FO_ERR_INVALID_ARG;
   if (!qt != !scale_t || (qt && block_rows == 1)) return FO_ERR_INVALID_ARG;
   // A grid has at most 65535 blocks in y: block rows of the matrix.
-  if (rows < 0 || rows > (int64_t)65535 * 128 || cols < 1 || cols > (int64_t)INT32_MAX - 128) return FO_ERR_SHAPE;
+  if (rows < 0 || rows > (int64_t)65535 * 128 || cols < 1 || cols > (int64_t)INT32_MAX - 1024) return FO_ERR_SHAPE;
   if (dtype != FO_BF16 && dtype != FO_F32) return FO_ERR_DTYPE;
   if (rows == 0) return FO_OK;
   const size_t es = dtype == FO_BF16 ? 2 : 4;
@@ -124,15 +263,41 @@ extern "C" fo_status fo_quant_fp8(int32_t R, int64_t rows, int64_t cols, int32_t
   k.groups = (int32_t)((cols + FO_FP8_BLOCK - 1) / FO_FP8_BLOCK);
   k.row_blocks = (int32_t)((rows + FO_FP8_BLOCK - 1) / FO_FP8_BLOCK);
   const cudaStream_t s = (cudaStream_t)stream;
+  const bool bf16 = dtype == FO_BF16;
+  const bool wide = (cols * es) % 16 == 0 && all_aligned(R, x, 16) && all_aligned(R, (A)q, 8);
   if (block_rows == 1) {
-    const int64_t want = (rows * k.groups + 7) / 8;
+    if (!wide) {
+      const int64_t want = (rows * k.groups + 7) / 8;
+      const dim3 grid((unsigned)(want < 65536 ? want : 65536), R);
+      if (bf16) quant_rows_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(k);
+      else quant_rows_kernel<float><<<grid, 256, 0, s>>>(k);
+      return launched("quant_rows", R, rows, cols, grid.x, 256);
+    }
+    const int piece = bf16 ? 256 : 128;
+    if (cols % FO_FP8_BLOCK == 0 && rows * cols <= INT32_MAX - 1024) {   // groups back to back: one long row
+      k.cols = rows * cols;
+      k.groups = (int32_t)(k.cols / FO_FP8_BLOCK);
+      k.rows = 1;
+    }
+    k.pieces = (int32_t)((k.cols + piece - 1) / piece);
+    // A warp for four pieces, few pieces: a warp each.
+    const int64_t n = k.rows * k.pieces, want = n >= 4096 ? (n + 31) / 32 : (n + 7) / 8;
     const dim3 grid((unsigned)(want < 65536 ? want : 65536), R);
-    if (dtype == FO_BF16) quant_rows_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(k);
-    else quant_rows_kernel<float><<<grid, 256, 0, s>>>(k);
-    return launched("quant_rows", R, rows, cols, grid.x, 256);
+    if (bf16) quant_rows_wide_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(k);
+    else quant_rows_wide_kernel<float><<<grid, 256, 0, s>>>(k);
+    return launched("quant_rows wide", R, rows, cols, grid.x, 256);
   }
   const dim3 grid(k.groups, k.row_blocks, R);
-  if (dtype == FO_BF16) quant_blocks_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(k);
-  else quant_blocks_kernel<float><<<grid, 256, 0, s>>>(k);
-  return launched("quant_blocks", R, rows, cols, grid.x * grid.y, 256);
+  const bool wide_blocks = wide && cols % 8 == 0 && (!qt || (rows % 8 == 0 && all_aligned(R, (A)qt, 8)));
+  if (!wide_blocks) {
+    if (bf16) quant_blocks_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(k);
+    else quant_blocks_kernel<float><<<grid, 256, 0, s>>>(k);
+  } else if (qt) {
+    if (bf16) quant_blocks_wide_kernel<__nv_bfloat16, true><<<grid, 256, 0, s>>>(k);
+    else quant_blocks_wide_kernel<float, true><<<grid, 256, 0, s>>>(k);
+  } else {
+    if (bf16) quant_blocks_wide_kernel<__nv_bfloat16, false><<<grid, 256, 0, s>>>(k);
+    else quant_blocks_wide_kernel<float, false><<<grid, 256, 0, s>>>(k);
+  }
+  return launched(wide_blocks ? "quant_blocks wide" : "quant_blocks", R, rows, cols, grid.x * grid.y, 256);
 }

@@ -1,5 +1,5 @@
 // Rotary positions on Q and K, V copied: packed rows to parted ones or back,
-// or in place.
+// or in place. Bandwidth-bound: each element is read and written once.
 #include <math.h>
 #include <string.h>
 
@@ -18,6 +18,7 @@ struct RopeParams {
   int32_t heads[3];
   int32_t D, rot;
   int32_t half;       // layout
+  int32_t lanes, tokens, heads_each;   // threads for a token, tokens a block, heads a thread
   float factor, sign;
   uint64_t turns[FO_ROPE_MAX_DIM / 2];
 };
@@ -25,8 +26,8 @@ struct RopeParams {
 // cos and sin (times the factor) of position * turns: the product modulo
 // 2^64 is the angle's fraction of a turn, exact but for the frequency's own
 // last bit; as a signed number it lies in [-1/2, 1/2).
-__device__ __forceinline__ float2 rotation(const RopeParams& p, int64_t pos, int pair) {
-  const int64_t frac = (int64_t)((uint64_t)pos * p.turns[pair]);
+__device__ __forceinline__ float2 rotation(const RopeParams& p, int64_t pos, uint64_t turns) {
+  const int64_t frac = (int64_t)((uint64_t)pos * turns);
   float s, c;
   sincospif((float)frac * 1.08420217e-19f, &s, &c);   // 2^-63: half turns
   return make_float2(c * p.factor, s * p.factor * p.sign);
@@ -38,13 +39,161 @@ __device__ __forceinline__ int64_t position_of(const RopeParams& p, int64_t t) {
                           : (int64_t)static_cast<const int32_t*>(p.positions)[t];
 }
 
-// One block for each row and rank: the angles once, then every pair.
-template <typename T>
+// V values of type T as one access.
+template <int BYTES>
+struct Bits;
+template <>
+struct Bits<2> { typedef uint16_t type; };
+template <>
+struct Bits<4> { typedef uint32_t type; };
+template <>
+struct Bits<8> { typedef uint2 type; };
+template <>
+struct Bits<16> { typedef uint4 type; };
+template <typename T, int V>
+union Piece {
+  typename Bits<sizeof(T) * V>::type bits;
+  T v[V];
+  __device__ __forceinline__ Piece() {}
+  __device__ __forceinline__ void load(const T* p) { bits = *reinterpret_cast<const decltype(bits)*>(p); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<decltype(bits)*>(p) = bits; }
+};
+
+// A thread has a place in the head and a token, computes its own angles once
+// and goes through its share of the heads, kHeads at a time with all loads
+// first. Its place is two pieces of V elements: in the half layout piece i of
+// the first half and of the second (V pairs); interleaved, pieces i and i +
+// lanes (V / 2 pairs each). The elements that are not rotated follow in pieces
+// of their own. V is the widest access that the sizes, strides and addresses
+// allow (at least a pair where pairs are neighbours).
+template <typename T, int V, bool HALF>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kHeads = 4;
+  // (Read lane by lane from the parameters, the frequencies would be one
+  // access to the constant cache for each.)
+  __shared__ uint64_t turns[FO_ROPE_MAX_DIM / 2];
+  if (threadIdx.x < p.rot / 2) turns[threadIdx.x] = p.turns[threadIdx.x];
+  __syncthreads();
+  const int lanes = p.lanes, tok = threadIdx.x / lanes, i = threadIdx.x - tok * lanes;
+  const int64_t t = (int64_t)blockIdx.x * p.tokens + tok;
+  if (tok >= p.tokens || t >= p.rows) return;
+  const int r = (int)blockIdx.z;
+  const int pieces = p.rot / V / (HALF ? 2 : 1);   // pieces of the first half / of all that is rotated
+  const int a = i, b = HALF ? i + pieces : i + lanes;
+  const bool has_a = i < pieces, has_b = HALF ? has_a : b < pieces;
+  float c[V], s[V];   // HALF: by element; else the first V / 2 for piece a, the others for b
+  const int64_t pos = position_of(p, t);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int pair = HALF ? i * V + j : j < V / 2 ? a * (V / 2) + j : b * (V / 2) + j - V / 2;
+    const float2 cs = 2 * pair < p.rot ? rotation(p, pos, turns[pair]) : make_float2(0.f, 0.f);
+    c[j] = cs.x, s[j] = cs.y;
+  }
+  const int turned = p.heads[0] + p.heads[1], all = turned + p.heads[2];
+  const int h0 = (int)blockIdx.y * p.heads_each, h1 = min(all, h0 + p.heads_each);
+  auto head_at = [&](int h, const T*& in, T*& out) {
+    const int part = h < p.heads[0] ? 0 : h < turned ? 1 : 2;
+    const int local = part == 0 ? h : part == 1 ? h - p.heads[0] : h - turned;
+    in = static_cast<const T*>(p.in[part][r]) + t * p.ld_in[part] + local * p.D;
+    out = static_cast<T*>(p.out[part][r]) + t * p.ld_out[part] + local * p.D;
+  };
+  // Rotated pieces.
+  if (has_a) {
+    for (int h = h0; h < min(h1, turned); h += kHeads) {
+      Piece<T, V> x[kHeads], y[kHeads];
+      const T* in;
+      T* out;
+#pragma unroll
+      for (int k = 0; k < kHeads; ++k)
+        if (h + k < min(h1, turned)) {
+          head_at(h + k, in, out);
+          x[k].load(in + a * V);
+          if (has_b) y[k].load(in + b * V);
+        }
+#pragma unroll
+      for (int k = 0; k < kHeads; ++k)
+        if (h + k < min(h1, turned)) {
+          head_at(h + k, in, out);
+          if constexpr (HALF) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              const float u = to_f(x[k].v[j]), w = to_f(y[k].v[j]);
+              from_f(u * c[j] - w * s[j], x[k].v[j]);
+              from_f(w * c[j] + u * s[j], y[k].v[j]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+              float u = to_f(x[k].v[2 * j]), w = to_f(x[k].v[2 * j + 1]);
+              from_f(u * c[j] - w * s[j], x[k].v[2 * j]);
+              from_f(w * c[j] + u * s[j], x[k].v[2 * j + 1]);
+              if (has_b) {
+                u = to_f(y[k].v[2 * j]), w = to_f(y[k].v[2 * j + 1]);
+                from_f(u * c[V / 2 + j] - w * s[V / 2 + j], y[k].v[2 * j]);
+                from_f(w * c[V / 2 + j] + u * s[V / 2 + j], y[k].v[2 * j + 1]);
+              }
+            }
+          }
+          x[k].store(out + a * V);
+          if (has_b) y[k].store(out + b * V);
+        }
+    }
+  }
+  // What is copied: the rest of a rotated head, whole heads of V; in place,
+  // nothing.
+  for (int h = h0; h < h1; ++h) {
+    const T* in;
+    T* out;
+    head_at(h, in, out);
+    if (in == out) continue;
+    for (int e = (h < turned ? p.rot : 0) + i * V; e < p.D; e += lanes * V * 2) {
+      Piece<T, V> x, y;
+      const bool two = e + lanes * V < p.D;
+      x.load(in + e);
+      if (two) y.load(in + e + lanes * V);
+      x.store(out + e);
+      if (two) y.store(out + e + lanes * V);
+    }
+  }
+}
+
+template <typename T, int V, bool HALF>
+fo_status launch_as(RopeParams& k, int R, cudaStream_t s) {
+  // Lanes for a token: two pieces each. Heads for a thread: all, unless that
+  // leaves the GPU short of threads.
+  k.lanes = (k.D / V + 1) / 2;
+  k.tokens = 256 / k.lanes;
+  const int all = k.heads[0] + k.heads[1] + k.heads[2];
+  const int64_t blocks = (k.rows + k.tokens - 1) / k.tokens * R;
+  int64_t cuts = (4 * FO_GB300_SMS + blocks - 1) / blocks;
+  if (cuts > (all + 3) / 4) cuts = (all + 3) / 4;
+  k.heads_each = (int)((all + cuts - 1) / cuts);
+  const dim3 grid((unsigned)((k.rows + k.tokens - 1) / k.tokens), (unsigned)((all + k.heads_each - 1) / k.heads_each), R);
+  rope_kernel<T, V, HALF><<<grid, 256, 0, s>>>(k);
+  return launched("rope", R, k.rows, k.D, grid.x * grid.y, 256);
+}
+template <typename T>
+fo_status launch_with(RopeParams& k, int R, int v, cudaStream_t s) {
+  constexpr int kMost = 16 / sizeof(T);
+  if (k.half) {
+    if (v == kMost) return launch_as<T, kMost, true>(k, R, s);
+    if (kMost == 8 && v == 4) return launch_as<T, 4, true>(k, R, s);
+    if (v >= 2) return launch_as<T, 2, true>(k, R, s);
+    return launch_as<T, 1, true>(k, R, s);
+  }
+  if (v == kMost) return launch_as<T, kMost, false>(k, R, s);
+  if (kMost == 8 && v == 4) return launch_as<T, 4, false>(k, R, s);
+  return launch_as<T, 2, false>(k, R, s);
+}
+
+// A head whose pairs are neighbours but do not start on a pair's address
+// (odd head dimensions): one element at a time, a block for a row and rank.
+template <typename T>
+__global__ void __launch_bounds__(256) rope_single_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 rot[FO_ROPE_MAX_DIM / 2];
   const int64_t t = blockIdx.x;
   const int r = blockIdx.y, pairs = p.rot / 2;
-  if (threadIdx.x < pairs) rot[threadIdx.x] = rotation(p, position_of(p, t), threadIdx.x);
+  if (threadIdx.x < pairs) rot[threadIdx.x] = rotation(p, position_of(p, t), p.turns[threadIdx.x]);
   __syncthreads();
 #pragma unroll
   for (int part = 0; part < 3; ++part) {
@@ -60,7 +209,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
       } else if (k >= pairs) {
         out[at + k + pairs] = in[at + k + pairs];
       } else {
-        const int ia = at + (p.half ? k : 2 * k), ib = p.half ? ia + pairs : ia + 1;
+        const int ia = at + 2 * k, ib = ia + 1;
         const float a = to_f(in[ia]), b = to_f(in[ib]);
         from_f(a * rot[k].x - b * rot[k].y, out[ia]);
         from_f(b * rot[k].x + a * rot[k].y, out[ib]);
@@ -166,9 +315,21 @@ extern "C" fo_status fo_rope(const fo_rope_desc* d, int64_t rows, const void* po
   k.factor = d->factor;
   k.sign = inverse ? -1.f : 1.f;
   memcpy(k.turns, d->turns, sizeof(k.turns));
-  const dim3 grid((unsigned)rows, R);
   const cudaStream_t s = (cudaStream_t)stream;
-  if (d->dtype == FO_BF16) rope_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(k);
-  else rope_kernel<float><<<grid, 256, 0, s>>>(k);
-  return launched("rope", R, rows, d->head_dim, (int)rows, 256);
+  // The widest piece of V elements that every head, half and row starts on.
+  int v = (int)(16 / es);
+  for (; v > 1; v /= 2) {
+    bool fits = d->head_dim % v == 0 && d->rot_dim % (k.half ? 2 * v : v) == 0;
+    for (int j = 0; j < 3 && fits; ++j)
+      if (heads[j])
+        fits = ld_in[j] % v == 0 && ld_out[j] % v == 0 && all_aligned(R, in[j], v * es) && all_aligned(R, out[j], v * es);
+    if (fits) break;
+  }
+  if (!k.half && v < 2) {
+    const dim3 grid((unsigned)rows, R);
+    if (d->dtype == FO_BF16) rope_single_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(k);
+    else rope_single_kernel<float><<<grid, 256, 0, s>>>(k);
+    return launched("rope single", R, rows, d->head_dim, (int)rows, 256);
+  }
+  return d->dtype == FO_BF16 ? launch_with<__nv_bfloat16>(k, R, v, s) : launch_with<float>(k, R, v, s);
 }

@@ -16,9 +16,9 @@ struct NormParams {
   float* scale[kMaxR];
   float* rstd[kMaxR];
   const void* w;
-  int64_t rows, total;   // rows of a shard, rows of all shards
+  int64_t rows;   // of a shard
   int32_t H, groups;
-  float eps, w_offset;
+  float eps, w_offset, inv_H;
   bool has_res, has_h, has_y, has_q, has_rstd, w_f32;
 };
 
@@ -101,8 +101,10 @@ struct Chunk {
             f[j + 2] = __uint_as_float(v.y << 16), f[j + 3] = __uint_as_float(v.y & 0xffff0000u);
           }
         }
+        if (offset != 0.f) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) f[j] += offset;
+          for (int j = 0; j < E; ++j) f[j] += offset;
+        }
       }
     } else {
 #pragma unroll
@@ -134,9 +136,8 @@ __global__ void __launch_bounds__(NW * 32) rmsnorm_kernel(const __grid_constant_
   using K = Chunk<T, WIDE>;
   __shared__ float smem[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int64_t row = blockIdx.x; row < p.total; row += gridDim.x) {
-    const int r = (int)(row / p.rows);
-    const int64_t at = row - r * p.rows;
+  const int r = blockIdx.y;
+  for (int64_t at = blockIdx.x; at < p.rows; at += gridDim.x) {
     const int64_t off = at * p.H;
     float s[C][K::E];
     float sum = 0.f;
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(NW * 32) rmsnorm_kernel(const __grid_constant_
 #pragma unroll
       for (int c = 0; c < C; ++c) K::store(static_cast<T*>(p.h[r]) + off, c * NW + warp, lane, p.H, s[c]);
     }
-    const float rstd = 1.f / sqrtf(block_sum<NW>(sum, smem) / (float)p.H + p.eps);
+    const float rstd = rsqrtf(fmaf(block_sum<NW>(sum, smem), p.inv_H, p.eps));
     if (p.has_rstd && threadIdx.x == 0) p.rstd[r][at] = rstd;
     if (!p.has_y && !p.has_q) continue;
 #pragma unroll
@@ -168,16 +169,12 @@ __global__ void __launch_bounds__(NW * 32) rmsnorm_kernel(const __grid_constant_
       const int chunk = c * NW + warp;
       float w[K::E];
       K::load_w(p.w, p.w_f32, p.w_offset, chunk, lane, p.H, w);
-      float amax = 0.f;
 #pragma unroll
-      for (int j = 0; j < K::E; ++j) {
-        s[c][j] = s[c][j] * rstd * w[j];
-        amax = max_nan(amax, fabsf(s[c][j]));
-      }
+      for (int j = 0; j < K::E; ++j) s[c][j] = s[c][j] * rstd * w[j];
       if (p.has_y) K::store(static_cast<T*>(p.y[r]) + off, chunk, lane, p.H, s[c]);
       if (p.has_q) {
-        const float scale = scale_of(lanes_max<K::GROUP_LANES>(amax));
-        const float inv = 1.f / scale;
+        const float scale = scale_of(lanes_max<K::GROUP_LANES>(amax_of(s[c])));
+        const float inv = inverse_of(scale);
 #pragma unroll
         for (int j = 0; j < K::E; ++j) s[c][j] *= inv;
         K::store_e4m3(p.q[r] + off, chunk, lane, p.H, s[c]);
@@ -198,7 +195,7 @@ struct NormBwdParams {
   float* part;   // [gridDim.x][H] partial sums of dweight
   int64_t rows, total;
   int32_t H;
-  float w_offset;
+  float w_offset, inv_H;
   bool has_dh, has_dw, w_f32;
 };
 
@@ -254,8 +251,12 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
   constexpr int CA = kAhead ? C : 1;
   Raw<T, WIDE> dy_n[CA], h_n[CA], dh_n[CA];
   float rstd_n = 0.f;
+  // (A 64-bit division costs as much as a third of a row.)
+  auto rank_of = [&](int64_t row) -> int {
+    return p.total == p.rows ? 0 : p.total <= UINT32_MAX ? (int)((uint32_t)row / (uint32_t)p.rows) : (int)(row / p.rows);
+  };
   auto fetch = [&](int64_t row) {
-    const int r = (int)(row / p.rows);
+    const int r = rank_of(row);
     const int64_t at = row - r * p.rows, off = at * p.H;
     rstd_n = p.rstd[r][at];
 #pragma unroll
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
   };
   if (kAhead && blockIdx.x < p.total) fetch(blockIdx.x);
   for (int64_t row = blockIdx.x; row < p.total; row += gridDim.x) {
-    const int r = (int)(row / p.rows);
+    const int r = rank_of(row);
     const int64_t at = row - r * p.rows, off = at * p.H;
     const T* const dy = static_cast<const T*>(p.dy[r]) + off;
     const T* const hp = static_cast<const T*>(p.h[r]) + off;
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
       for (int c = 0; c < C; ++c) dh[c] = dh_n[c];
       if (row + gridDim.x < p.total) fetch(row + gridDim.x);
     }
-    const float k = block_sum<NW>(sum, smem) / (float)p.H * rstd * rstd * rstd;
+    const float k = block_sum<NW>(sum, smem) * p.inv_H * rstd * rstd * rstd;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float(&uc)[E] = u[kHold ? c : 0];
@@ -403,9 +404,9 @@ struct LaunchFwd {
   int R;
   template <typename T, bool WIDE, int NW, int C>
   fo_status operator()() const {
-    const int grid = (int)(k.total < (1 << 30) ? k.total : (1 << 30));
+    const dim3 grid((unsigned)k.rows, R);
     rmsnorm_kernel<T, WIDE, NW, C><<<grid, NW * 32, 0, s>>>(k);
-    return launched("rmsnorm", R, k.rows, k.H, grid, NW * 32);
+    return launched("rmsnorm", R, k.rows, k.H, (int)k.rows, NW * 32);
   }
 };
 struct LaunchBwd {
@@ -460,11 +461,11 @@ extern "C" fo_status fo_rmsnorm(const fo_norm_desc* d, int64_t rows, const void*
   }
   k.w = weight;
   k.rows = rows;
-  k.total = rows * R;
   k.H = d->H;
   k.groups = (d->H + FO_FP8_BLOCK - 1) / FO_FP8_BLOCK;
   k.eps = d->eps;
   k.w_offset = d->w_offset;
+  k.inv_H = 1.f / (float)d->H;
   k.has_res = residual, k.has_h = h, k.has_y = y, k.has_q = q, k.has_rstd = rstd;
   k.w_f32 = d->w_dtype == FO_F32;
   const bool wide = (d->H * es) % 16 == 0 && aligned(weight, 16) && all_aligned(R, x, 16) && all_aligned(R, residual, 16) &&
@@ -530,6 +531,7 @@ extern "C" fo_status fo_rmsnorm_bwd(const fo_norm_desc* d, int64_t rows, const v
   k.total = rows * R;
   k.H = d->H;
   k.w_offset = d->w_offset;
+  k.inv_H = 1.f / (float)d->H;
   k.has_dh = dh, k.has_dw = dweight;
   k.w_f32 = d->w_dtype == FO_F32;
   const bool wide = (d->H * es) % 16 == 0 && aligned(weight, 16) && all_aligned(R, dy, 16) && all_aligned(R, dh, 16) &&

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
       v[j] = c < p.cols ? to_f(x[c]) : 0.f;
       amax = max_nan(amax, fabsf(v[j]));
     }
-    const float scale = scale_of(lanes_max<32>(amax)), inv = 1.f / scale;
+    const float scale = scale_of(lanes_max<32>(amax)), inv = inverse_of(scale);
     uint8_t* q = p.q[r] + row * p.cols;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -72,11 +72,9 @@ __global__ void __launch_bounds__(256) quant_rows_wide_kernel(const __grid_const
     }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      float v[E], amax = 0.f;
+      float v[E];
       Vec16<T>::unpack(raw[i], v);
-#pragma unroll
-      for (int j = 0; j < E; ++j) amax = max_nan(amax, fabsf(v[j]));
-      const float scale = scale_of(lanes_max<kLanes>(amax)), inv = 1.f / scale;
+      const float scale = scale_of(lanes_max<kLanes>(amax_of(v))), inv = inverse_of(scale);
       if (w + i * step >= n || col[i] >= p.cols) continue;
 #pragma unroll
       for (int j = 0; j < E; ++j) v[j] *= inv;
@@ -110,7 +108,7 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant
   amax = lanes_max<32>(amax);
   if (lane == 0) smem[warp] = amax;
   __syncthreads();
-  const float scale = scale_of(lanes_max<32>(smem[lane & 7])), inv = 1.f / scale;
+  const float scale = scale_of(lanes_max<32>(smem[lane & 7])), inv = inverse_of(scale);
 #pragma unroll
   for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -176,13 +174,12 @@ __global__ void __launch_bounds__(256) quant_blocks_wide_kernel(const __grid_con
     for (int k = 0; k < V; ++k) {
       float v[Vec16<T>::N];
       Vec16<T>::unpack(raw[i][k], v);
-#pragma unroll
-      for (int j = 0; j < Vec16<T>::N; ++j) amax = max_nan(amax, fabsf(v[j]));
+      amax = max_nan(amax, amax_of(v));
     }
   amax = lanes_max<32>(amax);
   if (lane == 0) smem[warp] = amax;
   __syncthreads();
-  const float scale = scale_of(lanes_max<8>(smem[lane & 7])), inv = 1.f / scale;
+  const float scale = scale_of(lanes_max<8>(smem[lane & 7])), inv = inverse_of(scale);
   uint32_t lo[8], hi[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {

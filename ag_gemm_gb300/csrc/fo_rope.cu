@@ -59,15 +59,16 @@ union Piece {
   __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<decltype(bits)*>(p) = bits; }
 };
 
-// A thread has a place in the head and a token, computes its own angles once
-// and goes through its share of the heads, kHeads at a time with all loads
-// first. Its place is two pieces of V elements: in the half layout piece i of
-// the first half and of the second (V pairs); interleaved, pieces i and i +
-// lanes (V / 2 pairs each). The elements that are not rotated follow in pieces
-// of their own. V is the widest access that the sizes, strides and addresses
-// allow (at least a pair where pairs are neighbours).
+// A thread has a token and two pieces of V elements in every head, computes
+// its own angles once and goes through its share of the heads, kHeads at a
+// time with all loads first. The pieces of a rotated head: in the half layout
+// piece i of the first half and of the second (V pairs); interleaved, pieces
+// i and i + lanes (V / 2 pairs each); the threads beyond the rotated pieces
+// copy the head's rest, two pieces each. Heads of V: pieces i and i + lanes.
+// V is the widest access that the sizes, strides and addresses allow (at
+// least a pair where pairs are neighbours).
 template <typename T, int V, bool HALF>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(256, 3) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kHeads = 4;
   // (Read lane by lane from the parameters, the frequencies would be one
   // access to the constant cache for each.)
@@ -78,9 +79,13 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
   const int64_t t = (int64_t)blockIdx.x * p.tokens + tok;
   if (tok >= p.tokens || t >= p.rows) return;
   const int r = (int)blockIdx.z;
-  const int pieces = p.rot / V / (HALF ? 2 : 1);   // pieces of the first half / of all that is rotated
-  const int a = i, b = HALF ? i + pieces : i + lanes;
-  const bool has_a = i < pieces, has_b = HALF ? has_a : b < pieces;
+  const int pieces = p.rot / V / (HALF ? 2 : 1);   // of the first half; of all that is rotated
+  const int whole = p.D / V;
+  // This thread's pieces of a rotated head, and whether they are rotated.
+  const bool turn_a = i < pieces, turn_b = HALF ? turn_a : i + lanes < pieces;
+  const int a = !HALF || turn_a ? i : i + pieces;
+  const int b = !HALF ? i + lanes : turn_a ? i + pieces : i + lanes;
+  const bool two = b < whole;
   float c[V], s[V];   // HALF: by element; else the first V / 2 for piece a, the others for b
   const int64_t pos = position_of(p, t);
 #pragma unroll
@@ -89,70 +94,55 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
     const float2 cs = 2 * pair < p.rot ? rotation(p, pos, turns[pair]) : make_float2(0.f, 0.f);
     c[j] = cs.x, s[j] = cs.y;
   }
-  const int turned = p.heads[0] + p.heads[1], all = turned + p.heads[2];
-  const int h0 = (int)blockIdx.y * p.heads_each, h1 = min(all, h0 + p.heads_each);
-  auto head_at = [&](int h, const T*& in, T*& out) {
-    const int part = h < p.heads[0] ? 0 : h < turned ? 1 : 2;
-    const int local = part == 0 ? h : part == 1 ? h - p.heads[0] : h - turned;
-    in = static_cast<const T*>(p.in[part][r]) + t * p.ld_in[part] + local * p.D;
-    out = static_cast<T*>(p.out[part][r]) + t * p.ld_out[part] + local * p.D;
-  };
-  // Rotated pieces.
-  if (has_a) {
-    for (int h = h0; h < min(h1, turned); h += kHeads) {
+  int h0 = (int)blockIdx.y * p.heads_each, h1 = h0 + p.heads_each;   // this block's heads, counted from each part's first
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {
+    const int first = max(h0, 0), last = min(h1, p.heads[part]);
+    h0 -= p.heads[part], h1 -= p.heads[part];
+    if (first >= last) continue;
+    const bool turned = part < 2;
+    const int pa = (turned ? a : i) * V, pb = (turned ? b : i + lanes) * V;
+    const bool has_b = turned ? two : i + lanes < whole;
+    const T* in = static_cast<const T*>(p.in[part][r]) + t * p.ld_in[part] + first * p.D;
+    T* out = static_cast<T*>(p.out[part][r]) + t * p.ld_out[part] + first * p.D;
+    const bool moves = in != out;   // in place, what is not rotated stays
+    for (int n = last - first; n > 0; n -= kHeads, in += kHeads * p.D, out += kHeads * p.D) {
       Piece<T, V> x[kHeads], y[kHeads];
-      const T* in;
-      T* out;
 #pragma unroll
       for (int k = 0; k < kHeads; ++k)
-        if (h + k < min(h1, turned)) {
-          head_at(h + k, in, out);
-          x[k].load(in + a * V);
-          if (has_b) y[k].load(in + b * V);
+        if (k < n) {
+          x[k].load(in + k * p.D + pa);
+          if (has_b) y[k].load(in + k * p.D + pb);
         }
 #pragma unroll
       for (int k = 0; k < kHeads; ++k)
-        if (h + k < min(h1, turned)) {
-          head_at(h + k, in, out);
-          if constexpr (HALF) {
+        if (k < n) {
+          if (turned) {
+            if constexpr (HALF) {
+              if (turn_a) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-              const float u = to_f(x[k].v[j]), w = to_f(y[k].v[j]);
-              from_f(u * c[j] - w * s[j], x[k].v[j]);
-              from_f(w * c[j] + u * s[j], y[k].v[j]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-              float u = to_f(x[k].v[2 * j]), w = to_f(x[k].v[2 * j + 1]);
-              from_f(u * c[j] - w * s[j], x[k].v[2 * j]);
-              from_f(w * c[j] + u * s[j], x[k].v[2 * j + 1]);
-              if (has_b) {
-                u = to_f(y[k].v[2 * j]), w = to_f(y[k].v[2 * j + 1]);
-                from_f(u * c[V / 2 + j] - w * s[V / 2 + j], y[k].v[2 * j]);
-                from_f(w * c[V / 2 + j] + u * s[V / 2 + j], y[k].v[2 * j + 1]);
+                for (int j = 0; j < V; ++j) {
+                  const float u = to_f(x[k].v[j]), w = to_f(y[k].v[j]);
+                  from_f(u * c[j] - w * s[j], x[k].v[j]);
+                  from_f(w * c[j] + u * s[j], y[k].v[j]);
+                }
               }
+            } else {
+              auto turn = [&](Piece<T, V>& z, int at) {
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                  const float u = to_f(z.v[2 * j]), w = to_f(z.v[2 * j + 1]);
+                  from_f(u * c[at + j] - w * s[at + j], z.v[2 * j]);
+                  from_f(w * c[at + j] + u * s[at + j], z.v[2 * j + 1]);
+                }
+              };
+              if (turn_a) turn(x[k], 0);
+              if (turn_b) turn(y[k], V / 2);
             }
           }
-          x[k].store(out + a * V);
-          if (has_b) y[k].store(out + b * V);
+          if (moves || (turned && turn_a)) x[k].store(out + k * p.D + pa);
+          if (has_b && (moves || (turned && turn_b))) y[k].store(out + k * p.D + pb);
         }
-    }
-  }
-  // What is copied: the rest of a rotated head, whole heads of V; in place,
-  // nothing.
-  for (int h = h0; h < h1; ++h) {
-    const T* in;
-    T* out;
-    head_at(h, in, out);
-    if (in == out) continue;
-    for (int e = (h < turned ? p.rot : 0) + i * V; e < p.D; e += lanes * V * 2) {
-      Piece<T, V> x, y;
-      const bool two = e + lanes * V < p.D;
-      x.load(in + e);
-      if (two) y.load(in + e + lanes * V);
-      x.store(out + e);
-      if (two) y.store(out + e + lanes * V);
     }
   }
 }

@@ -131,8 +131,11 @@ __device__ __forceinline__ float block_sum(float v, float* smem) {
   return v;
 }
 
+// (Six blocks of 8 warps on an SM: 41.5 us for 8192 x 4096 bf16 with residual and
+// 8-bit output, 43 us with the five that the compiler's own choice of
+// registers leaves, 45 us with rows on 4 warps, 56 us with rows on 16.)
 template <typename T, bool WIDE, int NW, int C>
-__global__ void __launch_bounds__(NW * 32) rmsnorm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(NW * 32, NW == 8 ? 6 : 1) rmsnorm_kernel(const __grid_constant__ NormParams p) {
   using K = Chunk<T, WIDE>;
   __shared__ float smem[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

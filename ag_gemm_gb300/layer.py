@@ -187,3 +187,106 @@ class TpspLayerProjections:
 
     def status(self) -> List[int]:
         return [B.fo_status_query(p, self.ws[k])[0] for k, p in self.plans.items()]
+
+
+class Fp8AttentionBlock:
+    """The attention half of a TP-SP layer with its projection in 8 bits, from the residual stream to the attention's
+    output, and the way of the gradients back through what precedes the attention:
+
+    forward
+        norm      s = x + residual, n = rmsnorm(s); n in 8 bits with a scale for 128 columns   fo_rmsnorm
+        QKV       Y_r = n . Wqkv_r^T, block-scaled 8-bit product, every rank in one launch    fo_gemm_fp8
+        rotary    Y_r's Q and K turned by their positions, Q, K, V parted                     fo_rope
+        attention + o projection + reduce-scatter                                             fo_attn_rs
+    backward (dQ, dK, dV from the attention's own backward pass, which this framework does not have)
+        rotary^-1 back into packed rows                                                       fo_rope
+        QKV       dY_r in 8 bits, dn = sum_r dY_r . Wqkv_r (the weight's transposed copy)     fo_quant_fp8, fo_gemm_fp8,
+                                                                                              fo_reduce_scatter_f32
+        norm      dx (= d residual) with the residual path's gradient, dweight                fo_rmsnorm_bwd
+
+    The T tokens of the R ranks' shards lie back to back, so the norm is one call and its output is the all-gathered
+    operand of every rank's product. Weights are given in bf16 ([3H/R x H] a rank, rows Q | K | V, the nn.Linear
+    layout) and quantised by set_weights, once for each version of them."""
+
+    def __init__(self, shape: LayerShape = LayerShape(), *, causal=True, eps=1e-6, rope_base=10000.0, device="cuda",
+                 **rope):
+        self.s = s = shape
+        R, T, H = s.R, s.T, s.H
+        if T % R or H % (R * 128):
+            raise ValueError("T must be divisible by R, and H by R heads of 128")
+        self.heads, self.causal = H // R // 128, causal
+        width = H // R
+        dev = torch.device(device)
+        bf, f32, e4m3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+        def new(*shp, dtype=bf):
+            return torch.empty(shp, dtype=dtype, device=dev)
+
+        def each(*shp, dtype=bf):
+            return [new(*shp, dtype=dtype) for _ in range(R)]
+
+        kb, nb = -(-H // 128), -(-3 * width // 128)
+        self.norm = B.fo_norm_desc(H, eps=eps)
+        self.qkv = B.fo_gemm_fp8_desc(3 * width, H, R=R)
+        self.qkv_dx = B.fo_gemm_fp8_desc(H, 3 * width, R=R, out_dtype="f32")
+        self.rope = B.fo_rope_desc(128, self.heads, self.heads, self.heads, R=R, base=rope_base, **rope)
+        self.plan = B.fo_plan("gemm_rs", R, T, H, H, out_dtype="bf16")
+        self.sum_plan = B.fo_plan("gemm_rs", R, T, H, H)          # its rows: the partial gradients' reduce-scatter
+        # weights in 8 bits, as they are and transposed
+        self.Wq, self.Wq_scale = each(3 * width, H, dtype=e4m3), each(nb, kb, dtype=f32)
+        self.Wt, self.Wt_scale = each(H, 3 * width, dtype=e4m3), each(kb, nb, dtype=f32)
+        # forward
+        self.h, self.n8, self.n_scale, self.rstd = new(T, H), new(T, H, dtype=e4m3), new(T, kb, dtype=f32), new(T, dtype=f32)
+        self.y_qkv = each(T, 3 * width)
+        self.Q, self.K, self.V, self.O = (each(T, width) for _ in range(4))
+        self.y = each(T // R, H)
+        # backward
+        self.d_qkv, self.d8, self.d_scale = each(T, 3 * width), each(T, 3 * width, dtype=e4m3), each(T, nb, dtype=f32)
+        self.dn_part, self.dn_whole = each(T, H, dtype=f32), new(T, H, dtype=f32)
+        self.dn = list(self.dn_whole.split(T // R))
+        self.dx, self.dweight = new(T, H), new(H, dtype=f32)
+        self.ws_attn = new(B.fo_workspace_size(self.plan), dtype=torch.uint8)
+        B.fo_workspace_init(self.plan, self.ws_attn)
+        size = max(B.fo_gemm_fp8_workspace(self.qkv, T), B.fo_gemm_fp8_workspace(self.qkv_dx, T))
+        self.ws = new(size, dtype=torch.uint8)
+        B.fo_ops_workspace_init(self.ws)
+        self.ws_norm = new(B.fo_rmsnorm_bwd_workspace(self.norm, T), dtype=torch.uint8)
+
+    def set_weights(self, weight, Wqkv, Wo, stream=None):
+        """The norm's weight [H], each rank's Wqkv [3H/R x H] and Wo [H/R x H], bf16."""
+        width = self.s.H // self.s.R
+        self.weight, self.Wo = weight, Wo
+        B.fo_quant_fp8(3 * width, self.s.H, Wqkv, self.Wq, self.Wq_scale, self.Wt, self.Wt_scale, block_rows=128,
+                       stream=stream)
+
+    def _parts(self, packed):
+        width = self.s.H // self.s.R
+        return [[p[:, j * width:(j + 1) * width] for p in packed] for j in range(3)]
+
+    def forward(self, x, residual=None, positions=None, stream=None):
+        """x, residual [T x H] bf16 (the R token shards back to back), positions [T]; returns the R output shards.
+        Five launches. h (the new residual) and rstd are kept for the backward pass."""
+        T, R = self.s.T, self.s.R
+        B.fo_rmsnorm(self.norm, T, [x], None if residual is None else [residual], self.weight, [self.h], None,
+                     [self.n8], [self.n_scale], [self.rstd], stream)
+        B.fo_gemm_fp8(self.qkv, T, [self.n8] * R, [self.n_scale] * R, self.Wq, self.Wq_scale, self.y_qkv, self.ws, stream)
+        B.fo_rope(self.rope, T, positions, *self._parts(self.y_qkv), self.Q, self.K, self.V, stream=stream)
+        B.fo_attn_rs(self.plan, self.Q, self.K, self.V, self.Wo, self.O, self.y, self.heads, self.causal, self.ws_attn,
+                     stream)
+        return self.y
+
+    def backward(self, dQ, dK, dV, dh=None, positions=None, stream=None):
+        """dQ, dK, dV [T x H/R] a rank, dh [T x H] the gradient that reaches the new residual by its own path; returns
+        (dx, dweight), dx being the gradient of x and of the residual alike."""
+        T, R, width = self.s.T, self.s.R, self.s.H // self.s.R
+        B.fo_rope(self.rope, T, positions, dQ, dK, dV, *self._parts(self.d_qkv), inverse=True, stream=stream)
+        B.fo_quant_fp8(T, 3 * width, self.d_qkv, self.d8, self.d_scale, stream=stream)
+        B.fo_gemm_fp8(self.qkv_dx, T, self.d8, self.d_scale, self.Wt, self.Wt_scale, self.dn_part, self.ws, stream)
+        B.fo_reduce_scatter_f32(self.sum_plan, self.dn_part, self.dn, stream)
+        dn = self.dn_whole.to(torch.bfloat16)
+        B.fo_rmsnorm_bwd(self.norm, T, [dn], None if dh is None else [dh], [self.h], self.weight, [self.rstd],
+                         [self.dx], self.dweight, self.ws_norm, stream)
+        return self.dx, self.dweight
+
+    def status(self) -> List[int]:
+        return [B.fo_status_query(self.plan, self.ws_attn)[0], B.fo_ops_status_query(self.ws)[0]]

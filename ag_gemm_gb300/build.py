@@ -1,4 +1,4 @@
-"""Build libflashoverlap.so in-tree with nvcc for sm_103a.
+"""Build libflashoverlap.so in-tree with nvcc for sm_103a, and the operators' argument marshalling beside it.
 
 Every translation unit is compiled in parallel to an object file under
 ``ag_gemm_gb300/_build/`` and then linked into one shared library with the
@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libflashoverlap.so")
+MARSHAL = os.path.join(BUILD, "_fo_marshal.so")
 
 SOURCES = ["fo_plan.cpp", "fo_api.cu", "fo_kern_rs.cu", "fo_kern_dp.cu", "fo_kern_ag.cu", "fo_kern_part.cu",
            "fo_noalloc.cu", "fo_attn.cu", "fo_norm.cu", "fo_quant.cu", "fo_rope.cu", "fo_gemm_fp8.cu"]
@@ -38,7 +40,7 @@ def _deps_mtime() -> float:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile (if stale) and return the path of libflashoverlap.so."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, MARSHAL)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -65,7 +67,22 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    _build_marshal()
     return LIB
+
+
+def _build_marshal() -> None:
+    """The operators' argument marshalling, a CPython module linked to the library beside it."""
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        raise RuntimeError("no C compiler found for the argument marshalling module")
+    tmp = MARSHAL + ".tmp"
+    cmd = [cc, "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           os.path.join(CSRC, "fo_marshal.c"), "-o", tmp, "-L", BUILD, "-lflashoverlap", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"building {MARSHAL} failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, MARSHAL)
 
 
 if __name__ == "__main__":

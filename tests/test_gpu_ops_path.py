@@ -171,3 +171,50 @@ def test_product_and_norm_on_two_streams_at_once(dev):
     for d, M, A, sA, W, sW, Y, ws, stream in jobs:
         assert B.fo_ops_status_query(ws)[0] == 0
         assert np.array_equal(f64(Y[0]), f64(A[0]) @ f64(W[0]).T)
+
+
+def test_addresses_and_tensors_make_the_same_call(dev):
+    # Tensors are checked and passed on by the native marshalling module, raw addresses by the Python binding.
+    from ag_gemm_gb300 import binding as B
+    e4m3 = torch.float8_e4m3fn
+    rows, H = 5, 640
+    x, res = (torch.randn(rows, H).to(torch.bfloat16).to(dev) for _ in range(2))
+    w = torch.rand(H).to(torch.bfloat16).to(dev)
+    got = []
+    for raw in (False, True):
+        a = (lambda t: t.data_ptr()) if raw else (lambda t: t)
+        h, q = torch.zeros_like(x), torch.zeros(rows, H, dtype=e4m3, device=dev)
+        s, r = torch.zeros(rows, 5, device=dev), torch.zeros(rows, device=dev)
+        B.fo_rmsnorm(B.fo_norm_desc(H), rows, [a(x)], [a(res)], a(w), [a(h)], None, [a(q)], [a(s)], [a(r)])
+        dx, dw = torch.zeros_like(x), torch.zeros(H, device=dev)
+        ws = torch.zeros(B.fo_rmsnorm_bwd_workspace(B.fo_norm_desc(H), rows), dtype=torch.uint8, device=dev)
+        B.fo_rmsnorm_bwd(B.fo_norm_desc(H), rows, [a(x)], [a(res)], [a(h)], a(w), [a(r)], [a(dx)], a(dw), a(ws))
+        wq, wsc = torch.zeros(rows, H, dtype=e4m3, device=dev), torch.zeros(1, 5, device=dev)
+        B.fo_quant_fp8(rows, H, [a(x)], [a(wq)], [a(wsc)], block_rows=128, dtype="bf16")
+        y, g = torch.zeros(rows, rows, device=dev), B.fo_gemm_fp8_desc(rows, H, out_dtype="f32")
+        gws = torch.zeros(B.fo_gemm_fp8_workspace(g, rows), dtype=torch.uint8, device=dev)
+        B.fo_gemm_fp8(g, rows, [a(q)], [a(s)], [a(wq)], [a(wsc)], [a(y)], a(gws))
+        turned, pos = torch.zeros_like(x), torch.arange(rows, device=dev)
+        B.fo_rope(B.fo_rope_desc(128, 5), rows, a(pos), [a(x)], None, None, [a(turned)], None, None)
+        got.append([h, q.view(torch.uint8), s, r, dx, dw, wq.view(torch.uint8), wsc, y, turned])
+    for u, v in zip(*got):
+        assert torch.equal(u, v) and torch.count_nonzero(u)
+
+
+def test_binding_refuses_small_workspaces_and_wrong_sizes(dev):
+    from ag_gemm_gb300 import binding as B
+    d = B.fo_norm_desc(256)
+    t = torch.zeros(4, 256, dtype=torch.bfloat16, device=dev)
+    r = torch.zeros(4, device=dev)
+    with pytest.raises(ValueError, match="workspace"):
+        B.fo_rmsnorm_bwd(d, 4, [t], None, [t], t[0], [r], [t], torch.zeros(256, device=dev), torch.zeros(16, dtype=torch.uint8, device=dev))
+    q, s = torch.zeros(4, 256, dtype=torch.uint8, device=dev), torch.zeros(4, 2, device=dev)
+    g = B.fo_gemm_fp8_desc(4, 256)
+    with pytest.raises(ValueError, match="workspace"):
+        B.fo_gemm_fp8(g, 4, [q], [s], [q], [s[:1]], [t[:, :4].contiguous()], torch.zeros(8, dtype=torch.uint8, device=dev))
+    with pytest.raises(ValueError, match="values given"):
+        B.fo_quant_fp8(4, 256, [t], [q], [s[:, :1].contiguous()])
+    with pytest.raises(ValueError, match="contiguous"):
+        B.fo_quant_fp8(256, 4, [t.t()], [q], [torch.zeros(256, 1, device=dev)])
+    with pytest.raises(ValueError, match="rows of"):
+        B.fo_rope(B.fo_rope_desc(128, 2), 4, None, [t[:, :128]], None, None, [t], None, None)

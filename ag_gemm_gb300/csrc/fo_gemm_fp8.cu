@@ -294,6 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_release();
+  grid_wait();
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -536,6 +538,7 @@ __global__ void __launch_bounds__(kThreads) gemm_fp8_narrow_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_wait();
   __syncwarp();
 
   f32x2 acc[TN / 2];
@@ -642,6 +645,10 @@ __global__ void __launch_bounds__(kThreads) gemm_fp8_narrow_kernel(const __grid_
   }
   tc_fence_before();
   __syncthreads();   // loads and MMAs are done: the ring is free
+  // Only now may the next kernel's blocks come: earlier ones would wait beside
+  // this kernel's, two to an SM, and leave other SMs idle when they start
+  // (333 x 1000 x 1744 back to back: 8.6 us instead of 6.8).
+  grid_release();
   if (warp == 1) {
     tc_fence_after();
     __syncwarp();
@@ -710,20 +717,8 @@ cudaError_t launch(const GemmParams& k, int split, cudaStream_t s, int* grid_out
   auto kern = gemm_fp8_narrow_kernel<TN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<TN>::kSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(split, k.nblocks, k.tiles_m * k.R);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<TN>::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = split;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
   *grid_out = split * k.nblocks * k.tiles_m * k.R;
-  return cudaLaunchKernelEx(&cfg, kern, k, split);
+  return launch_after(kern, dim3(split, k.nblocks, k.tiles_m * k.R), kThreads, Cfg<TN>::kSmem, split, s, k, split);
 }
 
 }  // namespace narrow
@@ -802,8 +797,8 @@ bool encode(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint3
 
 }  // namespace
 
-fo_status launched(const char* what, int R, int64_t rows, int64_t cols, int grid, int threads) {
-  const cudaError_t e = cudaGetLastError();
+fo_status launched(cudaError_t e, const char* what, int R, int64_t rows, int64_t cols, int grid, int threads) {
+  if (e != cudaSuccess) cudaGetLastError();
   if (fo_log_enabled())
     fprintf(stderr, "[flashoverlap] %s R=%d rows=%lld cols=%lld: %d blocks of %d: %s\n", what, R, (long long)rows,
             (long long)cols, grid, threads, cudaGetErrorString(e));
@@ -902,21 +897,7 @@ extern "C" fo_status fo_gemm_fp8(const fo_gemm_fp8_desc* d, int64_t M, const voi
     threads = wide::kThreads;
     grid = 2 * (int)(total < sms / 2 ? total : sms / 2);
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, wide::kSmem);
-    if (e == cudaSuccess) {
-      cudaLaunchConfig_t cfg;
-      memset(&cfg, 0, sizeof(cfg));
-      cfg.gridDim = dim3(grid);
-      cfg.blockDim = dim3(threads);
-      cfg.dynamicSmemBytes = wide::kSmem;
-      cfg.stream = s;
-      cudaLaunchAttribute at;
-      at.id = cudaLaunchAttributeClusterDimension;
-      at.val.clusterDim.x = 2;
-      at.val.clusterDim.y = at.val.clusterDim.z = 1;
-      cfg.attrs = &at;
-      cfg.numAttrs = 1;
-      e = cudaLaunchKernelEx(&cfg, kern, k);
-    }
+    if (e == cudaSuccess) e = launch_after(kern, dim3(grid), threads, wide::kSmem, 2, s, k);
   } else {
     k.tiles_m = (int32_t)((M + c.tn - 1) / c.tn);
     k.tiles_n = k.nblocks;
@@ -927,9 +908,5 @@ extern "C" fo_status fo_gemm_fp8(const fo_gemm_fp8_desc* d, int64_t M, const voi
       default: e = narrow::launch<64>(k, c.split, s, &grid); break;
     }
   }
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return FO_ERR_CUDA;
-  }
-  return launched(c.tn ? "gemm_fp8 narrow" : "gemm_fp8 wide", R, M, d->N, grid, threads);
+  return launched(e, c.tn ? "gemm_fp8 narrow" : "gemm_fp8 wide", R, M, d->N, grid, threads);
 }

@@ -140,6 +140,8 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 6 : 1) rmsnorm_kernel(const
   __shared__ float smem[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = blockIdx.y;
+  grid_release();
+  grid_wait();
   for (int64_t at = blockIdx.x; at < p.rows; at += gridDim.x) {
     const int64_t off = at * p.H;
     float s[C][K::E];
@@ -244,6 +246,8 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
   constexpr bool kAhead = C * E * (WIDE ? (int)sizeof(T) : 4) <= 32, kHold = kAhead || NW <= 16;
   __shared__ float smem[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_release();
+  grid_wait();
   float w[kAhead ? C : 1][E], dw[C][E];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -345,6 +349,8 @@ __global__ void __launch_bounds__(256) dweight_kernel(const float* part, int blo
   __shared__ float smem[8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
   float s = 0.f;
+  grid_release();
+  grid_wait();
   if (c < H) {
 #pragma unroll 8
     for (int b = warp; b < blocks; b += 8) s += part[(int64_t)b * H + c];
@@ -408,8 +414,7 @@ struct LaunchFwd {
   template <typename T, bool WIDE, int NW, int C>
   fo_status operator()() const {
     const dim3 grid((unsigned)k.rows, R);
-    rmsnorm_kernel<T, WIDE, NW, C><<<grid, NW * 32, 0, s>>>(k);
-    return launched("rmsnorm", R, k.rows, k.H, (int)k.rows, NW * 32);
+    return launched(launch_after(rmsnorm_kernel<T, WIDE, NW, C>, grid, NW * 32, 0, 0, s, k), "rmsnorm", R, k.rows, k.H, (int)k.rows, NW * 32);
   }
 };
 struct LaunchBwd {
@@ -420,8 +425,7 @@ struct LaunchBwd {
   template <typename T, bool WIDE, int NW, int C>
   fo_status operator()() const {
     const int grid = *blocks = bwd_blocks(k.total, NW);
-    rmsnorm_bwd_kernel<T, WIDE, NW, C><<<grid, NW * 32, 0, s>>>(k);
-    return launched("rmsnorm_bwd", R, k.rows, k.H, grid, NW * 32);
+    return launched(launch_after(rmsnorm_bwd_kernel<T, WIDE, NW, C>, dim3(grid), NW * 32, 0, 0, s, k), "rmsnorm_bwd", R, k.rows, k.H, grid, NW * 32);
   }
 };
 
@@ -543,6 +547,5 @@ extern "C" fo_status fo_rmsnorm_bwd(const fo_norm_desc* d, int64_t rows, const v
   if ((st = by_type(d->dtype, wide, d->H, LaunchBwd{k, s, R, &grid}))) return st;
   if (!dweight) return FO_OK;
   const int cols = (d->H + 31) / 32;
-  dweight_kernel<<<cols, 256, 0, s>>>(k.part, grid, d->H, dweight);
-  return launched("rmsnorm_dweight", R, grid, d->H, cols, 256);
+  return launched(launch_after(dweight_kernel, dim3(cols), 256, 0, 0, s, (const float*)k.part, grid, d->H, dweight), "rmsnorm_dweight", R, grid, d->H, cols, 256);
 }

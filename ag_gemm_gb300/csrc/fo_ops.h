@@ -7,6 +7,9 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
+
+#include <utility>
 
 #include "fo_internal.h"
 
@@ -51,10 +54,40 @@ struct PtrList {
 inline fo_status device_sms(int* sms) { return fo_internal_device_sms(sms); }
 // fo_check_device_pointers on the list.
 fo_status check_device(const PtrList& l, fo_stream_t stream);
-// After a launch: FO_OK or FO_ERR_CUDA, with FO_LOG's line.
-fo_status launched(const char* what, int R, int64_t rows, int64_t cols, int grid, int threads);
+// After a launch that returned `e`: FO_OK or FO_ERR_CUDA, with FO_LOG's line.
+fo_status launched(cudaError_t e, const char* what, int R, int64_t rows, int64_t cols, int grid, int threads);
+
+// Launches `kern` so that it may start while the kernel before it in the
+// stream still runs its last blocks (programmatic dependent launch): it sets
+// itself up and then waits, in grid_wait(), until that kernel has ended and
+// its writes can be seen. cluster = 0: no cluster.
+template <typename... A, typename... B>
+cudaError_t launch_after(void (*kern)(A...), dim3 grid, int threads, int smem, int cluster, cudaStream_t s, B&&... args) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<B>(args)...);
+}
 
 // ------------------------------------------------------------- device side
+
+// Lets the next kernel of the stream start once every block has come here;
+// it waits for this one's end by itself.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Waits until the kernels before this one have ended. Comes before the first
+// access to global memory of every thread.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 constexpr float kE4M3Top = 448.f;
 constexpr float kLeastScale = 1.17549435e-38f;   // 2^-126

@@ -25,6 +25,8 @@ template <typename T>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__ QuantParams p) {
   const int lane = threadIdx.x & 31, r = blockIdx.y;
   const int64_t n = p.rows * p.groups;
+  grid_release();
+  grid_wait();
   for (int64_t g = blockIdx.x * 8ll + (threadIdx.x >> 5); g < n; g += gridDim.x * 8ll) {
     const int64_t row = g / p.groups;
     const int64_t c0 = (g - row * p.groups) * FO_FP8_BLOCK;
@@ -56,6 +58,8 @@ __global__ void __launch_bounds__(256) quant_rows_wide_kernel(const __grid_const
   constexpr int E = Vec16<T>::N, kCols = 32 * E, kUnroll = 2, kLanes = FO_FP8_BLOCK / E;
   const int lane = threadIdx.x & 31, r = blockIdx.y;
   const int64_t n = p.rows * p.pieces, step = (int64_t)gridDim.x * 8;
+  grid_release();
+  grid_wait();
   for (int64_t w = blockIdx.x * 8ll + (threadIdx.x >> 5); w < n; w += step * kUnroll) {
     uint4 raw[kUnroll];
     int64_t row[kUnroll];
@@ -97,6 +101,8 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.z;
   const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
   float v[16][4], amax = 0.f;
+  grid_release();
+  grid_wait();
 #pragma unroll
   for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -158,6 +164,8 @@ __global__ void __launch_bounds__(256) quant_blocks_wide_kernel(const __grid_con
   const int rg = tid >> 4, cg = tid & 15;   // groups of 8 rows, of 8 columns
   const int64_t row0 = r0 + rg * 8, col = c0 + cg * 8;
   const bool in = col < p.cols;   // whole groups: the columns are a multiple of 8
+  grid_release();
+  grid_wait();
   uint4 raw[8][V];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -262,13 +270,13 @@ extern "C" fo_status fo_quant_fp8(int32_t R, int64_t rows, int64_t cols, int32_t
   const cudaStream_t s = (cudaStream_t)stream;
   const bool bf16 = dtype == FO_BF16;
   const bool wide = (cols * es) % 16 == 0 && all_aligned(R, x, 16) && all_aligned(R, (A)q, 8);
+  cudaError_t e;
   if (block_rows == 1) {
     if (!wide) {
       const int64_t want = (rows * k.groups + 7) / 8;
       const dim3 grid((unsigned)(want < 65536 ? want : 65536), R);
-      if (bf16) quant_rows_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(k);
-      else quant_rows_kernel<float><<<grid, 256, 0, s>>>(k);
-      return launched("quant_rows", R, rows, cols, grid.x, 256);
+      e = launch_after(bf16 ? quant_rows_kernel<__nv_bfloat16> : quant_rows_kernel<float>, grid, 256, 0, 0, s, k);
+      return launched(e, "quant_rows", R, rows, cols, grid.x, 256);
     }
     const int piece = bf16 ? 256 : 128;
     if (cols % FO_FP8_BLOCK == 0 && rows * cols <= INT32_MAX - 1024) {   // groups back to back: one long row
@@ -281,21 +289,15 @@ extern "C" fo_status fo_quant_fp8(int32_t R, int64_t rows, int64_t cols, int32_t
     // 21.7), few pieces: a warp each.
     const int64_t n = k.rows * k.pieces, want = n >= 4096 ? (n + 15) / 16 : (n + 7) / 8;
     const dim3 grid((unsigned)(want < 65536 ? want : 65536), R);
-    if (bf16) quant_rows_wide_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(k);
-    else quant_rows_wide_kernel<float><<<grid, 256, 0, s>>>(k);
-    return launched("quant_rows wide", R, rows, cols, grid.x, 256);
+    e = launch_after(bf16 ? quant_rows_wide_kernel<__nv_bfloat16> : quant_rows_wide_kernel<float>, grid, 256, 0, 0, s, k);
+    return launched(e, "quant_rows wide", R, rows, cols, grid.x, 256);
   }
   const dim3 grid(k.groups, k.row_blocks, R);
   const bool wide_blocks = wide && cols % 8 == 0 && (!qt || (rows % 8 == 0 && all_aligned(R, (A)qt, 8)));
-  if (!wide_blocks) {
-    if (bf16) quant_blocks_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(k);
-    else quant_blocks_kernel<float><<<grid, 256, 0, s>>>(k);
-  } else if (qt) {
-    if (bf16) quant_blocks_wide_kernel<__nv_bfloat16, true><<<grid, 256, 0, s>>>(k);
-    else quant_blocks_wide_kernel<float, true><<<grid, 256, 0, s>>>(k);
-  } else {
-    if (bf16) quant_blocks_wide_kernel<__nv_bfloat16, false><<<grid, 256, 0, s>>>(k);
-    else quant_blocks_wide_kernel<float, false><<<grid, 256, 0, s>>>(k);
-  }
-  return launched(wide_blocks ? "quant_blocks wide" : "quant_blocks", R, rows, cols, grid.x * grid.y, 256);
+  void (*kern)(const QuantParams) =
+      !wide_blocks ? (bf16 ? quant_blocks_kernel<__nv_bfloat16> : quant_blocks_kernel<float>)
+      : qt         ? (bf16 ? quant_blocks_wide_kernel<__nv_bfloat16, true> : quant_blocks_wide_kernel<float, true>)
+                   : (bf16 ? quant_blocks_wide_kernel<__nv_bfloat16, false> : quant_blocks_wide_kernel<float, false>);
+  e = launch_after(kern, grid, 256, 0, 0, s, k);
+  return launched(e, wide_blocks ? "quant_blocks wide" : "quant_blocks", R, rows, cols, grid.x * grid.y, 256);
 }

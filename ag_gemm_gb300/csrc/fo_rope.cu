@@ -75,6 +75,8 @@ __global__ void __launch_bounds__(256, 3) rope_kernel(const __grid_constant__ Ro
   __shared__ uint64_t turns[FO_ROPE_MAX_DIM / 2];
   if (threadIdx.x < p.rot / 2) turns[threadIdx.x] = p.turns[threadIdx.x];
   __syncthreads();
+  grid_release();
+  grid_wait();
   const int lanes = p.lanes, tok = threadIdx.x / lanes, i = threadIdx.x - tok * lanes;
   const int64_t t = (int64_t)blockIdx.x * p.tokens + tok;
   if (tok >= p.tokens || t >= p.rows) return;
@@ -159,8 +161,7 @@ fo_status launch_as(RopeParams& k, int R, cudaStream_t s) {
   if (cuts > (all + 3) / 4) cuts = (all + 3) / 4;
   k.heads_each = (int)((all + cuts - 1) / cuts);
   const dim3 grid((unsigned)((k.rows + k.tokens - 1) / k.tokens), (unsigned)((all + k.heads_each - 1) / k.heads_each), R);
-  rope_kernel<T, V, HALF><<<grid, 256, 0, s>>>(k);
-  return launched("rope", R, k.rows, k.D, grid.x * grid.y, 256);
+  return launched(launch_after(rope_kernel<T, V, HALF>, grid, 256, 0, 0, s, k), "rope", R, k.rows, k.D, grid.x * grid.y, 256);
 }
 template <typename T>
 fo_status launch_with(RopeParams& k, int R, int v, cudaStream_t s) {
@@ -183,6 +184,8 @@ __global__ void __launch_bounds__(256) rope_single_kernel(const __grid_constant_
   __shared__ float2 rot[FO_ROPE_MAX_DIM / 2];
   const int64_t t = blockIdx.x;
   const int r = blockIdx.y, pairs = p.rot / 2;
+  grid_release();
+  grid_wait();
   if (threadIdx.x < pairs) rot[threadIdx.x] = rotation(p, position_of(p, t), p.turns[threadIdx.x]);
   __syncthreads();
 #pragma unroll
@@ -317,9 +320,8 @@ extern "C" fo_status fo_rope(const fo_rope_desc* d, int64_t rows, const void* po
   }
   if (!k.half && v < 2) {
     const dim3 grid((unsigned)rows, R);
-    if (d->dtype == FO_BF16) rope_single_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(k);
-    else rope_single_kernel<float><<<grid, 256, 0, s>>>(k);
-    return launched("rope single", R, rows, d->head_dim, (int)rows, 256);
+    auto kern = d->dtype == FO_BF16 ? rope_single_kernel<__nv_bfloat16> : rope_single_kernel<float>;
+    return launched(launch_after(kern, grid, 256, 0, 0, s, k), "rope single", R, rows, d->head_dim, (int)rows, 256);
   }
   return d->dtype == FO_BF16 ? launch_with<__nv_bfloat16>(k, R, v, s) : launch_with<float>(k, R, v, s);
 }

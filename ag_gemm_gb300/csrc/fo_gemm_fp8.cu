@@ -29,6 +29,21 @@ using namespace fo;
 constexpr uint64_t kWaitNs = 2000000000ull;   // every wait's bound
 constexpr int kBlockK = FO_FP8_BLOCK;         // reduction bytes a stage
 
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery's: with s the
+// bits of d - 1, m = floor(2^32 (2^s - d) / d) + 1, the quotient is
+// (floor(m n / 2^32) + n) / 2^s). The hardware has no integer division; the
+// compiler's takes some 30 dependent instructions, three of them at every tile.
+struct Divisor {
+  uint32_t d, m, s;
+  void set(uint32_t divisor) {
+    d = divisor;
+    for (s = 0; (1ull << s) < d; ++s) {
+    }
+    m = (uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
+};
+
 struct GemmParams {
   CUtensorMap tmA[kMaxR];   // A_r [M x K] bytes
   CUtensorMap tmW[kMaxR];   // W_r [N x K] bytes
@@ -39,6 +54,7 @@ struct GemmParams {
   int32_t* status;
   int32_t R, M, N, kblocks, nblocks;   // nblocks: 128-row blocks of W
   int32_t tiles_m, tiles_n;
+  Divisor per_rank, per_panel, last_panel;   // wide: tiles of a rank, of a panel, rows of the last panel
   int32_t f32;
   int32_t vec;                         // rows of Y start on 16 bytes
 };
@@ -166,15 +182,13 @@ struct Tile {
   int r, mt, nt;
 };
 __device__ __forceinline__ Tile decode(const GemmParams& p, int L) {
-  const int per = p.tiles_m * p.tiles_n;
   Tile t;
-  t.r = L / per;
-  const int i = L - t.r * per;
-  const int panel = i / (kPanel * p.tiles_n);
-  const int rows = min(kPanel, p.tiles_m - panel * kPanel);
-  const int j = i - panel * kPanel * p.tiles_n;
-  t.nt = j / rows;
-  t.mt = panel * kPanel + j - t.nt * rows;
+  t.r = (int)p.per_rank((uint32_t)L);
+  const uint32_t i = (uint32_t)L - (uint32_t)t.r * p.per_rank.d;
+  const uint32_t panel = p.per_panel(i), j = i - panel * p.per_panel.d;
+  const bool full = (int)panel * kPanel + kPanel <= p.tiles_m;
+  t.nt = (int)(full ? j / kPanel : p.last_panel(j));
+  t.mt = (int)(panel * kPanel + j) - t.nt * (full ? kPanel : (int)p.last_panel.d);
   return t;
 }
 
@@ -205,41 +219,46 @@ __device__ __forceinline__ void store_part(const GemmParams& p, int r, int m, in
   if (m >= p.M || n >= p.N) return;
   constexpr int kCols = F32 ? 32 : 64, kParts = 128 / kCols;   // columns in 128 bytes
 #pragma unroll
-  for (int h = 0; h < kParts; ++h) {
-    const uint32_t buf = bufs + (uint32_t)(h & 1) * kOutBuf;
-    uint32_t w[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      float lo, hi;
-      if constexpr (F32) {
-        halves(acc[h * 16 + j / 2], lo, hi);
-        w[j] = __float_as_uint(j & 1 ? hi : lo);
-      } else {
-        halves(acc[h * 32 + j], lo, hi);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-        w[j] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-    }
-    if (lane == 0) bulk_wait_read<1>();   // the buffer's last store has read it
+  for (int h0 = 0; h0 < kParts; h0 += 2) {   // both buffers, then their stores behind one fence
+    if (lane == 0) bulk_wait_read<0>();   // the buffers' last stores have read them
     __syncwarp();
-    stage_row(buf, lane, w);
+#pragma unroll
+    for (int h = h0; h < h0 + 2; ++h) {
+      uint32_t w[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        float lo, hi;
+        if constexpr (F32) {
+          halves(acc[h * 16 + j / 2], lo, hi);
+          w[j] = __float_as_uint(j & 1 ? hi : lo);
+        } else {
+          halves(acc[h * 32 + j], lo, hi);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+          w[j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+      }
+      stage_row(bufs + (uint32_t)(h & 1) * kOutBuf, lane, w);
+    }
     if (p.vec) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if (n + h * kCols < p.N) tma_store_2d(&p.tmY[r], buf, n + h * kCols, m);   // clipped at Y's edges
+        tma_store_2d(&p.tmY[r], bufs, n + h0 * kCols, m);   // clipped at Y's edges
+        if (n + h0 * kCols + kCols < p.N) tma_store_2d(&p.tmY[r], bufs + kOutBuf, n + h0 * kCols + kCols, m);
         bulk_commit();
       }
     } else {   // rows of Y that no TMA store can start on: lanes along the columns
       __syncwarp();
-      for (int i = 0; i < 32 && m + i < p.M; ++i) {
-        const uint32_t v = staged_word(buf, i, lane);
+      for (int i = 0; i < 64; ++i) {
+        const int h = h0 + (i >> 5), row = m + (i & 31);
+        if (row >= p.M) continue;
+        const uint32_t v = staged_word(bufs + (uint32_t)(i >> 5) * kOutBuf, i & 31, lane);
         if constexpr (F32) {
           const int c = n + h * 32 + lane;
-          if (c < p.N) static_cast<float*>(p.Y[r])[(int64_t)(m + i) * p.N + c] = __uint_as_float(v);
+          if (c < p.N) static_cast<float*>(p.Y[r])[(int64_t)row * p.N + c] = __uint_as_float(v);
         } else {
           const int c = n + h * 64 + 2 * lane;
-          uint16_t* y = static_cast<uint16_t*>(p.Y[r]) + (int64_t)(m + i) * p.N + c;
+          uint16_t* y = static_cast<uint16_t*>(p.Y[r]) + (int64_t)row * p.N + c;
           if (c < p.N) y[0] = (uint16_t)v;
           if (c + 1 < p.N) y[1] = (uint16_t)(v >> 16);
         }
@@ -891,6 +910,9 @@ extern "C" fo_status fo_gemm_fp8(const fo_gemm_fp8_desc* d, int64_t M, const voi
   if (c.tn == 0) {
     k.tiles_m = (int32_t)((M + 255) / 256);
     k.tiles_n = (int32_t)((d->N + 255) / 256);
+    k.per_rank.set((uint32_t)(k.tiles_m * k.tiles_n));
+    k.per_panel.set((uint32_t)(wide::kPanel * k.tiles_n));
+    k.last_panel.set((uint32_t)(k.tiles_m % wide::kPanel ? k.tiles_m % wide::kPanel : wide::kPanel));
     const int64_t total = (int64_t)R * k.tiles_m * k.tiles_n;
     if (total > INT32_MAX / 2) return FO_ERR_SHAPE;
     auto kern = k.f32 ? wide::gemm_fp8_wide_kernel<true> : wide::gemm_fp8_wide_kernel<false>;

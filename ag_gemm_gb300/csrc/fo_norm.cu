@@ -204,47 +204,47 @@ struct NormBwdParams {
   bool has_dh, has_dw, w_f32;
 };
 
-// A thread's raw values of one row's chunk: 16 bytes (WIDE) or E values.
-template <typename T, bool WIDE>
-struct Raw {
-  using K = Chunk<T, WIDE>;
-  uint4 u;
-  float f[WIDE ? 1 : K::E];
-  __device__ __forceinline__ void load(const T* p, int chunk, int lane, int H) {
-    if constexpr (WIDE) {
-      const int c = K::col(chunk, lane, 0);
-      u = make_uint4(0, 0, 0, 0);
-      if (c < H) u = *reinterpret_cast<const uint4*>(p + c);
-    } else {
-      K::load(p, chunk, lane, H, f);
-    }
-  }
-  __device__ __forceinline__ void values(float (&v)[K::E]) const {
-    if constexpr (WIDE) {
-      Vec16<T>::unpack(u, v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < K::E; ++j) v[j] = f[j];
-    }
-  }
-};
-
 // Blocks of the backward kernel on an SM: sixteen warps' worth.
 constexpr int bwd_per_sm(int nw) { return nw <= 16 ? 16 / nw : 1; }
+
+// 16 bytes to shared memory in the background, or zeros.
+__device__ __forceinline__ void copy16_async(void* to, const void* from, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {   // all but the N newest groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows ahead that a block loads in the background.
+constexpr int kAheadRows = 3;
+template <typename T, bool WIDE, int NW, int C>
+struct BwdCfg {
+  // A thread's part of a row is at most 32 bytes of each input.
+  static constexpr bool kAhead = WIDE && C <= 2;
+  static constexpr bool kHold = kAhead || NW <= 16;
+  static constexpr int kSlot = NW * 32 * C;   // 16-byte pieces of one input's row
+  static constexpr int kSmem = kAhead ? kAheadRows * 3 * kSlot * 16 : 0;
+};
 
 // A block takes every gridDim.x-th row and keeps its columns' share of the
 // weight's gradient in registers. What else it keeps goes by the registers
 // that a thread's part of a row takes: where it is 32 bytes or less, the
-// weights too, and the next row's values are loaded before this row's sum is
-// known, so that loads are in flight through the two barriers; beyond, with
-// up to 16 warps, this row's values; else nothing, and the second pass over
-// the row reads it again, from L2.
+// weights too, and the next three rows come in the background, each thread
+// its own pieces, so that the loads go on through the two barriers of a row;
+// beyond, with up to 16 warps, this row's values; else nothing, and the second
+// pass over the row reads it again, from L2.
 template <typename T, bool WIDE, int NW, int C>
 __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
   using K = Chunk<T, WIDE>;
+  using Cfg = BwdCfg<T, WIDE, NW, C>;
   constexpr int E = K::E;
-  constexpr bool kAhead = C * E * (WIDE ? (int)sizeof(T) : 4) <= 32, kHold = kAhead || NW <= 16;
+  constexpr bool kAhead = Cfg::kAhead, kHold = Cfg::kHold;
   __shared__ float smem[32];
+  extern __shared__ uint4 ring[];   // kAhead: [row % kAheadRows][input][chunk][thread]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_release();
   grid_wait();
@@ -255,31 +255,47 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
 #pragma unroll
     for (int j = 0; j < E; ++j) dw[c][j] = 0.f;
   }
-  constexpr int CA = kAhead ? C : 1;
-  Raw<T, WIDE> dy_n[CA], h_n[CA], dh_n[CA];
-  float rstd_n = 0.f;
   // (A 64-bit division costs as much as a third of a row.)
   auto rank_of = [&](int64_t row) -> int {
     return p.total == p.rows ? 0 : p.total <= UINT32_MAX ? (int)((uint32_t)row / (uint32_t)p.rows) : (int)(row / p.rows);
   };
-  auto fetch = [&](int64_t row) {
-    const int r = rank_of(row);
-    const int64_t at = row - r * p.rows, off = at * p.H;
-    rstd_n = p.rstd[r][at];
+  auto fetch = [&](int64_t row, int slot) {
+    if (row < p.total) {
+      const int r = rank_of(row);
+      const int64_t off = (row - r * p.rows) * p.H;
+      uint4* const to = ring + slot * 3 * Cfg::kSlot + threadIdx.x;
 #pragma unroll
-    for (int c = 0; c < CA; ++c) {
-      dy_n[c].load(static_cast<const T*>(p.dy[r]) + off, c * NW + warp, lane, p.H);
-      h_n[c].load(static_cast<const T*>(p.h[r]) + off, c * NW + warp, lane, p.H);
-      if (p.has_dh) dh_n[c].load(static_cast<const T*>(p.dh[r]) + off, c * NW + warp, lane, p.H);
+      for (int c = 0; c < C; ++c) {
+        const int col = K::col(c * NW + warp, lane, 0);
+        const bool in = col < p.H;
+        const int64_t at = off + (in ? col : 0);
+        copy16_async(to + c * NW * 32, static_cast<const T*>(p.dy[r]) + at, in);
+        copy16_async(to + Cfg::kSlot + c * NW * 32, static_cast<const T*>(p.h[r]) + at, in);
+        if (p.has_dh) copy16_async(to + 2 * Cfg::kSlot + c * NW * 32, static_cast<const T*>(p.dh[r]) + at, in);
+      }
     }
+    copies_end();   // a group for every row, empty ones too: the waits count them
   };
-  if (kAhead && blockIdx.x < p.total) fetch(blockIdx.x);
+  auto piece = [&](int slot, int input, int c, float (&v)[E]) {
+    if constexpr (kAhead) Vec16<T>::unpack(ring[(slot * 3 + input) * Cfg::kSlot + c * NW * 32 + threadIdx.x], v);
+  };
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAheadRows - 1; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+  }
+  int slot = 0;
   for (int64_t row = blockIdx.x; row < p.total; row += gridDim.x) {
     const int r = rank_of(row);
     const int64_t at = row - r * p.rows, off = at * p.H;
     const T* const dy = static_cast<const T*>(p.dy[r]) + off;
     const T* const hp = static_cast<const T*>(p.h[r]) + off;
-    const float rstd = kAhead ? rstd_n : p.rstd[r][at];
+    const float rstd = p.rstd[r][at];
+    if constexpr (kAhead) {
+      // The slot of the row before this one is free: this thread has read its
+      // pieces, and no other thread reads them.
+      fetch(row + (int64_t)(kAheadRows - 1) * gridDim.x, slot == 0 ? kAheadRows - 1 : slot - 1);
+      copies_wait<kAheadRows - 1>();
+    }
     float h[kHold ? C : 1][E], u[kHold ? C : 1][E];
     float sum = 0.f;
 #pragma unroll
@@ -287,8 +303,8 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
       float(&uc)[E] = u[kHold ? c : 0];
       float(&hc)[E] = h[kHold ? c : 0];
       if constexpr (kAhead) {
-        dy_n[c].values(uc);
-        h_n[c].values(hc);
+        piece(slot, 0, c, uc);
+        piece(slot, 1, c, hc);
       } else {
         K::load(dy, c * NW + warp, lane, p.H, uc);
         K::load(hp, c * NW + warp, lane, p.H, hc);
@@ -300,12 +316,6 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
         uc[j] *= w[kAhead ? c : 0][j];
         sum = fmaf(uc[j], hc[j], sum);
       }
-    }
-    Raw<T, WIDE> dh[CA];
-    if constexpr (kAhead) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) dh[c] = dh_n[c];
-      if (row + gridDim.x < p.total) fetch(row + gridDim.x);
     }
     const float k = block_sum<NW>(sum, smem) * p.inv_H * rstd * rstd * rstd;
 #pragma unroll
@@ -324,13 +334,14 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
       for (int j = 0; j < E; ++j) d[j] = rstd * uc[j] - hc[j] * k;
       if (p.has_dh) {
         float t[E];
-        if constexpr (kAhead) dh[c].values(t);
+        if constexpr (kAhead) piece(slot, 2, c, t);
         else K::load(static_cast<const T*>(p.dh[r]) + off, c * NW + warp, lane, p.H, t);
 #pragma unroll
         for (int j = 0; j < E; ++j) d[j] += t[j];
       }
       K::store(static_cast<T*>(p.dx[r]) + off, c * NW + warp, lane, p.H, d);
     }
+    slot = slot + 1 == kAheadRows ? 0 : slot + 1;
   }
   if (p.has_dw) {
 #pragma unroll
@@ -343,23 +354,26 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
   }
 }
 
-// dweight[c] = sum of the blocks' partial sums: a warp adds every eighth
-// block's for 32 columns, then the eight warps' sums are added in order.
-__global__ void __launch_bounds__(256) dweight_kernel(const float* part, int blocks, int H, float* dw) {
-  __shared__ float smem[8][32];
+// dweight[c] = sum of the blocks' partial sums: a warp adds every 32nd
+// block's for 32 columns, then the 32 warps' sums are added in order. (As
+// many loads in flight as there are: with 8 warps the loads' latency alone,
+// five times over, was 5 us of the backward pass.)
+constexpr int kDwWarps = 32;
+__global__ void __launch_bounds__(kDwWarps * 32) dweight_kernel(const float* part, int blocks, int H, float* dw) {
+  __shared__ float smem[kDwWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
   float s = 0.f;
   grid_release();
   grid_wait();
   if (c < H) {
-#pragma unroll 8
-    for (int b = warp; b < blocks; b += 8) s += part[(int64_t)b * H + c];
+#pragma unroll 10
+    for (int b = warp; b < blocks; b += kDwWarps) s += part[(int64_t)b * H + c];
   }
   smem[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < H) {
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += smem[k][lane];
+    for (int k = 1; k < kDwWarps; ++k) s += smem[k][lane];
     dw[c] = s;
   }
 }
@@ -425,7 +439,13 @@ struct LaunchBwd {
   template <typename T, bool WIDE, int NW, int C>
   fo_status operator()() const {
     const int grid = *blocks = bwd_blocks(k.total, NW);
-    return launched(launch_after(rmsnorm_bwd_kernel<T, WIDE, NW, C>, dim3(grid), NW * 32, 0, 0, s, k), "rmsnorm_bwd", R, k.rows, k.H, grid, NW * 32);
+    constexpr int smem = BwdCfg<T, WIDE, NW, C>::kSmem;
+    auto kern = rmsnorm_bwd_kernel<T, WIDE, NW, C>;
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return launched(e, "rmsnorm_bwd", R, k.rows, k.H, grid, NW * 32);
+    }
+    return launched(launch_after(kern, dim3(grid), NW * 32, smem, 0, s, k), "rmsnorm_bwd", R, k.rows, k.H, grid, NW * 32);
   }
 };
 
@@ -547,5 +567,5 @@ extern "C" fo_status fo_rmsnorm_bwd(const fo_norm_desc* d, int64_t rows, const v
   if ((st = by_type(d->dtype, wide, d->H, LaunchBwd{k, s, R, &grid}))) return st;
   if (!dweight) return FO_OK;
   const int cols = (d->H + 31) / 32;
-  return launched(launch_after(dweight_kernel, dim3(cols), 256, 0, 0, s, (const float*)k.part, grid, d->H, dweight), "rmsnorm_dweight", R, grid, d->H, cols, 256);
+  return launched(launch_after(dweight_kernel, dim3(cols), kDwWarps * 32, 0, 0, s, (const float*)k.part, grid, d->H, dweight), "rmsnorm_dweight", R, grid, d->H, cols, kDwWarps * 32);
 }

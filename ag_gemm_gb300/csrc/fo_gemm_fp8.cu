@@ -488,6 +488,16 @@ constexpr uint32_t kWBytes = 128 * kBlockK;
 constexpr int kScaleBlocks = 32;   // blocks whose scales are in shared memory at a time
 constexpr int kMaxSplit = 8;       // CTAs that share a reduction (portable cluster size)
 
+// Blocks of weights that a CTA asks for while the kernel before it ends (4 x
+// 12288 x 4096 from HBM, back to back: none 11.8 us, four 10.7, sixteen 11.6).
+constexpr int kPrefetchBlocks = 4;
+
+__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 template <int TN>
 struct Cfg {
   static constexpr uint32_t kXBytes = TN * kBlockK;
@@ -557,6 +567,11 @@ __global__ void __launch_bounds__(kThreads) gemm_fp8_narrow_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // While the kernel before this one ends, the CTA's first weights come into
+  // L2: a hint that reads nothing, so it need not wait.
+  if (warp == 0 && elect_one())
+    for (int i = 0; i < blocks && i < kPrefetchBlocks; ++i) prefetch_box(&p.tmW[r], (kb0 + i) * kBlockK, nb * 128);
+  __syncwarp();
   grid_wait();
   __syncwarp();
 

@@ -243,7 +243,7 @@ __device__ __forceinline__ void store_part(const GemmParams& p, int r, int m, in
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tma_store_2d(&p.tmY[r], bufs, n + h0 * kCols, m);   // clipped at Y's edges
+        if (n + h0 * kCols < p.N) tma_store_2d(&p.tmY[r], bufs, n + h0 * kCols, m);   // clipped at Y's edges
         if (n + h0 * kCols + kCols < p.N) tma_store_2d(&p.tmY[r], bufs + kOutBuf, n + h0 * kCols + kCols, m);
         bulk_commit();
       }

@@ -240,7 +240,7 @@ extern "C" fo_status fo_quant_fp8(int32_t R, int64_t rows, int64_t cols, int32_t
   if (R < 1 || R > kMaxR || (block_rows != 1 && block_rows != FO_FP8_BLOCK)) return FO_ERR_INVALID_ARG;
   if (!qt != !scale_t || (qt && block_rows == 1)) return FO_ERR_INVALID_ARG;
   // A grid has at most 65535 blocks in y: block rows of the matrix.
-  if (rows < 0 || rows > (int64_t)65535 * 128 || cols < 1 || cols > (int64_t)INT32_MAX - 1024) return FO_ERR_SHAPE;
+  if (rows < 0 || rows > (block_rows == 1 ? (int64_t)INT32_MAX : (int64_t)65535 * 128) || cols < 1 || cols > (int64_t)INT32_MAX - 1024) return FO_ERR_SHAPE;
   if (dtype != FO_BF16 && dtype != FO_F32) return FO_ERR_DTYPE;
   if (rows == 0) return FO_OK;
   const size_t es = dtype == FO_BF16 ? 2 : 4;

@@ -142,7 +142,7 @@ def test_quant_refuses_bad_arguments():
     call = lambda rows=4, cols=128, x=ok, q=ok, s=ok, **k: code_of(B.fo_quant_fp8, rows, cols, x, q, s, **{**dict(dtype="bf16", stream=0), **k})  # noqa: E731
     assert call(rows=-1) == B.FO_ERR_SHAPE
     assert call(cols=0) == B.FO_ERR_SHAPE
-    assert call(rows=65535 * 128 + 1) == B.FO_ERR_SHAPE
+    assert call(rows=2 ** 31) == call(rows=65535 * 128 + 1, block_rows=128) == B.FO_ERR_SHAPE
     assert call(block_rows=64) == B.FO_ERR_INVALID_ARG
     assert call(qt=ok, scale_t=ok) == B.FO_ERR_INVALID_ARG               # only blocks of 128 rows
     assert call(qt=ok, block_rows=128) == B.FO_ERR_INVALID_ARG

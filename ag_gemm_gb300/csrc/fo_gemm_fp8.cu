@@ -56,7 +56,7 @@ struct GemmParams {
   int32_t tiles_m, tiles_n;
   Divisor per_rank, per_panel, last_panel;   // wide: tiles of a rank, of a panel, rows of the last panel
   int32_t f32;
-  int32_t vec;                         // rows of Y start on 16 bytes
+  int32_t vec, row8, row4;             // rows of Y start on 16, 8, 4 bytes
 };
 
 // kind::f8f6f4 instruction descriptor: D fp32 (bits 4-5 = 1), A and B e4m3
@@ -217,7 +217,7 @@ template <bool F32>
 __device__ __forceinline__ void store_part(const GemmParams& p, int r, int m, int n, uint32_t bufs, int lane,
                                            const f32x2 (&acc)[64]) {
   if (m >= p.M || n >= p.N) return;
-  constexpr int kCols = F32 ? 32 : 64, kParts = 128 / kCols;   // columns in 128 bytes
+  constexpr int kBytes = F32 ? 4 : 2, kCols = 128 / kBytes, kParts = 128 / kCols;   // columns in 128 bytes
 #pragma unroll
   for (int h0 = 0; h0 < kParts; h0 += 2) {   // both buffers, then their stores behind one fence
     if (lane == 0) bulk_wait_read<0>();   // the buffers' last stores have read them
@@ -249,18 +249,34 @@ __device__ __forceinline__ void store_part(const GemmParams& p, int r, int m, in
       }
     } else {   // rows of Y that no TMA store can start on: lanes along the columns
       __syncwarp();
-      for (int i = 0; i < 64; ++i) {
-        const int h = h0 + (i >> 5), row = m + (i & 31);
-        if (row >= p.M) continue;
-        const uint32_t v = staged_word(bufs + (uint32_t)(i >> 5) * kOutBuf, i & 31, lane);
-        if constexpr (F32) {
-          const int c = n + h * 32 + lane;
-          if (c < p.N) static_cast<float*>(p.Y[r])[(int64_t)row * p.N + c] = __uint_as_float(v);
+      for (int h = h0; h < h0 + 2; ++h) {
+        const uint32_t buf = bufs + (uint32_t)(h & 1) * kOutBuf;
+        const int c0 = n + h * kCols;
+        uint8_t* const y = static_cast<uint8_t*>(p.Y[r]) + ((int64_t)m * p.N + c0) * kBytes;
+        const int64_t ld = (int64_t)p.N * kBytes;
+        if (p.row8) {   // 8 bytes a lane, two rows at a time
+          const int col = c0 + (lane & 15) * (8 / kBytes);
+#pragma unroll 8
+          for (int i = lane >> 4; i < 32; i += 2) {
+            const uint32_t lo = staged_word(buf, i, 2 * (lane & 15)), hi = staged_word(buf, i, 2 * (lane & 15) + 1);
+            if (m + i < p.M && col < p.N) *reinterpret_cast<uint2*>(y + i * ld + (lane & 15) * 8) = make_uint2(lo, hi);
+          }
+        } else if (F32 || p.row4) {   // 4 bytes
+          const int col = c0 + lane * (4 / kBytes);
+#pragma unroll 8
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t v = staged_word(buf, i, lane);
+            if (m + i < p.M && col < p.N) *reinterpret_cast<uint32_t*>(y + i * ld + lane * 4) = v;
+          }
         } else {
-          const int c = n + h * 64 + 2 * lane;
-          uint16_t* y = static_cast<uint16_t*>(p.Y[r]) + (int64_t)row * p.N + c;
-          if (c < p.N) y[0] = (uint16_t)v;
-          if (c + 1 < p.N) y[1] = (uint16_t)(v >> 16);
+          const int col = c0 + 2 * lane;
+#pragma unroll 8
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t v = staged_word(buf, i, lane);
+            uint16_t* const to = reinterpret_cast<uint16_t*>(y + i * ld + lane * 4);
+            if (m + i < p.M && col < p.N) to[0] = (uint16_t)v;
+            if (m + i < p.M && col + 1 < p.N) to[1] = (uint16_t)(v >> 16);
+          }
         }
       }
       __syncwarp();
@@ -906,6 +922,8 @@ extern "C" fo_status fo_gemm_fp8(const fo_gemm_fp8_desc* d, int64_t M, const voi
   k.f32 = d->out_dtype == FO_F32;
   const int es = k.f32 ? 4 : 2;
   k.vec = (d->N * es) % 16 == 0;
+  k.row8 = (d->N * es) % 8 == 0;
+  k.row4 = (d->N * es) % 4 == 0;
   for (int r = 0; r < R; ++r) {
     if (c.tn == 0 && k.vec && !encode(&k.tmY[r], Y[r], (uint64_t)d->N, (uint64_t)M, 32, es)) return FO_ERR_CUDA;
     if (r && A[r] == A[r - 1]) k.tmA[r] = k.tmA[r - 1];

@@ -135,7 +135,7 @@ __device__ __forceinline__ float block_sum(float v, float* smem) {
 // 8-bit output, 43 us with the five that the compiler's own choice of
 // registers leaves, 45 us with rows on 4 warps, 56 us with rows on 16.)
 template <typename T, bool WIDE, int NW, int C>
-__global__ void __launch_bounds__(NW * 32, NW == 8 ? 6 : 1) rmsnorm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(NW * 32, NW == 8 ? 6 : NW == 16 ? (C <= 2 ? 3 : 2) : 1) rmsnorm_kernel(const __grid_constant__ NormParams p) {
   using K = Chunk<T, WIDE>;
   __shared__ float smem[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -393,9 +393,13 @@ size_t elem(int32_t dtype) { return dtype == FO_BF16 ? 2 : 4; }
 // Warps of a block for rows of n chunks (by_width's choice).
 int warps_for(int n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 16 ? 8 : n <= 64 ? 16 : 32; }
 // Blocks of the backward pass (its partial sums are one row each).
+// At least four rows each where that leaves a block for every SM: more
+// blocks' partial sums would cost more than the rows (2529 x 128: 9.5 us with
+// as many blocks as fit).
 int bwd_blocks(int64_t total, int nw) {
-  const int most = bwd_per_sm(nw) * FO_GB300_SMS;
-  return (int)(total < most ? total : most);
+  const int64_t most = bwd_per_sm(nw) * FO_GB300_SMS, least = total < FO_GB300_SMS ? total : FO_GB300_SMS;
+  const int64_t want = total / 4 > least ? total / 4 : least;
+  return (int)(want < most ? want : most);
 }
 
 // Calls f.template operator()<T, WIDE, NW, C>() with the fewest warps whose

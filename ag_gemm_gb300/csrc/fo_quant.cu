@@ -17,6 +17,7 @@ struct QuantParams {
   int64_t rows, cols;
   int32_t groups, row_blocks;
   int32_t pieces;   // quant_rows_wide_kernel: warp-wide pieces of a row
+  int32_t copy8;    // quant_blocks_wide_kernel: the copy's lines start on 8 bytes
 };
 
 // One warp for each group of 128 values of a row (rows that do not start on
@@ -219,13 +220,43 @@ __global__ void __launch_bounds__(256) quant_blocks_wide_kernel(const __grid_con
       tile[(cg * 8 + 4 + j) * 16 + (rg ^ cg)] = make_uint2(hi[j], hi[j + 4]);
     }
     __syncthreads();
-    // Sixteen threads store a line of the copy (the rows are a multiple of 8).
+    if (p.copy8) {   // lines of the copy start on 8 bytes: sixteen threads store one
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = i * 16 + rg;
-      const int64_t row = r0 + cg * 8;
-      if (c0 + c < p.cols && row < p.rows)
-        *reinterpret_cast<uint2*>(p.qt[r] + (c0 + c) * p.rows + row) = tile[c * 16 + (cg ^ (c >> 3))];
+      for (int i = 0; i < 8; ++i) {
+        const int c = i * 16 + rg;
+        const int64_t row = r0 + cg * 8;
+        if (c0 + c < p.cols && row < p.rows)
+          *reinterpret_cast<uint2*>(p.qt[r] + (c0 + c) * p.rows + row) = tile[c * 16 + (cg ^ (c >> 3))];
+      }
+    } else {
+      // A warp stores a line in the 4-byte words of memory, each put together
+      // from two words of the tile; bytes where a word is not the line's alone.
+      const int n = (int)min((int64_t)128, p.rows - r0);   // bytes of a line
+#pragma unroll 4
+      for (int c = warp; c < 128; c += 8) {
+        if (c0 + c >= p.cols) break;
+        uint8_t* const line = p.qt[r] + (c0 + c) * p.rows + r0;
+        const int off = (int)(reinterpret_cast<uintptr_t>(line) & 3u);
+        auto word = [&](int k) -> uint32_t {   // bytes 4 k .. 4 k + 3 of the line
+          const uint2 u = tile[c * 16 + ((k >> 1) ^ (c >> 3))];
+          return k & 1 ? u.y : u.x;
+        };
+        const uint32_t mine = word(lane);
+        const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);   // (lane 31's is not stored whole)
+        // Lane l has the word of memory that begins at byte 4 l + 4 - off (4 l
+        // where the line starts on a word).
+        const int at = off ? 4 * lane + 4 - off : 4 * lane;
+        const uint32_t v = off ? __byte_perm(mine, next, 0x7654u - 0x1111u * (uint32_t)off) : mine;
+        if (at + 4 <= n) {
+          *reinterpret_cast<uint32_t*>(line + at) = v;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            if (at + j < n) line[at + j] = (uint8_t)(v >> (8 * j));
+        }
+        const uint32_t first = __shfl_sync(0xffffffffu, mine, 0);
+        if (lane < 4 - off && off && lane < n) line[lane] = (uint8_t)(first >> (8 * lane));
+      }
     }
   }
 }
@@ -293,7 +324,8 @@ extern "C" fo_status fo_quant_fp8(int32_t R, int64_t rows, int64_t cols, int32_t
     return launched(e, "quant_rows wide", R, rows, cols, grid.x, 256);
   }
   const dim3 grid(k.groups, k.row_blocks, R);
-  const bool wide_blocks = wide && cols % 8 == 0 && (!qt || (rows % 8 == 0 && all_aligned(R, (A)qt, 8)));
+  const bool wide_blocks = wide && cols % 8 == 0;
+  k.copy8 = rows % 8 == 0 && all_aligned(R, (A)qt, 8);
   void (*kern)(const QuantParams) =
       !wide_blocks ? (bf16 ? quant_blocks_kernel<__nv_bfloat16> : quant_blocks_kernel<float>)
       : qt         ? (bf16 ? quant_blocks_wide_kernel<__nv_bfloat16, true> : quant_blocks_wide_kernel<float, true>)

@@ -18,7 +18,9 @@ struct RopeParams {
   int32_t heads[3];
   int32_t D, rot;
   int32_t half;       // layout
-  int32_t lanes, tokens, heads_each;   // threads for a token, tokens a block, heads a thread
+  int32_t R;
+  int32_t lanes, tokens;              // threads for a token, tokens a block
+  int32_t heads_each, ranks_each;     // heads and ranks a thread goes through
   float factor, sign;
   uint64_t turns[FO_ROPE_MAX_DIM / 2];
 };
@@ -60,14 +62,14 @@ union Piece {
 };
 
 // A thread has a token and two pieces of V elements in every head, computes
-// its own angles once and goes through its share of the heads, kHeads at a
-// time with all loads first. The pieces of a rotated head: in the half layout
+// its own angles once and goes through its share of the ranks and heads,
+// kHeads at a time with all loads first. The pieces of a rotated head: in the half layout
 // piece i of the first half and of the second (V pairs); interleaved, pieces
 // i and i + lanes (V / 2 pairs each); the threads beyond the rotated pieces
 // copy the head's rest, two pieces each. Heads of V: pieces i and i + lanes.
 // V is the widest access that the sizes, strides and addresses allow (at
 // least a pair where pairs are neighbours).
-template <typename T, int V, bool HALF>
+template <typename T, int V, bool HALF, bool RANKS>
 __global__ void __launch_bounds__(256, 3) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kHeads = 4;
   // (Read lane by lane from the parameters, the frequencies would be one
@@ -80,7 +82,6 @@ __global__ void __launch_bounds__(256, 3) rope_kernel(const __grid_constant__ Ro
   const int lanes = p.lanes, tok = threadIdx.x / lanes, i = threadIdx.x - tok * lanes;
   const int64_t t = (int64_t)blockIdx.x * p.tokens + tok;
   if (tok >= p.tokens || t >= p.rows) return;
-  const int r = (int)blockIdx.z;
   const int pieces = p.rot / V / (HALF ? 2 : 1);   // of the first half; of all that is rotated
   const int whole = p.D / V;
   // This thread's pieces of a rotated head, and whether they are rotated.
@@ -96,72 +97,85 @@ __global__ void __launch_bounds__(256, 3) rope_kernel(const __grid_constant__ Ro
     const float2 cs = 2 * pair < p.rot ? rotation(p, pos, turns[pair]) : make_float2(0.f, 0.f);
     c[j] = cs.x, s[j] = cs.y;
   }
-  int h0 = (int)blockIdx.y * p.heads_each, h1 = h0 + p.heads_each;   // this block's heads, counted from each part's first
+  // (A loop over one rank alone costs a tenth of the kernel: registers.)
+  const int first_r = RANKS ? (int)blockIdx.z * p.ranks_each : (int)blockIdx.z;
+  const int last_r = RANKS ? min(p.R, first_r + p.ranks_each) : first_r + 1;
+  for (int r = first_r; RANKS ? r < last_r : r == first_r; ++r) {
+    int h0 = (int)blockIdx.y * p.heads_each, h1 = h0 + p.heads_each;   // this block's heads, counted from each part's first
 #pragma unroll
-  for (int part = 0; part < 3; ++part) {
-    const int first = max(h0, 0), last = min(h1, p.heads[part]);
-    h0 -= p.heads[part], h1 -= p.heads[part];
-    if (first >= last) continue;
-    const bool turned = part < 2;
-    const int pa = (turned ? a : i) * V, pb = (turned ? b : i + lanes) * V;
-    const bool has_b = turned ? two : i + lanes < whole;
-    const T* in = static_cast<const T*>(p.in[part][r]) + t * p.ld_in[part] + first * p.D;
-    T* out = static_cast<T*>(p.out[part][r]) + t * p.ld_out[part] + first * p.D;
-    const bool moves = in != out;   // in place, what is not rotated stays
-    for (int n = last - first; n > 0; n -= kHeads, in += kHeads * p.D, out += kHeads * p.D) {
-      Piece<T, V> x[kHeads], y[kHeads];
+    for (int part = 0; part < 3; ++part) {
+      const int first = max(h0, 0), last = min(h1, p.heads[part]);
+      h0 -= p.heads[part], h1 -= p.heads[part];
+      if (first >= last) continue;
+      const bool turned = part < 2;
+      const int pa = (turned ? a : i) * V, pb = (turned ? b : i + lanes) * V;
+      const bool has_b = turned ? two : i + lanes < whole;
+      const T* in = static_cast<const T*>(p.in[part][r]) + t * p.ld_in[part] + first * p.D;
+      T* out = static_cast<T*>(p.out[part][r]) + t * p.ld_out[part] + first * p.D;
+      const bool moves = in != out;   // in place, what is not rotated stays
+      for (int n = last - first; n > 0; n -= kHeads, in += kHeads * p.D, out += kHeads * p.D) {
+        Piece<T, V> x[kHeads], y[kHeads];
 #pragma unroll
-      for (int k = 0; k < kHeads; ++k)
-        if (k < n) {
-          x[k].load(in + k * p.D + pa);
-          if (has_b) y[k].load(in + k * p.D + pb);
-        }
-#pragma unroll
-      for (int k = 0; k < kHeads; ++k)
-        if (k < n) {
-          if (turned) {
-            if constexpr (HALF) {
-              if (turn_a) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                  const float u = to_f(x[k].v[j]), w = to_f(y[k].v[j]);
-                  from_f(u * c[j] - w * s[j], x[k].v[j]);
-                  from_f(w * c[j] + u * s[j], y[k].v[j]);
-                }
-              }
-            } else {
-              auto turn = [&](Piece<T, V>& z, int at) {
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) {
-                  const float u = to_f(z.v[2 * j]), w = to_f(z.v[2 * j + 1]);
-                  from_f(u * c[at + j] - w * s[at + j], z.v[2 * j]);
-                  from_f(w * c[at + j] + u * s[at + j], z.v[2 * j + 1]);
-                }
-              };
-              if (turn_a) turn(x[k], 0);
-              if (turn_b) turn(y[k], V / 2);
-            }
+        for (int k = 0; k < kHeads; ++k)
+          if (k < n) {
+            x[k].load(in + k * p.D + pa);
+            if (has_b) y[k].load(in + k * p.D + pb);
           }
-          if (moves || (turned && turn_a)) x[k].store(out + k * p.D + pa);
-          if (has_b && (moves || (turned && turn_b))) y[k].store(out + k * p.D + pb);
-        }
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k)
+          if (k < n) {
+            if (turned) {
+              if constexpr (HALF) {
+                if (turn_a) {
+#pragma unroll
+                  for (int j = 0; j < V; ++j) {
+                    const float u = to_f(x[k].v[j]), w = to_f(y[k].v[j]);
+                    from_f(u * c[j] - w * s[j], x[k].v[j]);
+                    from_f(w * c[j] + u * s[j], y[k].v[j]);
+                  }
+                }
+              } else {
+                auto turn = [&](Piece<T, V>& z, int at) {
+#pragma unroll
+                  for (int j = 0; j < V / 2; ++j) {
+                    const float u = to_f(z.v[2 * j]), w = to_f(z.v[2 * j + 1]);
+                    from_f(u * c[at + j] - w * s[at + j], z.v[2 * j]);
+                    from_f(w * c[at + j] + u * s[at + j], z.v[2 * j + 1]);
+                  }
+                };
+                if (turn_a) turn(x[k], 0);
+                if (turn_b) turn(y[k], V / 2);
+              }
+            }
+            if (moves || (turned && turn_a)) x[k].store(out + k * p.D + pa);
+            if (has_b && (moves || (turned && turn_b))) y[k].store(out + k * p.D + pb);
+          }
+      }
     }
   }
 }
 
 template <typename T, int V, bool HALF>
 fo_status launch_as(RopeParams& k, int R, cudaStream_t s) {
-  // Lanes for a token: two pieces each. Heads for a thread: all, unless that
-  // leaves the GPU short of threads.
+  // Lanes for a token: two pieces each. Heads for a thread: all of a rank's,
+  // unless that leaves the GPU short of threads; with few heads a rank, those
+  // of several ranks, so that at least 8 share the angles (which take as long
+  // as four heads).
+  k.R = R;
   k.lanes = (k.D / V + 1) / 2;
   k.tokens = 256 / k.lanes;
   const int all = k.heads[0] + k.heads[1] + k.heads[2];
-  const int64_t blocks = (k.rows + k.tokens - 1) / k.tokens * R;
-  int64_t cuts = (4 * FO_GB300_SMS + blocks - 1) / blocks;
+  const int64_t blocks = (k.rows + k.tokens - 1) / k.tokens;
+  const int64_t enough = 4 * FO_GB300_SMS;
+  k.ranks_each = 1;
+  while (k.ranks_each < R && k.ranks_each * all < 8 && blocks * R >= enough * k.ranks_each) k.ranks_each *= 2;
+  int64_t cuts = (enough + blocks * R - 1) / (blocks * R);
   if (cuts > (all + 3) / 4) cuts = (all + 3) / 4;
   k.heads_each = (int)((all + cuts - 1) / cuts);
-  const dim3 grid((unsigned)((k.rows + k.tokens - 1) / k.tokens), (unsigned)((all + k.heads_each - 1) / k.heads_each), R);
-  return launched(launch_after(rope_kernel<T, V, HALF>, grid, 256, 0, 0, s, k), "rope", R, k.rows, k.D, grid.x * grid.y, 256);
+  const dim3 grid((unsigned)blocks, (unsigned)((all + k.heads_each - 1) / k.heads_each),
+                  (unsigned)((R + k.ranks_each - 1) / k.ranks_each));
+  auto kern = k.ranks_each > 1 ? rope_kernel<T, V, HALF, true> : rope_kernel<T, V, HALF, false>;
+  return launched(launch_after(kern, grid, 256, 0, 0, s, k), "rope", R, k.rows, k.D, grid.x * grid.y, 256);
 }
 template <typename T>
 fo_status launch_with(RopeParams& k, int R, int v, cudaStream_t s) {

@@ -67,7 +67,7 @@ def product(dev, M, N, K, out, R=1, whole=False, seed=0):
 
 SHAPES = [(1, 1, 16), (1, 128, 128), (3, 7, 16), (16, 64, 256), (17, 200, 144), (64, 256, 512), (65, 129, 272), (100, 1000, 1744),
           (128, 128, 2048), (129, 384, 400), (256, 256, 1024), (300, 520, 640), (512, 96, 128), (5, 2048, 4096), (33, 130, 4112),
-          (1, 12288, 512), (200, 72, 7168), (1025, 40, 96), (2, 56, 14336), (260, 1100, 512), (3, 19500, 5120), (2000, 1500, 384), (513, 5000, 1040)]
+          (1, 12288, 512), (200, 72, 7168), (1025, 40, 96), (2, 56, 14336), (260, 1100, 512), (3, 19500, 5120), (2000, 1500, 384), (513, 5000, 1040), (2001, 1501, 384), (1900, 1502, 256), (1800, 2004, 128)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])

@@ -57,7 +57,7 @@ def check_8_bits(q, scale, n, rel, up=1):
 
 
 CASES = [(1, 1), (3, 7), (2, 128), (5, 129), (1, 4096), (7, 1000), (33, 256), (4, 2880), (3, 5120), (2, 8192), (3, 8200),
-         (2, 16384), (1, 32768), (2, 32767), (3, 1357), (300, 512), (1000, 64), (700, 1024)]
+         (2, 16384), (1, 32768), (2, 32767), (3, 1357), (300, 512), (1000, 64), (700, 1024), (4000, 128), (2500, 9), (400, 4096)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -212,7 +212,8 @@ def test_quant_rows(dev, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,cols", [(1, 1), (128, 128), (129, 257), (1000, 144), (384, 4096), (50, 1357), (300, 16)])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (128, 128), (129, 257), (1000, 144), (384, 4096), (50, 1357), (300, 16), (1001, 264), (131, 128), (2, 8),
+                                       (130, 1000)])
 @pytest.mark.parametrize("transposed", [False, True])
 def test_quant_blocks(dev, rows, cols, dtype, transposed):
     g = torch.Generator().manual_seed(rows + cols)

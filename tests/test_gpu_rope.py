@@ -116,3 +116,19 @@ def test_rope_leaves_what_lies_between_the_rows(dev):
     mid[2, [3, 19]] = 0
     mid[4, 40] = 0
     assert np.all(np.isfinite(mid))
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rope_many_ranks_of_few_heads(dev, layout):
+    # Threads that go through several ranks, the last of them through fewer.
+    R, rows, D = 5, 16001, 64
+    d = B.fo_rope_desc(D, 1, 1, R=R, layout=layout)
+    f, factor = O.rope_frequencies(D, 10000.0)
+    g = torch.Generator().manual_seed(4)
+    q, k = ([torch.randn(rows, D, generator=g).to(torch.bfloat16).to(dev) for _ in range(R)] for _ in range(2))
+    qo, ko = ([torch.full_like(t, float("nan")) for t in ts] for ts in (q, k))
+    B.fo_rope(d, rows, None, q, k, None, qo, ko, None)
+    at = np.arange(rows).astype(np.float64)
+    for r in range(R):
+        check(f64(qo[r]), f64(q[r]), at, f, factor, D, layout, "bf16", False)
+        check(f64(ko[r]), f64(k[r]), at, f, factor, D, layout, "bf16", False)

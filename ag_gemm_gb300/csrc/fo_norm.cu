@@ -2,6 +2,8 @@
 // with one scale for 128 columns, or both; and its gradient.
 #include <string.h>
 
+#include <type_traits>
+
 #include "fo_ops.h"
 
 namespace fo_ops {
@@ -27,7 +29,8 @@ struct NormParams {
 // wide access), else four that are 32 apart (each access still covers whole
 // sectors). Either way a group of 128 columns belongs to one warp, or to one
 // half of it, so its maximum never leaves the warp.
-template <typename T, bool WIDE>
+// FULL: the row is exactly the block's chunks, so no column is beyond it.
+template <typename T, bool WIDE, bool FULL>
 struct Chunk {
   static constexpr int E = WIDE ? Vec16<T>::N : 4;
   static constexpr int COLS = 32 * E;
@@ -39,32 +42,32 @@ struct Chunk {
     if constexpr (WIDE) {
       const int c = col(chunk, lane, 0);
       uint4 u = make_uint4(0, 0, 0, 0);
-      if (c < H) u = *reinterpret_cast<const uint4*>(p + c);
+      if (FULL || c < H) u = *reinterpret_cast<const uint4*>(p + c);
       Vec16<T>::unpack(u, f);
     } else {
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const int c = col(chunk, lane, j);
-        f[j] = c < H ? to_f(p[c]) : 0.f;
+        f[j] = FULL || c < H ? to_f(p[c]) : 0.f;
       }
     }
   }
   static __device__ __forceinline__ void store(T* p, int chunk, int lane, int H, const float (&f)[E]) {
     if constexpr (WIDE) {
       const int c = col(chunk, lane, 0);
-      if (c < H) *reinterpret_cast<uint4*>(p + c) = Vec16<T>::pack(f);
+      if (FULL || c < H) *reinterpret_cast<uint4*>(p + c) = Vec16<T>::pack(f);
     } else {
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const int c = col(chunk, lane, j);
-        if (c < H) from_f(f[j], p[c]);
+        if (FULL || c < H) from_f(f[j], p[c]);
       }
     }
   }
   static __device__ __forceinline__ void store_e4m3(uint8_t* p, int chunk, int lane, int H, const float (&f)[E]) {
     if constexpr (WIDE) {
       const int c = col(chunk, lane, 0);
-      if (c < H) {
+      if (FULL || c < H) {
         if constexpr (E == 8)
           *reinterpret_cast<uint2*>(p + c) = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
         else
@@ -74,7 +77,7 @@ struct Chunk {
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const int c = col(chunk, lane, j);
-        if (c < H) p[c] = (uint8_t)e4m3x2(f[j], 0.f);
+        if (FULL || c < H) p[c] = (uint8_t)e4m3x2(f[j], 0.f);
       }
     }
   }
@@ -86,7 +89,7 @@ struct Chunk {
       const int c = col(chunk, lane, 0);
 #pragma unroll
       for (int j = 0; j < E; ++j) f[j] = 0.f;
-      if (c < H) {
+      if (FULL || c < H) {
         if (f32) {
 #pragma unroll
           for (int j = 0; j < E; j += 4) {
@@ -110,7 +113,7 @@ struct Chunk {
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const int c = col(chunk, lane, j);
-        f[j] = c >= H ? 0.f
+        f[j] = !FULL && c >= H ? 0.f
                       : offset + (f32 ? static_cast<const float*>(w)[c]
                                       : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c]));
       }
@@ -134,9 +137,9 @@ __device__ __forceinline__ float block_sum(float v, float* smem) {
 // (Six blocks of 8 warps on an SM: 41.5 us for 8192 x 4096 bf16 with residual and
 // 8-bit output, 43 us with the five that the compiler's own choice of
 // registers leaves, 45 us with rows on 4 warps, 56 us with rows on 16.)
-template <typename T, bool WIDE, int NW, int C>
+template <typename T, bool WIDE, int NW, int C, bool FULL>
 __global__ void __launch_bounds__(NW * 32, NW == 8 ? 6 : NW == 16 ? (C <= 2 ? 3 : 2) : 1) rmsnorm_kernel(const __grid_constant__ NormParams p) {
-  using K = Chunk<T, WIDE>;
+  using K = Chunk<T, WIDE, FULL>;
   __shared__ float smem[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = blockIdx.y;
@@ -237,9 +240,9 @@ struct BwdCfg {
 // its own pieces, so that the loads go on through the two barriers of a row;
 // beyond, with up to 16 warps, this row's values; else nothing, and the second
 // pass over the row reads it again, from L2.
-template <typename T, bool WIDE, int NW, int C>
+template <typename T, bool WIDE, int NW, int C, bool FULL>
 __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
-  using K = Chunk<T, WIDE>;
+  using K = Chunk<T, WIDE, FULL>;
   using Cfg = BwdCfg<T, WIDE, NW, C>;
   constexpr int E = K::E;
   constexpr bool kAhead = Cfg::kAhead, kHold = Cfg::kHold;
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int col = K::col(c * NW + warp, lane, 0);
-        const bool in = col < p.H;
+        const bool in = FULL || col < p.H;
         const int64_t at = off + (in ? col : 0);
         copy16_async(to + c * NW * 32, static_cast<const T*>(p.dy[r]) + at, in);
         copy16_async(to + Cfg::kSlot + c * NW * 32, static_cast<const T*>(p.h[r]) + at, in);
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const int col = K::col(c * NW + warp, lane, j);
-        if (col < p.H) p.part[(int64_t)blockIdx.x * p.H + col] = dw[c][j];
+        if (FULL || col < p.H) p.part[(int64_t)blockIdx.x * p.H + col] = dw[c][j];
       }
   }
 }
@@ -402,21 +405,31 @@ int bwd_blocks(int64_t total, int nw) {
   return (int)(want < most ? want : most);
 }
 
-// Calls f.template operator()<T, WIDE, NW, C>() with the fewest warps whose
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// Calls f.template operator()<T, WIDE, NW, C, FULL>() with the fewest warps whose
 // chunks cover H: one chunk a lane while 8 warps suffice, then up to 32 warps
 // and up to 8 chunks.
 template <typename T, bool WIDE, typename F>
 fo_status by_width(int H, F&& f) {
-  const int n = (H + Chunk<T, WIDE>::COLS - 1) / Chunk<T, WIDE>::COLS;
-  if (n <= 1) return f.template operator()<T, WIDE, 1, 1>();
-  if (n <= 2) return f.template operator()<T, WIDE, 2, 1>();
-  if (n <= 4) return f.template operator()<T, WIDE, 4, 1>();
-  if (n <= 8) return f.template operator()<T, WIDE, 8, 1>();
-  if (n <= 16) return f.template operator()<T, WIDE, 8, 2>();
-  if (n <= 32) return f.template operator()<T, WIDE, 16, 2>();
-  if (n <= 64) return f.template operator()<T, WIDE, 16, 4>();
-  if (n <= 128) return f.template operator()<T, WIDE, 32, 4>();
-  if constexpr (Chunk<T, WIDE>::COLS * 128 < FO_NORM_MAX_H) return f.template operator()<T, WIDE, 32, 8>();
+  constexpr int kCols = Chunk<T, WIDE, false>::COLS;
+  const int n = (H + kCols - 1) / kCols;
+  auto go = [&](auto nw, auto c) -> fo_status {
+    constexpr int NW = decltype(nw)::value, C = decltype(c)::value;
+    if constexpr (WIDE)
+      if (H == NW * C * kCols) return f.template operator()<T, WIDE, NW, C, true>();
+    return f.template operator()<T, WIDE, NW, C, false>();
+  };
+  if (n <= 1) return go(Int<1>(), Int<1>());
+  if (n <= 2) return go(Int<2>(), Int<1>());
+  if (n <= 4) return go(Int<4>(), Int<1>());
+  if (n <= 8) return go(Int<8>(), Int<1>());
+  if (n <= 16) return go(Int<8>(), Int<2>());
+  if (n <= 32) return go(Int<16>(), Int<2>());
+  if (n <= 64) return go(Int<16>(), Int<4>());
+  if (n <= 128) return go(Int<32>(), Int<4>());
+  if constexpr (kCols * 128 < FO_NORM_MAX_H) return go(Int<32>(), Int<8>());
   return FO_ERR_SHAPE;
 }
 template <typename F>
@@ -429,10 +442,10 @@ struct LaunchFwd {
   const NormParams& k;
   cudaStream_t s;
   int R;
-  template <typename T, bool WIDE, int NW, int C>
+  template <typename T, bool WIDE, int NW, int C, bool FULL>
   fo_status operator()() const {
     const dim3 grid((unsigned)k.rows, R);
-    return launched(launch_after(rmsnorm_kernel<T, WIDE, NW, C>, grid, NW * 32, 0, 0, s, k), "rmsnorm", R, k.rows, k.H, (int)k.rows, NW * 32);
+    return launched(launch_after(rmsnorm_kernel<T, WIDE, NW, C, FULL>, grid, NW * 32, 0, 0, s, k), "rmsnorm", R, k.rows, k.H, (int)k.rows, NW * 32);
   }
 };
 struct LaunchBwd {
@@ -440,11 +453,11 @@ struct LaunchBwd {
   cudaStream_t s;
   int R;
   int* blocks;
-  template <typename T, bool WIDE, int NW, int C>
+  template <typename T, bool WIDE, int NW, int C, bool FULL>
   fo_status operator()() const {
     const int grid = *blocks = bwd_blocks(k.total, NW);
     constexpr int smem = BwdCfg<T, WIDE, NW, C>::kSmem;
-    auto kern = rmsnorm_bwd_kernel<T, WIDE, NW, C>;
+    auto kern = rmsnorm_bwd_kernel<T, WIDE, NW, C, FULL>;
     if (smem > 48 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return launched(e, "rmsnorm_bwd", R, k.rows, k.H, grid, NW * 32);

@@ -54,14 +54,16 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
 // first; a group's scale is the maximum over the 16 (bf16) or 32 lanes that
 // hold it. A piece never crosses a row (rows of whole groups are one long
 // row to this kernel).
-template <typename T>
+// ONE: there is one such long row and a warp for every kUnroll pieces.
+template <typename T, bool ONE>
 __global__ void __launch_bounds__(256) quant_rows_wide_kernel(const __grid_constant__ QuantParams p) {
   constexpr int E = Vec16<T>::N, kCols = 32 * E, kUnroll = 2, kLanes = FO_FP8_BLOCK / E;
   const int lane = threadIdx.x & 31, r = blockIdx.y;
-  const int64_t n = p.rows * p.pieces, step = (int64_t)gridDim.x * 8;
+  const int64_t n = p.rows * p.pieces, step = ONE ? 8 : (int64_t)gridDim.x * 8;
   grid_release();
   grid_wait();
-  for (int64_t w = blockIdx.x * 8ll + (threadIdx.x >> 5); w < n; w += step * kUnroll) {
+  for (int64_t w = (int64_t)blockIdx.x * (ONE ? 8 * kUnroll : 8) + (threadIdx.x >> 5);; w += step * kUnroll) {
+    if (!ONE && w >= n) break;
     uint4 raw[kUnroll];
     int64_t row[kUnroll];
     int col[kUnroll];
@@ -69,10 +71,10 @@ __global__ void __launch_bounds__(256) quant_rows_wide_kernel(const __grid_const
     for (int i = 0; i < kUnroll; ++i) {
       const int64_t u = w + i * step;
       // (A 64-bit division costs as much as the rest of a piece.)
-      row[i] = p.rows == 1 ? 0 : n <= UINT32_MAX ? (int64_t)((uint32_t)u / (uint32_t)p.pieces) : u / p.pieces;
+      row[i] = ONE || p.rows == 1 ? 0 : n <= UINT32_MAX ? (int64_t)((uint32_t)u / (uint32_t)p.pieces) : u / p.pieces;
       col[i] = (int)(u - row[i] * p.pieces) * kCols + lane * E;
       raw[i] = make_uint4(0, 0, 0, 0);
-      if (u < n && col[i] < p.cols)
+      if ((ONE || u < n) && col[i] < p.cols)
         raw[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.x[r]) + row[i] * p.cols + col[i]));
     }
 #pragma unroll
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(256) quant_rows_wide_kernel(const __grid_const
       float v[E];
       Vec16<T>::unpack(raw[i], v);
       const float scale = scale_of(lanes_max<kLanes>(amax_of(v))), inv = inverse_of(scale);
-      if (w + i * step >= n || col[i] >= p.cols) continue;
+      if ((!ONE && w + i * step >= n) || col[i] >= p.cols) continue;
 #pragma unroll
       for (int j = 0; j < E; ++j) v[j] *= inv;
       uint8_t* q = p.q[r] + row[i] * p.cols + col[i];
@@ -90,6 +92,7 @@ __global__ void __launch_bounds__(256) quant_rows_wide_kernel(const __grid_const
         *reinterpret_cast<uint32_t*>(q) = e4m3x4(v[0], v[1], v[2], v[3]);
       if (lane % kLanes == 0) p.scale[r][row[i] * p.groups + col[i] / FO_FP8_BLOCK] = scale;
     }
+    if (ONE) break;
   }
 }
 
@@ -319,8 +322,12 @@ extern "C" fo_status fo_quant_fp8(int32_t R, int64_t rows, int64_t cols, int32_t
     // A warp for two pieces (20.0 us for 8192 x 4096 bf16; four: 21.2, eight:
     // 21.7), few pieces: a warp each.
     const int64_t n = k.rows * k.pieces, want = n >= 4096 ? (n + 15) / 16 : (n + 7) / 8;
-    const dim3 grid((unsigned)(want < 65536 ? want : 65536), R);
-    e = launch_after(bf16 ? quant_rows_wide_kernel<__nv_bfloat16> : quant_rows_wide_kernel<float>, grid, 256, 0, 0, s, k);
+    const bool one = k.rows == 1 && n >= 4096;
+    const dim3 grid((unsigned)(one || want < 65536 ? want : 65536), R);
+    void (*kern)(const QuantParams) =
+        one ? (bf16 ? quant_rows_wide_kernel<__nv_bfloat16, true> : quant_rows_wide_kernel<float, true>)
+            : (bf16 ? quant_rows_wide_kernel<__nv_bfloat16, false> : quant_rows_wide_kernel<float, false>);
+    e = launch_after(kern, grid, 256, 0, 0, s, k);
     return launched(e, "quant_rows wide", R, rows, cols, grid.x, 256);
   }
   const dim3 grid(k.groups, k.row_blocks, R);

@@ -69,6 +69,9 @@ union Piece {
 // copy the head's rest, two pieces each. Heads of V: pieces i and i + lanes.
 // V is the widest access that the sizes, strides and addresses allow (at
 // least a pair where pairs are neighbours).
+// Eight ranks' packed rows of 8192 x 12 heads of 128, bf16 (403 MB): 62 us,
+// 6.5 TB/s; with V's heads in a loop of their own, two loads at a time, and
+// 98 registers 101 us, one element at a time 193 us.
 template <typename T, int V, bool HALF, bool RANKS>
 __global__ void __launch_bounds__(256, 3) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kHeads = 4;

@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
     float a_next = 0.f, w_next = 0.f;
     if (unit < total) {
       scales_of(unit);
-      a_next = __ldg(sa), w_next = __ldg(sw);
+      a_next = load1(sa), w_next = load1(sw);
     }
     for (int L = unit; L < total && ok; L += units) {
       f32x2 acc[64];
@@ -442,10 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
         const float s = a_next * w_next;
         const f32x2 s2 = pair_of(s, s);
         if (kb + 1 < p.kblocks) {
-          a_next = __ldg(sa + kb + 1), w_next = __ldg(sw + kb + 1);
+          a_next = load1(sa + kb + 1), w_next = load1(sw + kb + 1);
         } else if (L + units < total) {
           scales_of(L + units);
-          a_next = __ldg(sa), w_next = __ldg(sw);
+          a_next = load1(sa), w_next = load1(sw);
         }
         const uint32_t b = it & 1u;
         if (!wait_bar(tfull_bar(b), (it >> 1) & 1u, abort_flag)) {
@@ -650,11 +650,11 @@ __global__ void __launch_bounds__(kThreads) gemm_fp8_narrow_kernel(const __grid_
     auto load_scales = [&](int first) {
       const int kb = kb0 + first + lane;
       const bool in = kb < kb1;
-      const float w = in ? __ldg(p.sW[r] + (int64_t)nb * p.kblocks + kb) : 0.f;
+      const float w = in ? load1(p.sW[r] + (int64_t)nb * p.kblocks + kb) : 0.f;
       const float* sa = p.sA[r] + (int64_t)m0 * p.kblocks + kb;
 #pragma unroll
       for (int c = warp - 2; c < TN; c += 4)
-        sScale[lane * C::kScaleLd + c] = in && c < rows ? w * __ldg(sa + (int64_t)c * p.kblocks) : 0.f;
+        sScale[lane * C::kScaleLd + c] = in && c < rows ? w * load1(sa + (int64_t)c * p.kblocks) : 0.f;
       asm volatile("bar.sync 1, 128;" ::: "memory");
     };
 #pragma unroll

@@ -100,13 +100,13 @@ struct Chunk {
         if (f32) {
 #pragma unroll
           for (int j = 0; j < E; j += 4) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + j));
+            const float4 v = load4(static_cast<const float*>(w) + c + j);
             f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
           }
         } else {
 #pragma unroll
           for (int j = 0; j < E; j += 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + c + j));
+            const uint2 v = load4(static_cast<const __nv_bfloat16*>(w) + c + j);
             f[j] = __uint_as_float(v.x << 16), f[j + 1] = __uint_as_float(v.x & 0xffff0000u);
             f[j + 2] = __uint_as_float(v.y << 16), f[j + 3] = __uint_as_float(v.y & 0xffff0000u);
           }

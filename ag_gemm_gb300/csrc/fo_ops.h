@@ -89,6 +89,25 @@ __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.la
 // access to global memory of every thread.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Loads of values that may be used again. (The read-only path, __ldg, is for
+// what nobody writes while the kernel exists; a kernel that starts before the
+// one ahead of it has ended exists while its inputs are written.)
+__device__ __forceinline__ float load1(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 load4(const float* p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 load4(const __nv_bfloat16* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
 constexpr float kE4M3Top = 448.f;
 constexpr float kLeastScale = 1.17549435e-38f;   // 2^-126
 

@@ -247,3 +247,20 @@ def test_quant_special_values(dev, block_rows):
     if block_rows == 1:
         assert scale[3, 0] == 2.0 ** -126
     assert np.all(np.isfinite(q[:128])) and np.all(np.isfinite(scale[at(127)]))
+
+
+@pytest.mark.parametrize("at_q,at_t", [(0, 0), (8, 0), (0, 8), (8, 1), (1, 16), (0, 3)])
+@pytest.mark.parametrize("rows,cols", [(272, 144), (16, 128), (400, 1040), (264, 256)])
+def test_quant_blocks_outputs_off_the_wide_grid(dev, rows, cols, at_q, at_t):
+    """The widths of the stores go by where rows and the copy's lines start; nothing beside them is touched."""
+    g = torch.Generator().manual_seed(at_q + at_t)
+    x = draw(g, rows, cols, "bf16", dev, 0.02)
+    n, pad = rows * cols, 32
+    qs, ts = (torch.full((n + 2 * pad,), 85, dtype=torch.uint8, device=dev) for _ in range(2))
+    q, qt = qs[pad + at_q:][:n].view(rows, cols), ts[pad + at_t:][:n].view(cols, rows)
+    scale, st = empty(dev, -(-rows // 128), -(-cols // 128)), empty(dev, -(-cols // 128), -(-rows // 128))
+    B.fo_quant_fp8(rows, cols, [x], [q], [scale], [qt], [st], block_rows=128)
+    check_8_bits(q.view(E4M3), scale, f64(x), 2 * U, up=128)
+    assert torch.equal(qt, q.t()) and torch.equal(st, scale.t())
+    for buf, at in ((qs, at_q), (ts, at_t)):
+        assert (buf[:pad + at] == 85).all() and (buf[pad + at + n:] == 85).all()

@@ -411,19 +411,18 @@ _marshal = None
 
 
 def _native():
-    """The marshalling module (csrc/fo_marshal.c): makes a call whose arguments are right and returns its status, or
+    """The marshalling module (csrc/fo_marshal.cpp): makes a call whose arguments are right and returns its status, or
     returns -1 and leaves it to the code below, which says what is wrong."""
     global _marshal
     if _marshal is None:
         import importlib.machinery
         import importlib.util
-        import torch
+        import torch  # noqa: F401  (whose libraries the module is linked to)
         load()
         path = os.path.join(_PKG, "_build", "_fo_marshal.so")
         loader = importlib.machinery.ExtensionFileLoader("_fo_marshal", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_fo_marshal", path, loader=loader))
         loader.exec_module(module)
-        module.setup(torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.uint8, torch.int32, torch.int64)
         _marshal = module
     return _marshal
 
@@ -492,10 +491,11 @@ def fo_rmsnorm(desc: NormDesc, rows: int, x, residual, weight, h=None, y=None, q
                stream=None) -> None:
     """x, residual, h, y [rows, H], q [rows, H] in 8 bits, scale [rows, ceil(H/128)], rstd [rows]: one tensor for each
     shard; all but x and weight may be None (see the header for what is computed)."""
-    stream = _stream(stream)
     code = (_marshal or _native()).rmsnorm(desc, rows, x, residual, weight, h, y, q, scale, rstd, stream)
-    if code >= 0:
-        return _check(code, "fo_rmsnorm")
+    if code == FO_OK:
+        return
+    if code > 0:
+        _check(code, "fo_rmsnorm")
     R, H, t = desc.R, desc.H, _types()
     n, types = rows * H, t[desc.dtype]
     groups = rows * -(-H // FO_FP8_BLOCK)
@@ -515,10 +515,11 @@ def fo_rmsnorm_bwd_workspace(desc: NormDesc, rows: int) -> int:
 
 def fo_rmsnorm_bwd(desc: NormDesc, rows: int, dy, dh, h, weight, rstd, dx, dweight=None, ws=None, stream=None) -> None:
     """dy, dh (may be None), h, dx [rows, H] and rstd [rows]: one tensor for each shard; dweight [H] fp32 or None."""
-    stream = _stream(stream)
     code = (_marshal or _native()).rmsnorm_bwd(desc, rows, dy, dh, h, weight, rstd, dx, dweight, ws, stream)
-    if code >= 0:
-        return _check(code, "fo_rmsnorm_bwd")
+    if code == FO_OK:
+        return
+    if code > 0:
+        _check(code, "fo_rmsnorm_bwd")
     R, H, t = desc.R, desc.H, _types()
     n, types = rows * H, t[desc.dtype]
     if ws is not None and not isinstance(ws, int) and ws.numel() * ws.element_size() < fo_rmsnorm_bwd_workspace(desc, rows):
@@ -540,10 +541,11 @@ def fo_quant_fp8(rows: int, cols: int, x, q, scale, qt=None, scale_t=None, *, bl
     if dtype is None:
         dtype = "bf16" if x[0].dtype in t[0] else "f32"
     R, code = len(x), DTYPES[dtype]
-    stream = _stream(stream)
     status = (_marshal or _native()).quant_fp8(rows, cols, code, block_rows, x, q, scale, qt, scale_t, stream)
-    if status >= 0:
-        return _check(status, "fo_quant_fp8")
+    if status == FO_OK:
+        return
+    if status > 0:
+        _check(status, "fo_quant_fp8")
     up, across = (-(-rows // block_rows) if block_rows > 0 else 0), -(-cols // FO_FP8_BLOCK)
     _check(load().fo_quant_fp8(R, rows, cols, code, block_rows, _addresses(x, R, rows * cols, t[code], "x"),
                                _addresses(q, R, rows * cols, t["q"], "q"),
@@ -568,10 +570,11 @@ def fo_gemm_fp8_workspace(desc: GemmFp8Desc, M: int) -> int:
 def fo_gemm_fp8(desc: GemmFp8Desc, M: int, A, sA, W, sW, Y, ws, stream=None) -> None:
     """Y_r [M, N] = (A_r scaled by sA_r) (W_r scaled by sW_r)^T: A [M, K] and W [N, K] in 8 bits, sA [M, ceil(K/128)],
     sW [ceil(N/128), ceil(K/128)]; one tensor for each rank."""
-    stream = _stream(stream)
     code = (_marshal or _native()).gemm_fp8(desc, M, A, sA, W, sW, Y, ws, stream)
-    if code >= 0:
-        return _check(code, "fo_gemm_fp8")
+    if code == FO_OK:
+        return
+    if code > 0:
+        _check(code, "fo_gemm_fp8")
     R, N, K, t = desc.R, desc.N, desc.K, _types()
     k = -(-K // FO_FP8_BLOCK)
     if not isinstance(ws, int) and ws.numel() * ws.element_size() < fo_gemm_fp8_workspace(desc, M):
@@ -644,10 +647,11 @@ def fo_rope(desc: RopeDesc, rows: int, positions, q_in, k_in, v_in, q_out, k_out
     """Turn Q and K by their positions ([rows] int32 or int64, None: 0, 1, ...) and copy V; one matrix [rows, heads *
     head_dim] for each rank, whose rows may be parts of packed ones; k_*, v_* are not looked at without heads of
     their kind. inverse: turn back (the gradient)."""
-    stream = _stream(stream)
     code = (_marshal or _native()).rope(desc, rows, positions, q_in, k_in, v_in, q_out, k_out, v_out, inverse, stream)
-    if code >= 0:
-        return _check(code, "fo_rope")
+    if code == FO_OK:
+        return
+    if code > 0:
+        _check(code, "fo_rope")
     types = _types()[desc.dtype]
     D, R = desc.head_dim, desc.R
     ins, outs, ld_in, ld_out = [], [], (c_int64 * 3)(), (c_int64 * 3)()

@@ -6,6 +6,7 @@ CUDA runtime linked statically. Nothing is written outside the package.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -59,29 +60,52 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             sys.stderr.write(res.stdout + res.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_compile_marshal, nvcc)
         objs = list(ex.map(compile_one, SOURCES))
+        marshal_obj = marshal.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
-    _build_marshal()
+    _link_marshal(marshal_obj)
     return LIB
 
 
-def _build_marshal() -> None:
-    """The operators' argument marshalling, a CPython module linked to the library beside it."""
-    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
-    if not cc:
-        raise RuntimeError("no C compiler found for the argument marshalling module")
-    tmp = MARSHAL + ".tmp"
-    cmd = [cc, "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
-           os.path.join(CSRC, "fo_marshal.c"), "-o", tmp, "-L", BUILD, "-lflashoverlap", "-Wl,-rpath,$ORIGIN"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        raise RuntimeError("torch not found: the argument marshalling module is compiled with its headers")
+    return os.path.dirname(spec.origin)
+
+
+def _cxx(cmd, what: str) -> None:
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler found for the argument marshalling module")
+    res = subprocess.run([cxx] + cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"building {MARSHAL} failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+        raise RuntimeError(f"{what} failed:\n{' '.join([cxx] + cmd)}\n{res.stdout}\n{res.stderr}")
+
+
+def _compile_marshal(nvcc: str) -> str:
+    """The operators' argument marshalling, a CPython module that reads torch's tensors directly."""
+    obj, torch_include = os.path.join(BUILD, "fo_marshal.o"), os.path.join(_torch_dir(), "include")
+    cuda_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    includes = [torch_include, os.path.join(torch_include, "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], cuda_include, INCLUDE]
+    _cxx(["-O2", "-std=c++17", "-fPIC"] + [f"-I{d}" for d in includes] +
+         ["-c", os.path.join(CSRC, "fo_marshal.cpp"), "-o", obj], "compiling the argument marshalling")
+    return obj
+
+
+def _link_marshal(obj: str) -> None:
+    """Link it to the library beside it and to torch's (loaded with torch, which comes first)."""
+    tmp = MARSHAL + ".tmp"
+    _cxx(["-shared", obj, "-o", tmp, "-L", BUILD, "-lflashoverlap", "-L", os.path.join(_torch_dir(), "lib"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], "linking the argument marshalling")
     os.replace(tmp, MARSHAL)
 
 

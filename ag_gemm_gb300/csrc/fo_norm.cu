@@ -128,18 +128,25 @@ struct Chunk {
   }
 };
 
-// Sum over the block's NW warps, the same in every thread. `smem`: NW floats.
+// Sum over the block's nw <= NW warps, the same in every thread. `smem`: nw floats.
 template <int NW>
-__device__ __forceinline__ float block_sum(float v, float* smem) {
+__device__ __forceinline__ float block_sum(float v, float* smem, int nw) {
   v = warp_sum(v);
   if constexpr (NW == 1) return v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) smem[warp] = v;
   __syncthreads();
-  v = warp_sum(lane < NW ? smem[lane] : 0.f);
+  v = warp_sum(lane < nw ? smem[lane] : 0.f);
   __syncthreads();
   return v;
 }
+
+// Blocks have no more warps than their row needs (8191 x 4098 bf16, 33 chunks
+// of 4 a thread: 78 us with 9 warps, 114 with 16; 8191 x 1280: 12.9 us with 5,
+// 18.2 with 8), but for the widest rows, where the number of warps would be one
+// register too many (2000 x 20001: 130 us with 32 warps, 240 with 20).
+template <int NW, int C>
+constexpr bool kAllWarps = NW == 32 && C == 8;
 
 // 8192 x 4096 bf16 with residual and 8-bit output (236 MB): 39.8 us, 5.9 TB/s.
 // Two thirds of the issue slots are taken, so instructions count: no 64-bit
@@ -151,6 +158,7 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 6 : NW == 16 ? (C <= 2 ? 3 
   using K = Chunk<T, WIDE, FULL>;
   __shared__ float smem[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nw = FULL || kAllWarps<NW, C> ? NW : (int)blockDim.x >> 5;
   const int r = blockIdx.y;
   grid_release();
   grid_wait();
@@ -159,12 +167,12 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 6 : NW == 16 ? (C <= 2 ? 3 
     float s[C][K::E];
     float sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) K::load(static_cast<const T*>(p.x[r]) + off, c * NW + warp, lane, p.H, s[c]);
+    for (int c = 0; c < C; ++c) K::load(static_cast<const T*>(p.x[r]) + off, c * nw + warp, lane, p.H, s[c]);
     if (p.has_res) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         float t[K::E];
-        K::load(static_cast<const T*>(p.res[r]) + off, c * NW + warp, lane, p.H, t);
+        K::load(static_cast<const T*>(p.res[r]) + off, c * nw + warp, lane, p.H, t);
 #pragma unroll
         for (int j = 0; j < K::E; ++j) s[c][j] += t[j];
       }
@@ -176,14 +184,14 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 6 : NW == 16 ? (C <= 2 ? 3 
     }
     if (p.has_h) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) K::store(static_cast<T*>(p.h[r]) + off, c * NW + warp, lane, p.H, s[c]);
+      for (int c = 0; c < C; ++c) K::store(static_cast<T*>(p.h[r]) + off, c * nw + warp, lane, p.H, s[c]);
     }
-    const float rstd = rsqrtf(fmaf(block_sum<NW>(sum, smem), p.inv_H, p.eps));
+    const float rstd = rsqrtf(fmaf(block_sum<NW>(sum, smem, nw), p.inv_H, p.eps));
     if (p.has_rstd && threadIdx.x == 0) p.rstd[r][at] = rstd;
     if (!p.has_y && !p.has_q) continue;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int chunk = c * NW + warp;
+      const int chunk = c * nw + warp;
       float w[K::E];
       K::load_w(p.w, p.w_f32, p.w_offset, chunk, lane, p.H, w);
 #pragma unroll
@@ -238,11 +246,14 @@ struct BwdCfg {
   // A thread's part of a row is at most 32 bytes of each input.
   static constexpr bool kAhead = WIDE && C <= 2;
   static constexpr bool kHold = kAhead || NW <= 16;
-  static constexpr int kSlot = NW * 32 * C;   // 16-byte pieces of one input's row
-  static constexpr int kSmem = kAhead ? kAheadRows * 3 * kSlot * 16 : 0;
+  // 16-byte pieces of one input's row, and the bytes of all, with nw warps.
+  static constexpr __host__ __device__ int slot(int nw) { return nw * 32 * C; }
+  static constexpr int smem(int nw) { return kAhead ? kAheadRows * 3 * slot(nw) * 16 : 0; }
 };
 
-// A block takes every gridDim.x-th row and keeps its columns' share of the
+// Where rows come ahead, blocks have no more warps than their row needs, and as
+// many blocks an SM as make up sixteen warps (8191 x 1280 bf16: 24.8 us with
+// 5 warps, 30.9 with 8). A block takes every gridDim.x-th row and keeps its columns' share of the
 // weight's gradient in registers. What else it keeps goes by the registers
 // that a thread's part of a row takes: where it is 32 bytes or less, the
 // weights too, and the next three rows come in the background, each thread
@@ -261,12 +272,13 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
   __shared__ float smem[32];
   extern __shared__ uint4 ring[];   // kAhead: [row % kAheadRows][input][chunk][thread]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nw = FULL || !kAhead ? NW : (int)blockDim.x >> 5;
   grid_release();
   grid_wait();
   float w[kAhead ? C : 1][E], dw[C][E];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    if constexpr (kAhead) K::load_w(p.w, p.w_f32, p.w_offset, c * NW + warp, lane, p.H, w[c]);
+    if constexpr (kAhead) K::load_w(p.w, p.w_f32, p.w_offset, c * nw + warp, lane, p.H, w[c]);
 #pragma unroll
     for (int j = 0; j < E; ++j) dw[c][j] = 0.f;
   }
@@ -278,21 +290,21 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
     if (row < p.total) {
       const int r = rank_of(row);
       const int64_t off = (row - r * p.rows) * p.H;
-      uint4* const to = ring + slot * 3 * Cfg::kSlot + threadIdx.x;
+      uint4* const to = ring + slot * 3 * Cfg::slot(nw) + threadIdx.x;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int col = K::col(c * NW + warp, lane, 0);
+        const int col = K::col(c * nw + warp, lane, 0);
         const bool in = FULL || col < p.H;
         const int64_t at = off + (in ? col : 0);
-        copy16_async(to + c * NW * 32, static_cast<const T*>(p.dy[r]) + at, in);
-        copy16_async(to + Cfg::kSlot + c * NW * 32, static_cast<const T*>(p.h[r]) + at, in);
-        if (p.has_dh) copy16_async(to + 2 * Cfg::kSlot + c * NW * 32, static_cast<const T*>(p.dh[r]) + at, in);
+        copy16_async(to + c * nw * 32, static_cast<const T*>(p.dy[r]) + at, in);
+        copy16_async(to + Cfg::slot(nw) + c * nw * 32, static_cast<const T*>(p.h[r]) + at, in);
+        if (p.has_dh) copy16_async(to + 2 * Cfg::slot(nw) + c * nw * 32, static_cast<const T*>(p.dh[r]) + at, in);
       }
     }
     copies_end();   // a group for every row, empty ones too: the waits count them
   };
   auto piece = [&](int slot, int input, int c, float (&v)[E]) {
-    if constexpr (kAhead) Vec16<T>::unpack(ring[(slot * 3 + input) * Cfg::kSlot + c * NW * 32 + threadIdx.x], v);
+    if constexpr (kAhead) Vec16<T>::unpack(ring[(slot * 3 + input) * Cfg::slot(nw) + c * nw * 32 + threadIdx.x], v);
   };
   if constexpr (kAhead) {
 #pragma unroll
@@ -321,9 +333,9 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
         piece(slot, 0, c, uc);
         piece(slot, 1, c, hc);
       } else {
-        K::load(dy, c * NW + warp, lane, p.H, uc);
-        K::load(hp, c * NW + warp, lane, p.H, hc);
-        K::load_w(p.w, p.w_f32, p.w_offset, c * NW + warp, lane, p.H, w[0]);
+        K::load(dy, c * nw + warp, lane, p.H, uc);
+        K::load(hp, c * nw + warp, lane, p.H, hc);
+        K::load_w(p.w, p.w_f32, p.w_offset, c * nw + warp, lane, p.H, w[0]);
       }
 #pragma unroll
       for (int j = 0; j < E; ++j) {
@@ -332,15 +344,15 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
         sum = fmaf(uc[j], hc[j], sum);
       }
     }
-    const float k = block_sum<NW>(sum, smem) * p.inv_H * rstd * rstd * rstd;
+    const float k = block_sum<NW>(sum, smem, nw) * p.inv_H * rstd * rstd * rstd;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float(&uc)[E] = u[kHold ? c : 0];
       float(&hc)[E] = h[kHold ? c : 0];
       if constexpr (!kHold) {
-        K::load(dy, c * NW + warp, lane, p.H, uc);
-        K::load(hp, c * NW + warp, lane, p.H, hc);
-        K::load_w(p.w, p.w_f32, p.w_offset, c * NW + warp, lane, p.H, w[0]);
+        K::load(dy, c * nw + warp, lane, p.H, uc);
+        K::load(hp, c * nw + warp, lane, p.H, hc);
+        K::load_w(p.w, p.w_f32, p.w_offset, c * nw + warp, lane, p.H, w[0]);
 #pragma unroll
         for (int j = 0; j < E; ++j) uc[j] *= w[0][j];
       }
@@ -350,11 +362,11 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
       if (p.has_dh) {
         float t[E];
         if constexpr (kAhead) piece(slot, 2, c, t);
-        else K::load(static_cast<const T*>(p.dh[r]) + off, c * NW + warp, lane, p.H, t);
+        else K::load(static_cast<const T*>(p.dh[r]) + off, c * nw + warp, lane, p.H, t);
 #pragma unroll
         for (int j = 0; j < E; ++j) d[j] += t[j];
       }
-      K::store(static_cast<T*>(p.dx[r]) + off, c * NW + warp, lane, p.H, d);
+      K::store(static_cast<T*>(p.dx[r]) + off, c * nw + warp, lane, p.H, d);
     }
     slot = slot + 1 == kAheadRows ? 0 : slot + 1;
   }
@@ -363,7 +375,7 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const int col = K::col(c * NW + warp, lane, j);
+        const int col = K::col(c * nw + warp, lane, j);
         if (FULL || col < p.H) p.part[(int64_t)blockIdx.x * p.H + col] = dw[c][j];
       }
   }
@@ -405,8 +417,11 @@ fo_status check_desc(const fo_norm_desc* d, int64_t rows) {
 
 size_t elem(int32_t dtype) { return dtype == FO_BF16 ? 2 : 4; }
 
-// Warps of a block for rows of n chunks (by_width's choice).
-int warps_for(int n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 16 ? 8 : n <= 64 ? 16 : 32; }
+// Chunks of a thread for rows of n chunks, the warps that cover them, and
+// the warps that a kernel is compiled for.
+int chunks_for(int n) { return n <= 8 ? 1 : n <= 32 ? 2 : n <= 128 ? 4 : 8; }
+int warps_for(int n) { return (n + chunks_for(n) - 1) / chunks_for(n); }
+int most_warps(int n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 16 ? 8 : n <= 64 ? 16 : 32; }
 // Blocks of the backward pass (its partial sums are one row each).
 // At least four rows each where that leaves a block for every SM: more
 // blocks' partial sums would cost more than the rows (2529 x 128: 9.5 us with
@@ -420,9 +435,9 @@ int bwd_blocks(int64_t total, int nw) {
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// Calls f.template operator()<T, WIDE, NW, C, FULL>() with the fewest warps whose
-// chunks cover H: one chunk a lane while 8 warps suffice, then up to 32 warps
-// and up to 8 chunks.
+// Calls f.template operator()<T, WIDE, NW, C, FULL>(n) for rows of n chunks:
+// one chunk a thread while 8 warps suffice, then up to 32 warps and up to 8
+// chunks.
 template <typename T, bool WIDE, typename F>
 fo_status by_width(int H, F&& f) {
   constexpr int kCols = Chunk<T, WIDE, false>::COLS;
@@ -430,8 +445,8 @@ fo_status by_width(int H, F&& f) {
   auto go = [&](auto nw, auto c) -> fo_status {
     constexpr int NW = decltype(nw)::value, C = decltype(c)::value;
     if constexpr (WIDE)
-      if (H == NW * C * kCols) return f.template operator()<T, WIDE, NW, C, true>();
-    return f.template operator()<T, WIDE, NW, C, false>();
+      if (H == NW * C * kCols) return f.template operator()<T, WIDE, NW, C, true>(n);
+    return f.template operator()<T, WIDE, NW, C, false>(n);
   };
   if (n <= 1) return go(Int<1>(), Int<1>());
   if (n <= 2) return go(Int<2>(), Int<1>());
@@ -455,9 +470,10 @@ struct LaunchFwd {
   cudaStream_t s;
   int R;
   template <typename T, bool WIDE, int NW, int C, bool FULL>
-  fo_status operator()() const {
+  fo_status operator()(int n) const {
+    const int nw = kAllWarps<NW, C> ? NW : warps_for(n);
     const dim3 grid((unsigned)k.rows, R);
-    return launched(launch_after(rmsnorm_kernel<T, WIDE, NW, C, FULL>, grid, NW * 32, 0, 0, s, k), "rmsnorm", R, k.rows, k.H, (int)k.rows, NW * 32);
+    return launched(launch_after(rmsnorm_kernel<T, WIDE, NW, C, FULL>, grid, nw * 32, 0, 0, s, k), "rmsnorm", R, k.rows, k.H, (int)k.rows, nw * 32);
   }
 };
 struct LaunchBwd {
@@ -466,15 +482,16 @@ struct LaunchBwd {
   int R;
   int* blocks;
   template <typename T, bool WIDE, int NW, int C, bool FULL>
-  fo_status operator()() const {
-    const int grid = *blocks = bwd_blocks(k.total, NW);
-    constexpr int smem = BwdCfg<T, WIDE, NW, C>::kSmem;
+  fo_status operator()(int n) const {
+    const int nw = BwdCfg<T, WIDE, NW, C>::kAhead ? warps_for(n) : NW;
+    const int grid = *blocks = bwd_blocks(k.total, nw);
+    const int smem = BwdCfg<T, WIDE, NW, C>::smem(nw);
     auto kern = rmsnorm_bwd_kernel<T, WIDE, NW, C, FULL>;
     if (smem > 48 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return launched(e, "rmsnorm_bwd", R, k.rows, k.H, grid, NW * 32);
+      if (e != cudaSuccess) return launched(e, "rmsnorm_bwd", R, k.rows, k.H, grid, nw * 32);
     }
-    return launched(launch_after(kern, dim3(grid), NW * 32, smem, 0, s, k), "rmsnorm_bwd", R, k.rows, k.H, grid, NW * 32);
+    return launched(launch_after(kern, dim3(grid), nw * 32, smem, 0, s, k), "rmsnorm_bwd", R, k.rows, k.H, grid, nw * 32);
   }
 };
 
@@ -534,10 +551,15 @@ extern "C" fo_status fo_rmsnorm_bwd_workspace(const fo_norm_desc* d, int64_t row
   const fo_status st = check_desc(d, rows);
   if (st) return st;
   if (!bytes) return FO_ERR_INVALID_ARG;
-  // With 16-byte alignment a chunk is wider and the warps are fewer, so the
-  // blocks are more: enough for either.
-  const int cols = d->dtype == FO_BF16 ? 256 : 128;
-  const size_t n = (size_t)bwd_blocks(rows * d->R, warps_for((d->H + cols - 1) / cols)) * (size_t)d->H * sizeof(float);
+  // Enough for rows on the 16-byte grid (chunks of 256 or 128 columns, maybe on
+  // fewer warps than the kernel's most) and off it (of 128).
+  const int cols = d->dtype == FO_BF16 ? 256 : 128, chunks = (d->H + cols - 1) / cols;
+  const int warps[3] = {warps_for(chunks), most_warps(chunks), most_warps((d->H + 127) / 128)};
+  size_t n = 0;
+  for (const int w : warps) {
+    const size_t b = (size_t)bwd_blocks(rows * d->R, w) * (size_t)d->H * sizeof(float);
+    n = b > n ? b : n;
+  }
   *bytes = n ? n : 16;
   return FO_OK;
 }

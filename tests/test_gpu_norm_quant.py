@@ -264,3 +264,42 @@ def test_quant_blocks_outputs_off_the_wide_grid(dev, rows, cols, at_q, at_t):
     assert torch.equal(qt, q.t()) and torch.equal(st, scale.t())
     for buf, at in ((qs, at_q), (ts, at_t)):
         assert (buf[:pad + at] == 85).all() and (buf[pad + at + n:] == 85).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("at", [0, 1, 3, 6])
+@pytest.mark.parametrize("rows,H", [(1, 1), (3, 5), (5, 257), (2, 255), (7, 1357), (3, 2050), (2, 4099), (2, 8193), (1, 20001)])
+def test_norm_of_rows_that_start_anywhere(dev, rows, H, at, dtype):
+    """Rows off the 16-byte grid, from any element of a larger buffer: the values of rows on it, forward and backward,
+    and nothing beside the outputs is touched."""
+    g = torch.Generator().manual_seed(rows + H + at)
+    T, n, pad = TYPES[dtype], rows * H, 40
+    d = B.fo_norm_desc(H, dtype=dtype)
+
+    def inside(t):
+        buf = torch.full((t.numel() + 2 * pad,), 7, dtype=t.dtype, device=dev)
+        buf[pad + at:][:t.numel()] = t.reshape(-1)
+        return buf, buf[pad + at:][:t.numel()].view(t.shape)
+
+    x, res, dy, dh = (torch.randn(rows, H, generator=g).to(T).to(dev) for _ in range(4))
+    w = (1 + torch.randn(H, generator=g)).to(T).to(dev)
+    outs = {k: torch.zeros(rows, H, dtype=T, device=dev) for k in ("h", "y", "dx")}
+    q, s, r = torch.zeros(rows, H, dtype=torch.uint8, device=dev), empty(dev, rows, -(-H // 128)), empty(dev, rows)
+    dw, ws = empty(dev, H), torch.empty(B.fo_rmsnorm_bwd_workspace(d, rows), dtype=torch.uint8, device=dev)
+    moved = {k: inside(v) for k, v in dict(outs, x=x, res=res, dy=dy, dh=dh, w=w, q=q).items()}
+    m = {k: v[1] for k, v in moved.items()}
+    B.fo_rmsnorm(d, rows, [m["x"]], [m["res"]], m["w"], [m["h"]], [m["y"]], [m["q"]], [s], [r])
+    want_s, want_n, want_r = O.rmsnorm(f64(x), f64(res), f64(w), 1e-6)
+    half = torch.finfo(T).eps / 2
+    assert np.all(np.abs(f64(m["h"]) - want_s) <= (half + U) * np.abs(want_s))
+    assert np.all(np.abs(f64(r) - want_r) <= 44 * U * want_r)
+    assert np.all(np.abs(f64(m["y"]) - want_n) <= (half + 48 * U) * np.abs(want_n) * (1 + 2.0 ** -7))
+    check_8_bits(m["q"].view(E4M3), s, want_n, 48 * U)
+    B.fo_rmsnorm_bwd(d, rows, [m["dy"]], [m["dh"]], [m["h"]], m["w"], [r], [m["dx"]], dw, ws)
+    hh, rr = m["h"].clone(), r.clone()
+    dx2, dw2 = torch.zeros(rows, H, dtype=T, device=dev), empty(dev, H)
+    B.fo_rmsnorm_bwd(d, rows, [dy], [dh], [hh], w, [rr], [dx2], dw2, ws)
+    assert torch.equal(m["dx"], dx2) and torch.equal(dw, dw2)
+    for k in ("h", "y", "dx", "q"):
+        buf, t = moved[k]
+        assert (buf[:pad + at] == 7).all() and (buf[pad + at + t.numel():] == 7).all()

@@ -31,19 +31,21 @@ struct NormParams {
   bool has_res, has_h, has_y, has_q, has_rstd, w_f32;
 };
 
-// Where a thread's values lie. A warp's chunk c is 32 * E columns: with
-// 16-byte alignment each lane holds E = 16 / sizeof(T) neighbouring ones (one
-// wide access), else four that are 32 apart (each access still covers whole
-// sectors). Either way a group of 128 columns belongs to one warp, or to one
-// half of it, so its maximum never leaves the warp.
+// Where a thread's values lie. An access has VEC neighbouring values, the most
+// that rows and tensors start on. With 16-byte accesses each lane holds E =
+// VEC neighbouring columns of a chunk of 32 * E, else E = 4 in 4 / VEC pieces
+// that are 32 * VEC apart (each access still covers whole sectors). Either way
+// a group of 128 columns belongs to one warp, or to one half of it, so its
+// maximum never leaves the warp.
 // FULL: the row is exactly the block's chunks, so no column is beyond it.
-template <typename T, bool WIDE, bool FULL>
+template <typename T, int VEC, bool FULL>
 struct Chunk {
-  static constexpr int E = WIDE ? Vec16<T>::N : 4;
+  static constexpr bool WIDE = VEC == Vec16<T>::N;
+  static constexpr int E = WIDE ? VEC : 4;
   static constexpr int COLS = 32 * E;
-  static constexpr int GROUP_LANES = WIDE ? 128 / E : 32;
+  static constexpr int GROUP_LANES = 128 / E;
   static __device__ __forceinline__ int col(int chunk, int lane, int j) {
-    return chunk * COLS + (WIDE ? lane * E + j : lane + 32 * j);
+    return chunk * COLS + j / VEC * 32 * VEC + lane * VEC + j % VEC;
   }
   static __device__ __forceinline__ void load(const T* p, int chunk, int lane, int H, float (&f)[E]) {
     if constexpr (WIDE) {
@@ -53,9 +55,43 @@ struct Chunk {
       Vec16<T>::unpack(u, f);
     } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
+      for (int j = 0; j < E; j += VEC) {
         const int c = col(chunk, lane, j);
-        f[j] = FULL || c < H ? to_f(p[c]) : 0.f;
+        if constexpr (VEC == 1) f[j] = FULL || c < H ? to_f(p[c]) : 0.f;
+        else load_some(p + c, FULL || c < H, &f[j]);
+      }
+    }
+  }
+  // VEC > 1 values, zeros when not `in`.
+  static __device__ __forceinline__ void load_some(const __nv_bfloat16* p, bool in, float* f) {
+    uint32_t w[VEC < 2 ? 1 : VEC / 2] = {};
+    if (in) {
+      if constexpr (VEC >= 4) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+          const uint2 u = load4(p + i);
+          w[i / 2] = u.x, w[i / 2 + 1] = u.y;
+        }
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+  static __device__ __forceinline__ void load_some(const float* p, bool in, float* f) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = 0.f;
+    if (in) {
+      if constexpr (VEC >= 4) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+          const float4 v = load4(p + i);
+          f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[i] = p[i];
       }
     }
   }
@@ -63,66 +99,67 @@ struct Chunk {
     if constexpr (WIDE) {
       const int c = col(chunk, lane, 0);
       if (FULL || c < H) *reinterpret_cast<uint4*>(p + c) = Vec16<T>::pack(f);
-    } else {
+    } else if constexpr (VEC == 1) {
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const int c = col(chunk, lane, j);
         if (FULL || c < H) from_f(f[j], p[c]);
       }
+    } else {   // bf16
+#pragma unroll
+      for (int j = 0; j < E; j += VEC) {
+        const int c = col(chunk, lane, j);
+        uint32_t w[VEC / 2];
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(f[j + i], f[j + i + 1]);
+          w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if (c < H) {
+          if constexpr (VEC == 4) *reinterpret_cast<uint2*>(p + c) = make_uint2(w[0], w[1]);
+          else *reinterpret_cast<uint32_t*>(p + c) = w[0];
+        }
+      }
     }
   }
   static __device__ __forceinline__ void store_e4m3(uint8_t* p, int chunk, int lane, int H, const float (&f)[E]) {
-    if constexpr (WIDE) {
-      const int c = col(chunk, lane, 0);
-      if (FULL || c < H) {
-        if constexpr (E == 8)
-          *reinterpret_cast<uint2*>(p + c) = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
-        else
-          *reinterpret_cast<uint32_t*>(p + c) = e4m3x4(f[0], f[1], f[2], f[3]);
-      }
-    } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int c = col(chunk, lane, j);
-        if (FULL || c < H) p[c] = (uint8_t)e4m3x2(f[j], 0.f);
+    for (int j = 0; j < E; j += VEC) {
+      const int c = col(chunk, lane, j);
+      if (FULL || c < H) {
+        if constexpr (VEC == 8)
+          *reinterpret_cast<uint2*>(p + c) = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+        else if constexpr (VEC == 4)
+          *reinterpret_cast<uint32_t*>(p + c) = e4m3x4(f[0], f[1], f[2], f[3]);
+        else if constexpr (VEC == 2)
+          *reinterpret_cast<uint16_t*>(p + c) = (uint16_t)e4m3x2(f[j], f[j + 1]);
+        else
+          p[c] = (uint8_t)e4m3x2(f[j], 0.f);
       }
     }
   }
-  // The chunk's weights plus the offset (WIDE: in 16- or 8-byte pieces, for
-  // which the weight starts on 16 bytes; zero beyond H).
+  // The chunk's weights plus the offset, zero beyond H.
   static __device__ __forceinline__ void load_w(const void* w, bool f32, float offset, int chunk, int lane, int H,
                                                 float (&f)[E]) {
-    if constexpr (WIDE) {
-      const int c = col(chunk, lane, 0);
-#pragma unroll
-      for (int j = 0; j < E; ++j) f[j] = 0.f;
-      if (FULL || c < H) {
-        if (f32) {
-#pragma unroll
-          for (int j = 0; j < E; j += 4) {
-            const float4 v = load4(static_cast<const float*>(w) + c + j);
-            f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < E; j += 4) {
-            const uint2 v = load4(static_cast<const __nv_bfloat16*>(w) + c + j);
-            f[j] = __uint_as_float(v.x << 16), f[j + 1] = __uint_as_float(v.x & 0xffff0000u);
-            f[j + 2] = __uint_as_float(v.y << 16), f[j + 3] = __uint_as_float(v.y & 0xffff0000u);
-          }
-        }
-        if (offset != 0.f) {
-#pragma unroll
-          for (int j = 0; j < E; ++j) f[j] += offset;
-        }
-      }
-    } else {
+    if constexpr (VEC == 1) {
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const int c = col(chunk, lane, j);
         f[j] = !FULL && c >= H ? 0.f
                       : offset + (f32 ? static_cast<const float*>(w)[c]
                                       : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c]));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; j += VEC) {
+        const int c = col(chunk, lane, j);
+        if (f32) load_some(static_cast<const float*>(w) + c, FULL || c < H, &f[j]);
+        else load_some(static_cast<const __nv_bfloat16*>(w) + c, FULL || c < H, &f[j]);
+      }
+      if (offset != 0.f) {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          if (FULL || col(chunk, lane, j) < H) f[j] += offset;
       }
     }
   }
@@ -153,9 +190,9 @@ constexpr bool kAllWarps = NW == 32 && C == 8;
 // division, approximate reciprocals, no bounds checks on full rows. Six blocks
 // of 8 warps on an SM: 1.5 us less than the five that the compiler's own
 // choice of registers leaves, 4 less than rows on 4 warps, 15 less than on 16.
-template <typename T, bool WIDE, int NW, int C, bool FULL>
+template <typename T, int VEC, int NW, int C, bool FULL>
 __global__ void __launch_bounds__(NW * 32, NW == 8 ? 6 : NW == 16 ? (C <= 2 ? 3 : 2) : 1) rmsnorm_kernel(const __grid_constant__ NormParams p) {
-  using K = Chunk<T, WIDE, FULL>;
+  using K = Chunk<T, VEC, FULL>;
   __shared__ float smem[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nw = FULL || kAllWarps<NW, C> ? NW : (int)blockDim.x >> 5;
@@ -241,10 +278,10 @@ __device__ __forceinline__ void copies_wait() {   // all but the N newest groups
 
 // Rows ahead that a block loads in the background.
 constexpr int kAheadRows = 3;
-template <typename T, bool WIDE, int NW, int C>
+template <typename T, int VEC, int NW, int C>
 struct BwdCfg {
   // A thread's part of a row is at most 32 bytes of each input.
-  static constexpr bool kAhead = WIDE && C <= 2;
+  static constexpr bool kAhead = VEC == Vec16<T>::N && C <= 2;
   static constexpr bool kHold = kAhead || NW <= 16;
   // 16-byte pieces of one input's row, and the bytes of all, with nw warps.
   static constexpr __host__ __device__ int slot(int nw) { return nw * 32 * C; }
@@ -263,10 +300,10 @@ struct BwdCfg {
 // 8192 x 4096 bf16 with the residual's gradient (268 MB): 48.9 us with the
 // sum below, 5.5 TB/s. With the next row in registers instead of three in
 // shared memory 53 us; three blocks an SM instead of two 64 us.
-template <typename T, bool WIDE, int NW, int C, bool FULL>
+template <typename T, int VEC, int NW, int C, bool FULL>
 __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
-  using K = Chunk<T, WIDE, FULL>;
-  using Cfg = BwdCfg<T, WIDE, NW, C>;
+  using K = Chunk<T, VEC, FULL>;
+  using Cfg = BwdCfg<T, VEC, NW, C>;
   constexpr int E = K::E;
   constexpr bool kAhead = Cfg::kAhead, kHold = Cfg::kHold;
   __shared__ float smem[32];
@@ -435,18 +472,19 @@ int bwd_blocks(int64_t total, int nw) {
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// Calls f.template operator()<T, WIDE, NW, C, FULL>(n) for rows of n chunks:
+// Calls f.template operator()<T, VEC, NW, C, FULL>(n) for rows of n chunks:
 // one chunk a thread while 8 warps suffice, then up to 32 warps and up to 8
 // chunks.
-template <typename T, bool WIDE, typename F>
+template <typename T, int VEC, typename F>
 fo_status by_width(int H, F&& f) {
-  constexpr int kCols = Chunk<T, WIDE, false>::COLS;
+  using K = Chunk<T, VEC, false>;
+  constexpr int kCols = K::COLS;
   const int n = (H + kCols - 1) / kCols;
   auto go = [&](auto nw, auto c) -> fo_status {
     constexpr int NW = decltype(nw)::value, C = decltype(c)::value;
-    if constexpr (WIDE)
-      if (H == NW * C * kCols) return f.template operator()<T, WIDE, NW, C, true>(n);
-    return f.template operator()<T, WIDE, NW, C, false>(n);
+    if constexpr (K::WIDE)
+      if (H == NW * C * kCols) return f.template operator()<T, VEC, NW, C, true>(n);
+    return f.template operator()<T, VEC, NW, C, false>(n);
   };
   if (n <= 1) return go(Int<1>(), Int<1>());
   if (n <= 2) return go(Int<2>(), Int<1>());
@@ -459,21 +497,35 @@ fo_status by_width(int H, F&& f) {
   if constexpr (kCols * 128 < FO_NORM_MAX_H) return go(Int<32>(), Int<8>());
   return FO_ERR_SHAPE;
 }
+// The values that an access may have: rows of H and every tensor start on them.
+struct Width {
+  int vec;
+  Width(int most, int H) : vec(most) { fit((uintptr_t)(unsigned)H); }
+  void fit(uintptr_t at) {   // `at`: in elements
+    while (at % vec) vec /= 2;
+  }
+  void add(int R, const void* const* a, int size) {
+    for (int r = 0; a && r < R; ++r) fit(reinterpret_cast<uintptr_t>(a[r]) / size);
+  }
+};
 template <typename F>
-fo_status by_type(int32_t dtype, bool wide, int H, F&& f) {
-  if (dtype == FO_BF16) return wide ? by_width<__nv_bfloat16, true>(H, f) : by_width<__nv_bfloat16, false>(H, f);
-  return wide ? by_width<float, true>(H, f) : by_width<float, false>(H, f);
+fo_status by_type(int32_t dtype, int vec, int H, F&& f) {
+  if (dtype == FO_F32) return vec == 4 ? by_width<float, 4>(H, f) : by_width<float, 1>(H, f);
+  return vec == 8   ? by_width<__nv_bfloat16, 8>(H, f)
+         : vec == 4 ? by_width<__nv_bfloat16, 4>(H, f)
+         : vec == 2 ? by_width<__nv_bfloat16, 2>(H, f)
+                    : by_width<__nv_bfloat16, 1>(H, f);
 }
 
 struct LaunchFwd {
   const NormParams& k;
   cudaStream_t s;
   int R;
-  template <typename T, bool WIDE, int NW, int C, bool FULL>
+  template <typename T, int VEC, int NW, int C, bool FULL>
   fo_status operator()(int n) const {
     const int nw = kAllWarps<NW, C> ? NW : warps_for(n);
     const dim3 grid((unsigned)k.rows, R);
-    return launched(launch_after(rmsnorm_kernel<T, WIDE, NW, C, FULL>, grid, nw * 32, 0, 0, s, k), "rmsnorm", R, k.rows, k.H, (int)k.rows, nw * 32);
+    return launched(launch_after(rmsnorm_kernel<T, VEC, NW, C, FULL>, grid, nw * 32, 0, 0, s, k), "rmsnorm", R, k.rows, k.H, (int)k.rows, nw * 32);
   }
 };
 struct LaunchBwd {
@@ -481,12 +533,12 @@ struct LaunchBwd {
   cudaStream_t s;
   int R;
   int* blocks;
-  template <typename T, bool WIDE, int NW, int C, bool FULL>
+  template <typename T, int VEC, int NW, int C, bool FULL>
   fo_status operator()(int n) const {
-    const int nw = BwdCfg<T, WIDE, NW, C>::kAhead ? warps_for(n) : NW;
+    const int nw = BwdCfg<T, VEC, NW, C>::kAhead ? warps_for(n) : NW;
     const int grid = *blocks = bwd_blocks(k.total, nw);
-    const int smem = BwdCfg<T, WIDE, NW, C>::smem(nw);
-    auto kern = rmsnorm_bwd_kernel<T, WIDE, NW, C, FULL>;
+    const int smem = BwdCfg<T, VEC, NW, C>::smem(nw);
+    auto kern = rmsnorm_bwd_kernel<T, VEC, NW, C, FULL>;
     if (smem > 48 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return launched(e, "rmsnorm_bwd", R, k.rows, k.H, grid, nw * 32);
@@ -541,9 +593,11 @@ extern "C" fo_status fo_rmsnorm(const fo_norm_desc* d, int64_t rows, const void*
   k.inv_H = 1.f / (float)d->H;
   k.has_res = residual, k.has_h = h, k.has_y = y, k.has_q = q, k.has_rstd = rstd;
   k.w_f32 = d->w_dtype == FO_F32;
-  const bool wide = (d->H * es) % 16 == 0 && aligned(weight, 16) && all_aligned(R, x, 16) && all_aligned(R, residual, 16) &&
-                    all_aligned(R, (A)h, 16) && all_aligned(R, (A)y, 16) && all_aligned(R, (A)q, 8);
-  return by_type(d->dtype, wide, d->H, LaunchFwd{k, (cudaStream_t)stream, R});
+  const int es_i = (int)es;
+  Width v(16 / es_i, d->H);
+  if (!aligned(weight, 16)) v.add(1, &weight, (int)elem(d->w_dtype));   // (no access is wider)
+  v.add(R, x, es_i), v.add(R, residual, es_i), v.add(R, (A)h, es_i), v.add(R, (A)y, es_i), v.add(R, (A)q, 1);
+  return by_type(d->dtype, v.vec, d->H, LaunchFwd{k, (cudaStream_t)stream, R});
 }
 
 extern "C" fo_status fo_rmsnorm_bwd_workspace(const fo_norm_desc* d, int64_t rows, size_t* bytes) {
@@ -612,10 +666,12 @@ extern "C" fo_status fo_rmsnorm_bwd(const fo_norm_desc* d, int64_t rows, const v
   k.inv_H = 1.f / (float)d->H;
   k.has_dh = dh, k.has_dw = dweight;
   k.w_f32 = d->w_dtype == FO_F32;
-  const bool wide = (d->H * es) % 16 == 0 && aligned(weight, 16) && all_aligned(R, dy, 16) && all_aligned(R, dh, 16) &&
-                    all_aligned(R, h, 16) && all_aligned(R, (A)dx, 16);
+  const int es_i = (int)es;
+  Width v(16 / es_i, d->H);
+  if (!aligned(weight, 16)) v.add(1, &weight, (int)elem(d->w_dtype));   // (no access is wider)
+  v.add(R, dy, es_i), v.add(R, dh, es_i), v.add(R, h, es_i), v.add(R, (A)dx, es_i);
   int grid = 0;
-  if ((st = by_type(d->dtype, wide, d->H, LaunchBwd{k, s, R, &grid}))) return st;
+  if ((st = by_type(d->dtype, v.vec, d->H, LaunchBwd{k, s, R, &grid}))) return st;
   if (!dweight) return FO_OK;
   const int cols = (d->H + 31) / 32;
   return launched(launch_after(dweight_kernel, dim3(cols), kDwWarps * 32, 0, 0, s, (const float*)k.part, grid, d->H, dweight), "rmsnorm_dweight", R, grid, d->H, cols, kDwWarps * 32);

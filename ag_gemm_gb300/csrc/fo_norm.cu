@@ -264,11 +264,15 @@ struct NormBwdParams {
 // Blocks of the backward kernel on an SM: sixteen warps' worth.
 constexpr int bwd_per_sm(int nw) { return nw <= 16 ? 16 / nw : 1; }
 
-// 16 bytes to shared memory in the background, or zeros.
-__device__ __forceinline__ void copy16_async(void* to, const void* from, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
-               "r"(in ? 16 : 0)
-               : "memory");
+// 16, 8 or 4 bytes to shared memory in the background, or zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from, bool in) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(in ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from), "n"(BYTES), "r"(in ? BYTES : 0)
+                 : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -276,27 +280,34 @@ __device__ __forceinline__ void copies_wait() {   // all but the N newest groups
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Rows ahead that a block loads in the background.
-constexpr int kAheadRows = 3;
 template <typename T, int VEC, int NW, int C>
 struct BwdCfg {
-  // A thread's part of a row is at most 32 bytes of each input.
-  static constexpr bool kAhead = VEC == Vec16<T>::N && C <= 2;
-  static constexpr bool kHold = kAhead || NW <= 16;
-  // 16-byte pieces of one input's row, and the bytes of all, with nw warps.
-  static constexpr __host__ __device__ int slot(int nw) { return nw * 32 * C; }
-  static constexpr int smem(int nw) { return kAhead ? kAheadRows * 3 * slot(nw) * 16 : 0; }
+  static constexpr int E = Chunk<T, VEC, false>::E;
+  static constexpr int kPiece = VEC * (int)sizeof(T);   // bytes of an access
+  static constexpr int kPart = C * E * (int)sizeof(T);  // of a thread's part of a row of one input
+  static constexpr bool kAhead = kPiece >= 4 && NW <= 16 && C * E <= 16;
+  static constexpr int kRows = kPart <= 32 ? 3 : 2;     // the row in hand and those loaded in the background
+  static constexpr bool kNext = !kAhead && NW <= 16 && C * E <= 8;
+  static constexpr bool kHold = NW <= 16;
+  static constexpr bool kWeights = kAhead || kNext;     // held
+  // Bytes of one input's row, and of all, with nw warps.
+  static constexpr __host__ __device__ int slot(int nw) { return nw * 32 * kPart; }
+  static constexpr int smem(int nw) { return kAhead ? kRows * 3 * slot(nw) : 0; }
 };
 
 // Where rows come ahead, blocks have no more warps than their row needs, and as
 // many blocks an SM as make up sixteen warps (8191 x 1280 bf16: 24.8 us with
-// 5 warps, 30.9 with 8). A block takes every gridDim.x-th row and keeps its columns' share of the
+// 5 warps, 30.9 with 8).
+// A block takes every gridDim.x-th row and keeps its columns' share of the
 // weight's gradient in registers. What else it keeps goes by the registers
-// that a thread's part of a row takes: where it is 32 bytes or less, the
-// weights too, and the next three rows come in the background, each thread
-// its own pieces, so that the loads go on through the two barriers of a row;
-// beyond, with up to 16 warps, this row's values; else nothing, and the second
-// pass over the row reads it again, from L2.
+// that a thread's part of a row takes. At most 16 values that start on 4 bytes
+// or more: the weights too, and the next rows come in the background, each
+// thread its own pieces, so that the loads go on through the two barriers of a
+// row (8191 x 4098 bf16: 69 us, 185 without; 4000 x 8192 fp32: 81, 120). At
+// most 8 values of odd rows: the weights, and the next row's values in
+// registers (8191 x 4095 bf16: 98 us, 161 without). Else, with up to 16 warps,
+// this row's values; else nothing, and the second pass over the row reads it
+// again, from L2.
 // 8192 x 4096 bf16 with the residual's gradient (268 MB): 48.9 us with the
 // sum below, 5.5 TB/s. With the next row in registers instead of three in
 // shared memory 53 us; three blocks an SM instead of two 64 us.
@@ -305,17 +316,18 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
   using K = Chunk<T, VEC, FULL>;
   using Cfg = BwdCfg<T, VEC, NW, C>;
   constexpr int E = K::E;
-  constexpr bool kAhead = Cfg::kAhead, kHold = Cfg::kHold;
+  constexpr bool kAhead = Cfg::kAhead, kNext = Cfg::kNext, kHold = Cfg::kHold, kWeights = Cfg::kWeights;
   __shared__ float smem[32];
-  extern __shared__ uint4 ring[];   // kAhead: [row % kAheadRows][input][chunk][thread]
+  extern __shared__ uint4 ring_mem[];   // kAhead: [row % Cfg::kRows][input][chunk][piece of E values][thread]
+  uint8_t* const ring = reinterpret_cast<uint8_t*>(ring_mem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nw = FULL || !kAhead ? NW : (int)blockDim.x >> 5;
   grid_release();
   grid_wait();
-  float w[kAhead ? C : 1][E], dw[C][E];
+  float w[kWeights ? C : 1][E], dw[C][E];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    if constexpr (kAhead) K::load_w(p.w, p.w_f32, p.w_offset, c * nw + warp, lane, p.H, w[c]);
+    if constexpr (kWeights) K::load_w(p.w, p.w_f32, p.w_offset, c * nw + warp, lane, p.H, w[c]);
 #pragma unroll
     for (int j = 0; j < E; ++j) dw[c][j] = 0.f;
   }
@@ -327,26 +339,70 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
     if (row < p.total) {
       const int r = rank_of(row);
       const int64_t off = (row - r * p.rows) * p.H;
-      uint4* const to = ring + slot * 3 * Cfg::slot(nw) + threadIdx.x;
+      uint8_t* const to = ring + slot * 3 * Cfg::slot(nw) + threadIdx.x * Cfg::kPiece;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int col = K::col(c * nw + warp, lane, 0);
+      for (int i = 0; i < C * E / VEC; ++i) {
+        const int col = K::col(i / (E / VEC) * nw + warp, lane, i % (E / VEC) * VEC), n = i * nw * 32 * Cfg::kPiece;
         const bool in = FULL || col < p.H;
         const int64_t at = off + (in ? col : 0);
-        copy16_async(to + c * nw * 32, static_cast<const T*>(p.dy[r]) + at, in);
-        copy16_async(to + Cfg::slot(nw) + c * nw * 32, static_cast<const T*>(p.h[r]) + at, in);
-        if (p.has_dh) copy16_async(to + 2 * Cfg::slot(nw) + c * nw * 32, static_cast<const T*>(p.dh[r]) + at, in);
+        copy_async<Cfg::kPiece>(to + n, static_cast<const T*>(p.dy[r]) + at, in);
+        copy_async<Cfg::kPiece>(to + Cfg::slot(nw) + n, static_cast<const T*>(p.h[r]) + at, in);
+        if (p.has_dh) copy_async<Cfg::kPiece>(to + 2 * Cfg::slot(nw) + n, static_cast<const T*>(p.dh[r]) + at, in);
       }
     }
     copies_end();   // a group for every row, empty ones too: the waits count them
   };
   auto piece = [&](int slot, int input, int c, float (&v)[E]) {
-    if constexpr (kAhead) Vec16<T>::unpack(ring[(slot * 3 + input) * Cfg::slot(nw) + c * nw * 32 + threadIdx.x], v);
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int j = 0; j < E; j += VEC) {
+        const uint8_t* const at = ring + (slot * 3 + input) * Cfg::slot(nw) +
+                                  ((c * (E / VEC) + j / VEC) * nw * 32 + threadIdx.x) * Cfg::kPiece;
+        if constexpr (Cfg::kPiece == 16) {
+          Vec16<T>::unpack(*reinterpret_cast<const uint4*>(at), v);
+        } else if constexpr (sizeof(T) == 4) {
+          v[j] = *reinterpret_cast<const float*>(at);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; i += 2) {
+            const uint32_t w = reinterpret_cast<const uint32_t*>(at)[i / 2];
+            v[j + i] = __uint_as_float(w << 16), v[j + i + 1] = __uint_as_float(w & 0xffff0000u);
+          }
+        }
+      }
+    }
   };
   if constexpr (kAhead) {
 #pragma unroll
-    for (int i = 0; i < kAheadRows - 1; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
+    for (int i = 0; i < Cfg::kRows - 1; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
   }
+  // kNext: the row after this one, as it was read (converted, each value would be waited for).
+  T nu[kNext ? C : 1][E], nh[kNext ? C : 1][E], nt[kNext ? C : 1][E];
+  auto next = [&](int64_t row) {
+    if constexpr (kNext)
+      if (row < p.total) {
+        const int r = rank_of(row);
+        const int64_t off = (row - r * p.rows) * p.H;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            const int col = K::col(c * nw + warp, lane, j);
+            if (col < p.H) {
+              nu[c][j] = static_cast<const T*>(p.dy[r])[off + col];
+              nh[c][j] = static_cast<const T*>(p.h[r])[off + col];
+              if (p.has_dh) nt[c][j] = static_cast<const T*>(p.dh[r])[off + col];
+            }
+          }
+      }
+  };
+  if constexpr (kNext) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int j = 0; j < E; ++j) from_f(0.f, nu[c][j]), from_f(0.f, nh[c][j]), from_f(0.f, nt[c][j]);   // beyond H
+  }
+  next(blockIdx.x);
   int slot = 0;
   for (int64_t row = blockIdx.x; row < p.total; row += gridDim.x) {
     const int r = rank_of(row);
@@ -357,11 +413,18 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
     if constexpr (kAhead) {
       // The slot of the row before this one is free: this thread has read its
       // pieces, and no other thread reads them.
-      fetch(row + (int64_t)(kAheadRows - 1) * gridDim.x, slot == 0 ? kAheadRows - 1 : slot - 1);
-      copies_wait<kAheadRows - 1>();
+      fetch(row + (int64_t)(Cfg::kRows - 1) * gridDim.x, slot == 0 ? Cfg::kRows - 1 : slot - 1);
+      copies_wait<Cfg::kRows - 1>();
     }
-    float h[kHold ? C : 1][E], u[kHold ? C : 1][E];
+    float h[kHold ? C : 1][E], u[kHold ? C : 1][E], t[kNext ? C : 1][E];
     float sum = 0.f;
+    if constexpr (kNext) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < E; ++j) u[c][j] = to_f(nu[c][j]), h[c][j] = to_f(nh[c][j]), t[c][j] = to_f(nt[c][j]);
+      next(row + gridDim.x);
+    }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float(&uc)[E] = u[kHold ? c : 0];
@@ -369,7 +432,7 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
       if constexpr (kAhead) {
         piece(slot, 0, c, uc);
         piece(slot, 1, c, hc);
-      } else {
+      } else if constexpr (!kNext) {
         K::load(dy, c * nw + warp, lane, p.H, uc);
         K::load(hp, c * nw + warp, lane, p.H, hc);
         K::load_w(p.w, p.w_f32, p.w_offset, c * nw + warp, lane, p.H, w[0]);
@@ -377,7 +440,7 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         dw[c][j] = fmaf(uc[j] * rstd, hc[j], dw[c][j]);
-        uc[j] *= w[kAhead ? c : 0][j];
+        uc[j] *= w[kWeights ? c : 0][j];
         sum = fmaf(uc[j], hc[j], sum);
       }
     }
@@ -397,15 +460,15 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
 #pragma unroll
       for (int j = 0; j < E; ++j) d[j] = rstd * uc[j] - hc[j] * k;
       if (p.has_dh) {
-        float t[E];
-        if constexpr (kAhead) piece(slot, 2, c, t);
-        else K::load(static_cast<const T*>(p.dh[r]) + off, c * nw + warp, lane, p.H, t);
+        float(&tc)[E] = t[kNext ? c : 0];
+        if constexpr (kAhead) piece(slot, 2, c, tc);
+        else if constexpr (!kNext) K::load(static_cast<const T*>(p.dh[r]) + off, c * nw + warp, lane, p.H, tc);
 #pragma unroll
-        for (int j = 0; j < E; ++j) d[j] += t[j];
+        for (int j = 0; j < E; ++j) d[j] += tc[j];
       }
       K::store(static_cast<T*>(p.dx[r]) + off, c * nw + warp, lane, p.H, d);
     }
-    slot = slot + 1 == kAheadRows ? 0 : slot + 1;
+    slot = slot + 1 == Cfg::kRows ? 0 : slot + 1;
   }
   if (p.has_dw) {
 #pragma unroll
@@ -608,7 +671,8 @@ extern "C" fo_status fo_rmsnorm_bwd_workspace(const fo_norm_desc* d, int64_t row
   // Enough for rows on the 16-byte grid (chunks of 256 or 128 columns, maybe on
   // fewer warps than the kernel's most) and off it (of 128).
   const int cols = d->dtype == FO_BF16 ? 256 : 128, chunks = (d->H + cols - 1) / cols;
-  const int warps[3] = {warps_for(chunks), most_warps(chunks), most_warps((d->H + 127) / 128)};
+  const int off = (d->H + 127) / 128;
+  const int warps[4] = {warps_for(chunks), most_warps(chunks), warps_for(off), most_warps(off)};
   size_t n = 0;
   for (const int w : warps) {
     const size_t b = (size_t)bwd_blocks(rows * d->R, w) * (size_t)d->H * sizeof(float);

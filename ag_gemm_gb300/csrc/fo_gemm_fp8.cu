@@ -33,21 +33,6 @@ using namespace fo;
 constexpr uint64_t kWaitNs = 2000000000ull;   // every wait's bound
 constexpr int kBlockK = FO_FP8_BLOCK;         // reduction bytes a stage
 
-// n / d for n < 2^31 by a multiplication (Granlund and Montgomery's: with s the
-// bits of d - 1, m = floor(2^32 (2^s - d) / d) + 1, the quotient is
-// (floor(m n / 2^32) + n) / 2^s). The hardware has no integer division; the
-// compiler's takes some 30 dependent instructions, three of them at every tile.
-struct Divisor {
-  uint32_t d, m, s;
-  void set(uint32_t divisor) {
-    d = divisor;
-    for (s = 0; (1ull << s) < d; ++s) {
-    }
-    m = (uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1);
-  }
-  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
-};
-
 struct GemmParams {
   CUtensorMap tmA[kMaxR];   // A_r [M x K] bytes
   CUtensorMap tmW[kMaxR];   // W_r [N x K] bytes

@@ -108,6 +108,21 @@ __device__ __forceinline__ uint2 load4(const __nv_bfloat16* p) {
   return v;
 }
 
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery's: with s the
+// bits of d - 1, m = floor(2^32 (2^s - d) / d) + 1, the quotient is
+// (floor(m n / 2^32) + n) / 2^s). The hardware has no integer division; the
+// compiler's takes some 30 dependent instructions.
+struct Divisor {
+  uint32_t d, m, s;
+  void set(uint32_t divisor) {
+    d = divisor;
+    for (s = 0; (1ull << s) < d; ++s) {
+    }
+    m = (uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
+};
+
 constexpr float kE4M3Top = 448.f;
 constexpr float kLeastScale = 1.17549435e-38f;   // 2^-126
 

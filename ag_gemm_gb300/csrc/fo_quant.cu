@@ -3,6 +3,8 @@
 // read once, in 16-byte pieces, and written once (twice with the copy).
 #include <string.h>
 
+#include <type_traits>
+
 #include "fo_ops.h"
 
 namespace fo_ops {
@@ -17,36 +19,114 @@ struct QuantParams {
   int64_t rows, cols;
   int32_t groups, row_blocks;
   int32_t pieces;   // quant_rows_wide_kernel: warp-wide pieces of a row
+  Divisor by_groups;   // quant_rows_kernel: where there are less than 2^31 groups
   int32_t copy8;    // quant_blocks_wide_kernel: the copy's lines start on 8 bytes
 };
 
-// One warp for each group of 128 values of a row (rows that do not start on
-// 16 bytes).
-template <typename T>
+// Four neighbouring values of a row as they are read, VEC at an access (the
+// most that rows and tensors start on). They are converted where they are
+// used: a conversion behind the load would wait for it.
+template <typename T, int VEC>
+struct Four {
+  static constexpr bool kWords = sizeof(T) == 2 && VEC > 1;
+  typename std::conditional<kWords, uint32_t, T>::type raw[kWords ? 2 : 4];
+  __device__ __forceinline__ void load(const T* p, int n) {   // n of them, the others zero
+    if constexpr (kWords) {
+      raw[0] = raw[1] = 0;
+      if constexpr (VEC == 4) {
+        if (n > 0) {
+          const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
+          raw[0] = u.x, raw[1] = u.y;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (2 * j < n) raw[j] = __ldcs(reinterpret_cast<const unsigned int*>(p) + j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) from_f(0.f, raw[j]);
+      if constexpr (VEC == 4) {
+        if (n > 0) {
+          const float4 v = __ldcs(reinterpret_cast<const float4*>(p));
+          raw[0] = v.x, raw[1] = v.y, raw[2] = v.z, raw[3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < n) raw[j] = p[j];
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[4]) const {
+    if constexpr (kWords) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        f[2 * j] = __uint_as_float(raw[j] << 16), f[2 * j + 1] = __uint_as_float(raw[j] & 0xffff0000u);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = to_f(raw[j]);
+    }
+  }
+};
+
+// A warp stores a line of n <= 128 bytes that starts anywhere, lane l holding
+// its bytes 4 l .. 4 l + 3, in the 4-byte words of memory, each put together
+// from two lanes' words; single bytes where a word is not the line's alone.
+__device__ __forceinline__ void store_line(uint8_t* line, uint32_t mine, int lane, int n) {
+  const int off = (int)(reinterpret_cast<uintptr_t>(line) & 3u);   // the same in every lane
+  int at = 4 * lane;
+  uint32_t v = mine;
+  if (off) {   // lane l has the word of memory that begins at byte 4 l + 4 - off
+    const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);   // (lane 31's is not stored whole)
+    const uint32_t first = __shfl_sync(0xffffffffu, mine, 0);
+    at += 4 - off;
+    v = __byte_perm(mine, next, 0x7654u - 0x1111u * (uint32_t)off);
+    if (lane < 4 - off && lane < n) line[lane] = (uint8_t)(first >> (8 * lane));
+  }
+  if (at + 4 <= n) {
+    *reinterpret_cast<uint32_t*>(line + at) = v;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (at + j < n) line[at + j] = (uint8_t)(v >> (8 * j));
+  }
+}
+
+// One warp for each group of 128 values of a row, kUnroll groups at a time
+// with all loads first (rows that do not start on 16 bytes). 8191 x 4098 bf16:
+// 35 us; 8191 x 4095: 35 (with accesses of one value and byte stores 45).
+template <typename T, int VEC>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__ QuantParams p) {
+  constexpr int kUnroll = 4;
   const int lane = threadIdx.x & 31, r = blockIdx.y;
-  const int64_t n = p.rows * p.groups;
+  const int64_t n = p.rows * p.groups, step = gridDim.x * 8ll;
   grid_release();
   grid_wait();
-  for (int64_t g = blockIdx.x * 8ll + (threadIdx.x >> 5); g < n; g += gridDim.x * 8ll) {
-    const int64_t row = g / p.groups;
-    const int64_t c0 = (g - row * p.groups) * FO_FP8_BLOCK;
-    const T* x = static_cast<const T*>(p.x[r]) + row * p.cols;
-    float v[4], amax = 0.f;
+  for (int64_t g = blockIdx.x * 8ll + (threadIdx.x >> 5); g < n; g += step * kUnroll) {
+    Four<T, VEC> x[kUnroll];
+    int64_t row[kUnroll];
+    int c0[kUnroll];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t c = c0 + lane + 32 * j;
-      v[j] = c < p.cols ? to_f(x[c]) : 0.f;
-      amax = max_nan(amax, fabsf(v[j]));
+    for (int i = 0; i < kUnroll; ++i) {
+      const int64_t u = g + i * step;
+      row[i] = p.by_groups.d ? (int64_t)p.by_groups((uint32_t)u) : u / p.groups;
+      c0[i] = (int)(u - row[i] * p.groups) * FO_FP8_BLOCK;
+      const int left = u < n ? (int)(p.cols - c0[i]) - 4 * lane : 0;
+      x[i].load(static_cast<const T*>(p.x[r]) + row[i] * p.cols + c0[i] + 4 * lane, left);
     }
-    const float scale = scale_of(lanes_max<32>(amax)), inv = inverse_of(scale);
-    uint8_t* q = p.q[r] + row * p.cols;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t c = c0 + lane + 32 * j;
-      if (c < p.cols) q[c] = (uint8_t)e4m3x2(v[j] * inv, 0.f);
+    for (int i = 0; i < kUnroll; ++i) {
+      const int64_t u = g + i * step;
+      if (u >= n) break;
+      float v[4];
+      x[i].get(v);
+      const float scale = scale_of(lanes_max<32>(amax_of(v))), inv = inverse_of(scale);
+      const int left = (int)(p.cols - c0[i]);
+      store_line(p.q[r] + row[i] * p.cols + c0[i], e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv), lane,
+                 left < FO_FP8_BLOCK ? left : FO_FP8_BLOCK);
+      if (lane == 0) p.scale[r][u] = scale;
     }
-    if (lane == 0) p.scale[r][g] = scale;
   }
 }
 
@@ -96,51 +176,6 @@ __global__ void __launch_bounds__(256) quant_rows_wide_kernel(const __grid_const
   }
 }
 
-// One block for each 128 x 128 block: warp w holds rows w, w + 8, ... (rows
-// that do not start on 16 bytes).
-template <typename T>
-__global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant__ QuantParams p) {
-  __shared__ float smem[8];
-  __shared__ uint8_t tile[128][132];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.z;
-  const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
-  float v[16][4], amax = 0.f;
-  grid_release();
-  grid_wait();
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t row = r0 + warp + 8 * i, c = c0 + lane + 32 * j;
-      v[i][j] = row < p.rows && c < p.cols ? to_f(static_cast<const T*>(p.x[r])[row * p.cols + c]) : 0.f;
-      amax = max_nan(amax, fabsf(v[i][j]));
-    }
-  amax = lanes_max<32>(amax);
-  if (lane == 0) smem[warp] = amax;
-  __syncthreads();
-  const float scale = scale_of(lanes_max<32>(smem[lane & 7])), inv = inverse_of(scale);
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t row = r0 + warp + 8 * i, c = c0 + lane + 32 * j;
-      const uint8_t b = (uint8_t)e4m3x2(v[i][j] * inv, 0.f);
-      if (row < p.rows && c < p.cols) p.q[r][row * p.cols + c] = b;
-      tile[lane + 32 * j][warp + 8 * i] = b;
-    }
-  if (threadIdx.x == 0) {
-    p.scale[r][(int64_t)blockIdx.y * p.groups + blockIdx.x] = scale;
-    if (p.qt[r]) p.scale_t[r][(int64_t)blockIdx.x * p.row_blocks + blockIdx.y] = scale;
-  }
-  if (!p.qt[r]) return;
-  __syncthreads();
-  for (int i = 0; i < 16; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t c = c0 + warp + 8 * i, row = r0 + lane + 32 * j;
-      if (row < p.rows && c < p.cols) p.qt[r][c * p.rows + row] = tile[warp + 8 * i][lane + 32 * j];
-    }
-}
-
 // Four words of four bytes each, transposed: byte j of word i becomes byte i
 // of word j.
 __device__ __forceinline__ void transpose4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
@@ -150,6 +185,64 @@ __device__ __forceinline__ void transpose4(uint32_t& a, uint32_t& b, uint32_t& c
   b = __byte_perm(ab_lo, cd_lo, 0x7632);
   c = __byte_perm(ab_hi, cd_hi, 0x5410);
   d = __byte_perm(ab_hi, cd_hi, 0x7632);
+}
+
+// One block for each 128 x 128 block (rows that do not start on 16 bytes):
+// warp w has rows 16 w .. 16 w + 15, lane l columns 4 l .. 4 l + 3, so its
+// bytes of a row are a word, and those of four rows, transposed, are words of
+// the copy's lines. 8191 x 4098 bf16 with the copy: 41 us, 8191 x 4095: 54
+// (with accesses of one value and byte stores 78).
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant__ QuantParams p) {
+  __shared__ float smem[8];
+  __shared__ uint32_t tile[128 * 32];   // [column][word of four rows, mixed with the column]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.z;
+  const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
+  const int rows = (int)min((int64_t)128, p.rows - r0), cols = (int)min((int64_t)128, p.cols - c0);
+  Four<T, VEC> x[16];
+  grid_release();
+  grid_wait();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int row = warp * 16 + i;
+    x[i].load(static_cast<const T*>(p.x[r]) + (r0 + (row < rows ? row : 0)) * p.cols + c0 + 4 * lane,
+              row < rows ? cols - 4 * lane : 0);
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float v[4];
+    x[i].get(v);
+    amax = max_nan(amax, amax_of(v));
+  }
+  amax = lanes_max<32>(amax);
+  if (lane == 0) smem[warp] = amax;
+  __syncthreads();
+  const float scale = scale_of(lanes_max<8>(smem[lane & 7])), inv = inverse_of(scale);
+  if (threadIdx.x == 0) {
+    p.scale[r][(int64_t)blockIdx.y * p.groups + blockIdx.x] = scale;
+    if (p.qt[r]) p.scale_t[r][(int64_t)blockIdx.x * p.row_blocks + blockIdx.y] = scale;
+  }
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v[4];
+      x[4 * g + i].get(v);
+      b[i] = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+      const int row = warp * 16 + 4 * g + i;
+      if (row < rows) store_line(p.q[r] + (r0 + row) * p.cols + c0, b[i], lane, cols);
+    }
+    transpose4(b[0], b[1], b[2], b[3]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tile[(4 * lane + j) * 32 + ((4 * warp + g) ^ lane)] = b[j];
+  }
+  if (!p.qt[r]) return;
+  __syncthreads();
+#pragma unroll 4
+  for (int c = warp; c < cols; c += 8)
+    store_line(p.qt[r] + (c0 + c) * p.rows + r0, tile[c * 32 + (lane ^ (c >> 2))], lane, rows);
 }
 
 // 12288 x 4096 bf16 with the copy (201 MB): 33.7 us, 6.0 TB/s (223 us with bytes
@@ -248,38 +341,28 @@ __global__ void __launch_bounds__(256) quant_blocks_wide_kernel(const __grid_con
           __stcs(reinterpret_cast<uint2*>(p.qt[r] + (c0 + c) * p.rows + row), tile[c * 16 + (cg ^ (c >> 3))]);
       }
     } else {
-      // A warp stores a line in the 4-byte words of memory, each put together
-      // from two words of the tile; bytes where a word is not the line's alone.
       const int n = (int)min((int64_t)128, p.rows - r0);   // bytes of a line
 #pragma unroll 4
       for (int c = warp; c < 128; c += 8) {
         if (c0 + c >= p.cols) break;
-        uint8_t* const line = p.qt[r] + (c0 + c) * p.rows + r0;
-        const int off = (int)(reinterpret_cast<uintptr_t>(line) & 3u);
-        auto word = [&](int k) -> uint32_t {   // bytes 4 k .. 4 k + 3 of the line
-          const uint2 u = tile[c * 16 + ((k >> 1) ^ (c >> 3))];
-          return k & 1 ? u.y : u.x;
-        };
-        const uint32_t mine = word(lane);
-        const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);   // (lane 31's is not stored whole)
-        // Lane l has the word of memory that begins at byte 4 l + 4 - off (4 l
-        // where the line starts on a word).
-        const int at = off ? 4 * lane + 4 - off : 4 * lane;
-        const uint32_t v = off ? __byte_perm(mine, next, 0x7654u - 0x1111u * (uint32_t)off) : mine;
-        if (at + 4 <= n) {
-          *reinterpret_cast<uint32_t*>(line + at) = v;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 3; ++j)
-            if (at + j < n) line[at + j] = (uint8_t)(v >> (8 * j));
-        }
-        const uint32_t first = __shfl_sync(0xffffffffu, mine, 0);
-        if (lane < 4 - off && off && lane < n) line[lane] = (uint8_t)(first >> (8 * lane));
+        const uint2 u = tile[c * 16 + ((lane >> 1) ^ (c >> 3))];
+        store_line(p.qt[r] + (c0 + c) * p.rows + r0, lane & 1 ? u.y : u.x, lane, n);
       }
     }
   }
 }
 
+// The kernels for rows off the 16-byte grid, `vec` values an access.
+template <typename T>
+auto rows_any(int vec) {
+  if constexpr (sizeof(T) == 4) return vec == 4 ? quant_rows_kernel<T, 4> : quant_rows_kernel<T, 1>;
+  else return vec == 4 ? quant_rows_kernel<T, 4> : vec == 2 ? quant_rows_kernel<T, 2> : quant_rows_kernel<T, 1>;
+}
+template <typename T>
+auto blocks_any(int vec) {
+  if constexpr (sizeof(T) == 4) return vec == 4 ? quant_blocks_kernel<T, 4> : quant_blocks_kernel<T, 1>;
+  else return vec == 4 ? quant_blocks_kernel<T, 4> : vec == 2 ? quant_blocks_kernel<T, 2> : quant_blocks_kernel<T, 1>;
+}
 template <typename T>
 auto blocks_wide(int copy) {
   return copy == 16 ? quant_blocks_wide_kernel<T, 16> : copy ? quant_blocks_wide_kernel<T, 8> : quant_blocks_wide_kernel<T, 0>;
@@ -325,12 +408,16 @@ extern "C" fo_status fo_quant_fp8(int32_t R, int64_t rows, int64_t cols, int32_t
   const cudaStream_t s = (cudaStream_t)stream;
   const bool bf16 = dtype == FO_BF16;
   const bool wide = (cols * es) % 16 == 0 && all_aligned(R, x, 16) && all_aligned(R, (A)q, 8);
+  int vec = 4;
+  while (cols % vec || !all_aligned(R, x, vec * es)) vec /= 2;
   cudaError_t e;
   if (block_rows == 1) {
     if (!wide) {
-      const int64_t want = (rows * k.groups + 7) / 8;
+      if (rows * k.groups < INT32_MAX - 65536 * 32) k.by_groups.set((uint32_t)k.groups);
+      // (Few groups: a warp each.)
+      const int64_t n = rows * k.groups, want = n >= 16384 ? (n + 31) / 32 : (n + 7) / 8;
       const dim3 grid((unsigned)(want < 65536 ? want : 65536), R);
-      e = launch_after(bf16 ? quant_rows_kernel<__nv_bfloat16> : quant_rows_kernel<float>, grid, 256, 0, 0, s, k);
+      e = launch_after(bf16 ? rows_any<__nv_bfloat16>(vec) : rows_any<float>(vec), grid, 256, 0, 0, s, k);
       return launched(e, "quant_rows", R, rows, cols, grid.x, 256);
     }
     const int piece = bf16 ? 256 : 128;
@@ -356,7 +443,7 @@ extern "C" fo_status fo_quant_fp8(int32_t R, int64_t rows, int64_t cols, int32_t
   const int copy = !qt ? 0 : rows % 16 == 0 && all_aligned(R, (A)qt, 16) ? 16 : 8;
   k.copy8 = rows % 8 == 0 && all_aligned(R, (A)qt, 8);
   void (*kern)(const QuantParams) =
-      !wide_blocks ? (bf16 ? quant_blocks_kernel<__nv_bfloat16> : quant_blocks_kernel<float>)
+      !wide_blocks ? (bf16 ? blocks_any<__nv_bfloat16>(vec) : blocks_any<float>(vec))
       : bf16       ? blocks_wide<__nv_bfloat16>(copy)
                    : blocks_wide<float>(copy);
   e = launch_after(kern, grid, 256, 0, 0, s, k);

@@ -9,7 +9,7 @@
 // while the tensor core fills the next buffer.
 //
 // Two kernels share the work by size (choose() below says which):
-//   wide    256 x 256 tiles on CTA pairs, persistent: many rows, tensor-bound
+//   wide    256 x 256 (or 128) tiles on CTA pairs, persistent: many rows, tensor-bound
 //           (8 ranks of 8192 x 1536 x 4096: 276 us, 2.99 PFLOP/s, 68% of the
 //           tensor pipe's cycles; in a loop for seconds, under the power cap,
 //           311 us);
@@ -155,16 +155,28 @@ namespace wide {
 // is released before the last additions. A finished tile goes through shared
 // memory to TMA stores (rows stored straight from registers took 6000 cycles
 // a tile); scales are loaded a block ahead, across tiles too.
+//
+// Tiles of 128 columns keep four buffers and 64 sums a thread. For the same
+// work they take a third longer (4096 x 4096 x 4096: 60.5 us, 54.0 with 256
+// columns, which leave a sixth of their waves empty), so choose() takes them
+// where tiles of 256 would leave more than that idle (256 x 9728 x 4096:
+// 12.0 us, 15.5 with 256; 4 ranks of 3836 x 64 x 13216: 27.9 us and 38.9).
 constexpr int kThreads = 384;
-constexpr int kStages = 5;
-constexpr int kTile = 256;
-constexpr uint32_t kOperand = 128 * kBlockK;          // 16 KB: this CTA's 128 rows of A, or its half of W's 256
-constexpr uint32_t kStageBytes = 2 * kOperand;
+constexpr int kTile = 256;                            // rows
 constexpr uint32_t kOutBuf = 32 * 128;                // a warp's piece of the output: 32 rows x 128 bytes
-constexpr uint32_t kOffOut = kStages * kStageBytes;
-constexpr uint32_t kOffBar = kOffOut + 16 * kOutBuf;
-constexpr int kSmem = 1024 + (int)kOffBar + 256;
-static_assert(kSmem <= 232448, "shared memory per CTA");
+template <int TN>
+struct Cfg {
+  static constexpr int kStages = TN == 256 ? 5 : 6;
+  static constexpr int kBufs = 512 / TN;                                // TMEM buffers of TN columns
+  static constexpr int kCols = TN / 2;                                  // a warp's columns
+  static constexpr uint32_t kOperandA = 128 * kBlockK;                  // this CTA's 128 rows of A
+  static constexpr uint32_t kStageBytes = kOperandA + kCols * kBlockK;  // and its half of W's TN rows
+  static constexpr uint32_t kOffOut = kStages * kStageBytes;
+  static constexpr uint32_t kOffBar = kOffOut + 16 * kOutBuf;
+  static constexpr int kSmem = 1024 + (int)kOffBar + 256;
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+  static_assert(8 * (2 * kStages + 2 * kBufs + 2) <= 256, "barriers");
+};
 constexpr int kPanel = 8;   // row tiles that go through all column tiles together (their A stays in L2)
 
 struct Tile {
@@ -201,18 +213,18 @@ __device__ __forceinline__ uint32_t staged_word(uint32_t buf, int row, int word)
   return v;
 }
 
-// A warp's 32 rows x 128 columns at (m, n) of Y_r, through its two buffers.
-template <bool F32>
+// A warp's 32 rows x COLS columns at (m, n) of Y_r, through its two buffers.
+template <bool F32, int COLS>
 __device__ __forceinline__ void store_part(const GemmParams& p, int r, int m, int n, uint32_t bufs, int lane,
-                                           const f32x2 (&acc)[64]) {
+                                           const f32x2 (&acc)[COLS / 2]) {
   if (m >= p.M || n >= p.N) return;
-  constexpr int kBytes = F32 ? 4 : 2, kCols = 128 / kBytes, kParts = 128 / kCols;   // columns in 128 bytes
+  constexpr int kBytes = F32 ? 4 : 2, kCols = 128 / kBytes, kParts = COLS / kCols;   // columns in 128 bytes
 #pragma unroll
   for (int h0 = 0; h0 < kParts; h0 += 2) {   // both buffers, then their stores behind one fence
     if (lane == 0) bulk_wait_read<0>();   // the buffers' last stores have read them
     __syncwarp();
 #pragma unroll
-    for (int h = h0; h < h0 + 2; ++h) {
+    for (int h = h0; h < h0 + 2 && h < kParts; ++h) {
       uint32_t w[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
@@ -233,12 +245,12 @@ __device__ __forceinline__ void store_part(const GemmParams& p, int r, int m, in
       __syncwarp();
       if (lane == 0) {
         if (n + h0 * kCols < p.N) tma_store_2d(&p.tmY[r], bufs, n + h0 * kCols, m);   // clipped at Y's edges
-        if (n + h0 * kCols + kCols < p.N) tma_store_2d(&p.tmY[r], bufs + kOutBuf, n + h0 * kCols + kCols, m);
+        if (h0 + 1 < kParts && n + h0 * kCols + kCols < p.N) tma_store_2d(&p.tmY[r], bufs + kOutBuf, n + h0 * kCols + kCols, m);
         bulk_commit();
       }
     } else {   // rows of Y that no TMA store can start on: lanes along the columns
       __syncwarp();
-      for (int h = h0; h < h0 + 2; ++h) {
+      for (int h = h0; h < h0 + 2 && h < kParts; ++h) {
         const uint32_t buf = bufs + (uint32_t)(h & 1) * kOutBuf;
         const int c0 = n + h * kCols;
         uint8_t* const y = static_cast<uint8_t*>(p.Y[r]) + ((int64_t)m * p.N + c0) * kBytes;
@@ -273,19 +285,22 @@ __device__ __forceinline__ void store_part(const GemmParams& p, int r, int m, in
   }
 }
 
-template <bool F32>
+template <bool F32, int TN>
 __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid_constant__ GemmParams p) {
+  using C = Cfg<TN>;
+  constexpr int kStages = C::kStages, NB = C::kBufs;
+  constexpr uint32_t kStageBytes = C::kStageBytes;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  const uint32_t sBar = base + kOffBar;
+  const uint32_t sBar = base + C::kOffBar;
   auto full_bar = [&](uint32_t i) { return sBar + 8u * i; };
   auto empty_bar = [&](uint32_t i) { return sBar + 8u * (kStages + i); };
   auto tfull_bar = [&](uint32_t a) { return sBar + 8u * (2 * kStages + a); };
-  auto tempty_bar = [&](uint32_t a) { return sBar + 8u * (2 * kStages + 2 + a); };
-  const uint32_t done_bar = sBar + 8u * (2 * kStages + 4);
-  const uint32_t slot = sBar + 8u * (2 * kStages + 5);
+  auto tempty_bar = [&](uint32_t a) { return sBar + 8u * (2 * kStages + NB + a); };
+  const uint32_t done_bar = sBar + 8u * (2 * kStages + 2 * NB);
+  const uint32_t slot = done_bar + 8u;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(gbase + (slot - base));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + (slot - base) + 4);
 
@@ -300,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
       mbar_init(full_bar(i), 1);
       mbar_init(empty_bar(i), 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < NB; ++a) {
       mbar_init(tfull_bar(a), 1);
       mbar_init(tempty_bar(a), 16);   // eight warps of each CTA
     }
@@ -330,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
       bool ok = true;
       for (int L = unit; L < total && ok; L += units) {
         const Tile t = decode(p, L);
-        const int m0 = t.mt * kTile + (int)prank * 128, n0 = t.nt * kTile + (int)prank * 128;
+        const int m0 = t.mt * kTile + (int)prank * 128, n0 = t.nt * TN + (int)prank * C::kCols;
         for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
           if (!wait_bar(empty_bar(st), ph ^ 1u, abort_flag)) {
             ok = false;
@@ -340,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
           if (leader) mbar_arrive_expect_tx(full_bar(st), 2 * kStageBytes);   // both CTAs' loads
           const uint32_t sa = base + st * kStageBytes;
           tma_load_2d_pair(sa, &p.tmA[t.r], fb, kb * kBlockK, m0);
-          tma_load_2d_pair(sa + kOperand, &p.tmW[t.r], fb, kb * kBlockK, n0);
+          tma_load_2d_pair(sa + C::kOperandA, &p.tmW[t.r], fb, kb * kBlockK, n0);
           if (++st == kStages) st = 0, ph ^= 1u;
         }
       }
@@ -360,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
       // and barrier addresses are then the same in every lane for the
       // compiler too and stay in uniform registers, where the MMA wants them.
       // (From a loop of one lane's own, each MMA took 85 cycles to issue.)
-      constexpr uint32_t id = idesc_fp8(256, 256);
-      const uint64_t a0 = smem_desc_sw128(base, 16, 1024), w0 = smem_desc_sw128(base + kOperand, 16, 1024);
+      constexpr uint32_t id = idesc_fp8(256, TN);
+      const uint64_t a0 = smem_desc_sw128(base, 16, 1024), w0 = smem_desc_sw128(base + C::kOperandA, 16, 1024);
       uint32_t st = 0, ph = 0, b = 0, bph = 1;
       bool ok = true;
       for (int L = unit; L < total && ok; L += units) {
@@ -374,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
           tc_fence_after();
           if (elect_one()) {
             const uint64_t da = a0 + st * (kStageBytes >> 4), dw = w0 + st * (kStageBytes >> 4);
-            const uint32_t d = tmem + b * 256u;
+            const uint32_t d = tmem + b * (uint32_t)TN;
             mma_fp8<2>(d, da, dw, id, 0);
             mma_fp8<2>(d, da + 2, dw + 2, id, 1);   // 32 bytes further along the rows
             mma_fp8<2>(d, da + 4, dw + 4, id, 1);
@@ -384,8 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
           }
           __syncwarp();
           if (++st == kStages) st = 0, ph ^= 1u;
-          b ^= 1u;
-          if (b == 0) bph ^= 1u;
+          if (++b == NB) b = 0, bph ^= 1u;
         }
       }
       // Every issued MMA completes before TMEM is released.
@@ -400,8 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
     // ---------------------------------------------------------- accumulate
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int q = warp & 3, h = (warp - 4) >> 2;
-    const uint32_t at0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)h * 128u;
-    const uint32_t bufs = base + kOffOut + (uint32_t)(warp - 4) * 2 * kOutBuf;
+    const uint32_t at0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * C::kCols);
+    const uint32_t bufs = base + C::kOffOut + (uint32_t)(warp - 4) * 2 * kOutBuf;
     const uint32_t free0 = mapa_shared(tempty_bar(0), 0);
     uint32_t it = 0;
     bool ok = true;
@@ -410,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
     const float *sa = nullptr, *sw = nullptr;
     auto scales_of = [&](int L) {
       const Tile t = decode(p, L);
-      const int m = t.mt * kTile + (int)prank * 128 + q * 32 + lane, nb = t.nt * 2 + h;
+      const int m = t.mt * kTile + (int)prank * 128 + q * 32 + lane, nb = t.nt * (TN / 128) + h * C::kCols / 128;
       sa = p.sA[t.r] + (int64_t)(m < p.M ? m : 0) * p.kblocks;
       sw = p.sW[t.r] + (int64_t)(nb < p.nblocks ? nb : 0) * p.kblocks;
     };
@@ -420,9 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
       a_next = load1(sa), w_next = load1(sw);
     }
     for (int L = unit; L < total && ok; L += units) {
-      f32x2 acc[64];
+      f32x2 acc[C::kCols / 2];
 #pragma unroll
-      for (int c = 0; c < 64; ++c) acc[c] = 0ull;
+      for (int c = 0; c < C::kCols / 2; ++c) acc[c] = 0ull;
       for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
         const float s = a_next * w_next;
         const f32x2 s2 = pair_of(s, s);
@@ -432,13 +446,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
           scales_of(L + units);
           a_next = load1(sa), w_next = load1(sw);
         }
-        const uint32_t b = it & 1u;
-        if (!wait_bar(tfull_bar(b), (it >> 1) & 1u, abort_flag)) {
+        const uint32_t b = it % NB;
+        if (!wait_bar(tfull_bar(b), (it / NB) & 1u, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t at = at0 + b * 256u;
+        const uint32_t at = at0 + b * (uint32_t)TN;
         auto add = [&](int c, const uint32_t(&v)[32]) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) acc[c * 16 + j] = fma2(pair_of(v[2 * j], v[2 * j + 1]), s2, acc[c * 16 + j]);
@@ -449,22 +463,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_wide_kernel(const __grid
         tmem_ld_wait();
         reg_fence(v0);
         reg_fence(v1);
-        add(0, v0);
-        tmem_ld32(at + 64, v0);
-        add(1, v1);
-        tmem_ld32(at + 96, v1);
-        tmem_ld_wait();
-        reg_fence(v0);
-        reg_fence(v1);
+        if constexpr (TN == 256) {
+          add(0, v0);
+          tmem_ld32(at + 64, v0);
+          add(1, v1);
+          tmem_ld32(at + 96, v1);
+          tmem_ld_wait();
+          reg_fence(v0);
+          reg_fence(v1);
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_at(free0 + b * 8u);   // read: the tensor core may fill it again
-        add(2, v0);
-        add(3, v1);
+        add(C::kCols / 32 - 2, v0);
+        add(C::kCols / 32 - 1, v1);
       }
       if (ok) {
         const Tile t = decode(p, L);
-        store_part<F32>(p, t.r, t.mt * kTile + (int)prank * 128 + q * 32, t.nt * kTile + h * 128, bufs, lane, acc);
+        store_part<F32, C::kCols>(p, t.r, t.mt * kTile + (int)prank * 128 + q * 32, t.nt * TN + h * C::kCols, bufs, lane, acc);
       }
     }
     if (lane == 0) bulk_wait<0>();   // the stores are done with shared memory
@@ -762,13 +778,25 @@ cudaError_t launch(const GemmParams& k, int split, cudaStream_t s, int* grid_out
 
 }  // namespace narrow
 
+namespace wide {
+
+template <int TN>
+cudaError_t launch(const GemmParams& k, int grid, cudaStream_t s) {
+  auto kern = k.f32 ? gemm_fp8_wide_kernel<true, TN> : gemm_fp8_wide_kernel<false, TN>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<TN>::kSmem);
+  return e != cudaSuccess ? e : launch_after(kern, dim3(grid), kThreads, Cfg<TN>::kSmem, 2, s, k);
+}
+
+}  // namespace wide
+
 struct Choice {
-  int tn, split;   // tn 0: wide
+  int tn, split;   // tn 0: wide, with tiles of `split` columns
 };
 
 // Which kernel, and how it is cut: the cheapest by a model of the time in ns,
 // fitted to GB300 runs (operands in L2):
-//   wide    5200 + waves of 76 tiles x (345 a block + 800)
+//   wide    5200 + waves of 76 tiles x (345 a block + 800), with tiles of 128
+//           columns 5000 + waves x (240 a block + 600)
 //   narrow  a start and an end, then per block of a CTA's share one time when
 //           it has the SM for itself and one when two share it; a split adds
 //           the cluster's barriers and sums.
@@ -778,9 +806,11 @@ struct Choice {
 // 12288 x 4096 8.9 us split in 3, 9.1 us whole; 1 x 4096 x 4096 5.5 us split in
 // 4, 9.1 us whole.
 Choice choose(int R, int64_t M, int64_t N, int64_t kblocks) {
-  const int64_t pairs = FO_GB300_SMS / 2, tiles_w = R * ((M + 255) / 256) * ((N + 255) / 256);
-  Choice best = {0, 1};
-  int64_t least = 5200 + (tiles_w + pairs - 1) / pairs * (kblocks * 345 + 800);
+  const int64_t pairs = FO_GB300_SMS / 2, rows_w = R * ((M + 255) / 256);
+  Choice best = {0, 256};
+  int64_t least = 5200 + (rows_w * ((N + 255) / 256) + pairs - 1) / pairs * (kblocks * 345 + 800);
+  const int64_t half = 5000 + (rows_w * ((N + 127) / 128) + pairs - 1) / pairs * (kblocks * 240 + 600);
+  if (half < least) least = half, best.split = 128;
   static const struct {
     int tn, fixed, alone, shared;
   } kNarrow[3] = {{16, 3300, 180, 400}, {32, 4350, 190, 320}, {64, 4900, 280, 520}};
@@ -917,7 +947,7 @@ extern "C" fo_status fo_gemm_fp8(const fo_gemm_fp8_desc* d, int64_t M, const voi
     if (c.tn == 0 && k.vec && !encode(&k.tmY[r], Y[r], (uint64_t)d->N, (uint64_t)M, 32, es)) return FO_ERR_CUDA;
     if (r && A[r] == A[r - 1]) k.tmA[r] = k.tmA[r - 1];
     else if (!encode(&k.tmA[r], A[r], (uint64_t)d->K, (uint64_t)M, c.tn ? c.tn : 128)) return FO_ERR_CUDA;
-    if (!encode(&k.tmW[r], W[r], (uint64_t)d->K, (uint64_t)d->N, 128)) return FO_ERR_CUDA;
+    if (!encode(&k.tmW[r], W[r], (uint64_t)d->K, (uint64_t)d->N, c.tn ? 128 : c.split / 2)) return FO_ERR_CUDA;
     k.sA[r] = sA[r];
     k.sW[r] = sW[r];
     k.Y[r] = Y[r];
@@ -931,17 +961,15 @@ extern "C" fo_status fo_gemm_fp8(const fo_gemm_fp8_desc* d, int64_t M, const voi
   int grid = 0, threads = 0;
   if (c.tn == 0) {
     k.tiles_m = (int32_t)((M + 255) / 256);
-    k.tiles_n = (int32_t)((d->N + 255) / 256);
+    k.tiles_n = (int32_t)((d->N + c.split - 1) / c.split);
     k.per_rank.set((uint32_t)(k.tiles_m * k.tiles_n));
     k.per_panel.set((uint32_t)(wide::kPanel * k.tiles_n));
     k.last_panel.set((uint32_t)(k.tiles_m % wide::kPanel ? k.tiles_m % wide::kPanel : wide::kPanel));
     const int64_t total = (int64_t)R * k.tiles_m * k.tiles_n;
     if (total > INT32_MAX / 2) return FO_ERR_SHAPE;
-    auto kern = k.f32 ? wide::gemm_fp8_wide_kernel<true> : wide::gemm_fp8_wide_kernel<false>;
     threads = wide::kThreads;
     grid = 2 * (int)(total < sms / 2 ? total : sms / 2);
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, wide::kSmem);
-    if (e == cudaSuccess) e = launch_after(kern, dim3(grid), threads, wide::kSmem, 2, s, k);
+    e = c.split == 256 ? wide::launch<256>(k, grid, s) : wide::launch<128>(k, grid, s);
   } else {
     k.tiles_m = (int32_t)((M + c.tn - 1) / c.tn);
     k.tiles_n = k.nblocks;

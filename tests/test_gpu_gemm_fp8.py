@@ -138,3 +138,16 @@ def test_gemm_fp8_input_gradient_with_the_transposed_weight(dev):
     real_dy, real_w = f64(dq) * O.spread(f64(ds), (M, N), 1), f64(q) * O.spread(f64(s), (N, K), 128)
     size = np.abs(real_dy) @ np.abs(real_w)
     assert np.all(np.abs(f64(dx) - real_dy @ real_w) <= (128 * 2.0 ** -23 + 5 * 2.0 ** -24) * size + 2.0 ** -24 * np.abs(real_dy @ real_w))
+
+
+# Sizes for which tiles of 128 columns are chosen (few of 256, or narrow outputs of many rows): whole and ragged tiles,
+# rows of Y that start on 16, 8, 4 and 2 bytes, reductions shorter and longer than the ring.
+HALF_TILES = [(1, 512, 4096, 1024), (1, 430, 4100, 272), (2, 511, 1998, 1296), (1, 513, 2051, 2000), (8, 931, 248, 512),
+              (4, 3000, 63, 1040), (8, 3000, 97, 640), (2, 3000, 130, 336)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("whole", [False, True])
+@pytest.mark.parametrize("R,M,N,K", HALF_TILES)
+def test_gemm_fp8_tiles_of_128_columns(dev, R, M, N, K, whole, out):
+    product(dev, M, N, K, out, R=R, whole=whole, seed=M + N)

@@ -165,7 +165,8 @@ struct Chunk {
   }
 };
 
-// Sum over the block's nw <= NW warps, the same in every thread. `smem`: nw floats.
+// Sum over the block's nw <= NW warps, the same in every thread. `smem`: nw
+// floats, which no thread may write again before the next barrier.
 template <int NW>
 __device__ __forceinline__ float block_sum(float v, float* smem, int nw) {
   v = warp_sum(v);
@@ -173,9 +174,7 @@ __device__ __forceinline__ float block_sum(float v, float* smem, int nw) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) smem[warp] = v;
   __syncthreads();
-  v = warp_sum(lane < nw ? smem[lane] : 0.f);
-  __syncthreads();
-  return v;
+  return warp_sum(lane < nw ? smem[lane] : 0.f);
 }
 
 // Blocks have no more warps than their row needs (8191 x 4098 bf16, 33 chunks
@@ -193,13 +192,14 @@ constexpr bool kAllWarps = NW == 32 && C == 8;
 template <typename T, int VEC, int NW, int C, bool FULL>
 __global__ void __launch_bounds__(NW * 32, NW == 8 ? 6 : NW == 16 ? (C <= 2 ? 3 : 2) : 1) rmsnorm_kernel(const __grid_constant__ NormParams p) {
   using K = Chunk<T, VEC, FULL>;
-  __shared__ float smem[32];
+  __shared__ float smem[2][32];   // by turns: a barrier a row is enough
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nw = FULL || kAllWarps<NW, C> ? NW : (int)blockDim.x >> 5;
   const int r = blockIdx.y;
   grid_release();
   grid_wait();
-  for (int64_t at = blockIdx.x; at < p.rows; at += gridDim.x) {
+  int turn = 0;
+  for (int64_t at = blockIdx.x; at < p.rows; at += gridDim.x, turn ^= 1) {
     const int64_t off = at * p.H;
     float s[C][K::E];
     float sum = 0.f;
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 6 : NW == 16 ? (C <= 2 ? 3 
 #pragma unroll
       for (int c = 0; c < C; ++c) K::store(static_cast<T*>(p.h[r]) + off, c * nw + warp, lane, p.H, s[c]);
     }
-    const float rstd = rsqrtf(fmaf(block_sum<NW>(sum, smem, nw), p.inv_H, p.eps));
+    const float rstd = rsqrtf(fmaf(block_sum<NW>(sum, smem[turn], nw), p.inv_H, p.eps));
     if (p.has_rstd && threadIdx.x == 0) p.rstd[r][at] = rstd;
     if (!p.has_y && !p.has_q) continue;
 #pragma unroll
@@ -261,8 +261,9 @@ struct NormBwdParams {
   bool has_dh, has_dw, w_f32;
 };
 
-// Blocks of the backward kernel on an SM: sixteen warps' worth.
-constexpr int bwd_per_sm(int nw) { return nw <= 16 ? 16 / nw : 1; }
+// Blocks of the backward kernel on an SM: sixteen warps' worth, or 32 where a
+// thread has one chunk (of four warps or more: fewer leave too many partial sums).
+constexpr int bwd_per_sm(int nw, int c) { return c == 1 && nw >= 4 ? 32 / nw : nw <= 16 ? 16 / nw : 1; }
 
 // 16, 8 or 4 bytes to shared memory in the background, or zeros.
 template <int BYTES>
@@ -285,39 +286,39 @@ struct BwdCfg {
   static constexpr int E = Chunk<T, VEC, false>::E;
   static constexpr int kPiece = VEC * (int)sizeof(T);   // bytes of an access
   static constexpr int kPart = C * E * (int)sizeof(T);  // of a thread's part of a row of one input
-  static constexpr bool kAhead = kPiece >= 4 && NW <= 16 && C * E <= 16;
-  static constexpr int kRows = kPart <= 32 ? 3 : 2;     // the row in hand and those loaded in the background
+  static constexpr bool kAhead = kPiece >= 4 && NW <= 16 && kPart <= 64;
+  static constexpr int kRows = kPart <= 16 && NW >= 8 ? 4 : kPart <= 32 ? 3 : 2;   // the row in hand and those loaded in the background
   static constexpr bool kNext = !kAhead && NW <= 16 && C * E <= 8;
-  static constexpr bool kHold = NW <= 16;
-  static constexpr bool kWeights = kAhead || kNext;     // held
+  static constexpr bool kHold = NW <= 16 && !(kAhead && C * E > 16);   // this row's values
+  static constexpr bool kWeights = kNext || (kAhead && C * E <= 16);     // held
   // Bytes of one input's row, and of all, with nw warps.
   static constexpr __host__ __device__ int slot(int nw) { return nw * 32 * kPart; }
   static constexpr int smem(int nw) { return kAhead ? kRows * 3 * slot(nw) : 0; }
 };
 
-// Where rows come ahead, blocks have no more warps than their row needs, and as
-// many blocks an SM as make up sixteen warps (8191 x 1280 bf16: 24.8 us with
-// 5 warps, 30.9 with 8).
 // A block takes every gridDim.x-th row and keeps its columns' share of the
-// weight's gradient in registers. What else it keeps goes by the registers
-// that a thread's part of a row takes. At most 16 values that start on 4 bytes
-// or more: the weights too, and the next rows come in the background, each
-// thread its own pieces, so that the loads go on through the two barriers of a
-// row (8191 x 4098 bf16: 69 us, 185 without; 4000 x 8192 fp32: 81, 120). At
-// most 8 values of odd rows: the weights, and the next row's values in
-// registers (8191 x 4095 bf16: 98 us, 161 without). Else, with up to 16 warps,
-// this row's values; else nothing, and the second pass over the row reads it
-// again, from L2.
-// 8192 x 4096 bf16 with the residual's gradient (268 MB): 48.9 us with the
+// weight's gradient in registers. Where a thread's part of a row is at most 64
+// bytes, in accesses of 4 or more, the next rows come in the background, each
+// thread its own pieces, so that the loads go on through a row's barrier
+// (8191 x 4098 bf16: 69 us, 185 without; 4000 x 8192 fp32: 81, 120); such
+// blocks have no more warps than their rows need (8191 x 1280 bf16: 20 us,
+// 31 with the next power of two and half as many blocks). The weights stay in
+// registers too where a thread has at most 16 values; with 32 it reads them,
+// and in the second pass the row in shared memory, again (2556 x 8704 bf16:
+// 51 us, 83 from L2). At most 8 values of odd rows: the weights, and the next
+// row's values in registers (8191 x 4095 bf16: 96 us, 161 without). Else, with
+// up to 16 warps, this row's values; else nothing, and the second pass reads
+// the row from L2.
+// 8192 x 4096 bf16 with the residual's gradient (268 MB): 48.5 us with the
 // sum below, 5.5 TB/s. With the next row in registers instead of three in
 // shared memory 53 us; three blocks an SM instead of two 64 us.
 template <typename T, int VEC, int NW, int C, bool FULL>
-__global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+__global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW, C)) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
   using K = Chunk<T, VEC, FULL>;
   using Cfg = BwdCfg<T, VEC, NW, C>;
   constexpr int E = K::E;
   constexpr bool kAhead = Cfg::kAhead, kNext = Cfg::kNext, kHold = Cfg::kHold, kWeights = Cfg::kWeights;
-  __shared__ float smem[32];
+  __shared__ float smem[2][32];   // by turns: a barrier a row is enough
   extern __shared__ uint4 ring_mem[];   // kAhead: [row % Cfg::kRows][input][chunk][piece of E values][thread]
   uint8_t* const ring = reinterpret_cast<uint8_t*>(ring_mem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -403,8 +404,8 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
       for (int j = 0; j < E; ++j) from_f(0.f, nu[c][j]), from_f(0.f, nh[c][j]), from_f(0.f, nt[c][j]);   // beyond H
   }
   next(blockIdx.x);
-  int slot = 0;
-  for (int64_t row = blockIdx.x; row < p.total; row += gridDim.x) {
+  int slot = 0, turn = 0;
+  for (int64_t row = blockIdx.x; row < p.total; row += gridDim.x, turn ^= 1) {
     const int r = rank_of(row);
     const int64_t at = row - r * p.rows, off = at * p.H;
     const T* const dy = static_cast<const T*>(p.dy[r]) + off;
@@ -435,8 +436,8 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
       } else if constexpr (!kNext) {
         K::load(dy, c * nw + warp, lane, p.H, uc);
         K::load(hp, c * nw + warp, lane, p.H, hc);
-        K::load_w(p.w, p.w_f32, p.w_offset, c * nw + warp, lane, p.H, w[0]);
       }
+      if constexpr (!kWeights) K::load_w(p.w, p.w_f32, p.w_offset, c * nw + warp, lane, p.H, w[0]);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         dw[c][j] = fmaf(uc[j] * rstd, hc[j], dw[c][j]);
@@ -444,14 +445,19 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW)) rmsnorm_bwd_kernel(co
         sum = fmaf(uc[j], hc[j], sum);
       }
     }
-    const float k = block_sum<NW>(sum, smem, nw) * p.inv_H * rstd * rstd * rstd;
+    const float k = block_sum<NW>(sum, smem[turn], nw) * p.inv_H * rstd * rstd * rstd;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float(&uc)[E] = u[kHold ? c : 0];
       float(&hc)[E] = h[kHold ? c : 0];
       if constexpr (!kHold) {
-        K::load(dy, c * nw + warp, lane, p.H, uc);
-        K::load(hp, c * nw + warp, lane, p.H, hc);
+        if constexpr (kAhead) {
+          piece(slot, 0, c, uc);
+          piece(slot, 1, c, hc);
+        } else {
+          K::load(dy, c * nw + warp, lane, p.H, uc);
+          K::load(hp, c * nw + warp, lane, p.H, hc);
+        }
         K::load_w(p.w, p.w_f32, p.w_offset, c * nw + warp, lane, p.H, w[0]);
 #pragma unroll
         for (int j = 0; j < E; ++j) uc[j] *= w[0][j];
@@ -526,8 +532,8 @@ int most_warps(int n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 16 ? 
 // At least four rows each where that leaves a block for every SM: more
 // blocks' partial sums would cost more than the rows (2529 x 128: 9.5 us with
 // as many blocks as fit).
-int bwd_blocks(int64_t total, int nw) {
-  const int64_t most = bwd_per_sm(nw) * FO_GB300_SMS, least = total < FO_GB300_SMS ? total : FO_GB300_SMS;
+int bwd_blocks(int64_t total, int nw, int c) {
+  const int64_t most = bwd_per_sm(nw, c) * FO_GB300_SMS, least = total < FO_GB300_SMS ? total : FO_GB300_SMS;
   const int64_t want = total / 4 > least ? total / 4 : least;
   return (int)(want < most ? want : most);
 }
@@ -599,10 +605,10 @@ struct LaunchBwd {
   template <typename T, int VEC, int NW, int C, bool FULL>
   fo_status operator()(int n) const {
     const int nw = BwdCfg<T, VEC, NW, C>::kAhead ? warps_for(n) : NW;
-    const int grid = *blocks = bwd_blocks(k.total, nw);
+    const int grid = *blocks = bwd_blocks(k.total, nw, C);
     const int smem = BwdCfg<T, VEC, NW, C>::smem(nw);
     auto kern = rmsnorm_bwd_kernel<T, VEC, NW, C, FULL>;
-    if (smem > 48 * 1024) {
+    if (smem > 47 * 1024) {   // (with the static part, beyond what needs no leave)
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return launched(e, "rmsnorm_bwd", R, k.rows, k.H, grid, nw * 32);
     }
@@ -668,15 +674,16 @@ extern "C" fo_status fo_rmsnorm_bwd_workspace(const fo_norm_desc* d, int64_t row
   const fo_status st = check_desc(d, rows);
   if (st) return st;
   if (!bytes) return FO_ERR_INVALID_ARG;
-  // Enough for rows on the 16-byte grid (chunks of 256 or 128 columns, maybe on
-  // fewer warps than the kernel's most) and off it (of 128).
-  const int cols = d->dtype == FO_BF16 ? 256 : 128, chunks = (d->H + cols - 1) / cols;
-  const int off = (d->H + 127) / 128;
-  const int warps[4] = {warps_for(chunks), most_warps(chunks), warps_for(off), most_warps(off)};
+  // Enough for rows on the 16-byte grid (chunks of 256 or 128 columns) and off
+  // it (of 128), with as many warps as the rows need and with the kernel's most.
+  const int cols[2] = {d->dtype == FO_BF16 ? 256 : 128, 128};
   size_t n = 0;
-  for (const int w : warps) {
-    const size_t b = (size_t)bwd_blocks(rows * d->R, w) * (size_t)d->H * sizeof(float);
-    n = b > n ? b : n;
+  for (const int c : cols) {
+    const int chunks = (d->H + c - 1) / c;
+    for (const int w : {warps_for(chunks), most_warps(chunks)}) {
+      const size_t b = (size_t)bwd_blocks(rows * d->R, w, chunks_for(chunks)) * (size_t)d->H * sizeof(float);
+      n = b > n ? b : n;
+    }
   }
   *bytes = n ? n : 16;
   return FO_OK;

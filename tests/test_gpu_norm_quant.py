@@ -303,3 +303,36 @@ def test_norm_of_rows_that_start_anywhere(dev, rows, H, at, dtype):
     for k in ("h", "y", "dx", "q"):
         buf, t = moved[k]
         assert (buf[:pad + at] == 7).all() and (buf[pad + at + t.numel():] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("H", [512, 640, 1024, 1280, 1408, 2048, 2304, 4096, 4352, 5610, 6016, 8192, 8704, 8886, 16384])
+def test_norm_backward_of_many_rows(dev, H, residual, dtype):
+    """More rows than blocks, at every number of warps and chunks: each ring of rows goes round, and the same row
+    gives the same gradient wherever it stands."""
+    g = torch.Generator().manual_seed(H)
+    T, few, times = TYPES[dtype], 7, 700
+    dy, h, dh = (torch.randn(few, H, generator=g).to(T).to(dev) for _ in range(3))
+    w = (1 + 0.2 * torch.randn(H, generator=g)).to(T).to(dev)
+    r = (0.5 + torch.rand(few, generator=g)).to(dev)
+    d = B.fo_norm_desc(H, dtype=dtype)
+
+    def run(n, dy, dh, h, r):
+        dx, dw = empty(dev, n, H, dtype=T), empty(dev, H)
+        ws = torch.empty(B.fo_rmsnorm_bwd_workspace(d, n), dtype=torch.uint8, device=dev)
+        B.fo_rmsnorm_bwd(d, n, [dy], [dh] if residual else None, [h], w, [r], [dx], dw, ws)
+        return dx, dw
+
+    dx, dw = run(few, dy, dh, h, r)
+    many = [t.repeat(times, *[1] * (t.dim() - 1)) for t in (dy, dh, h, r)]
+    dx2, dw2 = run(few * times, *many)
+    assert torch.equal(dx2, dx.repeat(times, 1))
+    # Sums of 4900 terms against 700 times sums of 7 in fp32: 4900 roundings of the magnitudes' sum.
+    size = (dy.double() * h.double() * r.double()[:, None]).abs().sum(dim=0) * times
+    assert ((dw2.double() - times * dw.double()).abs() <= 4910 * U * size).all()
+    want, _ = O.rmsnorm_bwd(f64(dy), f64(dh) if residual else None, f64(h), f64(w), f64(r))
+    a = np.abs(f64(r)[:, None] * f64(dy) * f64(w))
+    b = np.abs(f64(h)) * (f64(r) ** 3 * np.mean(np.abs(f64(dy) * f64(w) * f64(h)), axis=1))[:, None]
+    c = np.abs(f64(dh)) if residual else 0.0
+    assert np.all(np.abs(f64(dx) - want) <= HALF[dtype] * np.abs(want) * (1 + 2.0 ** -7) + 4 * U * (a + c) + 90 * U * b)

@@ -593,8 +593,17 @@ struct LaunchFwd {
   template <typename T, int VEC, int NW, int C, bool FULL>
   fo_status operator()(int n) const {
     const int nw = kAllWarps<NW, C> ? NW : warps_for(n);
-    const dim3 grid((unsigned)k.rows, R);
-    return launched(launch_after(rmsnorm_kernel<T, VEC, NW, C, FULL>, grid, nw * 32, 0, 0, s, k), "rmsnorm", R, k.rows, k.H, (int)k.rows, nw * 32);
+    // The GPU starts about a block a nanosecond, which is longer than a narrow
+    // row takes: its blocks take several, as many blocks as an SM holds, twice
+    // that from five warps on (16384 x 512 bf16: 8.1 us, 17.1 with a block for
+    // every row; 16384 x 128: 5.4 and 17.1; 8191 x 1280: 8.7 and 10.1).
+    int64_t blocks = k.rows;
+    if (C == 1) {
+      const int64_t most = (int64_t)FO_GB300_SMS * (nw == 1 ? 32 : nw <= 4 ? 64 / nw : 128 / nw) / R;
+      if (blocks > most) blocks = most;
+    }
+    const dim3 grid((unsigned)blocks, R);
+    return launched(launch_after(rmsnorm_kernel<T, VEC, NW, C, FULL>, grid, nw * 32, 0, 0, s, k), "rmsnorm", R, k.rows, k.H, (int)blocks, nw * 32);
   }
 };
 struct LaunchBwd {

@@ -336,3 +336,25 @@ def test_norm_backward_of_many_rows(dev, H, residual, dtype):
     b = np.abs(f64(h)) * (f64(r) ** 3 * np.mean(np.abs(f64(dy) * f64(w) * f64(h)), axis=1))[:, None]
     c = np.abs(f64(dh)) if residual else 0.0
     assert np.all(np.abs(f64(dx) - want) <= HALF[dtype] * np.abs(want) * (1 + 2.0 ** -7) + 4 * U * (a + c) + 90 * U * b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [64, 128, 201, 256, 390, 512, 768, 1000, 1280, 2048])
+def test_rmsnorm_of_many_rows(dev, H, dtype):
+    """More rows than blocks: the same row gives the same values wherever it stands, on every shard."""
+    g = torch.Generator().manual_seed(H)
+    few, times, R = 9, 900, 2
+    x, res = (draw(g, few, H, dtype, dev) for _ in range(2))
+    w = (1 + 0.2 * torch.randn(H, generator=g)).to(TYPES[dtype]).to(dev)
+    d = B.fo_norm_desc(H, R=R, dtype=dtype)
+
+    def run(n, x, res):
+        outs = [[empty(dev, n, H, dtype=TYPES[dtype]) for _ in range(R)] for _ in range(2)]
+        outs += [[empty(dev, n, H, dtype=torch.uint8) for _ in range(R)], [empty(dev, n, -(-H // 128)) for _ in range(R)],
+                 [empty(dev, n) for _ in range(R)]]
+        B.fo_rmsnorm(d, n, [x, res], [res, x], w, *outs)
+        return outs
+
+    for a, b in zip(run(few, x, res), run(few * times, x.repeat(times, 1), res.repeat(times, 1))):
+        for s, m in zip(a, b):
+            assert torch.equal(m, s.repeat(times, *[1] * (s.dim() - 1)))

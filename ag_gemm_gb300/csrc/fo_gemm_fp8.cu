@@ -589,8 +589,9 @@ __global__ void __launch_bounds__(kThreads) gemm_fp8_narrow_kernel(const __grid_
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // While the kernel before this one ends, the CTA's first weights come into
-  // L2: a hint that reads nothing, so it need not wait.
-  if (warp == 0 && elect_one())
+  // L2: a hint that reads nothing, so it need not wait. (From every tile of A's
+  // rows the same hints would queue for the same lines.)
+  if (warp == 0 && m0 == 0 && elect_one())
     for (int i = 0; i < blocks && i < kPrefetchBlocks; ++i) prefetch_box(&p.tmW[r], (kb0 + i) * kBlockK, nb * 128);
   __syncwarp();
   grid_wait();
@@ -795,34 +796,42 @@ struct Choice {
 
 // Which kernel, and how it is cut: the cheapest by a model of the time in ns,
 // fitted to GB300 runs (operands in L2):
-//   wide    5200 + waves of 76 tiles x (345 a block + 800), with tiles of 128
-//           columns 5000 + waves x (240 a block + 600)
-//   narrow  a start and an end, then per block of a CTA's share one time when
-//           it has the SM for itself and one when two share it; a split adds
-//           the cluster's barriers and sums.
+//   wide    3500 + waves of 76 tiles x (345 a block + 1200), with tiles of
+//           128 columns 3300 + waves x (240 a block + 1000)
+//   narrow  a start and an end for each wave, 10 for each tile of A's rows (all
+//           of them read the same weights at once), then per block of a CTA's
+//           share one time when it has the SM for itself and one when two share
+//           it; a split adds the cluster's barriers and sums, and its clusters
+//           fill the GPU less well.
 // Both sides, measured: 128 x 12288 x 4096 wide 16.5 us, narrow 20.8 us; 128 x
 // 4096 x 4096 wide 16.2 us, narrow 10.1 us (64 rows, split 4); 333 x 1000 x
 // 1744 wide 11.1 us, narrow 6.8 us (32 rows, no split; split 3: 7.7 us); 4 x
 // 12288 x 4096 8.9 us split in 3, 9.1 us whole; 1 x 4096 x 4096 5.5 us split in
-// 4, 9.1 us whole.
+// 4, 9.1 us whole; 6765 x 64 x 1104 wide (128) 5.6 us, narrow 8.5; 2729 x 64 x
+// 9952 11.2 us split in 6, 17.0 in 8 (43 clusters, of which 30 fit).
 Choice choose(int R, int64_t M, int64_t N, int64_t kblocks) {
   const int64_t pairs = FO_GB300_SMS / 2, rows_w = R * ((M + 255) / 256);
   Choice best = {0, 256};
-  int64_t least = 5200 + (rows_w * ((N + 255) / 256) + pairs - 1) / pairs * (kblocks * 345 + 800);
-  const int64_t half = 5000 + (rows_w * ((N + 127) / 128) + pairs - 1) / pairs * (kblocks * 240 + 600);
+  int64_t least = 3500 + (rows_w * ((N + 255) / 256) + pairs - 1) / pairs * (kblocks * 345 + 1200);
+  const int64_t half = 3300 + (rows_w * ((N + 127) / 128) + pairs - 1) / pairs * (kblocks * 240 + 1000);
   if (half < least) least = half, best.split = 128;
   static const struct {
     int tn, fixed, alone, shared;
   } kNarrow[3] = {{16, 3300, 180, 400}, {32, 4350, 190, 320}, {64, 4900, 280, 520}};
+  // CTAs that the GPU holds in whole clusters of 1 .. 8: one an SM (the runtime's
+  // occupancy query), and two (where more than these took another wave).
+  static const int kAlone[narrow::kMaxSplit] = {152, 152, 138, 144, 140, 138, 105, 120};
+  static const int kShared[narrow::kMaxSplit] = {304, 304, 288, 288, 280, 276, 210, 240};
   for (const auto& v : kNarrow) {
     if (v.tn > 16 && v.tn >= 2 * M) break;   // more than half of the columns would be empty
-    const int64_t tiles = R * ((M + v.tn - 1) / v.tn) * ((N + 127) / 128);
+    const int64_t tiles_m = (M + v.tn - 1) / v.tn, tiles = R * tiles_m * ((N + 127) / 128);
     if (tiles > 64 * FO_GB300_SMS) continue;   // long past the point where wide wins
     for (int64_t k = 1; k <= narrow::kMaxSplit && k <= kblocks; ++k) {
-      const int64_t full = tiles * k / (2 * FO_GB300_SMS), rest = tiles * k % (2 * FO_GB300_SMS);
-      const int64_t block = full * v.shared + (rest == 0 ? 0 : rest <= FO_GB300_SMS ? v.alone : v.shared);
+      const int64_t slots = kShared[k - 1], alone = kAlone[k - 1];
+      const int64_t full = tiles * k / slots, rest = tiles * k % slots;
+      const int64_t block = full * v.shared + (rest == 0 ? 0 : rest <= alone ? v.alone : v.shared);
       const int64_t waves = full + (rest ? 1 : 0);
-      const int64_t cost = v.fixed + (waves - 1) * v.fixed / 2 + (k > 1 ? 1200 : 0) + (kblocks + k - 1) / k * block;
+      const int64_t cost = waves * v.fixed + tiles_m * 10 + (k > 1 ? 1200 : 0) + (kblocks + k - 1) / k * block;
       if (cost < least) least = cost, best = {v.tn, (int)k};
     }
   }

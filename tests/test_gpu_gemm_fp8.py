@@ -151,3 +151,17 @@ HALF_TILES = [(1, 512, 4096, 1024), (1, 430, 4100, 272), (2, 511, 1998, 1296), (
 @pytest.mark.parametrize("R,M,N,K", HALF_TILES)
 def test_gemm_fp8_tiles_of_128_columns(dev, R, M, N, K, whole, out):
     product(dev, M, N, K, out, R=R, whole=whole, seed=M + N)
+
+
+# A size for each number of A's rows on a tile (16, 32, 64) and CTAs that share a reduction (1 to 8), as chosen; odd
+# outputs, reductions that no number of CTAs divides.
+SHARES = [(3, 1, 1945, 2000), (3, 1, 1555, 1376), (3, 1, 932, 1312), (1, 1, 33, 1056), (1, 1, 33, 1440), (1, 1, 32, 1584), (1, 1, 35, 912),
+          (3, 49, 3697, 32), (3, 772, 35, 2960), (3, 942, 33, 1840), (1, 1057, 37, 2480), (1, 765, 37, 2080), (3, 194, 33, 4240),
+          (2, 476, 33, 3280), (1, 891, 33, 2016), (3, 1538, 32, 4928), (2, 1370, 33, 3184), (1, 1983, 33, 3664), (1, 1785, 35, 4112),
+          (1, 1296, 32, 6352), (1, 1824, 67, 2624), (2, 921, 35, 3600), (2, 60, 250, 9008), (1, 128, 4096, 4096)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("R,M,N,K", SHARES)
+def test_gemm_fp8_shares_of_the_reduction(dev, R, M, N, K, out):
+    product(dev, M, N, K, out, R=R, seed=M + N + K)

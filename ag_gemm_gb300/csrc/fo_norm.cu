@@ -309,8 +309,8 @@ struct BwdCfg {
 // row's values in registers (8191 x 4095 bf16: 96 us, 161 without). Else, with
 // up to 16 warps, this row's values; else nothing, and the second pass reads
 // the row from L2.
-// 8192 x 4096 bf16 with the residual's gradient (268 MB): 48.5 us with the
-// sum below, 5.5 TB/s. With the next row in registers instead of three in
+// 8192 x 4096 bf16 with the residual's gradient (268 MB): 45.7 us with the
+// sum below, 5.9 TB/s (48.5 with partial sums stored value by value). With the next row in registers instead of three in
 // shared memory 53 us; three blocks an SM instead of two 64 us.
 template <typename T, int VEC, int NW, int C, bool FULL>
 __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW, C)) rmsnorm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
@@ -476,37 +476,52 @@ __global__ void __launch_bounds__(NW * 32, bwd_per_sm(NW, C)) rmsnorm_bwd_kernel
     }
     slot = slot + 1 == Cfg::kRows ? 0 : slot + 1;
   }
-  if (p.has_dw) {
+  if (p.has_dw) {   // (one value a store, a sector of memory would be written eight times over)
+    float* const part = p.part + (int64_t)blockIdx.x * p.H;
+    constexpr int kStore = VEC >= 4 ? 4 : VEC;
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
+      for (int j = 0; j < E; j += kStore) {
         const int col = K::col(c * nw + warp, lane, j);
-        if (FULL || col < p.H) p.part[(int64_t)blockIdx.x * p.H + col] = dw[c][j];
+        if (FULL || col < p.H) {
+          if constexpr (kStore == 4)
+            *reinterpret_cast<float4*>(part + col) = make_float4(dw[c][j], dw[c][j + 1], dw[c][j + 2], dw[c][j + 3]);
+          else if constexpr (kStore == 2)
+            *reinterpret_cast<float2*>(part + col) = make_float2(dw[c][j], dw[c][j + 1]);
+          else
+            part[col] = dw[c][j];
+        }
       }
   }
 }
 
-// dweight[c] = sum of the blocks' partial sums: a warp adds every 32nd
-// block's for 32 columns, then the 32 warps' sums are added in order. (As
-// many loads in flight as there are: with 8 warps the loads' latency alone,
-// five times over, was 5 us of the backward pass.)
-constexpr int kDwWarps = 32;
-__global__ void __launch_bounds__(kDwWarps * 32) dweight_kernel(const float* part, int blocks, int H, float* dw) {
-  __shared__ float smem[kDwWarps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
+// dweight[c] = sum of the blocks' partial sums. A block has COLS columns; a
+// warp adds every (warps * 32 / COLS)th block's for them, 32 / COLS at a time,
+// then the lanes' and the warps' sums are added in order. As many loads in
+// flight as there are: the loads' latency is what counts (8192 x 4096 bf16,
+// 304 partial sums: 3.5 us of the backward pass with 32 warps, 8 with eight),
+// and no more warps than there are sums for (18 x 4096: 5.4 us both kernels,
+// 6.7 with 32 warps).
+template <int COLS>
+__global__ void __launch_bounds__(1024) dweight_kernel(const float* part, int blocks, int H, float* dw) {
+  constexpr int kSub = 32 / COLS;
+  __shared__ float smem[32][COLS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = (int)blockDim.x >> 5;
+  const int c = blockIdx.x * COLS + lane % COLS;
   float s = 0.f;
   grid_release();
   grid_wait();
   if (c < H) {
 #pragma unroll 10
-    for (int b = warp; b < blocks; b += kDwWarps) s += part[(int64_t)b * H + c];
+    for (int b = warp * kSub + lane / COLS; b < blocks; b += warps * kSub) s += part[(int64_t)b * H + c];
   }
-  smem[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < H) {
 #pragma unroll
-    for (int k = 1; k < kDwWarps; ++k) s += smem[k][lane];
+  for (int o = COLS; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane < COLS) smem[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && lane < COLS && c < H) {
+    for (int k = 1; k < warps; ++k) s += smem[k][lane];
     dw[c] = s;
   }
 }
@@ -753,6 +768,11 @@ extern "C" fo_status fo_rmsnorm_bwd(const fo_norm_desc* d, int64_t rows, const v
   int grid = 0;
   if ((st = by_type(d->dtype, v.vec, d->H, LaunchBwd{k, s, R, &grid}))) return st;
   if (!dweight) return FO_OK;
-  const int cols = (d->H + 31) / 32;
-  return launched(launch_after(dweight_kernel, dim3(cols), kDwWarps * 32, 0, 0, s, (const float*)k.part, grid, d->H, dweight), "rmsnorm_dweight", R, grid, d->H, cols, kDwWarps * 32);
+  // Slices of 8 columns where 32 would make few blocks.
+  const int cols = d->H >= 32 * FO_GB300_SMS / 2 ? 32 : 8, slices = (d->H + cols - 1) / cols;
+  int warps = (grid + 4 * (32 / cols) - 1) / (4 * (32 / cols));
+  warps = warps < 2 ? 2 : warps > 32 ? 32 : warps;
+  auto kern = cols == 32 ? dweight_kernel<32> : dweight_kernel<8>;
+  return launched(launch_after(kern, dim3(slices), warps * 32, 0, 0, s, (const float*)k.part, grid, d->H, dweight),
+                  "rmsnorm_dweight", R, grid, d->H, slices, warps * 32);
 }

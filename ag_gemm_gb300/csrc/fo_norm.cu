@@ -232,13 +232,12 @@ __global__ void __launch_bounds__(NW * 32, NW == 8 ? 6 : NW == 16 ? (C <= 2 ? 3 
       float w[K::E];
       K::load_w(p.w, p.w_f32, p.w_offset, chunk, lane, p.H, w);
 #pragma unroll
-      for (int j = 0; j < K::E; ++j) s[c][j] = s[c][j] * rstd * w[j];
+      for (int j = 0; j < K::E; j += 2)
+        halves(mul2(mul2(pair_of(s[c][j], s[c][j + 1]), pair_of(rstd, rstd)), pair_of(w[j], w[j + 1])), s[c][j], s[c][j + 1]);
       if (p.has_y) K::store(static_cast<T*>(p.y[r]) + off, chunk, lane, p.H, s[c]);
       if (p.has_q) {
         const float scale = scale_of(lanes_max<K::GROUP_LANES>(amax_of(s[c])));
-        const float inv = inverse_of(scale);
-#pragma unroll
-        for (int j = 0; j < K::E; ++j) s[c][j] *= inv;
+        divide_by(scale, s[c]);
         K::store_e4m3(p.q[r] + off, chunk, lane, p.H, s[c]);
         const int group = K::col(chunk, lane, 0) / FO_FP8_BLOCK;
         if (lane % K::GROUP_LANES == 0 && group < p.groups) p.scale[r][at * p.groups + group] = scale;

@@ -121,9 +121,10 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
       if (u >= n) break;
       float v[4];
       x[i].get(v);
-      const float scale = scale_of(lanes_max<32>(amax_of(v))), inv = inverse_of(scale);
+      const float scale = scale_of(lanes_max<32>(amax_of(v)));
+      divide_by(scale, v);
       const int left = (int)(p.cols - c0[i]);
-      store_line(p.q[r] + row[i] * p.cols + c0[i], e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv), lane,
+      store_line(p.q[r] + row[i] * p.cols + c0[i], e4m3x4(v[0], v[1], v[2], v[3]), lane,
                  left < FO_FP8_BLOCK ? left : FO_FP8_BLOCK);
       if (lane == 0) p.scale[r][u] = scale;
     }
@@ -161,10 +162,9 @@ __global__ void __launch_bounds__(256) quant_rows_wide_kernel(const __grid_const
     for (int i = 0; i < kUnroll; ++i) {
       float v[E];
       Vec16<T>::unpack(raw[i], v);
-      const float scale = scale_of(lanes_max<kLanes>(amax_of(v))), inv = inverse_of(scale);
+      const float scale = scale_of(lanes_max<kLanes>(amax_of(v)));
       if ((!ONE && w + i * step >= n) || col[i] >= p.cols) continue;
-#pragma unroll
-      for (int j = 0; j < E; ++j) v[j] *= inv;
+      divide_by(scale, v);
       uint8_t* q = p.q[r] + row[i] * p.cols + col[i];
       if constexpr (E == 8)
         *reinterpret_cast<uint2*>(q) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant
   amax = lanes_max<32>(amax);
   if (lane == 0) smem[warp] = amax;
   __syncthreads();
-  const float scale = scale_of(lanes_max<8>(smem[lane & 7])), inv = inverse_of(scale);
+  const float scale = scale_of(lanes_max<8>(smem[lane & 7]));
   if (threadIdx.x == 0) {
     p.scale[r][(int64_t)blockIdx.y * p.groups + blockIdx.x] = scale;
     if (p.qt[r]) p.scale_t[r][(int64_t)blockIdx.x * p.row_blocks + blockIdx.y] = scale;
@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant
     for (int i = 0; i < 4; ++i) {
       float v[4];
       x[4 * g + i].get(v);
-      b[i] = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+      divide_by(scale, v);
+      b[i] = e4m3x4(v[0], v[1], v[2], v[3]);
       const int row = warp * 16 + 4 * g + i;
       if (row < rows) store_line(p.q[r] + (r0 + row) * p.cols + c0, b[i], lane, cols);
     }
@@ -245,7 +246,36 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant
     store_line(p.qt[r] + (c0 + c) * p.rows + r0, tile[c * 32 + (lane ^ (c >> 2))], lane, rows);
 }
 
-// 12288 x 4096 bf16 with the copy (201 MB): 33.7 us, 6.0 TB/s (223 us with bytes
+// Largest magnitude of the values in N x 16 bytes, NaN if one is NaN. Those of
+// bf16, as 15-bit numbers, have the order of their values, with infinity above
+// the finite ones and NaN above infinity: two at a time as they are read, in
+// two thirds of the instructions that their fp32 forms take (12288 x 4096 with
+// the copy: 33.8 us, 36.4 from the fp32 forms; but rows, with 8 values a
+// thread, 17.1 against 16.6).
+template <typename T, int N>
+__device__ __forceinline__ float amax_raw(const uint4 (&raw)[N]) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t a = __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu);
+      const uint32_t b = __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu);
+      m = __vmaxu2(m, __vmaxu2(a, b));
+    }
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  } else {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float v[4];
+      Vec16<float>::unpack(raw[i], v);
+      m = max_nan(m, amax_of(v));
+    }
+    return m;
+  }
+}
+
+// 12288 x 4096 bf16 with the copy (201 MB): 33.8 us, 6.0 TB/s (223 us with bytes
 // loaded and stored one by one). The stores are marked as streaming, since a
 // weight's copies are read much later, and the copy's are 16 bytes wide where
 // its lines allow it: 36.0 us with plain stores of 8 bytes, 34.7 with
@@ -257,7 +287,7 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant
 // reads meet in a bank.
 // COPY: 0 none, 8 the copy's lines start on 8 bytes or anywhere, 16 on 16.
 template <typename T, int COPY>
-__global__ void __launch_bounds__(256) quant_blocks_wide_kernel(const __grid_constant__ QuantParams p) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) quant_blocks_wide_kernel(const __grid_constant__ QuantParams p) {
   constexpr int V = 8 / Vec16<T>::N;   // 16-byte loads for 8 values
   __shared__ float smem[8];
   __shared__ uint2 tile[COPY ? 128 * 16 : 1];
@@ -277,19 +307,10 @@ __global__ void __launch_bounds__(256) quant_blocks_wide_kernel(const __grid_con
       if (in && row0 + i < p.rows)
         raw[i][k] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.x[r]) + (row0 + i) * p.cols + col) + k);
     }
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      float v[Vec16<T>::N];
-      Vec16<T>::unpack(raw[i][k], v);
-      amax = max_nan(amax, amax_of(v));
-    }
-  amax = lanes_max<32>(amax);
+  const float amax = lanes_max<32>(amax_raw<T>(reinterpret_cast<const uint4(&)[8 * V]>(raw)));
   if (lane == 0) smem[warp] = amax;
   __syncthreads();
-  const float scale = scale_of(lanes_max<8>(smem[lane & 7])), inv = inverse_of(scale);
+  const float scale = scale_of(lanes_max<8>(smem[lane & 7]));
   uint32_t lo[8], hi[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -300,8 +321,7 @@ __global__ void __launch_bounds__(256) quant_blocks_wide_kernel(const __grid_con
       Vec16<T>::unpack(raw[i][0], reinterpret_cast<float(&)[Vec16<T>::N]>(v[0]));
       Vec16<T>::unpack(raw[i][V - 1], reinterpret_cast<float(&)[Vec16<T>::N]>(v[4]));
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= inv;
+    divide_by(scale, v);
     lo[i] = e4m3x4(v[0], v[1], v[2], v[3]);
     hi[i] = e4m3x4(v[4], v[5], v[6], v[7]);
     if (in && row0 + i < p.rows)

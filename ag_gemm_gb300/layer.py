@@ -38,6 +38,7 @@ per-rank weight-gradient GEMMs).
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 from typing import Dict, List
 
@@ -189,6 +190,15 @@ class TpspLayerProjections:
         return [B.fo_status_query(p, self.ws[k])[0] for k, p in self.plans.items()]
 
 
+def _on(stream):
+    """torch's own work on a call's stream: None (the current one), a torch stream or a raw handle."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):   # (torch takes an external handle 0 for none)
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 class Fp8AttentionBlock:
     """The attention half of a TP-SP layer with its projection in 8 bits, from the residual stream to the attention's
     output, and the way of the gradients back through what precedes the attention:
@@ -202,11 +212,15 @@ class Fp8AttentionBlock:
         rotary^-1 back into packed rows                                                       fo_rope
         QKV       dY_r in 8 bits, dn = sum_r dY_r . Wqkv_r (the weight's transposed copy)     fo_quant_fp8, fo_gemm_fp8,
                                                                                               fo_reduce_scatter_f32
+                  (the products' partial sums by the unfused reduce kernel; the sum is rounded to bf16 by a torch copy)
         norm      dx (= d residual) with the residual path's gradient, dweight                fo_rmsnorm_bwd
 
     The T tokens of the R ranks' shards lie back to back, so the norm is one call and its output is the all-gathered
-    operand of every rank's product. Weights are given in bf16 ([3H/R x H] a rank, rows Q | K | V, the nn.Linear
-    layout) and quantised by set_weights, once for each version of them."""
+    operand of every rank's product. The projections' weight gradients are not part of the block: they contract the
+    tokens in bf16 (fo_gemm_partials_sharded), and the block keeps the norm's output in 8 bits alone. All of a call's
+    work is on its stream, and what it returns are the block's own buffers, written again by the next call. Weights are
+    given in bf16 ([3H/R x H] a rank, rows Q | K | V, the nn.Linear layout) and quantised by set_weights, once for each
+    version of them."""
 
     def __init__(self, shape: LayerShape = LayerShape(), *, causal=True, eps=1e-6, rope_base=10000.0, device="cuda",
                  **rope):
@@ -244,6 +258,7 @@ class Fp8AttentionBlock:
         self.d_qkv, self.d8, self.d_scale = each(T, 3 * width), each(T, 3 * width, dtype=e4m3), each(T, nb, dtype=f32)
         self.dn_part, self.dn_whole = each(T, H, dtype=f32), new(T, H, dtype=f32)
         self.dn = list(self.dn_whole.split(T // R))
+        self.dn_rounded = new(T, H)
         self.dx, self.dweight = new(T, H), new(H, dtype=f32)
         self.ws_attn = new(B.fo_workspace_size(self.plan), dtype=torch.uint8)
         B.fo_workspace_init(self.plan, self.ws_attn)
@@ -283,8 +298,9 @@ class Fp8AttentionBlock:
         B.fo_quant_fp8(T, 3 * width, self.d_qkv, self.d8, self.d_scale, stream=stream)
         B.fo_gemm_fp8(self.qkv_dx, T, self.d8, self.d_scale, self.Wt, self.Wt_scale, self.dn_part, self.ws, stream)
         B.fo_reduce_scatter_f32(self.sum_plan, self.dn_part, self.dn, stream)
-        dn = self.dn_whole.to(torch.bfloat16)
-        B.fo_rmsnorm_bwd(self.norm, T, [dn], None if dh is None else [dh], [self.h], self.weight, [self.rstd],
+        with _on(stream):
+            self.dn_rounded.copy_(self.dn_whole)
+        B.fo_rmsnorm_bwd(self.norm, T, [self.dn_rounded], None if dh is None else [dh], [self.h], self.weight, [self.rstd],
                          [self.dx], self.dweight, self.ws_norm, stream)
         return self.dx, self.dweight
 

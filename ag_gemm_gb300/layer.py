@@ -304,5 +304,6 @@ class Fp8AttentionBlock:
                          [self.dx], self.dweight, self.ws_norm, stream)
         return self.dx, self.dweight
 
-    def status(self) -> List[int]:
-        return [B.fo_status_query(self.plan, self.ws_attn)[0], B.fo_ops_status_query(self.ws)[0]]
+    def status(self, stream=None) -> List[int]:
+        """The status words once the stream's work so far is done (0: no device wait has run out)."""
+        return [B.fo_status_query(self.plan, self.ws_attn, stream)[0], B.fo_ops_status_query(self.ws, stream)[0]]

@@ -76,6 +76,17 @@ def test_block_on_a_stream_that_is_not_current(dev, how):
             assert all(torch.equal(a, b) for a, b in zip(results(block), want))
 
 
+def test_block_status_waits_for_the_stream_it_is_asked_on(dev):
+    block, x, res, pos, grads, dh = make(dev, T=256)
+    stream = torch.cuda.Stream()
+    for s in (stream, stream.cuda_stream):
+        torch.cuda.synchronize()
+        busy(dev, stream)
+        block.forward(x, res, pos, stream=s)
+        assert block.status(stream=s) == [0, 0]
+        assert stream.query()
+
+
 def test_block_backward_from_a_graph(dev):
     block, x, res, pos, grads, dh = make(dev, R=4, seed=3)
     block.forward(x, res, pos)

@@ -266,6 +266,7 @@ class Fp8AttentionBlock:
         self.ws = new(size, dtype=torch.uint8)
         B.fo_ops_workspace_init(self.ws)
         self.ws_norm = new(B.fo_rmsnorm_bwd_workspace(self.norm, T), dtype=torch.uint8)
+        torch.cuda.current_stream(dev).synchronize()   # the workspaces are zeroed before a call on any other stream
 
     def set_weights(self, weight, Wqkv, Wo, stream=None):
         """The norm's weight [H], each rank's Wqkv [3H/R x H] and Wo [H/R x H], bf16."""

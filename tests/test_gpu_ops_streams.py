@@ -87,6 +87,15 @@ def test_block_status_waits_for_the_stream_it_is_asked_on(dev):
         assert stream.query()
 
 
+def test_block_is_ready_for_any_stream_once_it_is_made(dev):
+    # The workspaces are zeroed on the stream that is current: a first call on another one finds them zeroed.
+    first = torch.cuda.Stream()
+    busy(dev, first)
+    with torch.cuda.stream(first):
+        block = Fp8AttentionBlock(LayerShape(R=2, T=256, H=256, F=256), device=dev)
+    assert first.query()
+
+
 def test_block_backward_from_a_graph(dev):
     block, x, res, pos, grads, dh = make(dev, R=4, seed=3)
     block.forward(x, res, pos)

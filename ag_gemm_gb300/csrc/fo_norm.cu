@@ -631,8 +631,12 @@ struct LaunchBwd {
     const int grid = *blocks = bwd_blocks(k.total, nw, C);
     const int smem = BwdCfg<T, VEC, NW, C>::smem(nw);
     auto kern = rmsnorm_bwd_kernel<T, VEC, NW, C, FULL>;
-    if (smem > 47 * 1024) {   // (with the static part, beyond what needs no leave)
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // Leave for what the kernel's most warps take, whatever this call takes: the
+    // leave is the process's, and another thread's launch may lie behind it.
+    constexpr int most = BwdCfg<T, VEC, NW, C>::smem(NW);
+    static_assert(most <= 232448 - 1024, "shared memory per block");
+    if (most > 47 * 1024) {   // (with the static part, beyond what needs no leave)
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
       if (e != cudaSuccess) return launched(e, "rmsnorm_bwd", R, k.rows, k.H, grid, nw * 32);
     }
     return launched(launch_after(kern, dim3(grid), nw * 32, smem, 0, s, k), "rmsnorm_bwd", R, k.rows, k.H, grid, nw * 32);

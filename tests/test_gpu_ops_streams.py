@@ -1,5 +1,7 @@
-"""The operators between the residual stream and the attention on streams that are not current and on
-several at once, and the block's way back replayed from a CUDA graph."""
+"""The operators between the residual stream and the attention on streams that are not current, on
+several at once and from several threads, and the block's way back replayed from a CUDA graph."""
+import threading
+
 import pytest
 import torch
 
@@ -162,3 +164,34 @@ def test_norms_quantiser_and_rotary_on_streams_at_once(dev):
     torch.cuda.synchronize()
     for (_, outs, width, _), ref in zip(jobs, want):
         assert all(torch.equal(a, b) for a, b in zip(values(outs, width), ref))
+
+
+@pytest.mark.parametrize("dtype,widths", [("bf16", (4352, 8184)), ("bf16", (8448, 16376)), ("f32", (2176, 4092))])
+def test_norm_backward_from_two_threads(dev, dtype, widths):
+    """Two widths that one kernel serves with different amounts of shared memory, from two threads: no call may change
+    what the other's launch is allowed."""
+    T = {"bf16": BF, "f32": torch.float32}[dtype]
+    errors, rows = [], 5
+
+    def work(H):
+        try:
+            dy, h, w, r = (torch.ones(s, dtype=t, device=dev) for s, t in (((rows, H), T), ((rows, H), T), ((H,), T), ((rows,), torch.float32)))
+            dx, dw, d = torch.empty_like(dy), torch.empty(H, device=dev), B.fo_norm_desc(H, dtype=dtype)
+            ws = torch.empty(B.fo_rmsnorm_bwd_workspace(d, rows), dtype=torch.uint8, device=dev)
+            stream = torch.cuda.Stream()
+            stream.wait_stream(torch.cuda.current_stream())
+            for i in range(6000):
+                B.fo_rmsnorm_bwd(d, rows, [dy], None, [h], w, [r], [dx], dw, ws, stream=stream)
+                if i % 500 == 499:
+                    stream.synchronize()
+            # Each row's gradient is 1 - 1 * mean(1); the weight's the number of rows.
+            assert torch.count_nonzero(dx).item() == 0 and (dw == rows).all()
+        except Exception as e:   # noqa: BLE001 (told by the test)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(H,)) for H in widths]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors

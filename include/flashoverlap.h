@@ -523,7 +523,10 @@ typedef struct {
  * A [M x K] e4m3 with sA [M x ceil(K/128)] (fo_rmsnorm's q and scale, or
  * fo_quant_fp8 with block_rows = 1), W [N x K] e4m3 (the nn.Linear layout)
  * with sW [ceil(N/128) x ceil(K/128)] (block_rows = 128), Y [M x N]. Products
- * and sums in fp32, Y rounded once. The gradient of A's real values is the
+ * and sums in fp32, Y rounded once. The two scales are multiplied first, in
+ * fp32: where their product is below 2^-126 it has a subnormal's precision,
+ * and the block's part of Y is off by up to 2^-125; where it is beyond fp32,
+ * the block's part is infinite or NaN. The gradient of A's real values is the
  * same call on dY in 8 bits and the transposed weight (qt, scale_t). A, W and
  * Y are 16-byte aligned; K a multiple of 16 (FO_ERR_ALIGN). `ws`: a workspace
  * of fo_gemm_fp8_workspace bytes for calls of up to M rows (16-byte aligned),

@@ -231,9 +231,9 @@ __global__ void __launch_bounds__(256) rope_single_kernel(const __grid_constant_
 }  // namespace
 }  // namespace fo_ops
 
-extern "C" fo_status fo_rope_init(fo_rope_desc* d) {
-  if (!d) return FO_ERR_INVALID_ARG;
-  d->ready = 0;
+// What fo_rope_init and every call look at: a caller may have changed the
+// description since.
+static fo_status check_rope_desc(const fo_rope_desc* d) {
   if (d->R < 1 || d->R > FO_MAX_R || d->reserved) return FO_ERR_INVALID_ARG;
   if (d->head_dim < 1 || d->head_dim > FO_ROPE_MAX_DIM || d->rot_dim < 2 || d->rot_dim % 2 ||
       d->rot_dim > d->head_dim || d->heads_q < 1 || d->heads_k < 0 || d->heads_v < 0 || d->heads_q > 65536 ||
@@ -248,6 +248,14 @@ extern "C" fo_status fo_rope_init(fo_rope_desc* d) {
   if (mixed && (!(d->trained >= 1.0) || !isfinite(d->trained) || !(d->slow > 0.0) || !(d->fast > d->slow) ||
                 !isfinite(d->fast)))
     return FO_ERR_INVALID_ARG;
+  return FO_OK;
+}
+
+extern "C" fo_status fo_rope_init(fo_rope_desc* d) {
+  if (!d) return FO_ERR_INVALID_ARG;
+  d->ready = 0;
+  if (const fo_status st = check_rope_desc(d)) return st;
+  const bool mixed = d->scaling == FO_ROPE_SCALE_WAVELENGTH || d->scaling == FO_ROPE_SCALE_PARTS;
   const double two_pi = 6.283185307179586476925286766559;
   const int pairs = d->rot_dim / 2;
   // PARTS: the (real) pair indices that make `fast` and `slow` turns.
@@ -282,8 +290,8 @@ extern "C" fo_status fo_rope(const fo_rope_desc* d, int64_t rows, const void* po
                              const int64_t ld_out[3], int32_t inverse, fo_stream_t stream) {
   using namespace fo_ops;
   if (!d || d->ready != 1 || !ld_in || !ld_out) return FO_ERR_INVALID_ARG;
-  if (d->R < 1 || d->R > kMaxR || d->rot_dim < 2 || d->rot_dim > d->head_dim || d->head_dim > FO_ROPE_MAX_DIM)
-    return FO_ERR_INVALID_ARG;
+  fo_status st;
+  if ((st = check_rope_desc(d))) return st;
   if ((inverse != 0 && inverse != 1) || (positions && pos_bytes != 4 && pos_bytes != 8)) return FO_ERR_INVALID_ARG;
   if (rows < 0 || rows > INT32_MAX) return FO_ERR_SHAPE;
   const int R = d->R;
@@ -291,7 +299,6 @@ extern "C" fo_status fo_rope(const fo_rope_desc* d, int64_t rows, const void* po
   typedef const void* const* A;
   const int32_t heads[3] = {d->heads_q, d->heads_k, d->heads_v};
   const A in[3] = {q_in, k_in, v_in}, out[3] = {(A)q_out, (A)k_out, (A)v_out};
-  fo_status st;
   for (int j = 0; j < 3; ++j) {
     if (!heads[j]) continue;
     if (ld_in[j] < (int64_t)heads[j] * d->head_dim || ld_out[j] < (int64_t)heads[j] * d->head_dim)

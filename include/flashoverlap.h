@@ -585,7 +585,8 @@ typedef struct {
   int32_t ready;
 } fo_rope_desc;
 
-/* Check the description and fill turns, factor and ready. Host only. */
+/* Check the description and fill turns, factor and ready. Host only. A
+ * description that is changed is initialised again. */
 fo_status fo_rope_init(fo_rope_desc* desc);
 
 /* Rotary positions. For each rank, row t and head of Q and K, each pair

@@ -1,5 +1,6 @@
 """The operators' Python calls with and without the native marshalling module, which is there to make them shorter and
 may be missing."""
+import ctypes
 import os
 import sysconfig
 
@@ -58,6 +59,21 @@ def test_calls_without_the_module_refuse_what_they_refuse_with_it(no_module):
         with pytest.raises(B.FlashOverlapError) as e:
             call()
         assert e.value.code == B.FO_ERR_SHAPE
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(heads_q=0, heads_k=0, heads_v=0), B.FO_ERR_SHAPE), (dict(heads_q=0), B.FO_ERR_SHAPE), (dict(heads_k=-1), B.FO_ERR_SHAPE),
+    (dict(heads_v=1 << 20), B.FO_ERR_SHAPE), (dict(rot_dim=63), B.FO_ERR_SHAPE), (dict(rot_dim=256), B.FO_ERR_SHAPE),
+    (dict(head_dim=0), B.FO_ERR_SHAPE), (dict(R=17), B.FO_ERR_INVALID_ARG), (dict(dtype=7), B.FO_ERR_DTYPE),
+    (dict(layout=2), B.FO_ERR_INVALID_ARG), (dict(scaling=-1), B.FO_ERR_INVALID_ARG), (dict(base=0.5), B.FO_ERR_INVALID_ARG),
+    (dict(reserved=1), B.FO_ERR_INVALID_ARG)])
+def test_rope_refuses_a_description_that_was_spoilt_after_its_check(change, code):
+    d = B.fo_rope_desc(128, 2, 1, 1)
+    for k, v in change.items():
+        setattr(d, k, v)
+    one = (ctypes.c_void_p * 17)(*[256] * 17)
+    ld = (ctypes.c_int64 * 3)(1 << 40, 1 << 40, 1 << 40)
+    assert B.load().fo_rope(d, 4, 256, 8, one, one, one, ld, one, one, one, ld, 0, None) == code
 
 
 @pytest.mark.gpu

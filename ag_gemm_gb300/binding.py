@@ -472,6 +472,8 @@ def _address(x, n: int, types, what: str) -> int:
     """The address of x: a dense CUDA tensor of n values of one of `types`, or a raw address."""
     if type(x) is int:
         return x
+    if x is None:
+        raise ValueError(f"{what}: None given, a tensor or an address expected")
     if x.dtype not in types or x.numel() != n or not x.is_contiguous() or not x.is_cuda:
         _refuse(x, n, types, what)
     return x.data_ptr()
@@ -492,7 +494,7 @@ def _addresses(xs, R: int, n: int, types, what: str):
         raise ValueError(f"{what}: {len(xs)} tensors given, one for each of {R} ranks expected")
     at, last = [], None
     for x in xs:
-        if x is not last:
+        if x is not last or x is None:
             here, last = _address(x, n, types, what), x
         at.append(here)
     return _array_of(R)(*at)
@@ -559,6 +561,8 @@ def fo_quant_fp8(rows: int, cols: int, x, q, scale, qt=None, scale_t=None, *, bl
     x holds raw addresses."""
     t = _types()
     if dtype is None:
+        if not len(x) or x[0] is None or isinstance(x[0], int):
+            raise ValueError("x: tensors expected, or addresses and their dtype")
         dtype = "bf16" if x[0].dtype in t[0] else "f32"
     R, code = len(x), DTYPES[dtype]
     status = (_marshal or _native()).quant_fp8(rows, cols, code, block_rows, x, q, scale, qt, scale_t, stream)
@@ -636,13 +640,15 @@ def fo_rope_desc(head_dim: int, heads_q: int, heads_k: int = 0, heads_v: int = 0
 def _rows_of(xs, R: int, rows: int, width: int, types, what: str):
     """Addresses and the common row stride of R matrices [rows, width] whose rows are dense (parts of packed rows
     among them)."""
-    if len(xs) != R:
-        raise ValueError(f"{what}: {len(xs)} tensors given, one for each of {R} ranks expected")
+    if xs is None or len(xs) != R:
+        raise ValueError(f"{what}: {0 if xs is None else len(xs)} tensors given, one for each of {R} ranks expected")
     ld, at, shape = None, [], (rows, width)
     for x in xs:
         if type(x) is int:
             at.append(x)
             continue
+        if x is None:
+            raise ValueError(f"{what}: None given, a tensor or an address expected")
         if x.dtype not in types:
             raise ValueError(f"{what}: {x.dtype} given, {' or '.join(map(str, types))} expected")
         if x.shape != shape:

@@ -61,6 +61,23 @@ def test_calls_without_the_module_refuse_what_they_refuse_with_it(no_module):
         assert e.value.code == B.FO_ERR_SHAPE
 
 
+def test_calls_refuse_missing_tensors():
+    d, x = B.fo_norm_desc(256), torch.zeros(4, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="x: None given"):
+        B.fo_rmsnorm(d, 4, [None], None, 256, [256], stream=0)
+    with pytest.raises(ValueError, match="q: None given"):
+        B.fo_quant_fp8(4, 256, [256], [None], [256], dtype="bf16", stream=0)
+    for bad in ([], [None], [256]):
+        with pytest.raises(ValueError, match="dtype"):
+            B.fo_quant_fp8(4, 256, bad, [256], [256], stream=0)
+    r = B.fo_rope_desc(128, 2, 1)
+    for k in (None, [None], []):
+        with pytest.raises(ValueError, match="K: "):
+            B.fo_rope(r, 4, None, [256], k, None, [256], [256], None, stream=0)
+    with pytest.raises(ValueError, match="weight"):
+        B.fo_rmsnorm(d, 4, [256], None, None, [256], stream=0)
+
+
 @pytest.mark.parametrize("change,code", [
     (dict(heads_q=0, heads_k=0, heads_v=0), B.FO_ERR_SHAPE), (dict(heads_q=0), B.FO_ERR_SHAPE), (dict(heads_k=-1), B.FO_ERR_SHAPE),
     (dict(heads_v=1 << 20), B.FO_ERR_SHAPE), (dict(rot_dim=63), B.FO_ERR_SHAPE), (dict(rot_dim=256), B.FO_ERR_SHAPE),

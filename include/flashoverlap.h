@@ -445,7 +445,9 @@ fo_status fo_gemm_rs_noalloc(fo_plan_t plan, const void* const* X, const void* c
  * the host first and launches nothing when it refuses; zero rows are FO_OK
  * and launch nothing. 8-bit values are e4m3 (largest 448), rounded to
  * nearest even; a scale is the number an 8-bit value is multiplied by,
- *     scale = max(max |v| / 448, 2^-126)   over the scale's block of v,
+ *     scale = max(max |v| / 448, 2^-126)   over the scale's block of v
+ * (the fp32 product with the number next to 1/448, within a last place of the
+ * quotient), and the value is v / scale, rounded to nearest in fp32 and then,
  * so a block of zeros has scale 2^-126 and zero values, and a block that
  * holds a NaN or an infinity has a scale of the same kind and NaN values
  * where the quotient is one. */

@@ -1,6 +1,6 @@
-"""The 8-bit outputs are what their definition gives in fp32, bit for bit: scale = largest magnitude / 448 (at least
-2^-126), value = the quotient by the scale, each division rounded to nearest, then e4m3 rounded to nearest even. (The
-norm's outputs in 8 bits are held to its own fp32 output, which is what they are made of.)"""
+"""The 8-bit outputs are what their definition gives in fp32, bit for bit: scale = largest magnitude times the fp32 number
+next to 1/448 (at least 2^-126), value = the quotient by that scale rounded to nearest, then e4m3 rounded to nearest
+even. (The norm's outputs in 8 bits are held to its own fp32 output, which is what they are made of.)"""
 import pytest
 import torch
 
@@ -21,13 +21,13 @@ def dev():
 
 
 def in_8_bits(x, up):
-    """x [rows, cols] fp32 on the CPU -> its e4m3 bytes and scales, by IEEE divisions."""
+    """x [rows, cols] fp32 on the CPU -> its e4m3 bytes and scales, by IEEE arithmetic."""
     rows, cols = x.shape
     a, b = -(-rows // up), -(-cols // 128)
     p = torch.zeros(a * up, b * 128)
     p[:rows, :cols] = x
     p = p.view(a, up, b, 128)
-    scale = torch.maximum(p.abs().amax(dim=(1, 3)) / 448.0, torch.tensor(2.0 ** -126))
+    scale = torch.maximum(p.abs().amax(dim=(1, 3)) * torch.tensor(1.0 / 448.0), torch.tensor(2.0 ** -126))
     q = (p / scale[:, None, :, None]).clamp(-448, 448).to(E4M3)
     return q.view(torch.uint8).reshape(a * up, b * 128)[:rows, :cols], scale
 

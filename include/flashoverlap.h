@@ -447,8 +447,8 @@ fo_status fo_gemm_rs_noalloc(fo_plan_t plan, const void* const* X, const void* c
  * nearest even; a scale is the number an 8-bit value is multiplied by,
  *     scale = max(max |v| / 448, 2^-126)   over the scale's block of v
  * (the fp32 product with the number next to 1/448, within a last place of the
- * quotient), and the value is v / scale, rounded to nearest in fp32 and then,
- * so a block of zeros has scale 2^-126 and zero values, and a block that
+ * quotient), and the value is v / scale, rounded to nearest in fp32 and then
+ * in e4m3. So a block of zeros has scale 2^-126 and zero values, and a block that
  * holds a NaN or an infinity has a scale of the same kind and NaN values
  * where the quotient is one. */
 
@@ -492,8 +492,8 @@ fo_status fo_rmsnorm(const fo_norm_desc* desc, int64_t rows, const void* const* 
  * may be dy or dh. dweight ([H] fp32, may be NULL) receives the sum over every row
  * of every shard of dy * h * rstd: the gradient of the replicated weight,
  * after its all-reduce. An 8-bit forward output passes its gradient straight
- * through. Sums run in fp32 in an order that the sizes alone fix, so results
- * repeat bit for bit. `ws` (16-byte aligned): fo_rmsnorm_bwd_workspace bytes
+ * through. Sums run in fp32 in an order that the sizes and the pointers'
+ * alignment alone fix, so results repeat bit for bit. `ws` (16-byte aligned): fo_rmsnorm_bwd_workspace bytes
  * of scratch, no initialisation needed; NULL is allowed when dweight is NULL.
  * Two launches (one without dweight). */
 fo_status fo_rmsnorm_bwd(const fo_norm_desc* desc, int64_t rows, const void* const* dy, const void* const* dh,
@@ -507,7 +507,8 @@ fo_status fo_rmsnorm_bwd_workspace(const fo_norm_desc* desc, int64_t rows, size_
  * one for every 128 x 128 block (weights), scale [ceil(rows/128) x
  * ceil(cols/128)]; qt and scale_t (both or neither; block_rows = 128 only)
  * also receive the transposed copy [cols x rows] and its scales, with which
- * the product gives the gradient of its left operand. One launch. */
+ * the product gives the gradient of its left operand. At most 65535 blocks of
+ * 128 rows (block_rows = 1: 2^31 - 1 rows), FO_ERR_SHAPE beyond. One launch. */
 fo_status fo_quant_fp8(int32_t R, int64_t rows, int64_t cols, int32_t dtype, int32_t block_rows,
                        const void* const* x, void* const* q, float* const* scale, void* const* qt,
                        float* const* scale_t, fo_stream_t stream);

@@ -99,3 +99,19 @@ def test_norms_8_bits_are_those_of_its_output(dev, rows, H):
     want, scales = in_8_bits(y.cpu(), 1)
     assert torch.equal(scale.cpu(), scales)
     assert torch.equal(q.cpu(), want)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,H", [(700, 4096), (300, 1024), (50, 1358), (90, 1357), (20, 16384), (400, 260)])
+def test_norms_8_bits_in_bf16_are_those_of_its_formula(dev, rows, H, residual):
+    """From its own rstd on, the norm's outputs are its formula's in fp32, operation by operation."""
+    g = torch.Generator().manual_seed(rows + H)
+    x, res = (torch.randn(rows, H, generator=g).bfloat16() for _ in range(2))
+    w = (1 + 0.2 * torch.randn(H, generator=g)).bfloat16()
+    y, q = torch.empty(rows, H, dtype=torch.bfloat16, device=dev), torch.empty(rows, H, dtype=torch.uint8, device=dev)
+    scale, rstd = torch.empty(rows, -(-H // 128), device=dev), torch.empty(rows, device=dev)
+    B.fo_rmsnorm(B.fo_norm_desc(H), rows, [x.to(dev)], [res.to(dev)] if residual else None, w.to(dev), None, [y], [q], [scale], [rstd])
+    s = x.float() + res.float() if residual else x.float()
+    n = s * rstd.cpu()[:, None] * w.float()
+    want, scales = in_8_bits(n, 1)
+    assert torch.equal(scale.cpu(), scales) and torch.equal(q.cpu(), want) and torch.equal(y.cpu(), n.bfloat16())

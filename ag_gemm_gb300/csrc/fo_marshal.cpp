@@ -2,10 +2,10 @@
  * attention, for Python callers: checks the tensors and hands their addresses to the C
  * ABI. The same checks exist in binding.py, which explains what is
  * wrong with an argument; this module only recognises calls that are right and
- * returns -1 for all others, having done nothing. A decode step's norm has
- * seven tensors: its call takes 11 us marshalled in Python, 6.5 us here
- * through the tensors' Python methods, 3.2 us here through torch's own
- * objects. */
+ * returns -1 for all others, having done nothing. A decode step's norm (8 x
+ * 4096, seven tensors) takes 4.9 us of host time this way, with its caller's
+ * lists, and 15.4 us marshalled in Python; of both, the driver's look at the
+ * seven addresses is 1.1 us. */
 #define PY_SSIZE_T_CLEAN
 #include <torch/csrc/autograd/python_variable.h>
 #include <c10/cuda/CUDAStream.h>

@@ -184,9 +184,9 @@ __device__ __forceinline__ float block_sum(float v, float* smem, int nw) {
 template <int NW, int C>
 constexpr bool kAllWarps = NW == 32 && C == 8;
 
-// 8192 x 4096 bf16 with residual and 8-bit output (236 MB): 39.8 us, 5.9 TB/s.
-// Two thirds of the issue slots are taken, so instructions count: no 64-bit
-// division, approximate reciprocals, no bounds checks on full rows. Six blocks
+// 8192 x 4096 bf16 with residual and 8-bit output (236 MB): 39.0 us, 6.0 TB/s.
+// Three fifths of the issue slots are taken, so instructions count: no 64-bit
+// division, packed products, no bounds checks on full rows. Six blocks
 // of 8 warps on an SM: 1.5 us less than the five that the compiler's own
 // choice of registers leaves, 4 less than rows on 4 warps, 15 less than on 16.
 template <typename T, int VEC, int NW, int C, bool FULL>

@@ -95,7 +95,7 @@ __device__ __forceinline__ void store_line(uint8_t* line, uint32_t mine, int lan
 
 // One warp for each group of 128 values of a row, kUnroll groups at a time
 // with all loads first (rows that do not start on 16 bytes). 8191 x 4098 bf16:
-// 35 us; 8191 x 4095: 35 (with accesses of one value and byte stores 45).
+// 36 us; 8191 x 4095: 39 (with accesses of one value and byte stores 45).
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__ QuantParams p) {
   constexpr int kUnroll = 4;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
   }
 }
 
-// 8192 x 4096 bf16 (102 MB): 16.3 us, 6.2 TB/s. A warp takes kUnroll pieces of
+// 8192 x 4096 bf16 (102 MB): 16.5 us, 6.2 TB/s. A warp takes kUnroll pieces of
 // 32 lanes x 16 bytes at a time, all loads first; a group's scale is the
 // maximum over the 16 (bf16) or 32 lanes that hold it. A piece never crosses a row (rows of whole groups are one long
 // row to this kernel).
@@ -190,7 +190,7 @@ __device__ __forceinline__ void transpose4(uint32_t& a, uint32_t& b, uint32_t& c
 // One block for each 128 x 128 block (rows that do not start on 16 bytes):
 // warp w has rows 16 w .. 16 w + 15, lane l columns 4 l .. 4 l + 3, so its
 // bytes of a row are a word, and those of four rows, transposed, are words of
-// the copy's lines. 8191 x 4098 bf16 with the copy: 41 us, 8191 x 4095: 54
+// the copy's lines. 8191 x 4098 bf16 with the copy: 43 us, 8191 x 4095: 55
 // (with accesses of one value and byte stores 78).
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) quant_blocks_kernel(const __grid_constant__ QuantParams p) {

@@ -215,6 +215,7 @@ class Fp8AttentionBlock:
                   (the products' partial sums by the unfused reduce kernel; the sum is rounded to bf16 by a torch copy)
         norm      dx (= d residual) with the residual path's gradient, dweight                fo_rmsnorm_bwd
 
+    Q, K and V have the same heads, of 128 (fo_attn_rs has no others).
     The T tokens of the R ranks' shards lie back to back, so the norm is one call and its output is the all-gathered
     operand of every rank's product. The projections' weight gradients are not part of the block: they contract the
     tokens in bf16 (fo_gemm_partials_sharded), and the block keeps the norm's output in 8 bits alone. All of a call's

@@ -76,7 +76,7 @@ def test_block_quantiser(dev, cols):
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_rotary_positions(dev, layout):
-    heads, D = 24, 128
+    heads, D = 20, 128
     width = heads * D
     few = torch.randn(FEW, 3 * width, generator=torch.Generator().manual_seed(1)).to(BF).to(dev)
     times = -(-(1 << 31) // (FEW * 3 * width)) + 30

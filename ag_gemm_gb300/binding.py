@@ -33,6 +33,7 @@ INTERLEAVES = {"auto": 0, "lockstep": 1, "skewed": 2, "rank_major": 3, "skewed_p
 RS_ALGOS = {"direct": 0, "ring": 1}
 TAIL_SPLITS = {"auto": 0, "off": 1, "on": 2}
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+CACHE_DTYPES = {"bf16": 0, "e4m3": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "wavelength": 2, "parts": 3}
 FO_ROPE_MAX_DIM = 256
 FO_NORM_MAX_H = 32768
@@ -48,6 +49,7 @@ EXPORTED = [
     "fo_gemm_a2a", "fo_all_to_all_copy", "fo_attn_rs", "fo_attention", "fo_gemm_partials_sharded",
     "fo_rmsnorm", "fo_rmsnorm_bwd", "fo_rmsnorm_bwd_workspace", "fo_quant_fp8", "fo_gemm_fp8",
     "fo_gemm_fp8_workspace", "fo_ops_workspace_init", "fo_ops_status_query", "fo_rope_init", "fo_rope",
+    "fo_kv_append", "fo_paged_attention", "fo_paged_attention_workspace",
 ]
 
 
@@ -86,6 +88,16 @@ class RopeDesc(ctypes.Structure):
                                        "scaling", "reserved")]
     _fields_ += [(n, ctypes.c_double) for n in ("base", "stretch", "trained", "slow", "fast")]
     _fields_ += [("turns", c_uint64 * (FO_ROPE_MAX_DIM // 2)), ("factor", ctypes.c_float), ("ready", c_int32)]
+
+
+class PagedDesc(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("R", "heads_q", "heads_k", "head_dim", "page", "cache_dtype", "window", "sinks")]
+    _fields_ += [("scale", ctypes.c_float), ("reserved", c_int32 * 3)]
+
+
+class PagedBatch(ctypes.Structure):
+    _fields_ = [("seqs", c_int32), ("max_new", c_int32), ("pages", c_int64), ("table_cols", c_int64),
+                ("lengths", c_void_p), ("starts", c_void_p), ("table", c_void_p)]
 
 
 _lib = None
@@ -141,6 +153,11 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "fo_rope_init": ([POINTER(RopeDesc)], c_int32),
         "fo_rope": ([POINTER(RopeDesc), c_int64, P, c_int32, PP, PP, PP, POINTER(c_int64), PP, PP, PP,
                      POINTER(c_int64), c_int32, P], c_int32),
+        "fo_kv_append": ([POINTER(PagedDesc), POINTER(RopeDesc), POINTER(PagedBatch), c_int64, P, c_int32, PP, PP, PP, PP,
+                          POINTER(c_int64), PP, PP, PP, PP, P, P], c_int32),
+        "fo_paged_attention": ([POINTER(PagedDesc), POINTER(PagedBatch), c_int64, PP, POINTER(c_int64), PP, PP, PP, PP, PP,
+                                PP, P, P], c_int32),
+        "fo_paged_attention_workspace": ([POINTER(PagedDesc), c_int32, c_int64, c_int32, POINTER(c_size_t)], c_int32),
         "fo_status_string": ([c_int32], ctypes.c_char_p),
         "fo_version": ([], c_int32),
     }
@@ -417,7 +434,7 @@ class _NoMarshal:
     def _leave(*args):
         return -1
 
-    rmsnorm = rmsnorm_bwd = quant_fp8 = gemm_fp8 = rope = _leave
+    rmsnorm = rmsnorm_bwd = quant_fp8 = gemm_fp8 = rope = kv_append = paged_attention = _leave
 
 
 def _native():
@@ -668,6 +685,18 @@ def _rows_of(xs, R: int, rows: int, width: int, types, what: str):
     return _array_of(R)(*at), width if ld is None else ld
 
 
+def _positions(positions, rows: int):
+    """Address and bytes of `rows` positions: an int32 or int64 tensor, a raw address (of int64), or None."""
+    if positions is None:
+        return 0, 8
+    if isinstance(positions, int):
+        return positions, 8
+    size = positions.element_size()
+    if positions.is_floating_point() or size not in (4, 8):
+        raise ValueError(f"positions: int32 or int64 expected, {positions.dtype} given")
+    return _address(positions, rows, (positions.dtype,), "positions"), size
+
+
 def fo_rope(desc: RopeDesc, rows: int, positions, q_in, k_in, v_in, q_out, k_out, v_out, *, inverse: bool = False,
             stream=None) -> None:
     """Turn Q and K by their positions ([rows] int32 or int64, None: 0, 1, ...) and copy V; one matrix [rows, heads *
@@ -691,16 +720,109 @@ def fo_rope(desc: RopeDesc, rows: int, positions, q_in, k_in, v_in, q_out, k_out
         b, ld_out[j] = _rows_of(o, R, rows, heads * D, types, what)
         ins.append(a)
         outs.append(b)
-    at, size = 0, 8
-    if positions is not None and not isinstance(positions, int):
-        size = positions.element_size()
-        if positions.is_floating_point() or size not in (4, 8):
-            raise ValueError(f"positions: int32 or int64 expected, {positions.dtype} given")
-        at = _address(positions, rows, (positions.dtype,), "positions")
-    elif positions is not None:
-        at = positions
+    at, size = _positions(positions, rows)
     _check(load().fo_rope(desc, rows, at, size, *ins, ld_in, *outs, ld_out, 1 if inverse else 0, _stream(stream)),
            "fo_rope")
+
+
+# ---- serving from a paged cache of keys and values
+
+def fo_paged_desc(heads_q: int, heads_k: int, *, head_dim: int = 128, R: int = 1, page: int = 64, cache="bf16",
+                  window: int = 0, sinks: int = 0, scale: float = 0.0) -> PagedDesc:
+    """Description of a paged cache and of the attention over it: heads a rank, tokens a page, how the cache is kept
+    ("bf16" or "e4m3" with a scale for each token's head), how many tokens a query sees (0: all before it), the first
+    tokens that stay visible, the scores' scale (0: 1 / sqrt(head_dim))."""
+    d = PagedDesc()
+    d.R, d.heads_q, d.heads_k, d.head_dim, d.page = R, heads_q, heads_k, head_dim, page
+    d.cache_dtype, d.window, d.sinks, d.scale = CACHE_DTYPES[cache], window, sinks, scale
+    return d
+
+
+def _whole(x, n: Optional[int], what: str) -> int:
+    """The address of x, a dense int32 CUDA tensor of n values (None: any number), or a raw address."""
+    if type(x) is int:
+        return x
+    if str(x.dtype) != "torch.int32":
+        raise ValueError(f"{what}: int32 expected, {x.dtype} given")
+    return _address(x, x.numel() if n is None else n, (x.dtype,), what)
+
+
+def fo_paged_batch(lengths, table, pages: int, *, starts=None, max_new: int = 1) -> PagedBatch:
+    """The sequences of a call: lengths [seqs] with the new tokens, table [seqs, columns] of page numbers, starts
+    [seqs + 1] of the new tokens' rows (None: one new token a sequence, sequence b's in row b), int32; pages of each
+    rank's cache; the most new tokens of a sequence. The tensors are kept, and what they hold is read when a call runs."""
+    b = PagedBatch()
+    if table.dim() != 2:
+        raise ValueError(f"table: [sequences, columns] expected, {tuple(table.shape)} given")
+    b.seqs, b.table_cols = table.shape
+    b.max_new, b.pages = max_new, pages
+    b.lengths, b.table = _whole(lengths, b.seqs, "lengths"), _whole(table, None, "table")
+    b.starts = None if starts is None else _whole(starts, b.seqs + 1, "starts")
+    b.kept = (lengths, table, starts)
+    return b
+
+
+def _cache_of(desc: PagedDesc, batch: PagedBatch):
+    """Values of a rank's cache, its scales, and the types of the cache."""
+    slots = batch.pages * desc.heads_k * desc.page
+    return slots * desc.head_dim, slots, _types()["q" if desc.cache_dtype == 1 else 0]
+
+
+def fo_kv_append(desc: PagedDesc, rope: Optional[RopeDesc], batch: PagedBatch, rows: int, q, k, v, q_out, k_cache, v_cache,
+                 k_scale=None, v_scale=None, positions=None, ws=None, stream=None) -> None:
+    """Append the batch's new tokens to each rank's cache, turned by `rope` (None: as they are) at their positions in
+    their sequences (or at positions [rows], int32 or int64), and turn their queries. q, q_out [rows, heads_q *
+    head_dim], k, v [rows, heads_k * head_dim]: one matrix for each rank, whose rows may be parts of packed ones;
+    k_cache, v_cache [pages, heads_k, page, head_dim], k_scale, v_scale [pages, heads_k, page] (8 bits only)."""
+    code = (_marshal or _native()).kv_append(desc, rope, batch, rows, q, k, v, q_out, k_cache, v_cache, k_scale, v_scale,
+                                             positions, ws, stream)
+    if code == FO_OK:
+        return
+    if code > 0:
+        _check(code, "fo_kv_append")
+    R, D, types = desc.R, desc.head_dim, _types()
+    values, slots, kept = _cache_of(desc, batch)
+    ld, rows_of = (c_int64 * 4)(), []
+    for j, (x, heads, what) in enumerate(((q, desc.heads_q, "q"), (k, desc.heads_k, "k"), (v, desc.heads_k, "v"),
+                                          (q_out, desc.heads_q, "q_out"))):
+        a, ld[j] = _rows_of(x, R, rows, heads * D, types[0], what)
+        rows_of.append(a)
+    at, size = _positions(positions, rows)
+    _check(load().fo_kv_append(desc, rope, batch, rows, at, size, *rows_of, ld,
+                               _addresses(k_cache, R, values, kept, "k_cache"), _addresses(v_cache, R, values, kept, "v_cache"),
+                               _addresses(k_scale, R, slots, types[1], "k_scale"),
+                               _addresses(v_scale, R, slots, types[1], "v_scale"), _ptr(ws), _stream(stream)), "fo_kv_append")
+
+
+def fo_paged_attention_workspace(desc: PagedDesc, seqs: int, rows: int, max_new: int = 1) -> int:
+    n = c_size_t()
+    _check(load().fo_paged_attention_workspace(desc, seqs, rows, max_new, ctypes.byref(n)), "fo_paged_attention_workspace")
+    return n.value
+
+
+def fo_paged_attention(desc: PagedDesc, batch: PagedBatch, rows: int, q, k_cache, v_cache, o, ws, k_scale=None, v_scale=None,
+                       lse=None, stream=None) -> None:
+    """Attention of the batch's new tokens over each rank's cache, which holds them already: q, o [rows, heads_q *
+    head_dim] (rows may be parts of wider ones), lse [rows, heads_q] fp32 or None; the cache as in fo_kv_append."""
+    code = (_marshal or _native()).paged_attention(desc, batch, rows, q, k_cache, v_cache, o, ws, k_scale, v_scale, lse, stream)
+    if code == FO_OK:
+        return
+    if code > 0:
+        _check(code, "fo_paged_attention")
+    R, types = desc.R, _types()
+    values, slots, kept = _cache_of(desc, batch)
+    ld = (c_int64 * 2)()
+    q_at, ld[0] = _rows_of(q, R, rows, desc.heads_q * desc.head_dim, types[0], "q")
+    o_at, ld[1] = _rows_of(o, R, rows, desc.heads_q * desc.head_dim, types[0], "o")
+    if ws is not None and not isinstance(ws, int) and \
+            ws.numel() * ws.element_size() < fo_paged_attention_workspace(desc, batch.seqs, rows, batch.max_new):
+        raise ValueError("fo_paged_attention: the workspace is smaller than fo_paged_attention_workspace says")
+    _check(load().fo_paged_attention(desc, batch, rows, q_at, ld, _addresses(k_cache, R, values, kept, "k_cache"),
+                                     _addresses(v_cache, R, values, kept, "v_cache"),
+                                     _addresses(k_scale, R, slots, types[1], "k_scale"),
+                                     _addresses(v_scale, R, slots, types[1], "v_scale"), o_at,
+                                     _addresses(lse, R, rows * desc.heads_q, types[1], "lse"), _ptr(ws), _stream(stream)),
+           "fo_paged_attention")
 
 
 def fo_plan_last_launches(plan: Plan) -> int:

@@ -1,5 +1,5 @@
 /* Argument marshalling of the operators between the residual stream and the
- * attention, for Python callers: checks the tensors and hands their addresses to the C
+ * attention and of those on a paged cache, for Python callers: checks the tensors and hands their addresses to the C
  * ABI. The same checks exist in binding.py, which explains what is
  * wrong with an argument; this module only recognises calls that are right and
  * returns -1 for all others, having done nothing. A decode step's norm (8 x
@@ -227,6 +227,19 @@ PyObject *m_gemm_fp8(PyObject *self, PyObject *const *v, Py_ssize_t n) {
   return code < 0 ? unknown() : PyLong_FromLong(code);
 }
 
+/* Positions: None, or `rows` of them in a dense int32 or int64 CUDA tensor. */
+bool positions_of(PyObject *o, long long rows, void **at, int32_t *bytes) {
+  *at = NULL;
+  *bytes = 8;
+  if (o == Py_None) return true;
+  const at::Tensor *t = tensor(o);
+  if (!t || !t->is_cuda() || (t->scalar_type() != at::kLong && t->scalar_type() != at::kInt) || t->numel() != rows ||
+      !t->is_contiguous())
+    return false;
+  *bytes = (int32_t)t->element_size();
+  return (*at = t->data_ptr()) != NULL;
+}
+
 /* (desc, rows, positions, q_in, k_in, v_in, q_out, k_out, v_out, inverse, stream) */
 PyObject *m_rope(PyObject *self, PyObject *const *v, Py_ssize_t n) {
   const Description<fo_rope_desc> held(n == 11 ? v[0] : NULL);
@@ -234,15 +247,9 @@ PyObject *m_rope(PyObject *self, PyObject *const *v, Py_ssize_t n) {
   if (!d) return unknown();
   const long long rows = PyLong_AsLongLong(v[1]);
   long code = -1;
-  bool ok = in_range(d->R) && rows > 0;
-  void *pos = NULL;
-  int32_t bytes = 8;
-  if (ok && v[2] != Py_None) {
-    const at::Tensor *t = tensor(v[2]);
-    ok = t && t->is_cuda() && (t->scalar_type() == at::kLong || t->scalar_type() == at::kInt) && t->numel() == rows &&
-         t->is_contiguous() && (pos = t->data_ptr()) != NULL;
-    if (ok) bytes = (int32_t)t->element_size();
-  }
+  void *pos;
+  int32_t bytes;
+  bool ok = in_range(d->R) && rows > 0 && positions_of(v[2], rows, &pos, &bytes);
   const int32_t heads[3] = {d->heads_q, d->heads_k, d->heads_v};
   array in[3], out[3];
   int64_t ld_in[3] = {0, 0, 0}, ld_out[3] = {0, 0, 0};
@@ -266,6 +273,80 @@ PyObject *m_rope(PyObject *self, PyObject *const *v, Py_ssize_t n) {
   return code < 0 ? unknown() : PyLong_FromLong(code);
 }
 
+/* Each rank's cache and, in 8 bits, its scales. */
+struct Cache {
+  array k, v, ks, vs;
+  bool of(const fo_paged_desc *d, const fo_paged_batch *b, PyObject *kc, PyObject *vc, PyObject *kss, PyObject *vss) {
+    if (!in_range(d->R) || d->heads_k < 1 || d->page < 1 || d->head_dim < 1 || b->pages < 1 || b->pages > INT32_MAX) return false;
+    const long long slots = b->pages * d->heads_k * d->page, values = slots * d->head_dim;
+    const bool eight = d->cache_dtype == FO_CACHE_E4M3;
+    const int kind = eight ? KIND_8BIT : KIND_BF16;
+    return arrays(kc, d->R, values, kind, 0, &k) && arrays(vc, d->R, values, kind, 0, &v) &&
+           arrays(kss, d->R, slots, KIND_F32, !eight, &ks) && arrays(vss, d->R, slots, KIND_F32, !eight, &vs);
+  }
+};
+
+/* (desc, rope, batch, rows, q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, positions, ws, stream) */
+PyObject *m_kv_append(PyObject *self, PyObject *const *v, Py_ssize_t n) {
+  const Description<fo_paged_desc> held(n == 15 ? v[0] : NULL);
+  const Description<fo_rope_desc> held_rope(n == 15 && v[1] != Py_None ? v[1] : NULL);
+  const Description<fo_paged_batch> held_batch(n == 15 ? v[2] : NULL);
+  const fo_paged_desc *d = held.get();
+  const fo_paged_batch *b = held_batch.get();
+  const fo_rope_desc *rope = held_rope.get();
+  if (!d || !b || (v[1] != Py_None && !rope)) return unknown();
+  const long long rows = PyLong_AsLongLong(v[3]);
+  long code = -1;
+  array x[4];
+  int64_t ld[4];
+  Cache c;
+  void *pos, *ws = NULL;
+  int32_t bytes;
+  bool ok = rows > 0 && c.of(d, b, v[8], v[9], v[10], v[11]) && positions_of(v[12], rows, &pos, &bytes) &&
+            (v[13] == Py_None || workspace(v[13], 64, &ws));
+  for (int j = 0; ok && j < 4; ++j)
+    ok = row_arrays(v[4 + j], d->R, rows, (long long)(j == 0 || j == 3 ? d->heads_q : d->heads_k) * d->head_dim, KIND_BF16,
+                    &x[j], &ld[j]);
+  fo_stream_t s;
+  if (ok && stream_of(v[14], &s)) {
+    Py_BEGIN_ALLOW_THREADS
+    code = fo_kv_append(d, rope, b, rows, pos, bytes, (const void *const *)x[0].p, (const void *const *)x[1].p,
+                        (const void *const *)x[2].p, x[3].p, ld, c.k.p, c.v.p, (float *const *)c.ks.p, (float *const *)c.vs.p,
+                        ws, s);
+    Py_END_ALLOW_THREADS
+  }
+  return code < 0 ? unknown() : PyLong_FromLong(code);
+}
+
+/* (desc, batch, rows, q, k_cache, v_cache, o, ws, k_scale, v_scale, lse, stream) */
+PyObject *m_paged_attention(PyObject *self, PyObject *const *v, Py_ssize_t n) {
+  const Description<fo_paged_desc> held(n == 12 ? v[0] : NULL);
+  const Description<fo_paged_batch> held_batch(n == 12 ? v[1] : NULL);
+  const fo_paged_desc *d = held.get();
+  const fo_paged_batch *b = held_batch.get();
+  if (!d || !b) return unknown();
+  const long long rows = PyLong_AsLongLong(v[2]);
+  long code = -1;
+  array q, o, lse;
+  int64_t ld[2];
+  Cache c;
+  void *ws;
+  size_t need;
+  fo_stream_t s;
+  if (rows > 0 && c.of(d, b, v[4], v[5], v[8], v[9]) &&
+      row_arrays(v[3], d->R, rows, (long long)d->heads_q * d->head_dim, KIND_BF16, &q, &ld[0]) &&
+      row_arrays(v[6], d->R, rows, (long long)d->heads_q * d->head_dim, KIND_BF16, &o, &ld[1]) &&
+      arrays(v[10], d->R, rows * d->heads_q, KIND_F32, 1, &lse) &&
+      fo_paged_attention_workspace(d, b->seqs, rows, b->max_new, &need) == FO_OK && workspace(v[7], need, &ws) &&
+      stream_of(v[11], &s)) {
+    Py_BEGIN_ALLOW_THREADS
+    code = fo_paged_attention(d, b, rows, (const void *const *)q.p, ld, (const void *const *)c.k.p, (const void *const *)c.v.p,
+                              (const float *const *)c.ks.p, (const float *const *)c.vs.p, o.p, (float *const *)lse.p, ws, s);
+    Py_END_ALLOW_THREADS
+  }
+  return code < 0 ? unknown() : PyLong_FromLong(code);
+}
+
 /* No C++ exception leaves the module: a call that meets one is for binding.py too. */
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
 PyObject *guarded(PyObject *self, PyObject *const *v, Py_ssize_t n) {
@@ -278,6 +359,7 @@ PyObject *guarded(PyObject *self, PyObject *const *v, Py_ssize_t n) {
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))guarded<m_##name>, METH_FASTCALL, NULL}
 PyMethodDef methods[] = {FAST(rmsnorm), FAST(rmsnorm_bwd), FAST(quant_fp8), FAST(gemm_fp8), FAST(rope),
+                         FAST(kv_append), FAST(paged_attention),
                          {NULL, NULL, 0, NULL}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fo_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -1,6 +1,6 @@
 // Host-side checks and device helpers shared by the operators between the
 // residual stream and the attention (norm, quantisation, 8-bit product,
-// rotary positions).
+// rotary positions) and by those on a paged cache.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -54,6 +54,8 @@ struct PtrList {
 inline fo_status device_sms(int* sms) { return fo_internal_device_sms(sms); }
 // fo_check_device_pointers on the list.
 fo_status check_device(const PtrList& l, fo_stream_t stream);
+// An initialised rotary description's fields (fo_rope.cu).
+fo_status check_rope_desc(const fo_rope_desc* d);
 // After a launch that returned `e`: FO_OK or FO_ERR_CUDA, with FO_LOG's line.
 fo_status launched(cudaError_t e, const char* what, int R, int64_t rows, int64_t cols, int grid, int threads);
 

@@ -1,0 +1,76 @@
+// What the operators on a paged cache share: host checks, the kernels' view of
+// a batch, and who sees whom.
+#pragma once
+
+#include "fo_device.cuh"
+#include "fo_ops.h"
+
+namespace fo_ops {
+
+// A call's sequences as kernels see them.
+struct Batch {
+  const int32_t* lengths;
+  const int32_t* starts;
+  const int32_t* table;
+  int64_t cols;        // entries of a row of the table
+  int32_t seqs, rows, max_new;
+  int32_t pages;
+  int32_t shift;       // log2 of the page's tokens
+  int32_t* status;     // workspace's status word, or NULL
+};
+
+// One sequence: its first row, new tokens and length. (n = 0 where there is
+// nothing to do.)
+struct Seq {
+  int32_t row, n, len;
+  // Positions of its new tokens are base + i.
+  __device__ __forceinline__ int32_t base() const { return len - n; }
+};
+
+enum : int32_t { kBadPage = 1, kBadCount = 2, kBadStarts = 3, kBadLength = 4 };
+
+__device__ __forceinline__ void report(const Batch& b, int seq, int what, int value) {
+  if (b.status) fo::record_error(b.status, FO_ERR_SHAPE, seq, what, value);
+}
+
+// Sequence `seq` of the batch, checked: rows lie within the call's, positions
+// within the table's row.
+__device__ __forceinline__ Seq sequence(const Batch& b, int seq) {
+  Seq s;
+  s.len = max(b.lengths[seq], 0);
+  s.row = seq;
+  s.n = 1;
+  if (b.starts) {
+    const int32_t first = b.starts[seq], last = b.starts[seq + 1];
+    s.row = first;
+    s.n = last - first;
+    if (first < 0 || last < first || last > b.rows) {
+      report(b, seq, kBadStarts, last);
+      s.row = s.n = 0;
+    }
+  }
+  if ((int64_t)s.len > b.cols << b.shift) {
+    report(b, seq, kBadLength, s.len);
+    s.n = 0;
+  }
+  return s;
+}
+
+// Tokens that a row at position p sees: those below `sinks_end` and those in
+// [lo, p]; the two do not overlap.
+struct Sight {
+  int32_t lo, sinks_end;
+};
+__device__ __forceinline__ Sight sight_of(int p, int window, int sinks) {
+  Sight s;
+  s.lo = window && p >= window ? p - window + 1 : 0;
+  s.sinks_end = min(sinks, s.lo);
+  return s;
+}
+
+// Host side (fo_kv_append.cu).
+fo_status check_paged(const fo_paged_desc* d);
+fo_status check_batch(const fo_paged_desc* d, const fo_paged_batch* b, int64_t rows);
+Batch batch_of(const fo_paged_desc* d, const fo_paged_batch* b, int64_t rows, void* ws);
+
+}  // namespace fo_ops

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(256) rope_single_kernel(const __grid_constant_
 
 // What fo_rope_init and every call look at: a caller may have changed the
 // description since.
-static fo_status check_rope_desc(const fo_rope_desc* d) {
+fo_status fo_ops::check_rope_desc(const fo_rope_desc* d) {
   if (d->R < 1 || d->R > FO_MAX_R || d->reserved) return FO_ERR_INVALID_ARG;
   if (d->head_dim < 1 || d->head_dim > FO_ROPE_MAX_DIM || d->rot_dim < 2 || d->rot_dim % 2 ||
       d->rot_dim > d->head_dim || d->heads_q < 1 || d->heads_k < 0 || d->heads_v < 0 || d->heads_q > 65536 ||
@@ -254,7 +254,7 @@ static fo_status check_rope_desc(const fo_rope_desc* d) {
 extern "C" fo_status fo_rope_init(fo_rope_desc* d) {
   if (!d) return FO_ERR_INVALID_ARG;
   d->ready = 0;
-  if (const fo_status st = check_rope_desc(d)) return st;
+  if (const fo_status st = fo_ops::check_rope_desc(d)) return st;
   const bool mixed = d->scaling == FO_ROPE_SCALE_WAVELENGTH || d->scaling == FO_ROPE_SCALE_PARTS;
   const double two_pi = 6.283185307179586476925286766559;
   const int pairs = d->rot_dim / 2;

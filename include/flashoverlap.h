@@ -611,6 +611,111 @@ fo_status fo_rope(const fo_rope_desc* desc, int64_t rows, const void* positions,
                   void* const* q_out, void* const* k_out, void* const* v_out, const int64_t ld_out[3],
                   int32_t inverse, fo_stream_t stream);
 
+/* ---- serving from a paged cache of keys and values -----------------------
+ *
+ * What follows the QKV product and the rotary positions when a model answers:
+ * a rank's keys and values are kept in pages of `page` tokens, which any
+ * sequence may hold in any order, and the new tokens of a batch of sequences
+ * are appended to them and attend over them. The conventions are the ones of
+ * the operators above. Values are bf16; sums, softmax statistics and scales
+ * fp32.
+ *
+ * A rank's cache (of keys, and one of values):
+ *     FO_CACHE_BF16   [pages x heads_k x page x head_dim] bf16
+ *     FO_CACHE_E4M3   the same of e4m3 bytes, with one scale for each token's
+ *                     head, [pages x heads_k x page] fp32 (the scale above,
+ *                     over the head's values)
+ * Every rank has heads of its own and its own cache; the batch, its page
+ * table and with it the numbers of the pages are the same for all. */
+
+typedef enum { FO_CACHE_BF16 = 0, FO_CACHE_E4M3 = 1 } fo_cache_dtype;
+
+#define FO_PAGED_MAX_GROUP 64     /* most query heads to a key head */
+
+typedef struct {
+  int32_t R;                  /* ranks, 1..16 */
+  int32_t heads_q, heads_k;   /* heads a rank: of queries (a multiple of heads_k, at most FO_PAGED_MAX_GROUP times
+                                 as many) and of keys and values. Query head h reads key head h / (heads_q / heads_k). */
+  int32_t head_dim;           /* 64 or 128 */
+  int32_t page;               /* tokens a page: 16, 32, 64, 128 or 256 */
+  int32_t cache_dtype;        /* fo_cache_dtype */
+  int32_t window;             /* 0: none; else how many tokens a query sees, its own the last */
+  int32_t sinks;              /* the first tokens, which stay visible beyond the window */
+  float scale;                /* of the scores; 0: 1 / sqrt(head_dim) */
+  int32_t reserved[3];        /* must be zero */
+} fo_paged_desc;
+
+/* The sequences of a call. The structure is host memory, read during the call
+ * only; lengths, starts and table are device memory and may be written anew
+ * before a captured call is replayed. Sequence b has lengths[b] tokens, its
+ * new ones included. Its new tokens are rows starts[b] .. starts[b + 1] - 1 of
+ * the call's matrices; without starts it has one, row b. Token p of it lies in
+ * place p % page of page table[b][p / page].
+ * What the device finds wrong is reported by fo_ops_status_query as
+ * FO_ERR_SHAPE, info[1] = the sequence, info[2] = what, info[3] = the value
+ * found: 1 a needed entry of the table that names no page (nothing is read or
+ * written through it), 2 more new tokens than max_new (those beyond it are
+ * left out), 3 starts that fall or leave the call's rows (the sequence is left
+ * out), 4 a length that the table has no entries for (the sequence is left
+ * out). Results of the sequence are then undefined, of the others not. */
+typedef struct {
+  int32_t seqs;               /* >= 0 */
+  int32_t max_new;            /* the most new tokens of a sequence; 1 without starts */
+  int64_t pages;              /* pages of a cache; pages * heads_k below 2^31 */
+  int64_t table_cols;         /* entries of a sequence's row of the table; table_cols * page below 2^31 */
+  const int32_t* lengths;     /* [seqs]; 0 (or less): a sequence that is not there */
+  const int32_t* starts;      /* [seqs + 1], or NULL */
+  const int32_t* table;       /* [seqs x table_cols] */
+} fo_paged_batch;
+
+/* Append the new tokens to the cache, turned by their rotary positions on the
+ * way. For each rank and each new token, at position p of its sequence (new
+ * token i of n at p = length - n + i):
+ *     q_out = turn(q), K cache[place of p] = turn(k), V cache[place of p] = v
+ * with fo_rope's turn by `rope` (its description, of the same R, heads
+ * heads_q, heads_k and heads_v = heads_k, head_dim and FO_BF16; NULL: nothing
+ * is turned), at angle positions[row] (int32 or int64, pos_bytes as in
+ * fo_rope) or, without positions, at p. Values are rounded once, to bf16 or
+ * (quotient by their scale) to e4m3. q, k, v, q_out: rows ld[0..3] elements
+ * apart as in fo_rope; q_out = q works in place. k_scale and v_scale: with an
+ * 8-bit cache only. A token before its sequence's beginning (p < 0: more new
+ * tokens than the length) is turned but not kept. Rows that no sequence has
+ * are left as they were, and so is every other place of the cache. Two new
+ * tokens of a call must not share a place. ws (may be NULL: nothing is
+ * reported): a workspace of fo_paged_attention. One launch. */
+fo_status fo_kv_append(const fo_paged_desc* desc, const fo_rope_desc* rope, const fo_paged_batch* batch, int64_t rows,
+                       const void* positions, int32_t pos_bytes, const void* const* q, const void* const* k,
+                       const void* const* v, void* const* q_out, const int64_t ld[4], void* const* k_cache,
+                       void* const* v_cache, float* const* k_scale, float* const* v_scale, void* ws,
+                       fo_stream_t stream);
+
+/* Attention of the new tokens over the cache, which holds them already. The
+ * new token at position p of its sequence sees the tokens j of it with
+ *     j <= p and (window = 0 or j > p - window or j < sinks)
+ * and for each of its heads
+ *     s_j = scale q . k_j,   m = max s_j,   l = sum exp(s_j - m)
+ *     o = sum exp(s_j - m) v_j / l,   lse = m + ln l
+ * over them. Weights are rounded to bf16 for the tensor cores' sum (by at most
+ * 2^-8 of each), o once to bf16. A row that sees nothing (a sequence that is not
+ * there, a token before its beginning) gets o = 0 and lse = -infinity. Rows
+ * that no sequence has are left as they were. Neither places behind a
+ * sequence's length nor pages that hold nothing any new token of it sees are
+ * looked at: their entries of the table may be anything, their places may hold
+ * NaN. q, o: rows ld[0..1] elements apart (a multiple of 8; 16-byte aligned),
+ * head h at h * head_dim; caches and scales 16-byte aligned; lse (may be NULL)
+ * [rows x heads_q] fp32. o must not overlap q. ws: fo_paged_attention_workspace
+ * bytes, 16-byte aligned, zeroed once by fo_ops_workspace_init; one call per
+ * workspace may be in flight. Results repeat bit for bit. */
+fo_status fo_paged_attention(const fo_paged_desc* desc, const fo_paged_batch* batch, int64_t rows,
+                             const void* const* q, const int64_t ld[2], const void* const* k_cache,
+                             const void* const* v_cache, const float* const* k_scale, const float* const* v_scale,
+                             void* const* o, float* const* lse, void* ws, fo_stream_t stream);
+
+/* Bytes of workspace for calls of up to `seqs` sequences, `rows` rows and
+ * `max_new` new tokens a sequence. */
+fo_status fo_paged_attention_workspace(const fo_paged_desc* desc, int32_t seqs, int64_t rows, int32_t max_new,
+                                       size_t* bytes);
+
 /* ---- tracing ------------------------------------------------------------ */
 
 /* Timestamps (%globaltimer, ns) of the last fused-kernel launch that used

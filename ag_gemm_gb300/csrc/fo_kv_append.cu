@@ -46,9 +46,7 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
   const Seq s = sequence(p.batch, b);
   const int i = row - s.row;
   if (i < 0 || i >= s.n) return;
-  if (s.n > p.batch.max_new) report(p.batch, b, kBadCount, s.n);
-  if (i >= p.batch.max_new) return;
-  const int pos = s.base() + i;
+  const int pos = s.base + i;
   int page = -1;
   if (pos >= 0) {
     page = p.batch.table[(int64_t)b * p.batch.cols + (pos >> p.batch.shift)];

@@ -19,12 +19,10 @@ struct Batch {
   int32_t* status;     // workspace's status word, or NULL
 };
 
-// One sequence: its first row, new tokens and length. (n = 0 where there is
-// nothing to do.)
+// One sequence: its first row, its new tokens (0 where there is nothing to
+// do), the first one's position, and the end of what the last one sees.
 struct Seq {
-  int32_t row, n, len;
-  // Positions of its new tokens are base + i.
-  __device__ __forceinline__ int32_t base() const { return len - n; }
+  int32_t row, n, base, end;
 };
 
 enum : int32_t { kBadPage = 1, kBadCount = 2, kBadStarts = 3, kBadLength = 4 };
@@ -37,7 +35,7 @@ __device__ __forceinline__ void report(const Batch& b, int seq, int what, int va
 // within the table's row.
 __device__ __forceinline__ Seq sequence(const Batch& b, int seq) {
   Seq s;
-  s.len = max(b.lengths[seq], 0);
+  const int32_t len = max(b.lengths[seq], 0);
   s.row = seq;
   s.n = 1;
   if (b.starts) {
@@ -49,10 +47,16 @@ __device__ __forceinline__ Seq sequence(const Batch& b, int seq) {
       s.row = s.n = 0;
     }
   }
-  if ((int64_t)s.len > b.cols << b.shift) {
-    report(b, seq, kBadLength, s.len);
+  if ((int64_t)len > b.cols << b.shift) {
+    report(b, seq, kBadLength, len);
     s.n = 0;
   }
+  s.base = len - s.n;
+  if (s.n > b.max_new) {
+    report(b, seq, kBadCount, s.n);
+    s.n = b.max_new;
+  }
+  s.end = max(s.base + s.n, 0);
   return s;
 }
 

@@ -77,4 +77,27 @@ fo_status check_paged(const fo_paged_desc* d);
 fo_status check_batch(const fo_paged_desc* d, const fo_paged_batch* b, int64_t rows);
 Batch batch_of(const fo_paged_desc* d, const fo_paged_batch* b, int64_t rows, void* ws);
 
+// A checked call of fo_paged_attention.
+struct PagedCall {
+  const fo_paged_desc* d;
+  const fo_paged_batch* b;
+  int64_t rows;
+  const int64_t* ld;
+  const void *const *q, *const *k, *const *v;
+  const float *const *ks, *const *vs;
+  void* const* o;
+  float* const* lse;
+  uint8_t* ws;
+  float scale_log2;
+  int sms;
+};
+// Many new tokens a sequence (fo_paged_prompt.cu).
+fo_status attend_prompts(const PagedCall& c, cudaStream_t s);
+size_t prompt_bytes(int32_t seqs);
+// Tensor maps (fo_paged_prompt.cu): pages of keys or values as [pages *
+// heads_k][page][D], in boxes of at most 128 bytes x `box` tokens, swizzled by
+// their own width; bf16 rows as [rows][heads][D], in boxes of 64 x heads x rows.
+bool encode_pages(CUtensorMap* m, const void* p, const fo_paged_desc* d, int64_t pages, int box);
+bool encode_rows(CUtensorMap* m, const void* p, int64_t rows, int64_t ld, int heads, int D, int box_heads, int box_rows);
+
 }  // namespace fo_ops

@@ -3,75 +3,15 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "fo_paged.h"
+#include "fo_paged_tiles.cuh"
 
 namespace fo_ops {
 namespace {
 
 using namespace fo;
-
-struct PagedParams {
-  const __nv_bfloat16* q[kMaxR];
-  const void* k[kMaxR];
-  const void* v[kMaxR];
-  const float* ks[kMaxR];
-  const float* vs[kMaxR];
-  __nv_bfloat16* o[kMaxR];
-  float* lse[kMaxR];
-  int64_t ld_q, ld_o;
-  Batch batch;
-  int32_t heads_q, heads_k, group, D, eight, window, sinks;
-  float scale;
-};
-
-// A warp for a row's head: key by key, the head's values over the lanes.
-__global__ void __launch_bounds__(128) row_kernel(const __grid_constant__ PagedParams p) {
-  grid_release();
-  grid_wait();
-  const int lane = threadIdx.x & 31, h = blockIdx.y * 4 + (threadIdx.x >> 5), r = blockIdx.z;
-  if (h >= p.heads_q) return;
-  const int each = p.D / 32, mask = (1 << p.batch.shift) - 1;
-  for (int b = blockIdx.x; b < p.batch.seqs; b += gridDim.x) {
-    const Seq s = sequence(p.batch, b);
-    for (int i = 0; i < s.n; ++i) {
-      const int64_t row = s.row + i;
-      const int pos = s.base + i;
-      const Sight see = sight_of(pos, p.window, p.sinks);
-      float q[4], acc[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-      for (int k = 0; k < each; ++k) q[k] = to_f(p.q[r][row * p.ld_q + h * p.D + lane + 32 * k]) * p.scale;
-      for (int j = 0; j <= pos; ++j) {
-        if (j >= see.sinks_end && j < see.lo) j = see.lo;
-        const int page = p.batch.table[(int64_t)b * p.batch.cols + (j >> p.batch.shift)];
-        if (page < 0 || page >= p.batch.pages) {
-          report(p.batch, b, kBadPage, page);
-          continue;
-        }
-        const int64_t slot = ((int64_t)page * p.heads_k + h / p.group << p.batch.shift) + (j & mask);
-        float kv[2][4];
-        for (int c = 0; c < 2; ++c) {
-          const void* base = c ? p.v[r] : p.k[r];
-          const float scale = p.eight ? (c ? p.vs[r] : p.ks[r])[slot] : 1.f;
-          for (int k = 0; k < each; ++k) {
-            const int64_t at = slot * p.D + lane + 32 * k;
-            kv[c][k] = p.eight ? (float)static_cast<const __nv_fp8_e4m3*>(base)[at] * scale
-                               : to_f(static_cast<const __nv_bfloat16*>(base)[at]);
-          }
-        }
-        float d = 0.f;
-        for (int k = 0; k < each; ++k) d = fmaf(q[k], kv[0][k], d);
-        d = warp_sum(d);
-        const float top = fmaxf(m, d), keep = m == -INFINITY ? 0.f : expf(m - top), w = expf(d - top);
-        m = top;
-        l = l * keep + w;
-        for (int k = 0; k < each; ++k) acc[k] = fmaf(w, kv[1][k], acc[k] * keep);
-      }
-      for (int k = 0; k < each; ++k)
-        from_f(m == -INFINITY ? 0.f : acc[k] / l, p.o[r][row * p.ld_o + h * p.D + lane + 32 * k]);
-      if (p.lse[r] && lane == 0) p.lse[r][row * p.heads_q + h] = m == -INFINITY ? -INFINITY : m + logf(l);
-    }
-  }
-}
-
 
 // ---- few new tokens a sequence: the cache's length is split
 //
@@ -99,8 +39,6 @@ constexpr int kRingBytes = 24576;      // of a warp
 constexpr int kFewThreads = 128;
 constexpr int kRadix = 16;             // parts joined at a time
 constexpr int kBlocksPerSm = 2;
-constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kLazy = 8.f;           // growth of a row's maximum (base 2) that is let pass
 
 struct FewParams {
   CUtensorMap k[kMaxR];   // [pages * heads_k][page][D]; boxes of 128 bytes x `box` tokens
@@ -170,81 +108,6 @@ struct Walk {
     } while (!tiles);
   }
 };
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(bar)
-               : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ float lds_f(uint32_t a) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&v)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-               : "r"(a));
-}
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (F16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 2^(a - b), and 0 for b = -infinity (a row that has seen nothing).
-__device__ __forceinline__ float ex2_below(float a, float b) { return b == -INFINITY ? 0.f : ex2(a - b); }
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Two e4m3 bytes (exactly) as two f16.
-__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
-  return r;
-}
-__device__ __forceinline__ uint32_t f16x2_of_e4m3_high(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(two));
-  return r;
-}
-
-// ln of the sum, from a maximum in base 2.
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l > 0.f || l != l ? m * 0.69314718055994531f + logf(l) : -INFINITY; 
-}
 
 template <int D, bool E8, int MT>
 __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm) few_kernel(const __grid_constant__ FewParams p) {
@@ -798,30 +661,6 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm) few_kernel(const __
   if (tid == 0 && *abort_flag && p.batch.status) fo::record_error(p.batch.status, FO_ERR_TIMEOUT, -1, -1, 0);
 }
 
-// Pages of keys or values as [pages * heads_k][page][D]; boxes of at most 128
-// bytes x `box` tokens, swizzled by their own width.
-bool encode(CUtensorMap* m, const void* p, const fo_paged_desc* d, int64_t pages, int box) {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      return nullptr;
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  if (!fn) return false;
-  const bool eight = d->cache_dtype == FO_CACHE_E4M3;
-  const cuuint64_t row = (cuuint64_t)d->head_dim * (eight ? 1 : 2);
-  const cuuint64_t dims[3] = {(cuuint64_t)d->head_dim, (cuuint64_t)d->page, (cuuint64_t)(pages * d->heads_k)};
-  const cuuint64_t strides[2] = {row, row * d->page};
-  const cuuint32_t boxes[3] = {eight ? (cuuint32_t)d->head_dim : 64u, (cuuint32_t)box, 1u}, steps[3] = {1, 1, 1};
-  return fn(m, eight ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides,
-            boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Rows of a unit that the split kernel takes: 16 a warp, four warps.
 constexpr int kFewRows = 64;
 constexpr int kMostBlocks = kBlocksPerSm * FO_GB300_SMS;
@@ -857,6 +696,7 @@ extern "C" fo_status fo_paged_attention_workspace(const fo_paged_desc* d, int32_
   if (seqs < 0 || rows < 0 || rows > INT32_MAX || max_new < 1) return FO_ERR_SHAPE;
   const int64_t most = (int64_t)max_new * (d->heads_q / d->heads_k);
   *bytes = fo_ops::few_bytes(d, most < fo_ops::kFewRows ? most : fo_ops::kFewRows);
+  if (most > fo_ops::kFewRows) *bytes = std::max(*bytes, fo_ops::prompt_bytes(seqs));
   return FO_OK;
 }
 
@@ -894,7 +734,7 @@ extern "C" fo_status fo_paged_attention(const fo_paged_desc* d, const fo_paged_b
     memset(static_cast<void*>(&f), 0, sizeof(f));
     f.box = d->page < kKeys ? d->page : kKeys;
     for (int r = 0; r < R; ++r) {
-      if (!encode(&f.k[r], k_cache[r], d, b->pages, f.box) || !encode(&f.v[r], v_cache[r], d, b->pages, f.box)) return FO_ERR_CUDA;
+      if (!encode_pages(&f.k[r], k_cache[r], d, b->pages, f.box) || !encode_pages(&f.v[r], v_cache[r], d, b->pages, f.box)) return FO_ERR_CUDA;
       f.ks[r] = eight ? k_scale[r] : nullptr;
       f.vs[r] = eight ? v_scale[r] : nullptr;
       f.q[r] = static_cast<const __nv_bfloat16*>(q[r]);
@@ -919,29 +759,11 @@ extern "C" fo_status fo_paged_attention(const fo_paged_desc* d, const fo_paged_b
     if (d->head_dim == 128) return eight ? launch_few<128, true>(f, mt, sms, s) : launch_few<128, false>(f, mt, sms, s);
     return eight ? launch_few<64, true>(f, mt, sms, s) : launch_few<64, false>(f, mt, sms, s);
   }
-  PagedParams p;
-  memset(&p, 0, sizeof(p));
-  for (int r = 0; r < R; ++r) {
-    p.q[r] = static_cast<const __nv_bfloat16*>(q[r]);
-    p.k[r] = k_cache[r];
-    p.v[r] = v_cache[r];
-    p.ks[r] = eight ? k_scale[r] : nullptr;
-    p.vs[r] = eight ? v_scale[r] : nullptr;
-    p.o[r] = static_cast<__nv_bfloat16*>(o[r]);
-    p.lse[r] = lse ? lse[r] : nullptr;
-  }
-  p.ld_q = ld[0];
-  p.ld_o = ld[1];
-  p.batch = batch_of(d, b, rows, ws);
-  p.heads_q = d->heads_q;
-  p.heads_k = d->heads_k;
-  p.group = d->heads_q / d->heads_k;
-  p.D = d->head_dim;
-  p.eight = eight;
-  p.window = d->window;
-  p.sinks = d->sinks;
-  p.scale = scale;
-  const dim3 grid(b->seqs, (d->heads_q + 3) / 4, R);
-  return launched(launch_after(row_kernel, grid, 128, 0, 0, (cudaStream_t)stream, p), "paged attention", R, rows, wide,
-                  b->seqs, 128);
+  PagedCall c;
+  c.d = d, c.b = b, c.rows = rows, c.ld = ld;
+  c.q = q, c.k = k_cache, c.v = v_cache, c.ks = k_scale, c.vs = v_scale, c.o = o, c.lse = lse;
+  c.ws = static_cast<uint8_t*>(ws);
+  c.scale_log2 = scale * 1.4426950408889634f;
+  c.sms = sms;
+  return attend_prompts(c, (cudaStream_t)stream);
 }

@@ -35,10 +35,9 @@ using namespace fo;
 // the parts in the blocks' order (16 at a time), so results repeat.
 
 constexpr int kKeys = 32;              // a warp's keys of a tile
-constexpr int kRingBytes = 24576;      // of a warp
 constexpr int kFewThreads = 128;
 constexpr int kRadix = 16;             // parts joined at a time
-constexpr int kBlocksPerSm = 2;
+constexpr int kPerSm = 2;              // blocks
 
 struct FewParams {
   CUtensorMap k[kMaxR];   // [pages * heads_k][page][D]; boxes of 128 bytes x `box` tokens
@@ -64,19 +63,20 @@ struct Few {
   static constexpr int kWidth = kRow < 128 ? kRow : 128;    // of a box
   static constexpr int kCuts = kRow / kWidth;
   static constexpr int kSlot = kKeys * kRow;
+  static constexpr int kRing = 24576;                       // bytes of a warp
   static constexpr int kGroups = 4 / MT;                    // warps with keys of their own
   static constexpr int kStep = kKeys * kGroups;             // keys of a tile
-  static constexpr int kSlots = kRingBytes * MT / kSlot;
+  static constexpr int kSlots = kRing * MT / kSlot;
   static constexpr int kRows = 16 * MT;
   static constexpr int kPart = kRows * (D + 2);             // floats of a part: output, maxima, sums
   // Shared memory: rings, scales, rows being joined, (m, l) of each warp, barriers.
-  static constexpr int kOffScale = 4 * kRingBytes;
+  static constexpr int kOffScale = 4 * kRing;
   static constexpr int kOffJoin = kOffScale + (E8 ? kGroups * kSlots * 128 : 0);
   static constexpr int kOffStat = kOffJoin + (4 - MT) * 8 * D * 4;
   static constexpr int kOffBar = kOffStat + 4 * 16 * 8;
   static constexpr int kOffMisc = kOffBar + 2 * kGroups * kSlots * 8;
   static constexpr int kSmem = 1024 + kOffMisc + 64;
-  static_assert(kSmem <= 115712, "two blocks an SM");
+  static_assert(kPerSm * (kSmem + 1024) <= 233472, "blocks an SM");
 };
 
 // Where a block is on the line of tiles.
@@ -110,7 +110,7 @@ struct Walk {
 };
 
 template <int D, bool E8, int MT>
-__global__ void __launch_bounds__(kFewThreads, kBlocksPerSm) few_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_constant__ FewParams p) {
   using C = Few<D, E8, MT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm) few_kernel(const __
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc);
   int* const misc = reinterpret_cast<int*>(gbase + C::kOffMisc);   // [0] abort, [1] flag, [2] sequence, [4..5] its first tile
   const uint32_t full = base + C::kOffBar + kg * C::kSlots * 8, empty = full + C::kGroups * C::kSlots * 8;
-  const uint32_t ring = base + kg * (kRingBytes * MT), scales = base + C::kOffScale + kg * C::kSlots * 128;
+  const uint32_t ring = base + kg * (C::kRing * MT), scales = base + C::kOffScale + kg * C::kSlots * 128;
   if (tid == 0) {
     for (int i = 0; i < C::kGroups * C::kSlots; ++i) {
       mbar_init(base + C::kOffBar + i * 8, 1);
@@ -320,23 +320,35 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm) few_kernel(const __
       mbar_wait(full + cslot * 8, cround & 1, abort_flag, kWaitNs);
       {
         const uint32_t at = ring + cslot * C::kSlot;
+        if constexpr (!E8) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = 8 * j + g;
-          if constexpr (!E8) {
+          for (int k = 0; k < D / 32; ++k) {
+            uint4 v[4];
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              const uint4 v = lds128(at + (k >> 1) * (kKeys * 128) + n * 128 + (((2 * c + (k & 1)) ^ g) << 4));
-              mma16816<false>(sc[j], qf[2 * k], v.x, v.y);
-              mma16816<false>(sc[j], qf[2 * k + 1], v.z, v.w);
+            for (int j = 0; j < 4; ++j)
+              v[j] = lds128(at + (k >> 1) * (kKeys * 128) + (8 * j + g) * 128 + (((2 * c + (k & 1)) ^ g) << 4));
+            // (Four sums in turn: one after the other they would wait for each product.)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma16816<false>(sc[j], qf[2 * k], v[j].x, v[j].y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma16816<false>(sc[j], qf[2 * k + 1], v[j].z, v[j].w);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 64; ++k) {
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int n = 8 * j + g;
+              v[j] = lds128(D == 128 ? at + n * 128 + (((2 * c + k) ^ g) << 4) : at + n * 64 + ((c ^ ((n >> 1) & 3)) << 4));
             }
-          } else {
 #pragma unroll
-            for (int k = 0; k < D / 64; ++k) {
-              const uint4 v = lds128(D == 128 ? at + n * 128 + (((2 * c + k) ^ g) << 4) : at + n * 64 + ((c ^ ((n >> 1) & 3)) << 4));
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int e = 0; e < 4; ++e) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) mma16816<true>(sc[j], qf[4 * k + e], f16x2_of_e4m3(w[e]), f16x2_of_e4m3_high(w[e]));
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t w = e == 0 ? v[j].x : e == 1 ? v[j].y : e == 2 ? v[j].z : v[j].w;
+                mma16816<true>(sc[j], qf[4 * k + e], f16x2_of_e4m3(w), f16x2_of_e4m3_high(w));
+              }
             }
           }
         }
@@ -663,7 +675,7 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm) few_kernel(const __
 
 // Rows of a unit that the split kernel takes: 16 a warp, four warps.
 constexpr int kFewRows = 64;
-constexpr int kMostBlocks = kBlocksPerSm * FO_GB300_SMS;
+constexpr int kMostBlocks = kPerSm * FO_GB300_SMS;
 constexpr size_t kCountBytes = (kMostBlocks * 3 * 4 + 255) / 256 * 256;
 int row_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 size_t few_bytes(const fo_paged_desc* d, int64_t rows) {
@@ -676,7 +688,7 @@ fo_status launch_few(FewParams& k, int sms, cudaStream_t s) {
   constexpr int smem = Few<D, E8, MT>::kSmem;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return launched(e, "paged attention", k.R, k.batch.rows, D, 0, kFewThreads);
-  const int blocks = sms * kBlocksPerSm < kMostBlocks ? sms * kBlocksPerSm : kMostBlocks;
+  const int blocks = std::min(sms, FO_GB300_SMS) * kPerSm;
   return launched(launch_after(kern, dim3(blocks), kFewThreads, smem, 0, s, k), "paged attention", k.R, k.batch.rows, D, blocks,
                   kFewThreads);
 }

@@ -27,14 +27,13 @@ using namespace fo;
 // for each of two blocks an SM, so that every SM reads the same bytes whatever
 // the lengths. A block finds its piece from the lengths on the device: a captured call may
 // be replayed with other ones. In a block, each of four warps takes 32 of a
-// tile's keys (with more than 16 rows, two or four warps share the keys and
+// tile's keys (64 in 8 bits) (with more than 16 rows, two or four warps share the keys and
 // part the rows), has TMA bring them into a ring of its own, and keeps its own
 // maximum, sum and output in registers: no barrier in the stream of tiles. At
 // a unit's end, or the piece's, the warps' parts are joined through shared
 // memory. A unit cut between blocks is joined by the last of them to arrive,
 // the parts in the blocks' order (16 at a time), so results repeat.
 
-constexpr int kKeys = 32;              // a warp's keys of a tile
 constexpr int kFewThreads = 128;
 constexpr int kRadix = 16;             // parts joined at a time
 constexpr int kPerSm = 2;              // blocks
@@ -50,7 +49,8 @@ struct FewParams {
   int64_t ld_q, ld_o;
   Batch batch;
   int32_t R, heads_q, heads_k, group, window, sinks;
-  int32_t box;            // tokens of a box: 16 or 32
+  int32_t box;            // tokens of a box: a page's, or a warp's tile's
+  int32_t boxes_log2;     // of a warp's tile
   int32_t least;          // tiles of a piece, at least
   float scale_log2;
   float* part;            // [blocks][2][rows * (D + 2)]
@@ -59,6 +59,7 @@ struct FewParams {
 
 template <int D, bool E8, int MT>
 struct Few {
+  static constexpr int kKeys = E8 ? 64 : 32;                // a warp's keys of a tile
   static constexpr int kRow = D * (E8 ? 1 : 2);             // bytes of a key
   static constexpr int kWidth = kRow < 128 ? kRow : 128;    // of a box
   static constexpr int kCuts = kRow / kWidth;
@@ -67,11 +68,14 @@ struct Few {
   static constexpr int kGroups = 4 / MT;                    // warps with keys of their own
   static constexpr int kStep = kKeys * kGroups;             // keys of a tile
   static constexpr int kSlots = kRing * MT / kSlot;
+  // Warps that share keys: a slot is filled again this much later than it is
+  // read, so that the one that loads need not wait for the others.
+  static constexpr int kLag = MT > 1 ? 2 : 0;
   static constexpr int kRows = 16 * MT;
   static constexpr int kPart = kRows * (D + 2);             // floats of a part: output, maxima, sums
   // Shared memory: rings, scales, rows being joined, (m, l) of each warp, barriers.
   static constexpr int kOffScale = 4 * kRing;
-  static constexpr int kOffJoin = kOffScale + (E8 ? kGroups * kSlots * 128 : 0);
+  static constexpr int kOffJoin = kOffScale + (E8 ? kGroups * kSlots * kKeys * 4 : 0);
   static constexpr int kOffStat = kOffJoin + (4 - MT) * 8 * D * 4;
   static constexpr int kOffBar = kOffStat + 4 * 16 * 8;
   static constexpr int kOffMisc = kOffBar + 2 * kGroups * kSlots * 8;
@@ -82,7 +86,7 @@ struct Few {
 // Where a block is on the line of tiles.
 template <int STEP>
 struct Walk {
-  int b, u, t, tiles;           // sequence, unit of it, tile of the unit, tiles of a unit
+  int b, r, h, t, tiles;        // sequence, rank and key head, tile of the unit, tiles of a unit
   Seq s;
   int lo, sinks_end, early, late;
   __device__ __forceinline__ void of(const Batch& batch, int window, int sinks) {
@@ -100,8 +104,10 @@ struct Walk {
   __device__ __forceinline__ void next(const FewParams& p) {
     if (++t < tiles) return;
     t = 0;
-    if (++u < p.R * p.heads_k) return;
-    u = 0;
+    if (++h < p.heads_k) return;
+    h = 0;
+    if (++r < p.R) return;
+    r = 0;
     do {
       if (++b >= p.batch.seqs) return;
       of(p.batch, p.window, p.sinks);
@@ -112,6 +118,7 @@ struct Walk {
 template <int D, bool E8, int MT>
 __global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_constant__ FewParams p) {
   using C = Few<D, E8, MT>;
+  constexpr int kKeys = C::kKeys;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw);
@@ -120,7 +127,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_c
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc);
   int* const misc = reinterpret_cast<int*>(gbase + C::kOffMisc);   // [0] abort, [1] flag, [2] sequence, [4..5] its first tile
   const uint32_t full = base + C::kOffBar + kg * C::kSlots * 8, empty = full + C::kGroups * C::kSlots * 8;
-  const uint32_t ring = base + kg * (C::kRing * MT), scales = base + C::kOffScale + kg * C::kSlots * 128;
+  const uint32_t ring = base + kg * (C::kRing * MT), scales = base + C::kOffScale + kg * C::kSlots * kKeys * 4;
   if (tid == 0) {
     for (int i = 0; i < C::kGroups * C::kSlots; ++i) {
       mbar_init(base + C::kOffBar + i * 8, 1);
@@ -178,8 +185,10 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_c
     cw.b = misc[2];
     cw.of(p.batch, p.window, p.sinks);
     const long long off = x0 - *reinterpret_cast<long long*>(misc + 4);
-    cw.u = (int)(off / cw.tiles);
-    cw.t = (int)(off - (long long)cw.u * cw.tiles);
+    const int u = (int)(off / cw.tiles);
+    cw.t = (int)(off - (long long)u * cw.tiles);
+    cw.r = u / p.heads_k;
+    cw.h = u - cw.r * p.heads_k;
   }
   __syncthreads();
 
@@ -193,44 +202,40 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_c
   };
   auto issue = [&]() {
     if (pleft <= 0) return;
-    if (!value && (pw.b != page_b || pw.t < page_t || pw.t >= page_t + 16)) {
-      // Page numbers of 16 tiles, two a tile (the halves of its keys).
+    if (!value && (pw.b != page_b || (uint32_t)(pw.t - page_t) >= 32u >> p.boxes_log2)) {
+      // Page numbers of the next tiles, a lane for a box.
       page_b = pw.b;
       page_t = pw.t;
       page_of = -1;
-      const int t = pw.t + (lane >> 1);
-      const int key = (t < pw.early ? t : t - pw.early + pw.late) * C::kStep + kg * kKeys + (lane & 1) * 16;
-      if (t < pw.tiles && pw.any(key, 16)) {
+      const int t = pw.t + (lane >> p.boxes_log2);
+      const int key = (t < pw.early ? t : t - pw.early + pw.late) * C::kStep + kg * kKeys + (lane & ((1 << p.boxes_log2) - 1)) * p.box;
+      if (t < pw.tiles && pw.any(key, p.box)) {
         const int id = p.batch.table[(long long)pw.b * p.batch.cols + (key >> p.batch.shift)];
         if (id < 0 || id >= p.batch.pages) report(p.batch, pw.b, kBadPage, id);
         else page_of = id;
       }
     }
-    const int id0 = __shfl_sync(0xffffffffu, page_of, (pw.t - page_t) * 2), id1 = __shfl_sync(0xffffffffu, page_of, (pw.t - page_t) * 2 + 1);
+    // Lane i < boxes: box i.
+    const int id = __shfl_sync(0xffffffffu, page_of, (((pw.t - page_t) << p.boxes_log2) + lane) & 31);
     if (MT > 1 && pround > 0) mbar_wait(empty + pslot * 8, (pround - 1) & 1, abort_flag, kWaitNs);
-    if (lane == 0) {
-      const int r = pw.u / p.heads_k, h = pw.u - r * p.heads_k, key = pw.first_key() + kg * kKeys;
-      const int in_page = key & ((1 << p.batch.shift) - 1);
-      const CUtensorMap* const map = value ? &p.v[r] : &p.k[r];
-      const uint32_t bar = full + pslot * 8, dst = ring + pslot * C::kSlot;
-      const bool two = p.box == 16;
-      // (A tile may begin in a page that is not needed and end in one that is.)
-      const int ids[2] = {two ? id0 : id0 >= 0 ? id0 : id1, id1};
-      uint32_t bytes = C::kSlot;
-      if constexpr (E8) bytes += (ids[0] >= 0 ? p.box * 4 : 0) + (two && ids[1] >= 0 ? 64 : 0);
-      mbar_arrive_expect_tx(bar, bytes);
+    const uint32_t bar = full + pslot * 8;
+    const bool mine = lane < 1 << p.boxes_log2;
+    uint32_t bytes = C::kSlot;
+    if constexpr (E8) bytes += __popc(__ballot_sync(0xffffffffu, mine && id >= 0)) * p.box * 4;
+    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+    __syncwarp();
+    if (mine) {
+      // What no page holds is read from behind the last one: zeros.
+      const int z = id >= 0 ? id * p.heads_k + pw.h : p.batch.pages * p.heads_k;
+      const int y = (pw.first_key() + kg * kKeys + lane * p.box) & ((1 << p.batch.shift) - 1);
+      const CUtensorMap* const map = value ? &p.v[pw.r] : &p.k[pw.r];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (i && !two) break;
-        // What no page holds is read from behind the last one: zeros.
-        const int z = ids[i] >= 0 ? ids[i] * p.heads_k + h : p.batch.pages * p.heads_k, y = two ? 0 : in_page;
-#pragma unroll
-        for (int cut = 0; cut < C::kCuts; ++cut)
-          tma_load_3d(dst + cut * kKeys * 128 + i * 16 * C::kWidth, map, bar, cut * 64, y, z);
-        if constexpr (E8)
-          if (ids[i] >= 0)
-            bulk_load(scales + pslot * 128 + i * 64, (value ? p.vs[r] : p.ks[r]) + ((long long)z << p.batch.shift) + y, p.box * 4, bar);
-      }
+      for (int cut = 0; cut < C::kCuts; ++cut)
+        tma_load_3d(ring + pslot * C::kSlot + cut * kKeys * 128 + lane * p.box * C::kWidth, map, bar, cut * 64, y, z);
+      if constexpr (E8)
+        if (id >= 0)
+          bulk_load(scales + (pslot * kKeys + lane * p.box) * 4, (value ? p.vs[pw.r] : p.ks[pw.r]) + ((long long)z << p.batch.shift) + y,
+                    p.box * 4, bar);
     }
     if (value) pw.next(p), --pleft, seek();
     value = !value;
@@ -246,7 +251,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_c
   };
   if (mt == 0) {
     seek();
-    for (int i = 0; i < C::kSlots; ++i) issue();
+    for (int i = 0; i < C::kSlots - C::kLag; ++i) issue();
   }
 
   for (long long x = x0; x < x1;) {
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_c
     const int here = (int)min((long long)(cw.tiles - cw.t), x1 - x);
     const long long unit = x - cw.t;
     const bool whole = here == cw.tiles;
-    const int tiles = cw.tiles, r = cw.u / p.heads_k, h = cw.u - r * p.heads_k, real = cw.s.n * p.group;
+    const int tiles = cw.tiles, r = cw.r, h = cw.h, real = cw.s.n * p.group;
     const Seq s = cw.s;
     int row[2], pos[2], lo[2];
     uint32_t qf[D / 16][4];
@@ -314,48 +319,50 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_c
       if (!cw.any(key, kKeys)) continue;
       // All of a tile's keys seen by all rows?
       const bool part = !(key + kKeys - 1 <= s.base && (key >= lo_last || key + kKeys <= p.sinks));
-      float sc[4][4];
+      constexpr int kJ = kKeys / 8;   // eights of keys
+      float sc[kJ][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+      for (int j = 0; j < kJ; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
       mbar_wait(full + cslot * 8, cround & 1, abort_flag, kWaitNs);
       {
         const uint32_t at = ring + cslot * C::kSlot;
         if constexpr (!E8) {
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
-            uint4 v[4];
+            uint4 v[kJ];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < kJ; ++j)
               v[j] = lds128(at + (k >> 1) * (kKeys * 128) + (8 * j + g) * 128 + (((2 * c + (k & 1)) ^ g) << 4));
             // (Four sums in turn: one after the other they would wait for each product.)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma16816<false>(sc[j], qf[2 * k], v[j].x, v[j].y);
+            for (int j = 0; j < kJ; ++j) mma16816<false>(sc[j], qf[2 * k], v[j].x, v[j].y);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma16816<false>(sc[j], qf[2 * k + 1], v[j].z, v[j].w);
+            for (int j = 0; j < kJ; ++j) mma16816<false>(sc[j], qf[2 * k + 1], v[j].z, v[j].w);
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < D / 64; ++k) {
+          for (int k = 0; k < kJ / 4 * (D / 64); ++k) {
+            const int j0 = k / (D / 64) * 4, half = k % (D / 64);
             uint4 v[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int n = 8 * j + g;
-              v[j] = lds128(D == 128 ? at + n * 128 + (((2 * c + k) ^ g) << 4) : at + n * 64 + ((c ^ ((n >> 1) & 3)) << 4));
+              const int n = 8 * (j0 + j) + g;
+              v[j] = lds128(D == 128 ? at + n * 128 + (((2 * c + half) ^ g) << 4) : at + n * 64 + ((c ^ ((n >> 1) & 3)) << 4));
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const uint32_t w = e == 0 ? v[j].x : e == 1 ? v[j].y : e == 2 ? v[j].z : v[j].w;
-                mma16816<true>(sc[j], qf[4 * k + e], f16x2_of_e4m3(w), f16x2_of_e4m3_high(w));
+                mma16816<true>(sc[j0 + j], qf[4 * half + e], f16x2_of_e4m3(w), f16x2_of_e4m3_high(w));
               }
             }
           }
         }
         if constexpr (E8) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint2 k2 = lds64(scales + cslot * 128 + (8 * j + 2 * c) * 4);
+          for (int j = 0; j < kJ; ++j) {
+            const uint2 k2 = lds64(scales + cslot * (kKeys * 4) + (8 * j + 2 * c) * 4);
             const float k0 = __uint_as_float(k2.x), k1 = __uint_as_float(k2.y);
             sc[j][0] *= k0, sc[j][1] *= k1, sc[j][2] *= k0, sc[j][3] *= k1;
           }
@@ -364,7 +371,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_c
       done();
       if (part) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kJ; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int at = key + 8 * j + 2 * c + (e & 1), a = e >> 1;
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_c
       for (int a = 0; a < 2; ++a) {
         float mx = fmaxf(sc[0][2 * a], sc[0][2 * a + 1]);
 #pragma unroll
-        for (int j = 1; j < 4; ++j) mx = fmaxf(mx, fmaxf(sc[j][2 * a], sc[j][2 * a + 1]));
+        for (int j = 1; j < kJ; ++j) mx = fmaxf(mx, fmaxf(sc[j][2 * a], sc[j][2 * a + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * qscale[a];
         const bool grows = mx > m[a] + kLazy || (m[a] == -INFINITY && mx > m[a]);
@@ -389,16 +396,19 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_c
           for (int j = 0; j < D / 8; ++j) o[j][2 * a] *= by, o[j][2 * a + 1] *= by;
         }
       }
-      uint32_t pf[2][4];
+      uint32_t pf[kJ / 2][4];
       mbar_wait(full + cslot * 8, cround & 1, abort_flag, kWaitNs);
-      float vs_pair[4][2];
       if constexpr (E8) {
         // Weights times the values' scales over sigma, the largest scale so
         // far: at most 2^(kLazy + 7) in f16.
-        const float mine = lds_f(scales + cslot * 128 + lane * 4);
-        const int at = key + lane;
-        const bool seen = at < s.end && (at >= cw.lo || at < cw.sinks_end);
-        const uint32_t top = __reduce_max_sync(0xffffffffu, seen ? __float_as_uint(mine) & 0x7fffffffu : 0u);
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < kKeys / 32; ++e) {
+          const int at = key + lane + 32 * e;
+          if (at < s.end && (at >= cw.lo || at < cw.sinks_end))
+            top = max(top, __float_as_uint(lds_f(scales + cslot * (kKeys * 4) + (lane + 32 * e) * 4)) & 0x7fffffffu);
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
         if (__uint_as_float(top) > sigma * 128.f || sigma == 0.f) {
           const uint32_t exponent = min(max((top + 0x7fffffu) >> 23, 9u), 253u);
           const float to = __uint_as_float((exponent - 7u) << 23), by = sigma == 0.f ? 0.f : sigma / to;
@@ -407,22 +417,22 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_c
           sigma = to;
           sigma_inv = 1.f / to;
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint2 v2 = lds64(scales + cslot * 128 + (8 * j + 2 * c) * 4);
-          vs_pair[j][0] = __uint_as_float(v2.x) * sigma_inv, vs_pair[j][1] = __uint_as_float(v2.y) * sigma_inv;
-        }
       }
+      const float down[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const float down = m[a] == -INFINITY ? 0.f : m[a];
+      for (int j = 0; j < kJ; ++j) {
+        float2 by = make_float2(1.f, 1.f);
+        if constexpr (E8) {
+          const uint2 v2 = lds64(scales + cslot * (kKeys * 4) + (8 * j + 2 * c) * 4);
+          by = make_float2(__uint_as_float(v2.x) * sigma_inv, __uint_as_float(v2.y) * sigma_inv);
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float w0 = ex2(fmaf(sc[j][2 * a], qscale[a], -down)), w1 = ex2(fmaf(sc[j][2 * a + 1], qscale[a], -down));
+        for (int a = 0; a < 2; ++a) {
+          float w0 = ex2(fmaf(sc[j][2 * a], qscale[a], down[a])), w1 = ex2(fmaf(sc[j][2 * a + 1], qscale[a], down[a]));
           l[a] += w0 + w1;
           if constexpr (E8) {
-            w0 = part && w0 == 0.f ? 0.f : w0 * vs_pair[j][0];
-            w1 = part && w1 == 0.f ? 0.f : w1 * vs_pair[j][1];
+            w0 = part && w0 == 0.f ? 0.f : w0 * by.x;
+            w1 = part && w1 == 0.f ? 0.f : w1 * by.y;
             pf[j >> 1][(j & 1) * 2 + a] = f16x2(w0, w1);
           } else {
             pf[j >> 1][(j & 1) * 2 + a] = bf16x2(w0, w1);
@@ -434,7 +444,7 @@ __global__ void __launch_bounds__(kFewThreads, kPerSm) few_kernel(const __grid_c
         // Places that no row sees may hold NaN: their values count as zeros.
         auto seen = [&](int k) { return k < s.end && (k >= cw.lo || k < cw.sinks_end); };
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
+        for (int kk = 0; kk < kJ / 2; ++kk) {
           if constexpr (!E8) {
             const int n = kk * 16 + (lane & 15);
             uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
@@ -744,7 +754,10 @@ extern "C" fo_status fo_paged_attention(const fo_paged_desc* d, const fo_paged_b
   if (unit_rows <= kFewRows) {
     FewParams f;
     memset(static_cast<void*>(&f), 0, sizeof(f));
-    f.box = d->page < kKeys ? d->page : kKeys;
+    const int keys = eight ? Few<128, true, 1>::kKeys : Few<128, false, 1>::kKeys;
+    f.box = std::min(d->page, keys);
+    for (f.boxes_log2 = 0; f.box << f.boxes_log2 < keys; ++f.boxes_log2) {
+    }
     for (int r = 0; r < R; ++r) {
       if (!encode_pages(&f.k[r], k_cache[r], d, b->pages, f.box) || !encode_pages(&f.v[r], v_cache[r], d, b->pages, f.box)) return FO_ERR_CUDA;
       f.ks[r] = eight ? k_scale[r] : nullptr;

@@ -91,6 +91,32 @@ struct PagedCall {
   float scale_log2;
   int sms;
 };
+// Few new tokens a sequence (fo_paged_few.cuh), `eights` times 8 rows (1, 2, 4
+// or 8) of a key head: kFewBlocks blocks an SM.
+constexpr int kFewThreads = 256, kFewBlocks = 2;
+// Keys of a tile: 32 for each warp that has keys of its own, 64 in 8 bits.
+constexpr int few_step(int eights, bool eight) { return (eights <= 2 ? 4 : eights == 4 ? 2 : 1) * (eight ? 64 : 32); }
+struct FewParams {
+  CUtensorMap k[kMaxR];   // [pages * heads_k][page][D]; boxes of 128 bytes x `box` tokens
+  CUtensorMap v[kMaxR];
+  const float* ks[kMaxR];
+  const float* vs[kMaxR];
+  const __nv_bfloat16* q[kMaxR];
+  __nv_bfloat16* o[kMaxR];
+  float* lse[kMaxR];
+  int64_t ld_q, ld_o;
+  Batch batch;
+  int32_t R, heads_q, heads_k, group, window, sinks;
+  int32_t box;            // tokens of a box: a page's, or a tile's
+  int32_t boxes_log2;     // of a tile
+  int32_t least;          // tiles of a piece, at least
+  float scale_log2;
+  float* part;            // [blocks][2][8 eights * (D + 2)]
+  uint32_t* count;        // [blocks][3], zero between calls
+};
+
+fo_status attend_few_64(FewParams& k, int eights, bool eight, int sms, cudaStream_t s);
+fo_status attend_few_128(FewParams& k, int eights, bool eight, int sms, cudaStream_t s);
 // Many new tokens a sequence (fo_paged_prompt.cu).
 fo_status attend_prompts(const PagedCall& c, cudaStream_t s);
 size_t prompt_bytes(int32_t seqs);

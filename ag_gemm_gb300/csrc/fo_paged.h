@@ -77,6 +77,13 @@ fo_status check_paged(const fo_paged_desc* d);
 fo_status check_batch(const fo_paged_desc* d, const fo_paged_batch* b, int64_t rows);
 Batch batch_of(const fo_paged_desc* d, const fo_paged_batch* b, int64_t rows, void* ws);
 
+// Workspace: header and deal (256 bytes), then the counters of both kernels,
+// zero between calls, then scratch that the one and the other use.
+constexpr int kFewThreads = 256, kFewBlocks = 2;   // blocks an SM
+constexpr int kMostParts = 4 * FO_GB300_SMS;       // of the prompts' kernel
+constexpr size_t kFewCountBytes = (kFewBlocks * FO_GB300_SMS * 3 * 4 + 255) / 256 * 256;
+constexpr size_t kScratchAt = 256 + kFewCountBytes + (size_t)kMostParts * 16 * 4;
+
 // A checked call of fo_paged_attention.
 struct PagedCall {
   const fo_paged_desc* d;
@@ -93,7 +100,6 @@ struct PagedCall {
 };
 // Few new tokens a sequence (fo_paged_few.cuh), `eights` times 8 rows (1, 2, 4
 // or 8) of a key head: kFewBlocks blocks an SM.
-constexpr int kFewThreads = 256, kFewBlocks = 2;
 // Keys of a tile: 32 for each warp that has keys of its own, 64 in 8 bits.
 constexpr int few_step(int eights, bool eight) { return (eights <= 2 ? 4 : eights == 4 ? 2 : 1) * (eight ? 64 : 32); }
 struct FewParams {
@@ -119,7 +125,7 @@ fo_status attend_few_64(FewParams& k, int eights, bool eight, int sms, cudaStrea
 fo_status attend_few_128(FewParams& k, int eights, bool eight, int sms, cudaStream_t s);
 // Many new tokens a sequence (fo_paged_prompt.cu).
 fo_status attend_prompts(const PagedCall& c, cudaStream_t s);
-size_t prompt_bytes(int32_t seqs);
+size_t prompt_bytes(const fo_paged_desc* d, int32_t seqs, int64_t rows, int32_t max_new);
 // Tensor maps (fo_paged_prompt.cu): pages of keys or values as [pages *
 // heads_k][page][D], in boxes of at most 128 bytes x `box` tokens, swizzled by
 // their own width; bf16 rows as [rows][heads][D], in boxes of 64 x heads x rows.

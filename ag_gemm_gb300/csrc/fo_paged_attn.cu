@@ -14,9 +14,8 @@ namespace {
 // takes; more are the prompts' kernel's, whose tiles have 128.
 constexpr int kFewRows = 64;
 int eights_of(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8; }
-constexpr size_t kCountBytes = (kFewBlocks * FO_GB300_SMS * 3 * 4 + 255) / 256 * 256;
 size_t few_bytes(const fo_paged_desc* d, int64_t rows) {
-  return 256 + kCountBytes + (size_t)kFewBlocks * FO_GB300_SMS * 2 * 8 * eights_of(rows) * (d->head_dim + 2) * 4;
+  return kScratchAt + (size_t)kFewBlocks * FO_GB300_SMS * 2 * 8 * eights_of(rows) * (d->head_dim + 2) * 4;
 }
 
 }  // namespace
@@ -30,7 +29,7 @@ extern "C" fo_status fo_paged_attention_workspace(const fo_paged_desc* d, int32_
   if (seqs < 0 || rows < 0 || rows > INT32_MAX || max_new < 1) return FO_ERR_SHAPE;
   const int64_t most = (int64_t)max_new * (d->heads_q / d->heads_k);
   *bytes = fo_ops::few_bytes(d, most < fo_ops::kFewRows ? most : fo_ops::kFewRows);
-  if (most > fo_ops::kFewRows) *bytes = std::max(*bytes, fo_ops::prompt_bytes(seqs));
+  if (most > fo_ops::kFewRows) *bytes = std::max(*bytes, fo_ops::prompt_bytes(d, seqs, rows, max_new));
   return FO_OK;
 }
 
@@ -90,7 +89,7 @@ extern "C" fo_status fo_paged_attention(const fo_paged_desc* d, const fo_paged_b
     f.least = 1;
     f.scale_log2 = scale * 1.4426950408889634f;
     f.count = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + 256);
-    f.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256 + kCountBytes);
+    f.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kScratchAt);
     return (d->head_dim == 128 ? attend_few_128 : attend_few_64)(f, eights, eight, sms, (cudaStream_t)stream);
   }
   PagedCall c;

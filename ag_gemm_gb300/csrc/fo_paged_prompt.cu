@@ -6,22 +6,27 @@
 // a block works on two tiles at a time over the same keys and values, 128 a
 // step. While the tensor core sums one tile's weights times values and
 // computes its next scores (1024 cycles of bf16 at D = 128), the other tile's
-// softmax runs; a thread has a row of its own, so no row needs another
-// thread. Per step and tile:
+// softmax runs. Per step and tile:
 //     S = Q K^T        in TMEM, 128 columns
-//     P = 2^(S - m)    in 16 bits over the same columns, by the tile's four warps
+//     P = 2^(S - m)    in 16 bits over the same columns, by the tile's eight
+//                      warps: two to a row, 64 keys each
 //     O += P V         in TMEM, D columns, P read from TMEM
-// The running maximum m moves when it grows by more than 2^8 (smaller growth
-// is cancelled by the division at the end); only then O is read and rescaled.
+// The two threads of a row swap their maxima through shared memory; each
+// computes its weights with the running maximum while the other's is on its
+// way, and scales them only if that moves (it does when it grows by more than
+// 2^8; smaller growth is cancelled by the division at the end). Only then O is
+// read and rescaled. With a thread for a whole row, no swap, but 128 scores one
+// after the other, a step took 1.6 times as long.
 //
-// Warps: 0 loads (and deals items), 1 issues the products, 2 and 3 put zeros
-// in the place of values that nobody sees, 4-7 and 8-11 are the tiles'
-// softmax. With an 8-bit cache 12-15 turn its bytes into f16 (which holds
+// Warps: 0 loads (and deals items), 1 and 2 issue the tiles' products (one
+// issuer for both fell behind: a wait for a barrier that is ready takes it 150
+// cycles), 3 puts zeros in the place of values that nobody sees, 4-11 and 12-19
+// are the tiles' softmax. With an 8-bit cache 3 and 20 turn its bytes into f16 (which holds
 // e4m3 exactly): queries and weights are f16 then, the keys' scales multiply
 // the scores' columns and the values' the weights.
 //
-// A first kernel of one block adds up the sequences' tile pairs; blocks take
-// pairs from a counter, the last (under the causal mask the costliest) first.
+// A first kernel of one block lists the items; blocks take them from a
+// counter, the last (under the causal mask the costliest) first.
 #include <cudaTypedefs.h>
 #include <math.h>
 #include <string.h>
@@ -53,67 +58,33 @@ struct PromptParams {
   int32_t R, heads_q, heads_k, group, tokens;   // tokens: of a tile
   int32_t window, sinks, box;
   float scale_log2;
+  int32_t sms;
   int64_t* before;        // [seqs + 1]: pairs of the sequences before
-  uint32_t* next;         // items dealt
+  uint32_t* next;         // [0] items dealt, [1] items of a key head
+  struct Record* items;   // [most_items]
+  long long most_items;
+  float* part;            // [most parts][slot_rows * (D + 4)]
+  uint32_t* arrived;      // [most parts][16], zero between calls
+  int32_t slot_rows;      // rows of a part: of one tile or two
 };
 
-// Pairs of tiles before each sequence, and the deal's counter at zero.
-__global__ void __launch_bounds__(1024) prompt_plan_kernel(const __grid_constant__ PromptParams p) {
-  __shared__ long long sums[32];
-  grid_release();
-  grid_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int run = (p.batch.seqs + 1023) / 1024, first = min(tid * run, p.batch.seqs), last = min(first + run, p.batch.seqs);
-  const int each = 2 * p.tokens;
-  long long mine = 0;
-  for (int b = first; b < last; ++b) mine += (sequence(p.batch, b).n + each - 1) / each;
-  long long upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) sums[warp] = upto;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) upto += sums[w];
-  long long at = upto - mine;
-  for (int b = first; b < last; ++b) {
-    p.before[b] = at;
-    at += (sequence(p.batch, b).n + each - 1) / each;
-  }
-  if (tid == 1023) p.before[p.batch.seqs] = upto, *p.next = 0;
-}
-
-template <int D, bool E8>
-struct Prompt {
-  static constexpr int kThreads = E8 ? 512 : 384;
-  static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kRawBytes = kTile * D;
-  static constexpr int kCuts = D / 64;               // 128-byte columns of a 16-bit tile
-  static constexpr int kStages = E8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
-  static constexpr int kRaws = E8 ? (D == 128 ? 3 : 4) : 0;
-  static constexpr int kOffRing = 2 * kTileBytes;    // after the two tiles of queries
-  static constexpr int kOffRaw = kOffRing + kStages * kTileBytes;
-  static constexpr int kOffScale = kOffRaw + kRaws * kRawBytes;
-  static constexpr int kOffRow = kOffScale + (E8 ? kScaleSlots * 2 * kTile * 4 : 0);   // the rows' factors, two items
-  static constexpr int kOffItem = kOffRow + (E8 ? 2 * 2 * kTile * 4 : 0);
-  static constexpr int kOffBar = kOffItem + 2 * 32;
-  static constexpr int kBars = 2 * kStages + 2 * kRaws + 24;
-  static constexpr int kOffMisc = kOffBar + kBars * 8;
-  static constexpr int kSmem = 1024 + kOffMisc + 16;
-  static_assert(kSmem <= 232448, "shared memory");
-  static constexpr uint32_t kS = 0, kO = 256;        // TMEM columns of the first tile's scores and output
+// An item: a pair of tiles, or some of its steps.
+struct Record {
+  int32_t b, row, n, base, token;   // token: the pair's first
+  int32_t from, to;                 // steps
+  int32_t slot, parts;              // the pair's first part, its parts (1: the item is the whole pair)
+  int32_t part, pad[2];
 };
-
-// An item, as the warps get it.
+// As the warps get it.
 struct Item {
-  int r, h, b, row, n, base, end, token;   // token: the pair's first
+  int r, h, b, row, n, base, token, from, to, slot, parts, part;
 };
 // The steps of a pair: blocks of 128 keys that one of its rows sees.
 struct Steps {
   int lo[2], sinks_end[2], end[2];   // of each tile's first row; tokens before `end` are seen by its last
   int early, late, n;
-  __device__ __forceinline__ void of(const Item& it, int tokens, int window, int sinks) {
+  template <typename T>
+  __device__ __forceinline__ void of(const T& it, int tokens, int window, int sinks) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int first = it.token + t * tokens, last = min(first + tokens, it.n) - 1;
@@ -143,6 +114,136 @@ struct Steps {
   }
 };
 
+
+// ---- the plan: one block lists the items of a key head.
+//
+// A pair of more steps than an even share among twice the SMs is cut into
+// parts, which are joined by the last warp of a row's to end: without that a
+// few long pairs (chunks of prompts on long prefixes, drafted tokens) left most
+// of the GPU idle.
+constexpr int kLeastSteps = 4;
+constexpr int kSharesPerSm = 2;
+// Parts of pairs that are cut, at most: sum of ceil(n / L) over pairs of n > L
+// steps, with L at least the sum of n over kSharesPerSm * SMs.
+static_assert(kMostParts == 2 * kSharesPerSm * FO_GB300_SMS, "parts");
+
+// Of 1024 threads: the sum of those up to this one, and of all.
+__device__ __forceinline__ long long block_scan(long long mine, long long* sums, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto scan = [&](long long v) {
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    return v;
+  };
+  mine = scan(mine);
+  __syncthreads();
+  if (lane == 31) sums[warp] = mine;
+  __syncthreads();
+  const long long warps = scan(sums[lane]);
+  *total = __shfl_sync(0xffffffffu, warps, 31);
+  const long long before = __shfl_sync(0xffffffffu, warps, (warp + 31) & 31);
+  return mine + (warp ? before : 0);
+}
+
+__global__ void __launch_bounds__(1024) prompt_plan_kernel(const __grid_constant__ PromptParams p) {
+  __shared__ long long sums[32];
+  grid_release();
+  grid_wait();
+  const int tid = threadIdx.x, each = 2 * p.tokens;
+  long long pairs, steps, items, parts;
+  {
+    const int run = (p.batch.seqs + 1023) / 1024, first = min(tid * run, p.batch.seqs), last = min(first + run, p.batch.seqs);
+    long long mine = 0;
+    for (int b = first; b < last; ++b) mine += (sequence(p.batch, b).n + each - 1) / each;
+    long long at = block_scan(mine, sums, &pairs) - mine;
+    for (int b = first; b < last; ++b) {
+      p.before[b] = at;
+      at += (sequence(p.batch, b).n + each - 1) / each;
+    }
+    if (tid == 0) p.before[p.batch.seqs] = pairs;
+    __syncthreads();
+  }
+  // A thread's run of pairs, from the last on; a visit to each.
+  const long long run = (pairs + 1023) / 1024, first = min(tid * run, pairs), last = min(first + run, pairs);   // (of pairs)
+  auto visit = [&](auto&& f) {
+    if (first >= last) return;
+    int lo = 0, hi = p.batch.seqs;   // before[lo] <= pair < before[hi]
+    const long long start = pairs - 1 - first;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.before[mid] <= start) lo = mid;
+      else hi = mid;
+    }
+    Seq s = sequence(p.batch, lo);
+    Record it;
+    Steps st;
+    for (long long e = first; e < last; ++e) {
+      const long long pair = pairs - 1 - e;
+      while (pair < p.before[lo]) s = sequence(p.batch, --lo);
+      it.b = lo, it.row = s.row, it.n = s.n, it.base = s.base;
+      it.token = (int)(pair - p.before[lo]) * each;
+      st.of(it, p.tokens, p.window, p.sinks);
+      f(it, st.n);
+    }
+  };
+  long long mine = 0;
+  visit([&](Record&, int n) { mine += max(n, 1); });
+  block_scan(mine, sums, &steps);
+  const long long shares = (long long)kSharesPerSm * p.sms;
+  const int most = (int)min((long long)INT32_MAX, max((steps * p.R * p.heads_k + shares - 1) / shares, (long long)kLeastSteps));
+  long long my_items = 0, my_parts = 0;
+  visit([&](Record&, int n) {
+    const int k = n > most ? (n + most - 1) / most : 1;
+    my_items += k;
+    my_parts += k > 1 ? k : 0;
+  });
+  long long at = block_scan(my_items, sums, &items) - my_items, slot = block_scan(my_parts, sums, &parts) - my_parts;
+  visit([&](Record& it, int n) {
+    const int k = n > most ? (n + most - 1) / most : 1;
+    it.parts = k;
+    it.slot = (int)slot;
+    for (int i = 0; i < k; ++i) {
+      it.part = i;
+      it.from = (int)((long long)n * i / k), it.to = (int)((long long)n * (i + 1) / k);
+      if (at < p.most_items) p.items[at] = it;
+      ++at;
+    }
+    slot += k > 1 ? k : 0;
+  });
+  if (tid == 0) {
+    // More rows than the call's: only starts that fall can say so.
+    if (items > p.most_items) report(p.batch, 0, kBadStarts, p.batch.rows);
+    p.next[0] = 0;
+    p.next[1] = items > p.most_items ? 0u : (uint32_t)items;
+    p.next[2] = (uint32_t)parts;
+  }
+}
+
+template <int D, bool E8>
+struct Prompt {
+  static constexpr int kThreads = E8 ? 672 : 640;
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kRawBytes = kTile * D;
+  static constexpr int kCuts = D / 64;               // 128-byte columns of a 16-bit tile
+  static constexpr int kStages = E8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
+  static constexpr int kRaws = E8 ? (D == 128 ? 3 : 4) : 0;
+  static constexpr int kOffRing = 2 * kTileBytes;    // after the two tiles of queries
+  static constexpr int kOffRaw = kOffRing + kStages * kTileBytes;
+  static constexpr int kOffScale = kOffRaw + kRaws * kRawBytes;
+  static constexpr int kOffRow = kOffScale + (E8 ? kScaleSlots * 2 * kTile * 4 : 0);   // the rows' factors, two items
+  static constexpr int kOffItem = kOffRow + (E8 ? 2 * 2 * kTile * 4 : 0);
+  static constexpr int kOffBox = kOffItem + 2 * 48;   // the softmax warps' mailboxes: 16 warps, two parities, 32 lanes
+  static constexpr int kOffBar = kOffBox + 16 * 2 * 32 * 8;
+  static constexpr int kBars = 3 * kStages + 2 * kRaws + 24;
+  static constexpr int kOffMisc = kOffBar + kBars * 8;
+  static constexpr int kSmem = 1024 + kOffMisc + 16;
+  static_assert(kSmem <= 232448, "shared memory");
+  static constexpr uint32_t kS = 0, kO = 256;        // TMEM columns of the first tile's scores and output
+};
+
 // kind::f16 instruction descriptor: fp32 sums, bf16 (or f16) operands, B
 // K-major (scores) or MN-major (weighted sum), 128 x n.
 __host__ __device__ constexpr uint32_t idesc(bool f16, bool b_mn, int n) {
@@ -161,21 +262,17 @@ __device__ __forceinline__ uint32_t elected() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
   return is;
 }
-template <int N>
-__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-// Sixteen columns of a thread's row.
-__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
 __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   f32x2 d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Products of two 16-bit numbers each.
+template <bool F16>
+__device__ __forceinline__ uint32_t mul_16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (F16) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 // The lowest n bits (none for n <= 0, all for n >= 32).
@@ -192,32 +289,31 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
   enum : int {
     kFull = 0, kEmpty = C::kStages, kRawFull = 2 * C::kStages, kRawEmpty = kRawFull + C::kRaws,
     kQFull = kRawEmpty + C::kRaws, kQReady, kQEmpty, kSFull, kPFull = kSFull + 2, kOFull = kPFull + 2, kOFree = kOFull + 2,
-    kDirty = kOFree + 2, kClean, kItemFull, kItemFree = kItemFull + 2, kDrain = kItemFree + 2, kLast
+    kReady = kOFree + 2, kItemFull = kReady + C::kStages, kItemFree = kItemFull + 2, kDrain = kItemFree + 2, kLast = kDrain + 2
   };
   static_assert(kLast <= C::kBars, "barriers");
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc);
   volatile uint32_t* const tmem_at = reinterpret_cast<volatile uint32_t*>(gbase + C::kOffMisc + 4);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) mbar_init(bar(kFull + i), E8 ? 4 : 1), mbar_init(bar(kEmpty + i), 1);
-    for (int i = 0; i < C::kRaws; ++i) mbar_init(bar(kRawFull + i), 1), mbar_init(bar(kRawEmpty + i), 4);
+    for (int i = 0; i < C::kStages; ++i) mbar_init(bar(kFull + i), E8 ? 2 : 1), mbar_init(bar(kEmpty + i), 2), mbar_init(bar(kReady + i), 1);
+    for (int i = 0; i < C::kRaws; ++i) mbar_init(bar(kRawFull + i), 1), mbar_init(bar(kRawEmpty + i), 2);
     mbar_init(bar(kQFull), 1);
-    mbar_init(bar(kQReady), 4);
-    mbar_init(bar(kQEmpty), 1);
+    mbar_init(bar(kQReady), 2);
+    mbar_init(bar(kQEmpty), 2);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(kSFull + t), 1);
-      mbar_init(bar(kPFull + t), 4);
+      mbar_init(bar(kPFull + t), 8);
       mbar_init(bar(kOFull + t), 1);
-      mbar_init(bar(kOFree + t), 4);
+      mbar_init(bar(kOFree + t), 8);
       mbar_init(bar(kItemFull + t), 1);
-      mbar_init(bar(kItemFree + t), E8 ? 15 : 11);   // issuer, cleaners, softmax and converting warps
+      mbar_init(bar(kDrain + t), 1);
+      mbar_init(bar(kItemFree + t), C::kThreads / 32 - 1);   // all warps but the first
     }
-    mbar_init(bar(kDirty), 1);
-    mbar_init(bar(kClean), 2);
-    mbar_init(bar(kDrain), 1);
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
+  for (int i = threadIdx.x; i < 16 * 2 * 32; i += C::kThreads) reinterpret_cast<volatile unsigned long long*>(gbase + C::kOffBox)[i] = 0ull;
   if (warp == 1) {
     __syncwarp();
     tmem_alloc<1>(base + C::kOffMisc + 4, 512);
@@ -235,24 +331,21 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
   auto take = [&](int n, Item& it) -> bool {   // false: no more
     const int sl = n & 1;
     if (!mbar_wait(bar(kItemFull + sl), (uint32_t)(n >> 1) & 1u, abort_flag, kWaitNs)) return false;
-    volatile int* const s = slots + sl * 8;
-    it.r = s[0], it.h = s[1], it.b = s[2], it.row = s[3], it.n = s[4], it.base = s[5], it.end = s[6], it.token = s[7];
+    volatile int* const s = slots + sl * 12;
+    it.r = s[0], it.h = s[1], it.b = s[2], it.row = s[3], it.n = s[4], it.base = s[5], it.token = s[6];
+    it.from = s[7], it.to = s[8], it.slot = s[9], it.parts = s[10], it.part = s[11];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kItemFree + sl));
     return it.r >= 0;
   };
   Item it;
   Steps st;
-  if (warp < 4) {
-    if constexpr (E8) fewer_registers<72>();
-    else fewer_registers<104>();
-  }
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
-    const long long pairs = p.before[p.batch.seqs];
+    const long long items = p.next[1], parts = p.next[2];
     const int units = p.R * p.heads_k;
-    const long long total = pairs * units;
+    const long long total = items * units;
     uint32_t n_load = 0;   // tiles of keys and values loaded so far
     bool ok = true;
     int n = 0;
@@ -264,27 +357,24 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       unsigned L32 = 0;
       if (lane == 0) L32 = atomicAdd(p.next, 1u);
       const long long L = __shfl_sync(0xffffffffu, L32, 0);
-      it.r = -1, it.h = it.b = it.row = it.n = it.base = it.end = it.token = 0;
+      it.r = -1;
       if (L < total) {
-        const long long set = L / (pairs * kHeadsTogether), rem = L - set * pairs * kHeadsTogether;
+        const long long set = L / (items * kHeadsTogether), rem = L - set * items * kHeadsTogether;
         const int width = min(kHeadsTogether, units - (int)set * kHeadsTogether);
-        const long long pr = rem / width;
-        const int u = (int)set * kHeadsTogether + (int)(rem - pr * width);
-        const long long pair = pairs - 1 - pr;
-        int lo = 0, hi = p.batch.seqs;   // before[lo] <= pair < before[hi]
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (p.before[mid] <= pair) lo = mid;
-          else hi = mid;
-        }
-        const Seq s = sequence(p.batch, lo);
-        it.r = u / p.heads_k, it.h = u - it.r * p.heads_k, it.b = lo;
-        it.row = s.row, it.n = s.n, it.base = s.base, it.end = s.end;
-        it.token = (int)(pair - p.before[lo]) * 2 * p.tokens;
+        const int at = (int)(rem / width), u = (int)set * kHeadsTogether + (int)(rem - (long long)at * width);
+        const Record rec = p.items[at];
+        it.r = u / p.heads_k, it.h = u - it.r * p.heads_k, it.b = rec.b;
+        it.row = rec.row, it.n = rec.n, it.base = rec.base, it.token = rec.token;
+        it.from = rec.from, it.to = rec.to, it.parts = rec.parts, it.part = rec.part;
+        it.slot = (int)(u * parts) + rec.slot;
       }
       if (lane == 0) {
-        volatile int* const s = slots + sl * 8;
-        s[0] = it.r, s[1] = it.h, s[2] = it.b, s[3] = it.row, s[4] = it.n, s[5] = it.base, s[6] = it.end, s[7] = it.token;
+        volatile int* const s = slots + sl * 12;
+        s[0] = it.r;
+        if (it.r >= 0) {
+          s[1] = it.h, s[2] = it.b, s[3] = it.row, s[4] = it.n, s[5] = it.base, s[6] = it.token;
+          s[7] = it.from, s[8] = it.to, s[9] = it.slot, s[10] = it.parts, s[11] = it.part;
+        }
         mbar_arrive(bar(kItemFull + sl));
       }
       __syncwarp();
@@ -301,22 +391,22 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
                         it.row + it.token + t * p.tokens);
       }
       const int boxes = kTile / p.box;
-      for (int i = 0; i < st.n && ok; ++i) {
-        const int key = st.block(i) * kTile;
-        // A lane for each box of tokens: its page.
-        int id = -1;
-        const int mine = key + lane * p.box;
-        if (lane < boxes) {
-          const int far = max(st.end[0], st.end[1]);
-          if (mine < far && (mine < max(st.sinks_end[0], st.sinks_end[1]) || mine + p.box > st.lo[0])) {
-            id = p.batch.table[(long long)it.b * p.batch.cols + (mine >> p.batch.shift)];
-            if (id < 0 || id >= p.batch.pages) {
-              report(p.batch, it.b, kBadPage, id);
-              id = -1;
-            }
-          }
-        }
-        const int z = id >= 0 ? id * p.heads_k + it.h : p.batch.pages * p.heads_k, y = mine & ((1 << p.batch.shift) - 1);
+      // The page of this lane's box of tokens in a step's keys; -1: not needed.
+      const int far = max(st.end[0], st.end[1]), sinks_end = max(st.sinks_end[0], st.sinks_end[1]);
+      auto page_of = [&](int i) -> int {
+        const int key = st.block(i) * kTile + lane * p.box;
+        if (lane >= boxes || key >= far || (key >= sinks_end && key + p.box <= st.lo[0])) return -1;
+        const int id = p.batch.table[(long long)it.b * p.batch.cols + (key >> p.batch.shift)];
+        if (id >= 0 && id < p.batch.pages) return id;
+        report(p.batch, it.b, kBadPage, id);
+        return -1;
+      };
+      int next_id = it.from < it.to ? page_of(it.from) : -1;
+      for (int i = it.from; i < it.to && ok; ++i) {
+        const int id = next_id;
+        if (i + 1 < it.to) next_id = page_of(i + 1);
+        const int z = id >= 0 ? id * p.heads_k + it.h : p.batch.pages * p.heads_k;
+        const int y = (st.block(i) * kTile + lane * p.box) & ((1 << p.batch.shift) - 1);
 #pragma unroll
         for (int value = 0; value < 2; ++value) {
           if (n_load >= kRing && !mbar_wait(bar(kBack + at_slot), (at_round - 1) & 1, abort_flag, kWaitNs)) {
@@ -355,330 +445,131 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       }
       if (n > 0) mbar_wait(bar(kQFull), (n - 1) & 1, &never, 100000000ull);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ products
-    uint32_t n_tile = 0;       // number of the item's first tile of keys, of all items
-    uint32_t soft[2] = {0, 0}; // steps of each tile so far
-    uint32_t cleaned = 0, outs[2] = {0, 0};
+  } else if (warp < 3) {
+    // ------------------------------------------------------------ products, a warp for each tile
+    const int t = warp - 1;
+    uint32_t n_tile = 0;                         // number of the item's first tile of keys, of all items
+    uint32_t soft = 0, outs = 0;                 // steps and outputs so far
     const uint32_t one = elected();
     bool ok = true;
-    auto stage_of = [&](uint32_t i) { return i % (uint32_t)C::kStages; };
-    auto full = [&](uint32_t i) { return mbar_wait(bar(kFull + stage_of(i)), (i / (uint32_t)C::kStages) & 1u, abort_flag, kWaitNs); };
+    auto full = [&](int which, uint32_t i) {
+      return mbar_wait(bar(which + i % (uint32_t)C::kStages), (i / (uint32_t)C::kStages) & 1u, abort_flag, kWaitNs);
+    };
+    const uint64_t q_desc = smem_desc_sw128(base + t * C::kTileBytes, 16, 1024);
+    const uint64_t k_desc = smem_desc_sw128(base + C::kOffRing, 16, 1024), v_desc = smem_desc_sw128(base + C::kOffRing, 8192, 1024);
+    const uint32_t s_col = tmem + C::kS + t * 128, o_col = tmem + C::kO + t * D;
     for (int n = 0; ok; ++n) {
       if (!take(n, it)) break;
       st.of(it, p.tokens, p.window, p.sinks);
-      if (!mbar_wait(bar(E8 ? kQReady : kQFull), (uint32_t)n & 1u, abort_flag, kWaitNs)) break;
+      const int steps = it.to - it.from;
+      if (!(ok = mbar_wait(bar(E8 ? kQReady : kQFull), (uint32_t)n & 1u, abort_flag, kWaitNs))) break;
       tc_fence_after();
-      int from[2], last[2], scoring = 0;   // each tile's first and last step
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        from[t] = 0, last[t] = st.n - 1;
-        while (from[t] < st.n && !st.active(t, from[t])) ++from[t];
-        while (last[t] >= 0 && !st.active(t, last[t])) --last[t];
-        scoring += last[t] >= 0;
+      // Of 32 steps at a time, a lane for each: which this tile takes part in.
+      uint32_t mine = 0;
+      auto look = [&](int i) {
+        const int at = it.from + i + lane;
+        mine = __ballot_sync(0xffffffffu, at < it.to && st.active(t, at));
+      };
+      int last = -1;   // this tile's last step
+      for (int i = 0; i < steps; i += 32) {
+        look(i);
+        if (mine) last = i + 31 - __clz(mine);
       }
-      if (scoring == 0 && one) tc_commit<1>(bar(kQEmpty));
-      // The scores of tile t's step i; with the last of them the queries are
-      // free, with the second tile's the keys.
-      auto scores = [&](int t, int i) -> bool {
+      if (last < 0 && one) mbar_arrive(bar(kQEmpty));
+      // The scores of step i.
+      auto scores = [&](int i) -> bool {
         const uint32_t k = n_tile + 2u * (uint32_t)i;
-        if (!full(k)) return false;
+        if (!full(kFull, k)) return false;
         tc_fence_after();
-        if (i == last[t]) --scoring;
         if (one) {
-          const uint32_t a = base + t * C::kTileBytes, b = base + C::kOffRing + stage_of(k) * C::kTileBytes;
+          const uint64_t b = k_desc + (uint64_t)((k % (uint32_t)C::kStages) * (C::kTileBytes >> 4));
 #pragma unroll
           for (int e = 0; e < D / 16; ++e) {
-            const uint32_t off = (uint32_t)(e >> 2) * (kTile * 128) + (uint32_t)(e & 3) * 32u;
-            tc_mma<1, false>(tmem + C::kS + t * 128, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024),
-                             idesc(E8, false, kTile), e > 0 ? 1u : 0u);
+            const uint64_t off = (uint64_t)(((e >> 2) * (kTile * 128) + (e & 3) * 32) >> 4);
+            tc_mma<1, false>(s_col, q_desc + off, b + off, idesc(E8, false, kTile), e > 0 ? 1u : 0u);
           }
           tc_commit<1>(bar(kSFull + t));
-          if (t == 1 || !st.active(1, i)) tc_commit<1>(bar(kEmpty + stage_of(k)));
-          if (i == last[t] && scoring == 0) tc_commit<1>(bar(kQEmpty));
+          tc_commit<1>(bar(kEmpty + k % (uint32_t)C::kStages));
+          if (i == last) tc_commit<1>(bar(kQEmpty));
         }
         __syncwarp();
         return true;
       };
-      // Both tiles' first scores, unless one begins later: then in its turn.
-      bool begun[2] = {from[0] < st.n && from[0] <= from[1], from[1] < st.n && from[1] <= from[0]}, first[2] = {true, true};
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (ok && begun[t]) ok = scores(t, from[t]);
-      for (int i = 0; i < st.n && ok; ++i) {
-        const uint32_t v = n_tile + 2u * (uint32_t)i + 1u;
-        const bool dirty = !E8 && st.dirty(i);
-        if (dirty) {
-          if (!(ok = full(v))) break;
-          if (one) mbar_arrive(bar(kDirty));
-          __syncwarp();
+      bool begun = false, first = true;   // this step's scores are under way; no output yet
+      for (int i = 0; i < steps; ++i) {
+        if ((i & 31) == 0) look(i);
+        const uint32_t bit = 1u << (i & 31), v = n_tile + 2u * (uint32_t)i + 1u;
+        if (!(mine & bit)) {   // the stages are the other tile's alone (but each is released in its turn)
+          for (uint32_t x = v - 1u; ok && x <= v; ++x) {
+            ok = full(kFull, x);
+            if (ok && one) mbar_arrive(bar(kEmpty + x % (uint32_t)C::kStages));
+            __syncwarp();
+          }
+          if (!ok) break;
+          continue;
         }
-        bool waited = false;
+        if (!begun && !(ok = scores(i))) break;
+        if (!(ok = full(E8 ? kFull : kReady, v) && (!first || mbar_wait(bar(kOFree + t), (outs & 1u) ^ 1u, abort_flag, kWaitNs)) &&
+                   mbar_wait(bar(kPFull + t), soft & 1u, abort_flag, kWaitNs)))
+          break;
+        ++soft;
+        tc_fence_after();
+        if (one) {
+          const uint64_t b = v_desc + (uint64_t)((v % (uint32_t)C::kStages) * (C::kTileBytes >> 4));
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || !st.active(t, i)) continue;
-          if (!begun[t]) {
-            begun[t] = true;
-            if (!(ok = scores(t, i))) continue;
-          }
-          ok = mbar_wait(bar(kPFull + t), soft[t] & 1u, abort_flag, kWaitNs) &&
-               (!first[t] || mbar_wait(bar(kOFree + t), (outs[t] & 1u) ^ 1u, abort_flag, kWaitNs));
-          if (ok && !waited) {
-            waited = true;
-            ok = full(v) && (!dirty || mbar_wait(bar(kClean), cleaned & 1u, abort_flag, kWaitNs));
-          }
-          if (!ok) continue;
-          ++soft[t];
-          tc_fence_after();
-          if (one) {
-            const uint32_t b = base + C::kOffRing + stage_of(v) * C::kTileBytes;
-#pragma unroll
-            for (int e = 0; e < kTile / 16; ++e)
-              mma_ts(tmem + C::kO + t * D, tmem + C::kS + t * 128 + e * 8,
-                     smem_desc_sw128(b + (uint32_t)(e >> 2) * (C::kTileBytes / 2) + (uint32_t)(e & 3) * 2048u, 8192, 1024),
-                     idesc(E8, true, D), !first[t] || e > 0 ? 1u : 0u);
-            if (t == 1 || !st.active(1, i)) tc_commit<1>(bar(kEmpty + stage_of(v)));
-            if (i == last[t]) tc_commit<1>(bar(kOFull + t));
-          }
-          __syncwarp();
-          first[t] = false;
-          if (i == last[t]) {
-            ++outs[t];
-          } else if (st.active(t, i + 1)) {
-            ok = scores(t, i + 1);
-          } else {
-            begun[t] = false;   // (between first tokens and window)
-          }
+          for (int e = 0; e < kTile / 16; ++e)
+            // (The weights of keys 0-63 lie in columns 0-31, of the others in 64-95.)
+            mma_ts(o_col, s_col + (e >> 2) * 64 + (e & 3) * 8, b + (uint64_t)(((e >> 2) * (C::kTileBytes / 2) + (e & 3) * 2048) >> 4),
+                   idesc(E8, true, D), e > 0 || !first ? 1u : 0u);
+          tc_commit<1>(bar(kEmpty + v % (uint32_t)C::kStages));
+          if (i == last) tc_commit<1>(bar(kOFull + t));
         }
-        if (dirty) ++cleaned;
+        __syncwarp();
+        first = false;
+        // The next scores, unless the tile passes over steps (between first
+        // tokens and window) or these are the next 32's: then in their turn.
+        begun = bit << 1 & mine;
+        if (begun && !(ok = scores(i + 1))) break;
       }
-      n_tile += 2u * (uint32_t)st.n;
+      outs += last >= 0;
+      n_tile += 2u * (uint32_t)steps;
     }
     // Every product has ended before TMEM is given back.
     volatile int never = 0;
-    if (one) tc_commit<1>(bar(kDrain));
+    if (one) tc_commit<1>(bar(kDrain + t));
     __syncwarp();
-    mbar_wait(bar(kDrain), 0, &never, 100000000ull);
-  } else if (warp < 4) {
-    // ------------------------------------------------------------ values that nobody sees
-    uint32_t n_tile = 0, asked = 0;
-    bool ok = true;
-    for (int n = 0; ok; ++n) {
-      if (!take(n, it)) break;
-      if constexpr (!E8) {
+    mbar_wait(bar(kDrain + t), 0, &never, 100000000ull);
+  } else if (warp == 3 || (E8 && warp == 20)) {
+    if constexpr (!E8) {
+      // ---------------------------------------------------------- values that nobody sees
+      uint32_t n_tile = 0;
+      for (int n = 0, ok = 1; ok; ++n) {
+        if (!take(n, it)) break;
         st.of(it, p.tokens, p.window, p.sinks);
-        for (int i = 0; i < st.n; ++i) {
-          if (!st.dirty(i)) continue;
-          const uint32_t v = n_tile + 2u * (uint32_t)i + 1u, stage = v % (uint32_t)C::kStages;
-          // The issuer calls for each of them: only then is the stage's phase known.
-          if (!mbar_wait(bar(kDirty), asked++ & 1u, abort_flag, kWaitNs) ||
-              !mbar_wait(bar(kFull + stage), (v / (uint32_t)C::kStages) & 1u, abort_flag, kWaitNs)) {
-            ok = false;
-            break;
-          }
-          const int key = st.block(i) * kTile;
-          uint8_t* const at = gbase + C::kOffRing + stage * C::kTileBytes;
-          // Eight lanes a row of 128 bytes.
-          for (int row = (warp - 2) * 4 + (lane >> 3); row < kTile; row += 8) {
-            if (st.any(key + row)) continue;
+        for (int i = it.from; i < it.to; ++i) {
+          const uint32_t v = n_tile + 2u * (uint32_t)(i - it.from) + 1u, stage = v % (uint32_t)C::kStages;
+          if (!(ok = mbar_wait(bar(kFull + stage), (v / (uint32_t)C::kStages) & 1u, abort_flag, kWaitNs))) break;
+          if (st.dirty(i)) {
+            const int key = st.block(i) * kTile;
+            uint8_t* const at = gbase + C::kOffRing + stage * C::kTileBytes;
+            // Eight lanes a row of 128 bytes.
+            for (int row = lane >> 3; row < kTile; row += 4) {
+              if (st.any(key + row)) continue;
 #pragma unroll
-            for (int cut = 0; cut < C::kCuts; ++cut)
-              *reinterpret_cast<uint4*>(at + (row >> 6) * (C::kTileBytes / 2) + cut * 8192 + (row & 63) * 128 + (lane & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kClean));
-        }
-        n_tile += 2u * (uint32_t)st.n;
-      }
-    }
-  } else if (warp < 12) {
-    // ------------------------------------------------------------ softmax
-    if constexpr (E8) more_registers<184>();
-    else more_registers<200>();
-    const int t = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + C::kS + t * 128, o_at = tmem + lanes + C::kO + t * D;
-    uint32_t step = 0, outs = 0;   // this tile's steps and outputs so far
-    uint32_t n_step = 0;           // steps of the items before
-    bool ok = true;
-    for (int n = 0; ok; ++n) {
-      if (!take(n, it)) break;
-      st.of(it, p.tokens, p.window, p.sinks);
-      const int token = it.token + t * p.tokens + row / p.group;
-      const bool real = row < p.tokens * p.group && token < it.n;
-      const int pos = real ? it.base + token : -1, lo = sight_of(max(pos, 0), p.window, p.sinks).lo;
-      // Blocks all of whose keys all of the tile's rows see need no mask.
-      const int first_pos = it.base + it.token + t * p.tokens;
-      const int last_lo = sight_of(max(first_pos + p.tokens - 1, 0), p.window, p.sinks).lo;
-      float m = -INFINITY, l = 0.f, factor = p.scale_log2, sigma = 0.f, sigma_inv = 0.f;
-      bool any = false;
-      for (int i = 0; i < st.n && ok; ++i) {
-        if (!st.active(t, i)) continue;
-        const int key = st.block(i) * kTile;
-        if (!mbar_wait(bar(kSFull + t), step & 1u, abort_flag, kWaitNs)) {
-          ok = false;
-          break;
-        }
-        ++step;
-        tc_fence_after();
-        uint32_t v[4][32];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) tmem_ld32(s_at + 32 * e, v[e]);
-        const float* const ks = reinterpret_cast<const float*>(gbase + C::kOffScale) + ((n_step + i) % kScaleSlots) * 2 * kTile;
-        if constexpr (E8)
-          if (!any) factor = p.scale_log2 * reinterpret_cast<const float*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + row];
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 4; ++e) reg_fence(v[e]);
-        if constexpr (E8) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(ks + e * 32 + k);
-              float a, b;
-              halves(mul2(pair_of(v[e][k], v[e][k + 1]), pair_of(f.x, f.y)), a, b);
-              v[e][k] = __float_as_uint(a), v[e][k + 1] = __float_as_uint(b);
-              halves(mul2(pair_of(v[e][k + 2], v[e][k + 3]), pair_of(f.z, f.w)), a, b);
-              v[e][k + 2] = __float_as_uint(a), v[e][k + 3] = __float_as_uint(b);
+              for (int cut = 0; cut < C::kCuts; ++cut)
+                *reinterpret_cast<uint4*>(at + (row >> 6) * (C::kTileBytes / 2) + cut * 8192 + (row & 63) * 128 + (lane & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
             }
-        }
-        if (key + kTile - 1 > first_pos || !(key >= last_lo || key + kTile <= p.sinks)) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int at = key + 32 * e;
-            const uint32_t seen = low_bits(pos + 1 - at) & (~low_bits(lo - at) | low_bits(p.sinks - at));
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!(seen >> k & 1u)) v[e][k] = 0xff800000u;   // -infinity
+            fence_proxy_async_smem();
+            __syncwarp();
           }
+          if (lane == 0) mbar_arrive(bar(kReady + stage));
         }
-        float tops[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) tops[k] = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 64; ++k)
-          tops[k & 7] = max3(tops[k & 7], __uint_as_float(v[k >> 4][(2 * k) & 31]), __uint_as_float(v[k >> 4][(2 * k + 1) & 31]));
-        const float top = max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]), fmaxf(tops[6], tops[7])) * factor;
-        const bool grows = top > m + kLazy || (m == -INFINITY && top > m);
-        float by = 1.f;
-        if (grows) by = ex2_below(m, top), l *= by, m = top;
-        if constexpr (E8) {
-          // The values' scales over sigma, as for single tokens; sigma is one
-          // for all rows.
-          float mx = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int at = key + lane + 32 * k;
-            if (st.any(at)) mx = fmaxf(mx, ks[kTile + lane + 32 * k]);
-          }
-          const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(mx) & 0x7fffffffu);
-          if (__uint_as_float(bits) > sigma * 128.f || sigma == 0.f) {
-            const uint32_t exponent = min(max((bits + 0x7fffffu) >> 23, 9u), 253u);
-            const float to = __uint_as_float((exponent - 7u) << 23);
-            by *= sigma == 0.f ? 0.f : sigma / to;
-            sigma = to;
-            sigma_inv = 1.f / to;
-          }
-        }
-        if (any && __any_sync(0xffffffffu, by != 1.f)) {
-          // (These scores come after the sums before them in the issuer's
-          // order: those are done.)
-          const f32x2 by2 = pair_of(by, by);
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) {
-            uint32_t o[32];
-            tmem_ld32(o_at + 32 * e, o);
-            tmem_ld_wait();
-            reg_fence(o);
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float a, b;
-              halves(mul2(pair_of(o[k], o[k + 1]), by2), a, b);
-              o[k] = __float_as_uint(a), o[k + 1] = __float_as_uint(b);
-            }
-            tmem_st32(o_at + 32 * e, o);
-          }
-        }
-        any = true;
-        const float down = m == -INFINITY ? 0.f : -m;
-        const f32x2 factor2 = pair_of(factor, factor), down2 = pair_of(down, down);
-        f32x2 sums[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            float x[4];
-            halves(fma2(pair_of(v[e][k], v[e][k + 1]), factor2, down2), x[0], x[1]);
-            halves(fma2(pair_of(v[e][k + 2], v[e][k + 3]), factor2, down2), x[2], x[3]);
-#pragma unroll
-            for (int a = 0; a < 4; ++a) x[a] = ex2(x[a]);
-            sums[(k >> 1) & 2] = add2(sums[(k >> 1) & 2], pair_of(x[0], x[1]));
-            sums[((k >> 1) & 2) + 1] = add2(sums[((k >> 1) & 2) + 1], pair_of(x[2], x[3]));
-            if constexpr (E8) {
-              const float4 f = *reinterpret_cast<const float4*>(ks + kTile + 32 * e + k);
-              w[k / 2] = f16x2(x[0] * f.x * sigma_inv, x[1] * f.y * sigma_inv);
-              w[k / 2 + 1] = f16x2(x[2] * f.z * sigma_inv, x[3] * f.w * sigma_inv);
-            } else {
-              w[k / 2] = bf16x2(x[0], x[1]), w[k / 2 + 1] = bf16x2(x[2], x[3]);
-            }
-          }
-          tmem_st16(s_at + 16 * e, w);
-        }
-        float s0, s1, s2, s3;
-        halves(add2(sums[0], sums[1]), s0, s1);
-        halves(add2(sums[2], sums[3]), s2, s3);
-        l += (s0 + s1) + (s2 + s3);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kPFull + t));
+        n_tile += 2u * (uint32_t)(it.to - it.from);
       }
-      if (!ok) break;
-      n_step += st.n;
-      // ---- the rows' results
-      if (any) {
-        if (!mbar_wait(bar(kOFull + t), outs & 1u, abort_flag, kWaitNs)) break;
-        ++outs;
-        tc_fence_after();
-      }
-      uint32_t w[D / 2];
-      const bool none = m == -INFINITY && l == 0.f;   // (O holds nothing then, or zeros)
-      const float by = E8 ? sigma / l : 1.f / l;
-#pragma unroll
-      for (int e = 0; e < D / 2; ++e) w[e] = 0u;
-      if (any) {
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-          uint32_t o[32];
-          tmem_ld32(o_at + 32 * e, o);
-          tmem_ld_wait();
-          reg_fence(o);
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            w[16 * e + k] = none ? 0u : bf16x2(__uint_as_float(o[2 * k]) * by, __uint_as_float(o[2 * k + 1]) * by);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kOFree + t));
-      }
-      if (real) {
-        const int64_t out = it.row + token;
-        const int head = it.h * p.group + row % p.group;
-        uint4* const to = reinterpret_cast<uint4*>(p.o[it.r] + out * p.ld_o + head * D);
-#pragma unroll
-        for (int e = 0; e < D / 8; ++e) to[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-        if (p.lse[it.r]) p.lse[it.r][out * p.heads_q + head] = lse_of(m, l);
-      }
-    }
-  } else {
-    // ------------------------------------------------------------ 8 bits to f16
-    if constexpr (E8) {
-      fewer_registers<72>();
-      const int tid = threadIdx.x - 384;   // a thread for a row (of queries) or key
+    } else {
+      // ---------------------------------------------------------- 8 bits to f16
+      const int tid = (warp == 3 ? 0 : 32) + lane;   // a thread for two rows (of queries) or keys
       uint32_t n_tile = 0, n_step = 0;
       bool ok = true;
       for (int n = 0; ok; ++n) {
@@ -688,21 +579,22 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         // The queries, each row times a power of two that brings its largest
         // magnitude to [128, 256); in place.
 #pragma unroll 1
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t at = base + t * C::kTileBytes + tid * 128;
+        for (int rows = 0; rows < 4; ++rows) {
+          const int t = rows >> 1, row = tid + (rows & 1) * 64;
+          const uint32_t at = base + t * C::kTileBytes + row * 128;
           float top = 0.f;
 #pragma unroll 4
           for (int k = 0; k < D / 8; ++k) {
             float f[8];
-            Vec16<__nv_bfloat16>::unpack(lds128(at + (k >> 3) * (kTile * 128) + (((k & 7) ^ (tid & 7)) << 4)), f);
+            Vec16<__nv_bfloat16>::unpack(lds128(at + (k >> 3) * (kTile * 128) + (((k & 7) ^ (row & 7)) << 4)), f);
             top = max_nan(top, amax_of(f));
           }
           const uint32_t exponent = min(max(__float_as_uint(top) >> 23, 8u), 254u);
           const float by = top <= 3.4e38f ? __uint_as_float((261u - exponent) << 23) : 1.f;
-          reinterpret_cast<float*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + tid] = 1.f / by;
+          reinterpret_cast<float*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + row] = 1.f / by;
 #pragma unroll 4
           for (int k = 0; k < D / 8; ++k) {
-            const uint32_t a = at + (k >> 3) * (kTile * 128) + (((k & 7) ^ (tid & 7)) << 4);
+            const uint32_t a = at + (k >> 3) * (kTile * 128) + (((k & 7) ^ (row & 7)) << 4);
             float f[8];
             Vec16<__nv_bfloat16>::unpack(lds128(a), f);
             sts128(a, make_uint4(f16x2(f[0] * by, f[1] * by), f16x2(f[2] * by, f[3] * by), f16x2(f[4] * by, f[5] * by),
@@ -712,20 +604,21 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kQReady));
-        for (int i = 0; i < st.n && ok; ++i) {
-          const int key = st.block(i) * kTile + tid;
-          const bool seen = st.any(key);
-          float scale[2] = {0.f, 0.f};
-          if (seen) {
+        for (int i = it.from; i < it.to && ok; ++i) {
+          float scale[2][2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = st.block(i) * kTile + tid + 64 * e;
+            scale[e][0] = scale[e][1] = 0.f;
+            if (!st.any(key)) continue;
             const int id = p.batch.table[(long long)it.b * p.batch.cols + (key >> p.batch.shift)];
-            if (id >= 0 && id < p.batch.pages) {
-              const long long at = ((long long)(id * p.heads_k + it.h) << p.batch.shift) + (key & ((1 << p.batch.shift) - 1));
-              scale[0] = p.ks[it.r][at], scale[1] = p.vs[it.r][at];
-            }
+            if (id < 0 || id >= p.batch.pages) continue;
+            const long long at = ((long long)(id * p.heads_k + it.h) << p.batch.shift) + (key & ((1 << p.batch.shift) - 1));
+            scale[e][0] = p.ks[it.r][at], scale[e][1] = p.vs[it.r][at];
           }
 #pragma unroll 1
           for (int value = 0; value < 2; ++value) {
-            const uint32_t x = n_tile + 2u * (uint32_t)i + (uint32_t)value;
+            const uint32_t x = n_tile + 2u * (uint32_t)(i - it.from) + (uint32_t)value;
             const uint32_t rs = x % (uint32_t)C::kRaws, ss = x % (uint32_t)C::kStages;
             if (!mbar_wait(bar(kRawFull + rs), (x / (uint32_t)C::kRaws) & 1u, abort_flag, kWaitNs) ||
                 (x >= (uint32_t)C::kStages &&
@@ -734,15 +627,15 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
               break;
             }
             if (value == 0) {
-              float* const to = reinterpret_cast<float*>(gbase + C::kOffScale) + ((n_step + i) % kScaleSlots) * 2 * kTile + tid;
-              to[0] = scale[0], to[kTile] = scale[1];
+              float* const to = reinterpret_cast<float*>(gbase + C::kOffScale) + ((n_step + i - it.from) % kScaleSlots) * 2 * kTile + tid;
+              to[0] = scale[0][0], to[64] = scale[1][0], to[kTile] = scale[0][1], to[kTile + 64] = scale[1][1];
             }
             // Sixteen bytes a time: lanes side by side in a key's bytes, so
             // that reads and writes meet no bank twice.
             const uint32_t from = base + C::kOffRaw + rs * C::kRawBytes, to = base + C::kOffRing + ss * C::kTileBytes;
             constexpr int kPieces = D / 16;
 #pragma unroll 4
-            for (int k = tid; k < kTile * kPieces; k += kTile) {
+            for (int k = tid; k < kTile * kPieces; k += 64) {
               const int row = k / kPieces, piece = k % kPieces;
               const uint4 v = lds128(D == 128 ? from + row * 128 + ((piece ^ (row & 7)) << 4) : from + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
               uint4 a = make_uint4(f16x2_of_e4m3(v.x), f16x2_of_e4m3_high(v.x), f16x2_of_e4m3(v.y), f16x2_of_e4m3_high(v.y));
@@ -759,8 +652,305 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
             if (lane == 0) mbar_arrive(bar(kRawEmpty + rs)), mbar_arrive(bar(kFull + ss));
           }
         }
-        n_tile += 2u * (uint32_t)st.n;
-        n_step += (uint32_t)st.n;
+        n_tile += 2u * (uint32_t)(it.to - it.from);
+        n_step += (uint32_t)(it.to - it.from);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int sw = warp - 4, t = sw >> 3, half = (sw >> 2) & 1, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + C::kS + t * 128 + half * 64, o_at = tmem + lanes + C::kO + t * D + half * (D / 2);
+    constexpr int kHalf = D / 2;   // columns of O that a thread reads
+    // What a row's two threads tell each other: a number and which exchange
+    // it is of. Exchange x + 2 takes x's place only after the other's x + 1
+    // has been read, which was written after x had been.
+    volatile unsigned long long* const box = reinterpret_cast<volatile unsigned long long*>(gbase + C::kOffBox);
+    uint32_t x = 0;
+    auto post = [&](float mine) {
+      ++x;
+      box[(sw * 2 + (int)(x & 1u)) * 32 + lane] = ((unsigned long long)x << 32) | __float_as_uint(mine);
+    };
+    auto peek = [&]() -> unsigned long long { return box[((sw ^ 4) * 2 + (int)(x & 1u)) * 32 + lane]; };
+    auto fetch = [&](unsigned long long w, float& theirs) -> bool {   // w: what peek saw
+      if ((uint32_t)(w >> 32) != x) {
+        volatile unsigned long long* const at = box + (((sw ^ 4) * 2 + (int)(x & 1u)) * 32 + lane);
+        const uint64_t t0 = globaltimer();
+        uint32_t tries = 0;
+        while ((uint32_t)((w = *at) >> 32) != x) {
+          if ((++tries & 63u) == 0) {
+            if (*abort_flag) return false;
+            if (globaltimer() - t0 > kWaitNs) {
+              *abort_flag = 1;
+              return false;
+            }
+          }
+        }
+      }
+      theirs = __uint_as_float((uint32_t)w);
+      return true;
+    };
+    uint32_t step = 0, outs = 0;   // this tile's steps and outputs so far
+    uint32_t n_step = 0;           // steps of the items before
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      if (!take(n, it)) break;
+      st.of(it, p.tokens, p.window, p.sinks);
+      const int token = it.token + t * p.tokens + row / p.group;
+      const bool real = row < p.tokens * p.group && token < it.n;
+      const int pos = real ? it.base + token : -1, lo = sight_of(max(pos, 0), p.window, p.sinks).lo;
+      // Blocks all of whose keys all of the tile's rows see need no mask.
+      const int first_pos = it.base + it.token + t * p.tokens;
+      const int last_lo = sight_of(max(first_pos + p.tokens - 1, 0), p.window, p.sinks).lo;
+      float m = -INFINITY, l = 0.f, factor = p.scale_log2, sigma = 0.f, sigma_inv = 0.f;
+      bool any = false;
+      for (int i = it.from; i < it.to; ++i) {
+        if (!st.active(t, i)) continue;
+        const int key = st.block(i) * kTile;
+        if (!(ok = mbar_wait(bar(kSFull + t), step & 1u, abort_flag, kWaitNs))) break;
+        ++step;
+        tc_fence_after();
+        // The steps' scales: keys' and values'.
+        const float* const ks = reinterpret_cast<const float*>(gbase + C::kOffScale) + ((n_step + i - it.from) % kScaleSlots) * 2 * kTile;
+        if constexpr (E8)
+          if (!any) factor = p.scale_log2 * reinterpret_cast<const float*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + row];
+        const bool masked = key + kTile - 1 > first_pos || !(key >= last_lo || key + kTile <= p.sinks);
+        uint32_t v[2][32];   // the row's 64 scores
+        tmem_ld32(s_at, v[0]);
+        tmem_ld32(s_at + 32, v[1]);
+        tmem_ld_wait();
+        reg_fence(v[0]);
+        reg_fence(v[1]);
+        if constexpr (E8) {
+#pragma unroll
+          for (int k = 0; k < 64; k += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(ks + half * 64 + k);
+            uint32_t* const u = &v[k >> 5][k & 31];
+            float a, b;
+            halves(mul2(pair_of(u[0], u[1]), pair_of(f.x, f.y)), a, b);
+            u[0] = __float_as_uint(a), u[1] = __float_as_uint(b);
+            halves(mul2(pair_of(u[2], u[3]), pair_of(f.z, f.w)), a, b);
+            u[2] = __float_as_uint(a), u[3] = __float_as_uint(b);
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int at = key + half * 64 + 32 * e;
+            const uint32_t seen = low_bits(pos + 1 - at) & (~low_bits(lo - at) | low_bits(p.sinks - at));
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!(seen >> k & 1u)) v[e][k] = 0xff800000u;   // -infinity
+          }
+        }
+        float tops[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tops[k] = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          tops[k & 3] = max3(tops[k & 3], __uint_as_float(v[k >> 4][(2 * k) & 31]), __uint_as_float(v[k >> 4][(2 * k + 1) & 31]));
+        const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * factor;
+        post(top);
+        float by = 1.f;   // what O is rescaled with
+        if constexpr (E8) {
+          // The values' scales over sigma, as for few tokens; sigma is one for
+          // all rows.
+          float mx = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (st.any(key + lane + 32 * k)) mx = fmaxf(mx, ks[kTile + lane + 32 * k]);
+          const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(mx) & 0x7fffffffu);
+          if (__uint_as_float(bits) > sigma * 128.f || sigma == 0.f) {
+            const uint32_t exponent = min(max((bits + 0x7fffffu) >> 23, 9u), 253u);
+            const float to = __uint_as_float((exponent - 7u) << 23);
+            by = sigma == 0.f ? 0.f : sigma / to;
+            sigma = to;
+            sigma_inv = 1.f / to;
+          }
+        }
+        // Weights and their sum, with the maximum as far as this half knows
+        // (the scores die one by one as the weights come); the other half's is
+        // looked for on the way. Maxima are whole numbers (base 2), so that
+        // weights of one are exactly those of another times a power of two.
+        const float m_before = m;
+        if (top > m + kLazy || m == -INFINITY) m = fmaxf(m, ceilf(top));
+        uint32_t w[32];
+        f32x2 sums[2] = {0ull, 0ull};
+        unsigned long long letter = 0;
+        {
+          const float down = m == -INFINITY ? 0.f : -m;
+          const f32x2 factor2 = pair_of(factor, factor), down2 = pair_of(down, down);
+#pragma unroll
+          for (int k = 0; k < 64; k += 4) {
+            if (k == 32) letter = peek();
+            float f[4];
+            halves(fma2(pair_of(v[k >> 5][k & 31], v[k >> 5][(k & 31) + 1]), factor2, down2), f[0], f[1]);
+            halves(fma2(pair_of(v[k >> 5][(k & 31) + 2], v[k >> 5][(k & 31) + 3]), factor2, down2), f[2], f[3]);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) f[a] = ex2(f[a]);
+            sums[0] = add2(sums[0], pair_of(f[0], f[1]));
+            sums[1] = add2(sums[1], pair_of(f[2], f[3]));
+            if constexpr (E8) {
+              const float4 u = *reinterpret_cast<const float4*>(ks + kTile + half * 64 + k);
+              w[k / 2] = f16x2(f[0] * u.x * sigma_inv, f[1] * u.y * sigma_inv);
+              w[k / 2 + 1] = f16x2(f[2] * u.z * sigma_inv, f[3] * u.w * sigma_inv);
+            } else {
+              w[k / 2] = bf16x2(f[0], f[1]), w[k / 2 + 1] = bf16x2(f[2], f[3]);
+            }
+          }
+        }
+        float s0, s1, other;
+        halves(add2(sums[0], sums[1]), s0, s1);
+        float sum = s0 + s1;
+        if (!(ok = __all_sync(0xffffffffu, fetch(letter, other)))) break;
+        const float mx = fmaxf(top, other);
+        const bool grows = mx > m_before + kLazy || (m_before == -INFINITY && mx > m_before);
+        const float m_guess = m;
+        m = grows ? fmaxf(m_before, ceilf(mx)) : m_before;
+        if (__any_sync(0xffffffffu, m != m_guess)) {   // (then it is larger)
+          const float less = m == m_guess ? 1.f : ex2_below(m_guess, m);
+          sum *= less;
+          const uint32_t less2 = E8 ? f16x2(less, less) : bf16x2(less, less);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) w[k] = mul_16<E8>(w[k], less2);
+        }
+        if (grows) {
+          const float less = ex2_below(m_before, m);
+          by *= less, l *= less;
+        }
+        tmem_st32(s_at, w);   // over the first half of the scores
+        if (any && __any_sync(0xffffffffu, by != 1.f)) {
+          // (These scores come after the sums before them in the issuer's
+          // order: those are done.)
+          const f32x2 by2 = pair_of(by, by);
+#pragma unroll
+          for (int e = 0; e < kHalf / 32; ++e) {
+            uint32_t o[32];
+            tmem_ld32(o_at + 32 * e, o);
+            tmem_ld_wait();
+            reg_fence(o);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float a, b;
+              halves(mul2(pair_of(o[k], o[k + 1]), by2), a, b);
+              o[k] = __float_as_uint(a), o[k + 1] = __float_as_uint(b);
+            }
+            tmem_st32(o_at + 32 * e, o);
+          }
+        }
+        any = true;
+        l += sum;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPFull + t));
+      }
+      if (!ok) break;
+      n_step += it.to - it.from;
+      // ---- the rows' results: a thread has half of the columns
+      post(l);
+      float l_other;
+      if (!__all_sync(0xffffffffu, fetch(peek(), l_other))) break;
+      l += l_other;
+      if (any) {
+        if (!mbar_wait(bar(kOFull + t), outs & 1u, abort_flag, kWaitNs)) break;
+        ++outs;
+        tc_fence_after();
+      }
+      const int64_t out = it.row + token;
+      const int head = it.h * p.group + row % p.group;
+      auto finish = [&](const uint32_t (&w)[kHalf / 2], float top, float sum) {
+        uint4* const to = reinterpret_cast<uint4*>(p.o[it.r] + out * p.ld_o + head * D + half * kHalf);
+#pragma unroll
+        for (int e = 0; e < kHalf / 8; ++e) to[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        if (p.lse[it.r] && half == 0) p.lse[it.r][out * p.heads_q + head] = lse_of(top, sum);
+      };
+      uint32_t w[kHalf / 2];
+      if (it.parts == 1) {
+        const bool none = m == -INFINITY && l == 0.f;   // (O holds nothing then, or zeros)
+        const float by = E8 ? sigma / l : 1.f / l;
+#pragma unroll
+        for (int e = 0; e < kHalf / 2; ++e) w[e] = 0u;
+        if (any) {
+#pragma unroll
+          for (int e = 0; e < kHalf / 32; ++e) {
+            uint32_t o[32];
+            tmem_ld32(o_at + 32 * e, o);
+            tmem_ld_wait();
+            reg_fence(o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              w[16 * e + k] = none ? 0u : bf16x2(__uint_as_float(o[2 * k]) * by, __uint_as_float(o[2 * k + 1]) * by);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kOFree + t));
+        }
+        if (real) finish(w, m, l);
+        continue;
+      }
+      // A part: four columns of all rows side by side, then both threads'
+      // maxima and sums.
+      const int place = t * kTile + row, rows = p.slot_rows;
+      auto part_of = [&](int i) { return p.part + (int64_t)(it.slot + i) * rows * (D + 4); };
+      const int stat = (D + 2 * half) * rows + place;
+      if (any) {
+        float4* const to = reinterpret_cast<float4*>(part_of(it.part)) + half * (kHalf / 4) * rows + place;
+#pragma unroll
+        for (int e = 0; e < kHalf / 32; ++e) {
+          uint32_t o[32];
+          tmem_ld32(o_at + 32 * e, o);
+          tmem_ld_wait();
+          reg_fence(o);
+          const float by = E8 ? sigma : 1.f;
+          if (real)
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              to[(8 * e + k / 4) * rows] = make_float4(__uint_as_float(o[k]) * by, __uint_as_float(o[k + 1]) * by,
+                                                       __uint_as_float(o[k + 2]) * by, __uint_as_float(o[k + 3]) * by);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kOFree + t));
+      }
+      if (real) part_of(it.part)[stat] = m, part_of(it.part)[stat + rows] = l;
+      __threadfence();
+      __syncwarp();
+      uint32_t* const counter = p.arrived + (int64_t)it.slot * 16 + sw;
+      uint32_t came = 0;
+      if (lane == 0) {
+        came = atom_add_acq_rel_u32(counter, 1u);
+        if (came == (uint32_t)it.parts - 1u) *counter = 0u;
+      }
+      if (__shfl_sync(0xffffffffu, came, 0) != (uint32_t)it.parts - 1u) continue;
+      __threadfence();
+      if (real) {
+        // The last of the parts' warps of these rows joins them, in their order.
+        float top = -INFINITY, total = 0.f;
+        for (int i = 0; i < it.parts; ++i) top = fmaxf(top, __ldcg(part_of(i) + stat));
+        for (int i = 0; i < it.parts; ++i) total += ex2_below(__ldcg(part_of(i) + stat), top) * __ldcg(part_of(i) + stat + rows);
+        const float inv = top == -INFINITY && total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+        for (int e = 0; e < kHalf / 32; ++e) {
+          float acc[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+          for (int i = 0; i < it.parts; ++i) {
+            const float mi = __ldcg(part_of(i) + stat), li = __ldcg(part_of(i) + stat + rows);
+            if (mi == -INFINITY && li == 0.f) continue;   // (nothing was written)
+            const float f = ex2_below(mi, top) * inv;
+            const float4* const from = reinterpret_cast<const float4*>(part_of(i)) + (half * (kHalf / 4) + 8 * e) * rows + place;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 u = __ldcg(from + k * rows);
+              acc[4 * k] = fmaf(f, u.x, acc[4 * k]), acc[4 * k + 1] = fmaf(f, u.y, acc[4 * k + 1]);
+              acc[4 * k + 2] = fmaf(f, u.z, acc[4 * k + 2]), acc[4 * k + 3] = fmaf(f, u.w, acc[4 * k + 3]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[16 * e + k] = bf16x2(acc[2 * k], acc[2 * k + 1]);
+        }
+        finish(w, top, total);
       }
     }
   }
@@ -783,9 +973,7 @@ fo_status launch_prompt(PromptParams& k, int sms, cudaStream_t s) {
   fo_status st = launched(e, "paged prompt", k.R, k.batch.rows, D, 0, C::kThreads);
   if (st || (st = launched(launch_after(prompt_plan_kernel, dim3(1), 1024, 0, 0, s, k), "paged prompt plan", k.R, k.batch.rows, D, 1, 1024)))
     return st;
-  // No more blocks than pairs there can be.
-  const int64_t pairs = (k.batch.rows / (2 * k.tokens) + k.batch.seqs) * (int64_t)(k.R * k.heads_k);
-  const int blocks = (int)std::min<int64_t>(pairs, sms);
+  const int blocks = sms;
   return launched(launch_after(kern, dim3(blocks), C::kThreads, C::kSmem, 0, s, k), "paged prompt", k.R, k.batch.rows, D, blocks, C::kThreads);
 }
 
@@ -827,8 +1015,28 @@ bool encode_rows(CUtensorMap* m, const void* p, int64_t rows, int64_t ld, int he
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Workspace: header, the deal's counter, pairs before each sequence.
-size_t prompt_bytes(int32_t seqs) { return 256 + ((size_t)seqs + 1) * 8; }
+// Workspace: header, deal, arrivals, pairs before each sequence, items, parts.
+namespace {
+struct PromptPlaces {
+  size_t arrived, before, items, part, bytes;
+  int64_t most_items;
+  int32_t slot_rows;
+  PromptPlaces(const fo_paged_desc* d, int64_t seqs, int64_t rows, int64_t max_new) {
+    const int tokens = kTile / (d->heads_q / d->heads_k);
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    slot_rows = max_new > tokens ? 2 * kTile : kTile;
+    most_items = rows / (2 * tokens) + seqs + kMostParts;
+    arrived = 256 + kFewCountBytes;
+    before = kScratchAt;
+    items = before + up((size_t)(seqs + 1) * 8);
+    part = items + up((size_t)most_items * sizeof(Record));
+    bytes = part + (size_t)kMostParts * slot_rows * (d->head_dim + 4) * 4;
+  }
+};
+}  // namespace
+size_t prompt_bytes(const fo_paged_desc* d, int32_t seqs, int64_t rows, int32_t max_new) {
+  return PromptPlaces(d, seqs, rows, max_new).bytes;
+}
 
 fo_status attend_prompts(const PagedCall& c, cudaStream_t s) {
   const fo_paged_desc* const d = c.d;
@@ -856,8 +1064,15 @@ fo_status attend_prompts(const PagedCall& c, cudaStream_t s) {
   k.window = d->window;
   k.sinks = d->sinks;
   k.scale_log2 = c.scale_log2;
+  const PromptPlaces at(d, c.b->seqs, c.rows, c.b->max_new);
+  k.sms = std::min(c.sms, FO_GB300_SMS);
   k.next = reinterpret_cast<uint32_t*>(c.ws + 128);
-  k.before = reinterpret_cast<int64_t*>(c.ws + 256);
+  k.arrived = reinterpret_cast<uint32_t*>(c.ws + at.arrived);
+  k.before = reinterpret_cast<int64_t*>(c.ws + at.before);
+  k.items = reinterpret_cast<Record*>(c.ws + at.items);
+  k.most_items = at.most_items;
+  k.part = reinterpret_cast<float*>(c.ws + at.part);
+  k.slot_rows = at.slot_rows;
   if (d->head_dim == 128) return eight ? launch_prompt<128, true>(k, c.sms, s) : launch_prompt<128, false>(k, c.sms, s);
   return eight ? launch_prompt<64, true>(k, c.sms, s) : launch_prompt<64, false>(k, c.sms, s);
 }

@@ -188,6 +188,8 @@ PROMPTS = [
     (1, 8, 1, 128, 256, [400, 600], [100, 33]),
     (1, 64, 1, 128, 16, [80, 7], [5, 7]),
     (1, 20, 4, 64, 16, [100, 30], [64, 40]),              # rows before the beginning of the second
+    (1, 2, 1, 128, 32, [2500, 130, 5], [70, 65, 1]),      # one long context: its steps are cut and joined
+    (2, 20, 1, 64, 16, [1800], [33]),
 ]
 
 

@@ -237,7 +237,7 @@ struct Prompt {
   static constexpr int kOffItem = kOffRow + (E8 ? 2 * 2 * kTile * 4 : 0);
   static constexpr int kOffBox = kOffItem + 2 * 48;   // the softmax warps' mailboxes: 16 warps, two parities, 32 lanes
   static constexpr int kOffBar = kOffBox + 16 * 2 * 32 * 8;
-  static constexpr int kBars = 3 * kStages + 2 * kRaws + 24;
+  static constexpr int kBars = 3 * kStages + 2 * kRaws + 26;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kSmem = 1024 + kOffMisc + 16;
   static_assert(kSmem <= 232448, "shared memory");
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
   enum : int {
     kFull = 0, kEmpty = C::kStages, kRawFull = 2 * C::kStages, kRawEmpty = kRawFull + C::kRaws,
     kQFull = kRawEmpty + C::kRaws, kQReady, kQEmpty, kSFull, kPFull = kSFull + 2, kOFull = kPFull + 2, kOFree = kOFull + 2,
-    kReady = kOFree + 2, kItemFull = kReady + C::kStages, kItemFree = kItemFull + 2, kDrain = kItemFree + 2, kLast = kDrain + 2
+    kReady = kOFree + 2, kItemFull = kReady + C::kStages, kItemFree = kItemFull + 2, kDrain = kItemFree + 2, kTurn = kDrain + 2, kLast = kTurn + 2
   };
   static_assert(kLast <= C::kBars, "barriers");
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc);
@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       mbar_init(bar(kOFree + t), 8);
       mbar_init(bar(kItemFull + t), 1);
       mbar_init(bar(kDrain + t), 1);
+      mbar_init(bar(kTurn + t), 1);
       mbar_init(bar(kItemFree + t), C::kThreads / 32 - 1);   // all warps but the first
     }
     *abort_flag = 0;
@@ -449,11 +450,19 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
     // ------------------------------------------------------------ products, a warp for each tile
     const int t = warp - 1;
     uint32_t n_tile = 0;                         // number of the item's first tile of keys, of all items
-    uint32_t soft = 0, outs = 0;                 // steps and outputs so far
+    uint32_t soft = 0, outs = 0, turns = 0;      // steps, outputs, turns so far
     const uint32_t one = elected();
     bool ok = true;
     auto full = [&](int which, uint32_t i) {
       return mbar_wait(bar(which + i % (uint32_t)C::kStages), (i / (uint32_t)C::kStages) & 1u, abort_flag, kWaitNs);
+    };
+    // The tiles take turns, each with its weighted sum and its next scores:
+    // mixed in the tensor pipe they would end together, and so would their
+    // softmax, instead of one beside the other's products.
+    auto my_turn = [&]() { return mbar_wait(bar(kTurn + t), (turns++ & 1u) ^ (t == 0 ? 1u : 0u), abort_flag, kWaitNs); };
+    auto your_turn = [&]() {
+      if (one) mbar_arrive(bar(kTurn + (t ^ 1)));
+      __syncwarp();
     };
     const uint64_t q_desc = smem_desc_sw128(base + t * C::kTileBytes, 16, 1024);
     const uint64_t k_desc = smem_desc_sw128(base + C::kOffRing, 16, 1024), v_desc = smem_desc_sw128(base + C::kOffRing, 8192, 1024);
@@ -476,24 +485,23 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         if (mine) last = i + 31 - __clz(mine);
       }
       if (last < 0 && one) mbar_arrive(bar(kQEmpty));
-      // The scores of step i.
-      auto scores = [&](int i) -> bool {
+      // The scores of step i, whose keys have been waited for. The other tile's
+      // turn is called for with half of them to go: it takes as long to come.
+      auto scores = [&](int i, bool call) {
         const uint32_t k = n_tile + 2u * (uint32_t)i;
-        if (!full(kFull, k)) return false;
-        tc_fence_after();
         if (one) {
           const uint64_t b = k_desc + (uint64_t)((k % (uint32_t)C::kStages) * (C::kTileBytes >> 4));
 #pragma unroll
           for (int e = 0; e < D / 16; ++e) {
             const uint64_t off = (uint64_t)(((e >> 2) * (kTile * 128) + (e & 3) * 32) >> 4);
             tc_mma<1, false>(s_col, q_desc + off, b + off, idesc(E8, false, kTile), e > 0 ? 1u : 0u);
+            if (e == D / 32 - 1 && call) mbar_arrive(bar(kTurn + (t ^ 1)));
           }
           tc_commit<1>(bar(kSFull + t));
           tc_commit<1>(bar(kEmpty + k % (uint32_t)C::kStages));
           if (i == last) tc_commit<1>(bar(kQEmpty));
         }
         __syncwarp();
-        return true;
       };
       bool begun = false, first = true;   // this step's scores are under way; no output yet
       for (int i = 0; i < steps; ++i) {
@@ -505,12 +513,21 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
             if (ok && one) mbar_arrive(bar(kEmpty + x % (uint32_t)C::kStages));
             __syncwarp();
           }
-          if (!ok) break;
+          if (!ok || !(ok = my_turn())) break;
+          your_turn();
           continue;
         }
-        if (!begun && !(ok = scores(i))) break;
+        if (!begun) {
+          if (!(ok = full(kFull, v - 1u))) break;
+          tc_fence_after();
+          scores(i, false);
+        }
+        // The next scores come with this step's sum, unless the tile passes
+        // over steps (between first tokens and window) or they are the next
+        // 32's: then in their turn.
+        begun = bit << 1 & mine;
         if (!(ok = full(E8 ? kFull : kReady, v) && (!first || mbar_wait(bar(kOFree + t), (outs & 1u) ^ 1u, abort_flag, kWaitNs)) &&
-                   mbar_wait(bar(kPFull + t), soft & 1u, abort_flag, kWaitNs)))
+                   (!begun || full(kFull, v + 1u)) && mbar_wait(bar(kPFull + t), soft & 1u, abort_flag, kWaitNs) && my_turn()))
           break;
         ++soft;
         tc_fence_after();
@@ -526,10 +543,8 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         }
         __syncwarp();
         first = false;
-        // The next scores, unless the tile passes over steps (between first
-        // tokens and window) or these are the next 32's: then in their turn.
-        begun = bit << 1 & mine;
-        if (begun && !(ok = scores(i + 1))) break;
+        if (begun) scores(i + 1, true);
+        else your_turn();
       }
       outs += last >= 0;
       n_tile += 2u * (uint32_t)steps;

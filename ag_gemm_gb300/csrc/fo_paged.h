@@ -82,7 +82,7 @@ Batch batch_of(const fo_paged_desc* d, const fo_paged_batch* b, int64_t rows, vo
 constexpr int kFewThreads = 256, kFewBlocks = 2;   // blocks an SM
 constexpr int kMostParts = 4 * FO_GB300_SMS;       // of the prompts' kernel
 constexpr size_t kFewCountBytes = (kFewBlocks * FO_GB300_SMS * 3 * 4 + 255) / 256 * 256;
-constexpr size_t kScratchAt = 256 + kFewCountBytes + (size_t)kMostParts * 16 * 4;
+constexpr size_t kScratchAt = 256 + kFewCountBytes + (size_t)kMostParts * 8 * 4;
 
 // A checked call of fo_paged_attention.
 struct PagedCall {
@@ -100,8 +100,9 @@ struct PagedCall {
 };
 // Few new tokens a sequence (fo_paged_few.cuh), `eights` times 8 rows (1, 2, 4
 // or 8) of a key head: kFewBlocks blocks an SM.
-// Keys of a tile: 32 for each warp that has keys of its own, 64 in 8 bits.
-constexpr int few_step(int eights, bool eight) { return (eights <= 2 ? 4 : eights == 4 ? 2 : 1) * (eight ? 64 : 32); }
+// Keys of a tile: 32 for each warp that has keys of its own, 64 in 8 bits or
+// where warps share keys.
+constexpr int few_step(int eights, bool eight) { return (eights <= 2 ? 4 : eights == 4 ? 2 : 1) * (eight || eights > 2 ? 64 : 32); }
 struct FewParams {
   CUtensorMap k[kMaxR];   // [pages * heads_k][page][D]; boxes of 128 bytes x `box` tokens
   CUtensorMap v[kMaxR];

@@ -8,22 +8,20 @@
 // computes its next scores (1024 cycles of bf16 at D = 128), the other tile's
 // softmax runs. Per step and tile:
 //     S = Q K^T        in TMEM, 128 columns
-//     P = 2^(S - m)    in 16 bits over the same columns, by the tile's eight
-//                      warps: two to a row, 64 keys each
+//     P = 2^(S - m)    in 16 bits over the same columns, by the tile's four warps
 //     O += P V         in TMEM, D columns, P read from TMEM
-// The two threads of a row swap their maxima through shared memory; each
-// computes its weights with the running maximum while the other's is on its
-// way, and scales them only if that moves (it does when it grows by more than
-// 2^8; smaller growth is cancelled by the division at the end). Only then O is
-// read and rescaled. With a thread for a whole row, no swap, but 128 scores one
-// after the other, a step took 1.6 times as long.
+// A thread has a row of its own, so no row needs another thread. The running
+// maximum m moves when it grows by more than 2^8 (smaller growth is cancelled
+// by the division at the end); only then O is read and rescaled.
 //
 // Warps: 0 loads (and deals items), 1 and 2 issue the tiles' products (one
 // issuer for both fell behind: a wait for a barrier that is ready takes it 150
-// cycles), 3 puts zeros in the place of values that nobody sees, 4-11 and 12-19
-// are the tiles' softmax. With an 8-bit cache 3 and 20 turn its bytes into f16 (which holds
-// e4m3 exactly): queries and weights are f16 then, the keys' scales multiply
-// the scores' columns and the values' the weights.
+// cycles), 3 puts zeros in the place of values that nobody sees, 4-7 and 8-11
+// are the tiles' softmax. With an 8-bit cache 12-15 turn its bytes into f16,
+// times their scales over a power of two for each 32 keys: queries and weights
+// are f16 then. (The scales' columns in the softmax, an earlier form, took it
+// twice the time.) A key's or value's element is rounded to f16's 11 bits by
+// that, 2^-11 of it at most.
 //
 // A first kernel of one block lists the items; blocks take them from a
 // counter, the last (under the causal mask the costliest) first.
@@ -63,8 +61,8 @@ struct PromptParams {
   uint32_t* next;         // [0] items dealt, [1] items of a key head
   struct Record* items;   // [most_items]
   long long most_items;
-  float* part;            // [most parts][slot_rows * (D + 4)]
-  uint32_t* arrived;      // [most parts][16], zero between calls
+  float* part;            // [most parts][slot_rows * (D + 2)]
+  uint32_t* arrived;      // [most parts][8], zero between calls
   int32_t slot_rows;      // rows of a part: of one tile or two
 };
 
@@ -224,7 +222,8 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const __grid_constant
 
 template <int D, bool E8>
 struct Prompt {
-  static constexpr int kThreads = E8 ? 672 : 640;
+  static constexpr int kThreads = E8 ? 512 : 384;
+  static constexpr int kConverters = 4;              // warps
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kRawBytes = kTile * D;
   static constexpr int kCuts = D / 64;               // 128-byte columns of a 16-bit tile
@@ -233,10 +232,9 @@ struct Prompt {
   static constexpr int kOffRing = 2 * kTileBytes;    // after the two tiles of queries
   static constexpr int kOffRaw = kOffRing + kStages * kTileBytes;
   static constexpr int kOffScale = kOffRaw + kRaws * kRawBytes;
-  static constexpr int kOffRow = kOffScale + (E8 ? kScaleSlots * 2 * kTile * 4 : 0);   // the rows' factors, two items
+  static constexpr int kOffRow = kOffScale + (E8 ? kScaleSlots * 8 * 4 : 0);   // the rows' factors, two items
   static constexpr int kOffItem = kOffRow + (E8 ? 2 * 2 * kTile * 4 : 0);
-  static constexpr int kOffBox = kOffItem + 2 * 48;   // the softmax warps' mailboxes: 16 warps, two parities, 32 lanes
-  static constexpr int kOffBar = kOffBox + 16 * 2 * 32 * 8;
+  static constexpr int kOffBar = kOffItem + 2 * 48;
   static constexpr int kBars = 3 * kStages + 2 * kRaws + 26;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kSmem = 1024 + kOffMisc + 16;
@@ -262,18 +260,38 @@ __device__ __forceinline__ uint32_t elected() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
   return is;
 }
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// Sixteen columns of a thread's row.
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   f32x2 d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// Products of two 16-bit numbers each.
-template <bool F16>
-__device__ __forceinline__ uint32_t mul_16(uint32_t a, uint32_t b) {
+// Two f16 times two others (plus two).
+__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
   uint32_t d;
-  if constexpr (F16) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+__device__ __forceinline__ uint32_t fma_f16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ float half_of(uint32_t two) {   // the first of two f16
+  float f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(two));
+  return f;
 }
 // The lowest n bits (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
@@ -295,16 +313,16 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc);
   volatile uint32_t* const tmem_at = reinterpret_cast<volatile uint32_t*>(gbase + C::kOffMisc + 4);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) mbar_init(bar(kFull + i), E8 ? 2 : 1), mbar_init(bar(kEmpty + i), 2), mbar_init(bar(kReady + i), 1);
-    for (int i = 0; i < C::kRaws; ++i) mbar_init(bar(kRawFull + i), 1), mbar_init(bar(kRawEmpty + i), 2);
+    for (int i = 0; i < C::kStages; ++i) mbar_init(bar(kFull + i), E8 ? C::kConverters : 1), mbar_init(bar(kEmpty + i), 2), mbar_init(bar(kReady + i), 1);
+    for (int i = 0; i < C::kRaws; ++i) mbar_init(bar(kRawFull + i), 1), mbar_init(bar(kRawEmpty + i), C::kConverters);
     mbar_init(bar(kQFull), 1);
-    mbar_init(bar(kQReady), 2);
+    mbar_init(bar(kQReady), C::kConverters);
     mbar_init(bar(kQEmpty), 2);
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(kSFull + t), 1);
-      mbar_init(bar(kPFull + t), 8);
+      mbar_init(bar(kPFull + t), 4);
       mbar_init(bar(kOFull + t), 1);
-      mbar_init(bar(kOFree + t), 8);
+      mbar_init(bar(kOFree + t), 4);
       mbar_init(bar(kItemFull + t), 1);
       mbar_init(bar(kDrain + t), 1);
       mbar_init(bar(kTurn + t), 1);
@@ -314,7 +332,6 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  for (int i = threadIdx.x; i < 16 * 2 * 32; i += C::kThreads) reinterpret_cast<volatile unsigned long long*>(gbase + C::kOffBox)[i] = 0ull;
   if (warp == 1) {
     __syncwarp();
     tmem_alloc<1>(base + C::kOffMisc + 4, 512);
@@ -341,6 +358,8 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
   };
   Item it;
   Steps st;
+  // (What two warpgroups take more, the others leave.)
+  if (warp < 4) fewer_registers<E8 ? 72 : 104>();
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
@@ -535,8 +554,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
           const uint64_t b = v_desc + (uint64_t)((v % (uint32_t)C::kStages) * (C::kTileBytes >> 4));
 #pragma unroll
           for (int e = 0; e < kTile / 16; ++e)
-            // (The weights of keys 0-63 lie in columns 0-31, of the others in 64-95.)
-            mma_ts(o_col, s_col + (e >> 2) * 64 + (e & 3) * 8, b + (uint64_t)(((e >> 2) * (C::kTileBytes / 2) + (e & 3) * 2048) >> 4),
+            mma_ts(o_col, s_col + e * 8, b + (uint64_t)(((e >> 2) * (C::kTileBytes / 2) + (e & 3) * 2048) >> 4),
                    idesc(E8, true, D), e > 0 || !first ? 1u : 0u);
           tc_commit<1>(bar(kEmpty + v % (uint32_t)C::kStages));
           if (i == last) tc_commit<1>(bar(kOFull + t));
@@ -554,7 +572,12 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
     if (one) tc_commit<1>(bar(kDrain + t));
     __syncwarp();
     mbar_wait(bar(kDrain + t), 0, &never, 100000000ull);
-  } else if (warp == 3 || (E8 && warp == 20)) {
+  } else if (warp == 3 && E8) {
+    // ------------------------------------------------------------ (nothing to do: 8-bit values are cleaned as they are turned)
+    for (int n = 0; take(n, it); ++n) {
+    }
+  } else if (warp == 3 || warp >= 12) {
+    if constexpr (E8) fewer_registers<72>();
     if constexpr (!E8) {
       // ---------------------------------------------------------- values that nobody sees
       uint32_t n_tile = 0;
@@ -584,7 +607,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       }
     } else {
       // ---------------------------------------------------------- 8 bits to f16
-      const int tid = (warp == 3 ? 0 : 32) + lane;   // a thread for two rows (of queries) or keys
+      const int tid = (warp - 12) * 32 + lane;   // a thread for a row (of queries) or key
       uint32_t n_tile = 0, n_step = 0;
       bool ok = true;
       for (int n = 0; ok; ++n) {
@@ -594,8 +617,8 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         // The queries, each row times a power of two that brings its largest
         // magnitude to [128, 256); in place.
 #pragma unroll 1
-        for (int rows = 0; rows < 4; ++rows) {
-          const int t = rows >> 1, row = tid + (rows & 1) * 64;
+        for (int t = 0; t < 2; ++t) {
+          const int row = tid;
           const uint32_t at = base + t * C::kTileBytes + row * 128;
           float top = 0.f;
 #pragma unroll 4
@@ -619,18 +642,22 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kQReady));
+        // A key's place in the scales (its page looked up), and its scales: of
+        // the next step while this one's bytes are turned.
+        auto place_of = [&](int i) -> long long {
+          const int key = st.block(i) * kTile + tid;
+          if (i >= it.to || !st.any(key)) return -1;
+          const int id = p.batch.table[(long long)it.b * p.batch.cols + (key >> p.batch.shift)];
+          if (id < 0 || id >= p.batch.pages) return -1;
+          return ((long long)(id * p.heads_k + it.h) << p.batch.shift) + (key & ((1 << p.batch.shift) - 1));
+        };
+        auto scale_of = [&](const float* from, long long at) { return at >= 0 ? from[at] : 0.f; };
+        long long next = place_of(it.from);
+        float k_scale = scale_of(p.ks[it.r], next), v_scale = scale_of(p.vs[it.r], next);
         for (int i = it.from; i < it.to && ok; ++i) {
-          float scale[2][2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int key = st.block(i) * kTile + tid + 64 * e;
-            scale[e][0] = scale[e][1] = 0.f;
-            if (!st.any(key)) continue;
-            const int id = p.batch.table[(long long)it.b * p.batch.cols + (key >> p.batch.shift)];
-            if (id < 0 || id >= p.batch.pages) continue;
-            const long long at = ((long long)(id * p.heads_k + it.h) << p.batch.shift) + (key & ((1 << p.batch.shift) - 1));
-            scale[e][0] = p.ks[it.r][at], scale[e][1] = p.vs[it.r][at];
-          }
+          const bool seen = st.any(st.block(i) * kTile + tid);
+          next = place_of(i + 1);
+          float k_next = 0.f, v_next = 0.f;
 #pragma unroll 1
           for (int value = 0; value < 2; ++value) {
             const uint32_t x = n_tile + 2u * (uint32_t)(i - it.from) + (uint32_t)value;
@@ -641,31 +668,43 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
               ok = false;
               break;
             }
-            if (value == 0) {
-              float* const to = reinterpret_cast<float*>(gbase + C::kOffScale) + ((n_step + i - it.from) % kScaleSlots) * 2 * kTile + tid;
-              to[0] = scale[0][0], to[64] = scale[1][0], to[kTile] = scale[0][1], to[kTile + 64] = scale[1][1];
-            }
-            // Sixteen bytes a time: lanes side by side in a key's bytes, so
-            // that reads and writes meet no bank twice.
+            if (value) k_next = scale_of(p.ks[it.r], next), v_next = scale_of(p.vs[it.r], next);
+            // A power of two not below the warp's 32 scales: they are divided
+            // by it, and the softmax knows it.
+            const float scale = value ? v_scale : k_scale;
+            const uint32_t top = __reduce_max_sync(0xffffffffu, seen ? __float_as_uint(scale) & 0x7fffffffu : 0u);
+            const uint32_t exponent = min(max((top + 0x7fffffu) >> 23, 40u), 253u);
+            if (lane == 0)
+              reinterpret_cast<float*>(gbase + C::kOffScale)[((n_step + i - it.from) % kScaleSlots) * 8 + value * 4 + (tid >> 5)] =
+                  __uint_as_float(exponent << 23);
+            const float by = scale * __uint_as_float((254u - exponent) << 23);
+            // The multiplier in two f16 parts for keys: a rounding of a key's
+            // scale would move all of its score, those of its values do not
+            // add up. For values one part.
+            const uint32_t hi = f16x2(by, by);
+            const float rest = by - half_of(hi);
+            const uint32_t lo = value ? 0u : f16x2(rest, rest);
+            // A thread's key, sixteen bytes a time (the swizzle has neighbours'
+            // in other banks).
             const uint32_t from = base + C::kOffRaw + rs * C::kRawBytes, to = base + C::kOffRing + ss * C::kTileBytes;
-            constexpr int kPieces = D / 16;
-#pragma unroll 4
-            for (int k = tid; k < kTile * kPieces; k += 64) {
-              const int row = k / kPieces, piece = k % kPieces;
-              const uint4 v = lds128(D == 128 ? from + row * 128 + ((piece ^ (row & 7)) << 4) : from + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
-              uint4 a = make_uint4(f16x2_of_e4m3(v.x), f16x2_of_e4m3_high(v.x), f16x2_of_e4m3(v.y), f16x2_of_e4m3_high(v.y));
-              uint4 b = make_uint4(f16x2_of_e4m3(v.z), f16x2_of_e4m3_high(v.z), f16x2_of_e4m3(v.w), f16x2_of_e4m3_high(v.w));
-              if (value && !st.any(st.block(i) * kTile + row)) a = b = make_uint4(0, 0, 0, 0);
-              const int cut = piece >> 2, c16 = (piece & 3) * 2;
-              const uint32_t at = value ? to + (row >> 6) * (C::kTileBytes / 2) + cut * 8192 + (row & 63) * 128
-                                        : to + cut * (kTile * 128) + row * 128;
-              sts128(at + ((c16 ^ (row & 7)) << 4), a);
-              sts128(at + (((c16 + 1) ^ (row & 7)) << 4), b);
+            const uint32_t row_at = value ? to + (tid >> 6) * (C::kTileBytes / 2) + (tid & 63) * 128 : to + tid * 128;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint4 u = lds128(D == 128 ? from + tid * 128 + ((k ^ (tid & 7)) << 4) : from + tid * 64 + ((k ^ ((tid >> 1) & 3)) << 4));
+              uint32_t w[8] = {f16x2_of_e4m3(u.x), f16x2_of_e4m3_high(u.x), f16x2_of_e4m3(u.y), f16x2_of_e4m3_high(u.y),
+                               f16x2_of_e4m3(u.z), f16x2_of_e4m3_high(u.z), f16x2_of_e4m3(u.w), f16x2_of_e4m3_high(u.w)};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = value ? mul_f16(w[e], hi) : fma_f16(w[e], hi, mul_f16(w[e], lo));
+              const uint32_t at = row_at + (k >> 2) * (value ? 8192 : kTile * 128);
+              const int c16 = (k & 3) * 2;
+              sts128(at + ((c16 ^ (tid & 7)) << 4), seen ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0));
+              sts128(at + (((c16 + 1) ^ (tid & 7)) << 4), seen ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(0, 0, 0, 0));
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kRawEmpty + rs)), mbar_arrive(bar(kFull + ss));
           }
+          k_scale = k_next, v_scale = v_next;
         }
         n_tile += 2u * (uint32_t)(it.to - it.from);
         n_step += (uint32_t)(it.to - it.from);
@@ -673,38 +712,11 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int sw = warp - 4, t = sw >> 3, half = (sw >> 2) & 1, row = (warp & 3) * 32 + lane;
+    if constexpr (E8) more_registers<184>();
+    else more_registers<200>();
+    const int t = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + C::kS + t * 128 + half * 64, o_at = tmem + lanes + C::kO + t * D + half * (D / 2);
-    constexpr int kHalf = D / 2;   // columns of O that a thread reads
-    // What a row's two threads tell each other: a number and which exchange
-    // it is of. Exchange x + 2 takes x's place only after the other's x + 1
-    // has been read, which was written after x had been.
-    volatile unsigned long long* const box = reinterpret_cast<volatile unsigned long long*>(gbase + C::kOffBox);
-    uint32_t x = 0;
-    auto post = [&](float mine) {
-      ++x;
-      box[(sw * 2 + (int)(x & 1u)) * 32 + lane] = ((unsigned long long)x << 32) | __float_as_uint(mine);
-    };
-    auto peek = [&]() -> unsigned long long { return box[((sw ^ 4) * 2 + (int)(x & 1u)) * 32 + lane]; };
-    auto fetch = [&](unsigned long long w, float& theirs) -> bool {   // w: what peek saw
-      if ((uint32_t)(w >> 32) != x) {
-        volatile unsigned long long* const at = box + (((sw ^ 4) * 2 + (int)(x & 1u)) * 32 + lane);
-        const uint64_t t0 = globaltimer();
-        uint32_t tries = 0;
-        while ((uint32_t)((w = *at) >> 32) != x) {
-          if ((++tries & 63u) == 0) {
-            if (*abort_flag) return false;
-            if (globaltimer() - t0 > kWaitNs) {
-              *abort_flag = 1;
-              return false;
-            }
-          }
-        }
-      }
-      theirs = __uint_as_float((uint32_t)w);
-      return true;
-    };
+    const uint32_t s_at = tmem + lanes + C::kS + t * 128, o_at = tmem + lanes + C::kO + t * D;
     uint32_t step = 0, outs = 0;   // this tile's steps and outputs so far
     uint32_t n_step = 0;           // steps of the items before
     bool ok = true;
@@ -717,7 +729,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       // Blocks all of whose keys all of the tile's rows see need no mask.
       const int first_pos = it.base + it.token + t * p.tokens;
       const int last_lo = sight_of(max(first_pos + p.tokens - 1, 0), p.window, p.sinks).lo;
-      float m = -INFINITY, l = 0.f, factor = p.scale_log2, sigma = 0.f, sigma_inv = 0.f;
+      float m = -INFINITY, l = 0.f, row_factor = p.scale_log2, sigma = 0.f;
       bool any = false;
       for (int i = it.from; i < it.to; ++i) {
         if (!st.active(t, i)) continue;
@@ -725,121 +737,101 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         if (!(ok = mbar_wait(bar(kSFull + t), step & 1u, abort_flag, kWaitNs))) break;
         ++step;
         tc_fence_after();
-        // The steps' scales: keys' and values'.
-        const float* const ks = reinterpret_cast<const float*>(gbase + C::kOffScale) + ((n_step + i - it.from) % kScaleSlots) * 2 * kTile;
+        uint32_t v[4][32];   // the row's scores
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tmem_ld32(s_at + 32 * e, v[e]);
+        // In 8 bits, of each 32 keys: the power of two that their scores, and
+        // that their values, are still to be multiplied with.
+        const float* const pow2 = reinterpret_cast<const float*>(gbase + C::kOffScale) + ((n_step + i - it.from) % kScaleSlots) * 8;
         if constexpr (E8)
-          if (!any) factor = p.scale_log2 * reinterpret_cast<const float*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + row];
-        const bool masked = key + kTile - 1 > first_pos || !(key >= last_lo || key + kTile <= p.sinks);
-        uint32_t v[2][32];   // the row's 64 scores
-        tmem_ld32(s_at, v[0]);
-        tmem_ld32(s_at + 32, v[1]);
+          if (!any) row_factor = p.scale_log2 * reinterpret_cast<const float*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + row];
+        float factor[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) factor[e] = E8 ? row_factor * pow2[e] : row_factor;
         tmem_ld_wait();
-        reg_fence(v[0]);
-        reg_fence(v[1]);
-        if constexpr (E8) {
 #pragma unroll
-          for (int k = 0; k < 64; k += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(ks + half * 64 + k);
-            uint32_t* const u = &v[k >> 5][k & 31];
-            float a, b;
-            halves(mul2(pair_of(u[0], u[1]), pair_of(f.x, f.y)), a, b);
-            u[0] = __float_as_uint(a), u[1] = __float_as_uint(b);
-            halves(mul2(pair_of(u[2], u[3]), pair_of(f.z, f.w)), a, b);
-            u[2] = __float_as_uint(a), u[3] = __float_as_uint(b);
-          }
-        }
-        if (masked) {
+        for (int e = 0; e < 4; ++e) reg_fence(v[e]);
+        if (key + kTile - 1 > first_pos || !(key >= last_lo || key + kTile <= p.sinks)) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int at = key + half * 64 + 32 * e;
+          for (int e = 0; e < 4; ++e) {
+            const int at = key + 32 * e;
             const uint32_t seen = low_bits(pos + 1 - at) & (~low_bits(lo - at) | low_bits(p.sinks - at));
 #pragma unroll
             for (int k = 0; k < 32; ++k)
               if (!(seen >> k & 1u)) v[e][k] = 0xff800000u;   // -infinity
           }
         }
-        float tops[4];
+        float top = -INFINITY;
+        {
+          float tops[8];   // two chains for each 32 keys
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tops[k] = -INFINITY;
+          for (int k = 0; k < 8; ++k) tops[k] = max3(__uint_as_float(v[k >> 1][2 * (k & 1)]), __uint_as_float(v[k >> 1][2 * (k & 1) + 1]), -INFINITY);
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          tops[k & 3] = max3(tops[k & 3], __uint_as_float(v[k >> 4][(2 * k) & 31]), __uint_as_float(v[k >> 4][(2 * k + 1) & 31]));
-        const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * factor;
-        post(top);
-        float by = 1.f;   // what O is rescaled with
-        if constexpr (E8) {
-          // The values' scales over sigma, as for few tokens; sigma is one for
-          // all rows.
-          float mx = 0.f;
+          for (int k = 4; k < 32; k += 2)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (st.any(key + lane + 32 * k)) mx = fmaxf(mx, ks[kTile + lane + 32 * k]);
-          const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(mx) & 0x7fffffffu);
-          if (__uint_as_float(bits) > sigma * 128.f || sigma == 0.f) {
-            const uint32_t exponent = min(max((bits + 0x7fffffu) >> 23, 9u), 253u);
-            const float to = __uint_as_float((exponent - 7u) << 23);
-            by = sigma == 0.f ? 0.f : sigma / to;
-            sigma = to;
-            sigma_inv = 1.f / to;
+            for (int e = 0; e < 4; ++e)
+              tops[2 * e + (k >> 1 & 1)] = max3(tops[2 * e + (k >> 1 & 1)], __uint_as_float(v[e][k]), __uint_as_float(v[e][k + 1]));
+          if constexpr (E8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(tops[2 * e], tops[2 * e + 1]) * factor[e]);
+          } else {
+            top = max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]), fmaxf(tops[6], tops[7])) * row_factor;
           }
         }
-        // Weights and their sum, with the maximum as far as this half knows
-        // (the scores die one by one as the weights come); the other half's is
-        // looked for on the way. Maxima are whole numbers (base 2), so that
-        // weights of one are exactly those of another times a power of two.
-        const float m_before = m;
-        if (top > m + kLazy || m == -INFINITY) m = fmaxf(m, ceilf(top));
-        uint32_t w[32];
-        f32x2 sums[2] = {0ull, 0ull};
-        unsigned long long letter = 0;
-        {
-          const float down = m == -INFINITY ? 0.f : -m;
-          const f32x2 factor2 = pair_of(factor, factor), down2 = pair_of(down, down);
+        float by = 1.f;   // what O is rescaled with
+        if (top > m + kLazy || (m == -INFINITY && top > m)) {
+          by = ex2_below(m, top);
+          l *= by;
+          m = top;
+        }
+        if constexpr (E8) {
+          // Weights are kept over sigma, 2^-7 times the largest power of two of
+          // the values so far (so they stay below 2^15 in f16); it is one for
+          // all rows.
+          const float mx = fmaxf(fmaxf(pow2[4], pow2[5]), fmaxf(pow2[6], pow2[7])) * 0.0078125f;
+          if (mx > sigma) {
+            by *= sigma == 0.f ? 0.f : sigma / mx;
+            sigma = mx;
+          }
+        }
+        // Weights, over the scores' first 64 columns (the row's scores are in
+        // registers), and their sum.
+        const float down = m == -INFINITY ? 0.f : -m;
+        const f32x2 down2 = pair_of(down, down);
+        f32x2 sums[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-          for (int k = 0; k < 64; k += 4) {
-            if (k == 32) letter = peek();
+        for (int e = 0; e < 4; ++e) {
+          const f32x2 factor2 = pair_of(factor[e], factor[e]);
+          // In 8 bits what multiplies a value is its weight times its 32's
+          // power of two over sigma; the sum is of the weights alone.
+          const float more = E8 ? pow2[4 + e] / sigma : 1.f;
+          const f32x2 more2 = pair_of(more, more);
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
             float f[4];
-            halves(fma2(pair_of(v[k >> 5][k & 31], v[k >> 5][(k & 31) + 1]), factor2, down2), f[0], f[1]);
-            halves(fma2(pair_of(v[k >> 5][(k & 31) + 2], v[k >> 5][(k & 31) + 3]), factor2, down2), f[2], f[3]);
+            halves(fma2(pair_of(v[e][k], v[e][k + 1]), factor2, down2), f[0], f[1]);
+            halves(fma2(pair_of(v[e][k + 2], v[e][k + 3]), factor2, down2), f[2], f[3]);
 #pragma unroll
             for (int a = 0; a < 4; ++a) f[a] = ex2(f[a]);
-            sums[0] = add2(sums[0], pair_of(f[0], f[1]));
-            sums[1] = add2(sums[1], pair_of(f[2], f[3]));
+            sums[(k >> 1) & 2] = add2(sums[(k >> 1) & 2], pair_of(f[0], f[1]));
+            sums[((k >> 1) & 2) + 1] = add2(sums[((k >> 1) & 2) + 1], pair_of(f[2], f[3]));
             if constexpr (E8) {
-              const float4 u = *reinterpret_cast<const float4*>(ks + kTile + half * 64 + k);
-              w[k / 2] = f16x2(f[0] * u.x * sigma_inv, f[1] * u.y * sigma_inv);
-              w[k / 2 + 1] = f16x2(f[2] * u.z * sigma_inv, f[3] * u.w * sigma_inv);
+              halves(mul2(pair_of(f[0], f[1]), more2), f[0], f[1]);
+              halves(mul2(pair_of(f[2], f[3]), more2), f[2], f[3]);
+              w[k / 2] = f16x2(f[0], f[1]), w[k / 2 + 1] = f16x2(f[2], f[3]);
             } else {
               w[k / 2] = bf16x2(f[0], f[1]), w[k / 2 + 1] = bf16x2(f[2], f[3]);
             }
           }
+          tmem_st16(s_at + 16 * e, w);
         }
-        float s0, s1, other;
-        halves(add2(sums[0], sums[1]), s0, s1);
-        float sum = s0 + s1;
-        if (!(ok = __all_sync(0xffffffffu, fetch(letter, other)))) break;
-        const float mx = fmaxf(top, other);
-        const bool grows = mx > m_before + kLazy || (m_before == -INFINITY && mx > m_before);
-        const float m_guess = m;
-        m = grows ? fmaxf(m_before, ceilf(mx)) : m_before;
-        if (__any_sync(0xffffffffu, m != m_guess)) {   // (then it is larger)
-          const float less = m == m_guess ? 1.f : ex2_below(m_guess, m);
-          sum *= less;
-          const uint32_t less2 = E8 ? f16x2(less, less) : bf16x2(less, less);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) w[k] = mul_16<E8>(w[k], less2);
-        }
-        if (grows) {
-          const float less = ex2_below(m_before, m);
-          by *= less, l *= less;
-        }
-        tmem_st32(s_at, w);   // over the first half of the scores
         if (any && __any_sync(0xffffffffu, by != 1.f)) {
           // (These scores come after the sums before them in the issuer's
           // order: those are done.)
           const f32x2 by2 = pair_of(by, by);
 #pragma unroll
-          for (int e = 0; e < kHalf / 32; ++e) {
+          for (int e = 0; e < D / 32; ++e) {
             uint32_t o[32];
             tmem_ld32(o_at + 32 * e, o);
             tmem_ld_wait();
@@ -853,20 +845,19 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
             tmem_st32(o_at + 32 * e, o);
           }
         }
-        any = true;
-        l += sum;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kPFull + t));
+        float s0, s1, s2, s3;
+        halves(add2(sums[0], sums[1]), s0, s1);
+        halves(add2(sums[2], sums[3]), s2, s3);
+        l += (s0 + s1) + (s2 + s3);
+        any = true;
       }
       if (!ok) break;
       n_step += it.to - it.from;
-      // ---- the rows' results: a thread has half of the columns
-      post(l);
-      float l_other;
-      if (!__all_sync(0xffffffffu, fetch(peek(), l_other))) break;
-      l += l_other;
+      // ---- the rows' results
       if (any) {
         if (!mbar_wait(bar(kOFull + t), outs & 1u, abort_flag, kWaitNs)) break;
         ++outs;
@@ -874,21 +865,21 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       }
       const int64_t out = it.row + token;
       const int head = it.h * p.group + row % p.group;
-      auto finish = [&](const uint32_t (&w)[kHalf / 2], float top, float sum) {
-        uint4* const to = reinterpret_cast<uint4*>(p.o[it.r] + out * p.ld_o + head * D + half * kHalf);
+      auto finish = [&](const uint32_t (&w)[D / 2], float top, float sum) {
+        uint4* const to = reinterpret_cast<uint4*>(p.o[it.r] + out * p.ld_o + head * D);
 #pragma unroll
-        for (int e = 0; e < kHalf / 8; ++e) to[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-        if (p.lse[it.r] && half == 0) p.lse[it.r][out * p.heads_q + head] = lse_of(top, sum);
+        for (int e = 0; e < D / 8; ++e) to[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        if (p.lse[it.r]) p.lse[it.r][out * p.heads_q + head] = lse_of(top, sum);
       };
-      uint32_t w[kHalf / 2];
+      uint32_t w[D / 2];
       if (it.parts == 1) {
         const bool none = m == -INFINITY && l == 0.f;   // (O holds nothing then, or zeros)
         const float by = E8 ? sigma / l : 1.f / l;
 #pragma unroll
-        for (int e = 0; e < kHalf / 2; ++e) w[e] = 0u;
+        for (int e = 0; e < D / 2; ++e) w[e] = 0u;
         if (any) {
 #pragma unroll
-          for (int e = 0; e < kHalf / 32; ++e) {
+          for (int e = 0; e < D / 32; ++e) {
             uint32_t o[32];
             tmem_ld32(o_at + 32 * e, o);
             tmem_ld_wait();
@@ -904,20 +895,19 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         if (real) finish(w, m, l);
         continue;
       }
-      // A part: four columns of all rows side by side, then both threads'
-      // maxima and sums.
+      // A part: four columns of all rows side by side, then maxima and sums.
       const int place = t * kTile + row, rows = p.slot_rows;
-      auto part_of = [&](int i) { return p.part + (int64_t)(it.slot + i) * rows * (D + 4); };
-      const int stat = (D + 2 * half) * rows + place;
+      auto part_of = [&](int i) { return p.part + (int64_t)(it.slot + i) * rows * (D + 2); };
+      const int stat = D * rows + place;
       if (any) {
-        float4* const to = reinterpret_cast<float4*>(part_of(it.part)) + half * (kHalf / 4) * rows + place;
+        float4* const to = reinterpret_cast<float4*>(part_of(it.part)) + place;
+        const float by = E8 ? sigma : 1.f;
 #pragma unroll
-        for (int e = 0; e < kHalf / 32; ++e) {
+        for (int e = 0; e < D / 32; ++e) {
           uint32_t o[32];
           tmem_ld32(o_at + 32 * e, o);
           tmem_ld_wait();
           reg_fence(o);
-          const float by = E8 ? sigma : 1.f;
           if (real)
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
@@ -931,7 +921,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       if (real) part_of(it.part)[stat] = m, part_of(it.part)[stat + rows] = l;
       __threadfence();
       __syncwarp();
-      uint32_t* const counter = p.arrived + (int64_t)it.slot * 16 + sw;
+      uint32_t* const counter = p.arrived + (int64_t)it.slot * 8 + (warp - 4);
       uint32_t came = 0;
       if (lane == 0) {
         came = atom_add_acq_rel_u32(counter, 1u);
@@ -946,7 +936,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         for (int i = 0; i < it.parts; ++i) total += ex2_below(__ldcg(part_of(i) + stat), top) * __ldcg(part_of(i) + stat + rows);
         const float inv = top == -INFINITY && total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
-        for (int e = 0; e < kHalf / 32; ++e) {
+        for (int e = 0; e < D / 32; ++e) {
           float acc[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) acc[k] = 0.f;
@@ -954,7 +944,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
             const float mi = __ldcg(part_of(i) + stat), li = __ldcg(part_of(i) + stat + rows);
             if (mi == -INFINITY && li == 0.f) continue;   // (nothing was written)
             const float f = ex2_below(mi, top) * inv;
-            const float4* const from = reinterpret_cast<const float4*>(part_of(i)) + (half * (kHalf / 4) + 8 * e) * rows + place;
+            const float4* const from = reinterpret_cast<const float4*>(part_of(i)) + 8 * e * rows + place;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const float4 u = __ldcg(from + k * rows);
@@ -1045,7 +1035,7 @@ struct PromptPlaces {
     before = kScratchAt;
     items = before + up((size_t)(seqs + 1) * 8);
     part = items + up((size_t)most_items * sizeof(Record));
-    bytes = part + (size_t)kMostParts * slot_rows * (d->head_dim + 4) * 4;
+    bytes = part + (size_t)kMostParts * slot_rows * (d->head_dim + 2) * 4;
   }
 };
 }  // namespace

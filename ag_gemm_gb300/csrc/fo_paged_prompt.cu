@@ -166,8 +166,14 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const __grid_constant
   }
   // A thread's run of pairs, from the last on; a visit to each.
   const long long run = (pairs + 1023) / 1024, first = min(tid * run, pairs), last = min(first + run, pairs);   // (of pairs)
+  Record own;
+  int own_n = -1;   // of a run of one, which is looked at once
   auto visit = [&](auto&& f) {
     if (first >= last) return;
+    if (own_n >= 0) {
+      f(own, own_n);
+      return;
+    }
     int lo = 0, hi = p.batch.seqs;   // before[lo] <= pair < before[hi]
     const long long start = pairs - 1 - first;
     while (hi - lo > 1) {
@@ -184,6 +190,7 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const __grid_constant
       it.b = lo, it.row = s.row, it.n = s.n, it.base = s.base;
       it.token = (int)(pair - p.before[lo]) * each;
       st.of(it, p.tokens, p.window, p.sinks);
+      if (run == 1) own = it, own_n = st.n;
       f(it, st.n);
     }
   };
@@ -234,7 +241,10 @@ struct Prompt {
   static constexpr int kOffScale = kOffRaw + kRaws * kRawBytes;
   static constexpr int kOffRow = kOffScale + (E8 ? kScaleSlots * 8 * 4 : 0);   // the rows' factors, two items
   static constexpr int kOffItem = kOffRow + (E8 ? 2 * 2 * kTile * 4 : 0);
-  static constexpr int kOffBar = kOffItem + 2 * 48;
+  // The rows' results on their way out: 32 rows of a warp, so many bytes each.
+  static constexpr int kOutBytes = E8 && D == 128 ? 32 : 128;
+  static constexpr int kOffOut = (kOffItem + 2 * 48 + 127) / 128 * 128;
+  static constexpr int kOffBar = kOffOut + 8 * 32 * kOutBytes;
   static constexpr int kBars = 3 * kStages + 2 * kRaws + 26;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kSmem = 1024 + kOffMisc + 16;
@@ -621,7 +631,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
           const int row = tid;
           const uint32_t at = base + t * C::kTileBytes + row * 128;
           float top = 0.f;
-#pragma unroll 4
+#pragma unroll 8
           for (int k = 0; k < D / 8; ++k) {
             float f[8];
             Vec16<__nv_bfloat16>::unpack(lds128(at + (k >> 3) * (kTile * 128) + (((k & 7) ^ (row & 7)) << 4)), f);
@@ -630,7 +640,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
           const uint32_t exponent = min(max(__float_as_uint(top) >> 23, 8u), 254u);
           const float by = top <= 3.4e38f ? __uint_as_float((261u - exponent) << 23) : 1.f;
           reinterpret_cast<float*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + row] = 1.f / by;
-#pragma unroll 4
+#pragma unroll 8
           for (int k = 0; k < D / 8; ++k) {
             const uint32_t a = at + (k >> 3) * (kTile * 128) + (((k & 7) ^ (row & 7)) << 4);
             float f[8];
@@ -756,6 +766,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
           for (int e = 0; e < 4; ++e) {
             const int at = key + 32 * e;
             const uint32_t seen = low_bits(pos + 1 - at) & (~low_bits(lo - at) | low_bits(p.sinks - at));
+            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
 #pragma unroll
             for (int k = 0; k < 32; ++k)
               if (!(seen >> k & 1u)) v[e][k] = 0xff800000u;   // -infinity
@@ -797,15 +808,15 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         // Weights, over the scores' first 64 columns (the row's scores are in
         // registers), and their sum.
         const float down = m == -INFINITY ? 0.f : -m;
-        const f32x2 down2 = pair_of(down, down);
-        f32x2 sums[4] = {0ull, 0ull, 0ull, 0ull};
+        float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const f32x2 factor2 = pair_of(factor[e], factor[e]);
           // In 8 bits what multiplies a value is its weight times its 32's
-          // power of two over sigma; the sum is of the weights alone.
-          const float more = E8 ? pow2[4 + e] / sigma : 1.f;
-          const f32x2 more2 = pair_of(more, more);
+          // power of two over sigma, which goes into the exponent; the sum is
+          // of the weights alone. (Below 2^-60 nothing is left of them in f16.)
+          const int lift = E8 ? max((int)(__float_as_uint(pow2[4 + e]) >> 23) - (int)(__float_as_uint(sigma) >> 23), -60) : 0;
+          const f32x2 factor2 = pair_of(factor[e], factor[e]), down2 = pair_of(down + (float)lift, down + (float)lift);
+          f32x2 sums[2] = {0ull, 0ull};
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
@@ -814,17 +825,15 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
             halves(fma2(pair_of(v[e][k + 2], v[e][k + 3]), factor2, down2), f[2], f[3]);
 #pragma unroll
             for (int a = 0; a < 4; ++a) f[a] = ex2(f[a]);
-            sums[(k >> 1) & 2] = add2(sums[(k >> 1) & 2], pair_of(f[0], f[1]));
-            sums[((k >> 1) & 2) + 1] = add2(sums[((k >> 1) & 2) + 1], pair_of(f[2], f[3]));
-            if constexpr (E8) {
-              halves(mul2(pair_of(f[0], f[1]), more2), f[0], f[1]);
-              halves(mul2(pair_of(f[2], f[3]), more2), f[2], f[3]);
-              w[k / 2] = f16x2(f[0], f[1]), w[k / 2 + 1] = f16x2(f[2], f[3]);
-            } else {
-              w[k / 2] = bf16x2(f[0], f[1]), w[k / 2 + 1] = bf16x2(f[2], f[3]);
-            }
+            sums[0] = add2(sums[0], pair_of(f[0], f[1]));
+            sums[1] = add2(sums[1], pair_of(f[2], f[3]));
+            w[k / 2] = E8 ? f16x2(f[0], f[1]) : bf16x2(f[0], f[1]);
+            w[k / 2 + 1] = E8 ? f16x2(f[2], f[3]) : bf16x2(f[2], f[3]);
           }
           tmem_st16(s_at + 16 * e, w);
+          float s0, s1;
+          halves(add2(sums[0], sums[1]), s0, s1);
+          sum = E8 ? fmaf(s0 + s1, __uint_as_float((uint32_t)(127 - lift) << 23), sum) : sum + (s0 + s1);
         }
         if (any && __any_sync(0xffffffffu, by != 1.f)) {
           // (These scores come after the sums before them in the issuer's
@@ -849,10 +858,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kPFull + t));
-        float s0, s1, s2, s3;
-        halves(add2(sums[0], sums[1]), s0, s1);
-        halves(add2(sums[2], sums[3]), s2, s3);
-        l += (s0 + s1) + (s2 + s3);
+        l += sum;
         any = true;
       }
       if (!ok) break;
@@ -865,11 +871,31 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       }
       const int64_t out = it.row + token;
       const int head = it.h * p.group + row % p.group;
+      // A warp's rows into global memory, through shared memory: a thread's own
+      // row would be 16 bytes of each of 32 rows an access (which took an
+      // item's end 5000 cycles).
+      const long long mine_at = real ? out * p.ld_o + head * D : -1;
       auto finish = [&](const uint32_t (&w)[D / 2], float top, float sum) {
-        uint4* const to = reinterpret_cast<uint4*>(p.o[it.r] + out * p.ld_o + head * D);
+        constexpr int kPieces = C::kOutBytes / 16;
+        const uint32_t buf = base + C::kOffOut + (warp - 4) * 32 * C::kOutBytes;
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) to[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-        if (p.lse[it.r]) p.lse[it.r][out * p.heads_q + head] = lse_of(top, sum);
+        for (int e = 0; e < D * 2 / C::kOutBytes; ++e) {
+#pragma unroll
+          for (int k = 0; k < kPieces; ++k) {
+            const uint32_t* const u = &w[(e * kPieces + k) * 4];
+            sts128(buf + lane * C::kOutBytes + ((k ^ (lane & (kPieces - 1))) << 4), make_uint4(u[0], u[1], u[2], u[3]));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < kPieces; ++k) {
+            const int r = k * (32 / kPieces) + lane / kPieces, piece = lane & (kPieces - 1);
+            const long long at = __shfl_sync(0xffffffffu, mine_at, r);
+            const uint4 u = lds128(buf + r * C::kOutBytes + ((piece ^ (r & (kPieces - 1))) << 4));
+            if (at >= 0) *reinterpret_cast<uint4*>(p.o[it.r] + at + e * (C::kOutBytes / 2) + piece * 8) = u;
+          }
+          __syncwarp();
+        }
+        if (real && p.lse[it.r]) p.lse[it.r][out * p.heads_q + head] = lse_of(top, sum);
       };
       uint32_t w[D / 2];
       if (it.parts == 1) {
@@ -892,7 +918,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kOFree + t));
         }
-        if (real) finish(w, m, l);
+        finish(w, m, l);
         continue;
       }
       // A part: four columns of all rows side by side, then maxima and sums.
@@ -929,9 +955,11 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       }
       if (__shfl_sync(0xffffffffu, came, 0) != (uint32_t)it.parts - 1u) continue;
       __threadfence();
+      // The last of the parts' warps of these rows joins them, in their order.
+      float top = -INFINITY, total = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 2; ++e) w[e] = 0u;
       if (real) {
-        // The last of the parts' warps of these rows joins them, in their order.
-        float top = -INFINITY, total = 0.f;
         for (int i = 0; i < it.parts; ++i) top = fmaxf(top, __ldcg(part_of(i) + stat));
         for (int i = 0; i < it.parts; ++i) total += ex2_below(__ldcg(part_of(i) + stat), top) * __ldcg(part_of(i) + stat + rows);
         const float inv = top == -INFINITY && total == 0.f ? 0.f : 1.f / total;
@@ -955,8 +983,8 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
 #pragma unroll
           for (int k = 0; k < 16; ++k) w[16 * e + k] = bf16x2(acc[2 * k], acc[2 * k + 1]);
         }
-        finish(w, top, total);
       }
+      finish(w, top, total);
     }
   }
 

@@ -239,12 +239,10 @@ struct Prompt {
   static constexpr int kOffRing = 2 * kTileBytes;    // after the two tiles of queries
   static constexpr int kOffRaw = kOffRing + kStages * kTileBytes;
   static constexpr int kOffScale = kOffRaw + kRaws * kRawBytes;
-  static constexpr int kOffRow = kOffScale + (E8 ? kScaleSlots * 8 * 4 : 0);   // the rows' factors, two items
-  static constexpr int kOffItem = kOffRow + (E8 ? 2 * 2 * kTile * 4 : 0);
-  // The rows' results on their way out: 32 rows of a warp, so many bytes each.
-  static constexpr int kOutBytes = E8 && D == 128 ? 32 : 128;
-  static constexpr int kOffOut = (kOffItem + 2 * 48 + 127) / 128 * 128;
-  static constexpr int kOffBar = kOffOut + 8 * 32 * kOutBytes;
+  static constexpr int kOffRow = kOffScale + (E8 ? kScaleSlots * 8 * 4 : 0);   // the rows' factors (bf16: powers of two), two items
+  static constexpr int kOffItem = kOffRow + (E8 ? 2 * 2 * kTile * 2 : 0);
+  static constexpr int kOffOut = (kOffItem + 2 * 48 + 127) / 128 * 128;   // results on their way out: a warp's 32 rows x 64 bytes
+  static constexpr int kOffBar = kOffOut + 8 * 2048;
   static constexpr int kBars = 3 * kStages + 2 * kRaws + 26;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kSmem = 1024 + kOffMisc + 16;
@@ -639,7 +637,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
           }
           const uint32_t exponent = min(max(__float_as_uint(top) >> 23, 8u), 254u);
           const float by = top <= 3.4e38f ? __uint_as_float((261u - exponent) << 23) : 1.f;
-          reinterpret_cast<float*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + row] = 1.f / by;
+          reinterpret_cast<__nv_bfloat16*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + row] = __float2bfloat16_rn(1.f / by);
 #pragma unroll 8
           for (int k = 0; k < D / 8; ++k) {
             const uint32_t a = at + (k >> 3) * (kTile * 128) + (((k & 7) ^ (row & 7)) << 4);
@@ -754,7 +752,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         // that their values, are still to be multiplied with.
         const float* const pow2 = reinterpret_cast<const float*>(gbase + C::kOffScale) + ((n_step + i - it.from) % kScaleSlots) * 8;
         if constexpr (E8)
-          if (!any) row_factor = p.scale_log2 * reinterpret_cast<const float*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + row];
+          if (!any) row_factor = p.scale_log2 * to_f(reinterpret_cast<const __nv_bfloat16*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + row]);
         float factor[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) factor[e] = E8 ? row_factor * pow2[e] : row_factor;
@@ -871,54 +869,48 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       }
       const int64_t out = it.row + token;
       const int head = it.h * p.group + row % p.group;
-      // A warp's rows into global memory, through shared memory: a thread's own
-      // row would be 16 bytes of each of 32 rows an access (which took an
-      // item's end 5000 cycles).
+      // Half a line of a row (32 columns) at a time, into global memory by way of
+      // shared memory: a thread's own row would be 16 bytes of each of 32 rows
+      // an access. The loops over columns stay loops: code that runs once an
+      // item is fetched each time.
       const long long mine_at = real ? out * p.ld_o + head * D : -1;
-      auto finish = [&](const uint32_t (&w)[D / 2], float top, float sum) {
-        constexpr int kPieces = C::kOutBytes / 16;
-        const uint32_t buf = base + C::kOffOut + (warp - 4) * 32 * C::kOutBytes;
+      auto store = [&](int e, const uint32_t (&w)[16]) {
+        const uint32_t buf = base + C::kOffOut + (warp - 4) * 2048;
 #pragma unroll
-        for (int e = 0; e < D * 2 / C::kOutBytes; ++e) {
+        for (int k = 0; k < 4; ++k) sts128(buf + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+        __syncwarp();
 #pragma unroll
-          for (int k = 0; k < kPieces; ++k) {
-            const uint32_t* const u = &w[(e * kPieces + k) * 4];
-            sts128(buf + lane * C::kOutBytes + ((k ^ (lane & (kPieces - 1))) << 4), make_uint4(u[0], u[1], u[2], u[3]));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < kPieces; ++k) {
-            const int r = k * (32 / kPieces) + lane / kPieces, piece = lane & (kPieces - 1);
-            const long long at = __shfl_sync(0xffffffffu, mine_at, r);
-            const uint4 u = lds128(buf + r * C::kOutBytes + ((piece ^ (r & (kPieces - 1))) << 4));
-            if (at >= 0) *reinterpret_cast<uint4*>(p.o[it.r] + at + e * (C::kOutBytes / 2) + piece * 8) = u;
-          }
-          __syncwarp();
+        for (int k = 0; k < 4; ++k) {
+          const int r = k * 8 + (lane >> 2), piece = lane & 3;
+          const long long at = __shfl_sync(0xffffffffu, mine_at, r);
+          const uint4 u = lds128(buf + r * 64 + ((piece ^ (r >> 1 & 3)) << 4));
+          if (at >= 0) *reinterpret_cast<uint4*>(p.o[it.r] + at + e * 32 + piece * 8) = u;
         }
-        if (real && p.lse[it.r]) p.lse[it.r][out * p.heads_q + head] = lse_of(top, sum);
+        __syncwarp();
       };
-      uint32_t w[D / 2];
       if (it.parts == 1) {
         const bool none = m == -INFINITY && l == 0.f;   // (O holds nothing then, or zeros)
         const float by = E8 ? sigma / l : 1.f / l;
+#pragma unroll 1
+        for (int e = 0; e < D / 32; ++e) {
+          uint32_t o[32], w[16];
 #pragma unroll
-        for (int e = 0; e < D / 2; ++e) w[e] = 0u;
-        if (any) {
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) {
-            uint32_t o[32];
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
+          if (any) {
             tmem_ld32(o_at + 32 * e, o);
             tmem_ld_wait();
             reg_fence(o);
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              w[16 * e + k] = none ? 0u : bf16x2(__uint_as_float(o[2 * k]) * by, __uint_as_float(o[2 * k + 1]) * by);
           }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = none ? 0u : bf16x2(__uint_as_float(o[2 * k]) * by, __uint_as_float(o[2 * k + 1]) * by);
+          store(e, w);
+        }
+        if (any) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kOFree + t));
         }
-        finish(w, m, l);
+        if (real && p.lse[it.r]) p.lse[it.r][out * p.heads_q + head] = lse_of(m, l);
         continue;
       }
       // A part: four columns of all rows side by side, then maxima and sums.
@@ -928,7 +920,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       if (any) {
         float4* const to = reinterpret_cast<float4*>(part_of(it.part)) + place;
         const float by = E8 ? sigma : 1.f;
-#pragma unroll
+#pragma unroll 1
         for (int e = 0; e < D / 32; ++e) {
           uint32_t o[32];
           tmem_ld32(o_at + 32 * e, o);
@@ -957,34 +949,35 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       __threadfence();
       // The last of the parts' warps of these rows joins them, in their order.
       float top = -INFINITY, total = 0.f;
-#pragma unroll
-      for (int e = 0; e < D / 2; ++e) w[e] = 0u;
       if (real) {
         for (int i = 0; i < it.parts; ++i) top = fmaxf(top, __ldcg(part_of(i) + stat));
         for (int i = 0; i < it.parts; ++i) total += ex2_below(__ldcg(part_of(i) + stat), top) * __ldcg(part_of(i) + stat + rows);
-        const float inv = top == -INFINITY && total == 0.f ? 0.f : 1.f / total;
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-          float acc[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) acc[k] = 0.f;
-          for (int i = 0; i < it.parts; ++i) {
-            const float mi = __ldcg(part_of(i) + stat), li = __ldcg(part_of(i) + stat + rows);
-            if (mi == -INFINITY && li == 0.f) continue;   // (nothing was written)
-            const float f = ex2_below(mi, top) * inv;
-            const float4* const from = reinterpret_cast<const float4*>(part_of(i)) + 8 * e * rows + place;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 u = __ldcg(from + k * rows);
-              acc[4 * k] = fmaf(f, u.x, acc[4 * k]), acc[4 * k + 1] = fmaf(f, u.y, acc[4 * k + 1]);
-              acc[4 * k + 2] = fmaf(f, u.z, acc[4 * k + 2]), acc[4 * k + 3] = fmaf(f, u.w, acc[4 * k + 3]);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 16; ++k) w[16 * e + k] = bf16x2(acc[2 * k], acc[2 * k + 1]);
-        }
       }
-      finish(w, top, total);
+      const float inv = top == -INFINITY && total == 0.f ? 0.f : 1.f / total;
+#pragma unroll 1
+      for (int e = 0; e < D / 32; ++e) {
+        float acc[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+        for (int i = 0; real && i < it.parts; ++i) {
+          const float mi = __ldcg(part_of(i) + stat), li = __ldcg(part_of(i) + stat + rows);
+          if (mi == -INFINITY && li == 0.f) continue;   // (nothing was written)
+          const float f = ex2_below(mi, top) * inv;
+          const float4* const from = reinterpret_cast<const float4*>(part_of(i)) + 8 * e * rows + place;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 u = __ldcg(from + k * rows);
+            acc[4 * k] = fmaf(f, u.x, acc[4 * k]), acc[4 * k + 1] = fmaf(f, u.y, acc[4 * k + 1]);
+            acc[4 * k + 2] = fmaf(f, u.z, acc[4 * k + 2]), acc[4 * k + 3] = fmaf(f, u.w, acc[4 * k + 3]);
+          }
+        }
+        __syncwarp();
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) w[k] = bf16x2(acc[2 * k], acc[2 * k + 1]);
+        store(e, w);
+      }
+      if (real && p.lse[it.r]) p.lse[it.r][out * p.heads_q + head] = lse_of(top, total);
     }
   }
 

@@ -28,8 +28,7 @@ LIB = os.path.join(BUILD, "libflashoverlap.so")
 
 SOURCES = ["fo_plan.cpp", "fo_api.cu", "fo_kern_rs.cu", "fo_kern_dp.cu", "fo_kern_ag.cu", "fo_kern_part.cu",
            "fo_noalloc.cu", "fo_attn.cu", "fo_norm.cu", "fo_quant.cu", "fo_rope.cu", "fo_gemm_fp8.cu",
-           "fo_kv_append.cu", "fo_paged_attn.cu", "fo_paged_few64.cu", "fo_paged_few128.cu",
-           "fo_paged_prompt.cu"]
+           "fo_kv_append.cu", "fo_paged_attn.cu", "fo_paged_few.cu", "fo_paged_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -77,12 +77,12 @@ fo_status check_paged(const fo_paged_desc* d);
 fo_status check_batch(const fo_paged_desc* d, const fo_paged_batch* b, int64_t rows);
 Batch batch_of(const fo_paged_desc* d, const fo_paged_batch* b, int64_t rows, void* ws);
 
-// Workspace: header and deal (256 bytes), then the counters of both kernels,
-// zero between calls, then scratch that the one and the other use.
+// Workspace: header and deal (256 bytes), then the counters of few tokens'
+// kernel, zero between calls, then scratch that either kind of call uses.
 constexpr int kFewThreads = 256, kFewBlocks = 2;   // blocks an SM
 constexpr int kMostParts = 4 * FO_GB300_SMS;       // of the prompts' kernel
 constexpr size_t kFewCountBytes = (kFewBlocks * FO_GB300_SMS * 3 * 4 + 255) / 256 * 256;
-constexpr size_t kScratchAt = 256 + kFewCountBytes + (size_t)kMostParts * 8 * 4;
+constexpr size_t kScratchAt = 256 + kFewCountBytes;
 
 // A checked call of fo_paged_attention.
 struct PagedCall {
@@ -98,11 +98,8 @@ struct PagedCall {
   float scale_log2;
   int sms;
 };
-// Few new tokens a sequence (fo_paged_few.cuh), `eights` times 8 rows (1, 2, 4
-// or 8) of a key head: kFewBlocks blocks an SM.
-// Keys of a tile: 32 for each warp that has keys of its own, 64 in 8 bits or
-// where warps share keys.
-constexpr int few_step(int eights, bool eight) { return (eights <= 2 ? 4 : eights == 4 ? 2 : 1) * (eight || eights > 2 ? 64 : 32); }
+// Few new tokens a sequence (fo_paged_few.cu): up to 8 or 16 rows of a key head.
+constexpr int few_keys(bool eight) { return eight ? 64 : 32; }   // of a warp's, of a tile
 struct FewParams {
   CUtensorMap k[kMaxR];   // [pages * heads_k][page][D]; boxes of 128 bytes x `box` tokens
   CUtensorMap v[kMaxR];
@@ -118,15 +115,14 @@ struct FewParams {
   int32_t boxes_log2;     // of a tile
   int32_t least;          // tiles of a piece, at least
   float scale_log2;
-  float* part;            // [blocks][2][8 eights * (D + 2)]
+  float* part;            // [blocks][2][8 or 16 * (D + 2)]
   uint32_t* count;        // [blocks][3], zero between calls
 };
 
-fo_status attend_few_64(FewParams& k, int eights, bool eight, int sms, cudaStream_t s);
-fo_status attend_few_128(FewParams& k, int eights, bool eight, int sms, cudaStream_t s);
+fo_status attend_few(FewParams& k, int D, bool wide, bool eight, int sms, cudaStream_t s);   // wide: more than 8 rows
 // Many new tokens a sequence (fo_paged_prompt.cu).
 fo_status attend_prompts(const PagedCall& c, cudaStream_t s);
-size_t prompt_bytes(const fo_paged_desc* d, int32_t seqs, int64_t rows, int32_t max_new);
+size_t prompt_bytes(const fo_paged_desc* d, int32_t seqs, int64_t rows);
 // Tensor maps (fo_paged_prompt.cu): pages of keys or values as [pages *
 // heads_k][page][D], in boxes of at most 128 bytes x `box` tokens, swizzled by
 // their own width; bf16 rows as [rows][heads][D], in boxes of 64 x heads x rows.

@@ -1,5 +1,5 @@
 // Attention of a batch's new tokens over a paged cache of keys and values: the
-// calls. The kernels are in fo_paged_few.cuh and fo_paged_prompt.cu.
+// calls. The kernels are in fo_paged_few.cu and fo_paged_prompt.cu.
 #include <math.h>
 #include <string.h>
 
@@ -11,11 +11,14 @@ namespace fo_ops {
 namespace {
 
 // Rows of a key head (new tokens x heads of its group) that the split kernel
-// takes; more are the prompts' kernel's, whose tiles have 128.
-constexpr int kFewRows = 64;
-int eights_of(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8; }
-size_t few_bytes(const fo_paged_desc* d, int64_t rows) {
-  return kScratchAt + (size_t)kFewBlocks * FO_GB300_SMS * 2 * 8 * eights_of(rows) * (d->head_dim + 2) * 4;
+// takes. More are the prompts' kernel's, whose tiles have 128: 17 contexts of
+// up to 4100 on two ranks with 24, 40 and 64 rows take it 40, 43 and 44 us, and
+// took the split kernel (with two and four warps to a warp's keys) 53, 73 and
+// 89. With 16 rows the split kernel takes 37 us, the prompts' 45; over 64
+// contexts of up to 8192, 79 and 112.
+constexpr int kFewRows = 16;
+size_t few_bytes(const fo_paged_desc* d) {
+  return kScratchAt + (size_t)kFewBlocks * FO_GB300_SMS * 2 * kFewRows * (d->head_dim + 2) * 4;
 }
 
 }  // namespace
@@ -27,9 +30,8 @@ extern "C" fo_status fo_paged_attention_workspace(const fo_paged_desc* d, int32_
   if (st) return st;
   if (!bytes) return FO_ERR_INVALID_ARG;
   if (seqs < 0 || rows < 0 || rows > INT32_MAX || max_new < 1) return FO_ERR_SHAPE;
-  const int64_t most = (int64_t)max_new * (d->heads_q / d->heads_k);
-  *bytes = fo_ops::few_bytes(d, most < fo_ops::kFewRows ? most : fo_ops::kFewRows);
-  if (most > fo_ops::kFewRows) *bytes = std::max(*bytes, fo_ops::prompt_bytes(d, seqs, rows, max_new));
+  const bool prompts = (int64_t)max_new * (d->heads_q / d->heads_k) > fo_ops::kFewRows;
+  *bytes = prompts ? std::max(fo_ops::few_bytes(d), fo_ops::prompt_bytes(d, seqs, rows)) : fo_ops::few_bytes(d);
   return FO_OK;
 }
 
@@ -65,7 +67,7 @@ extern "C" fo_status fo_paged_attention(const fo_paged_desc* d, const fo_paged_b
   if (unit_rows <= kFewRows) {
     FewParams f;
     memset(static_cast<void*>(&f), 0, sizeof(f));
-    const int eights = eights_of(unit_rows), step = few_step(eights, eight);
+    const int step = 4 * few_keys(eight);
     f.box = std::min(d->page, step);
     for (f.boxes_log2 = 0; f.box << f.boxes_log2 < step; ++f.boxes_log2) {
     }
@@ -90,7 +92,7 @@ extern "C" fo_status fo_paged_attention(const fo_paged_desc* d, const fo_paged_b
     f.scale_log2 = scale * 1.4426950408889634f;
     f.count = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + 256);
     f.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kScratchAt);
-    return (d->head_dim == 128 ? attend_few_128 : attend_few_64)(f, eights, eight, sms, (cudaStream_t)stream);
+    return attend_few(f, d->head_dim, unit_rows > 8, eight, sms, (cudaStream_t)stream);
   }
   PagedCall c;
   c.d = d, c.b = b, c.rows = rows, c.ld = ld;

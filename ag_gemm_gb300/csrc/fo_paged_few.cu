@@ -4,7 +4,7 @@
 // Reading the visible keys and values once is what a call cannot do without:
 // 4 D flops for 4 D bytes (bf16), times the query heads that share a key head.
 // So a unit of work is a sequence's key head with all rows (new tokens x heads
-// of the group) that read it, up to 64 of them. Keys are the rows of the
+// of the group) that read it, up to 16 of them. Keys are the rows of the
 // products and a unit's rows their columns, eight at a time:
 //     S^T [16 keys x 8 rows] = K Q^T,   O^T [16 of D x 8 rows] += V^T P^T
 // (mma.sync m16n8k16; tcgen05's 128 x 8 at least would have every tile's
@@ -21,17 +21,14 @@
 // replayed with other ones. In a block, one warp has TMA bring the tiles into a
 // ring, running ahead over units and sequences (when each warp loaded for
 // itself, two thirds of the instructions were that); each of four others takes
-// 32 or 64 keys of a tile (with more than 16 rows, two or four share the keys
-// and part the rows) and keeps its own maximum, sum and output in registers. At
-// a unit's end, or the piece's, the warps' parts are joined through shared
-// memory. A unit cut between blocks is joined by the last of them to arrive,
+// 32 or 64 keys of a tile and keeps its own maximum, sum and output in
+// registers. At a unit's end, or the piece's, the warps' parts are joined through
+// shared memory. A unit cut between blocks is joined by the last of them to arrive,
 // the parts in the blocks' order (16 at a time), so results repeat.
 //
 // An 8-bit cache's e4m3 values become f16, which holds them exactly; queries
 // and weights are f16 then, the queries' rows times powers of two, the weights
 // times their values' scales over a running power of two.
-#pragma once
-
 #include <math.h>
 
 #include <algorithm>
@@ -46,18 +43,16 @@ using namespace fo;
 
 constexpr int kRadix = 16;             // parts joined at a time
 
-template <int D, bool E8, int NT, int RG>
+template <int D, bool E8, int NT>
 struct Few {
-  static constexpr int kGroups = 4 / RG;                    // warps with keys of their own
-  static constexpr int kStep = few_step(NT * RG, E8);       // keys of a tile
-  static constexpr int kKeys = kStep / kGroups;             // of a warp
+  static constexpr int kKeys = few_keys(E8), kStep = 4 * kKeys;   // keys of a tile: of a warp, of all
   static constexpr int kM = kKeys / 16;
   static constexpr int kRow = D * (E8 ? 1 : 2);             // bytes of a key
   static constexpr int kWidth = kRow < 128 ? kRow : 128;    // of a box
   static constexpr int kCuts = kRow / kWidth;
   static constexpr int kSlot = kStep * kRow;                // a tile's keys, or its values
   static constexpr int kSlots = 98304 / kSlot;
-  static constexpr int kRows = 8 * NT * RG;
+  static constexpr int kRows = 8 * NT;
   static constexpr int kPart = kRows * (D + 2);             // floats of a part: output, maxima, sums
   // Shared memory: ring, scales, rows being joined (four of a warp at a time,
   // apart so that a warp's columns meet no bank twice), (m, l) of each warp,
@@ -65,7 +60,7 @@ struct Few {
   static constexpr int kOffScale = kSlots * kSlot;
   static constexpr int kApart = D + 8;
   static constexpr int kOffJoin = kOffScale + (E8 ? kSlots * kStep * 4 : 0);
-  static constexpr int kOffStat = kOffJoin + (RG == 4 ? 4 : 4 - RG) * 4 * kApart * 4;
+  static constexpr int kOffStat = kOffJoin + 3 * 4 * kApart * 4;
   static constexpr int kOffBar = kOffStat + 4 * 8 * NT * 8;
   static constexpr int kOffMisc = kOffBar + 2 * kSlots * 8;
   static constexpr int kSmem = 1024 + kOffMisc + 64;
@@ -110,9 +105,9 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {   // 8 x 8 of 16 bi
   return d;
 }
 
-template <int D, bool E8, int NT, int RG>
+template <int D, bool E8, int NT>
 __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __grid_constant__ FewParams p) {
-  using C = Few<D, E8, NT, RG>;
+  using C = Few<D, E8, NT>;
   constexpr int kKeys = C::kKeys, kM = C::kM;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -241,7 +236,6 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
     return;
   }
   asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  const int kg = warp / RG, rg = warp % RG;
   int cslot = 0, cround = 0;
   // The slot that has been read is free again.
   auto done = [&]() {
@@ -265,7 +259,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
     float qscale[NT][2];                // with what their scores are to be multiplied
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int rho = (rg * NT + i) * 8 + g, token = rho / p.group, head = rho - token * p.group;
+      const int rho = i * 8 + g, token = rho / p.group, head = rho - token * p.group;
       const bool is = rho < real;
       const __nv_bfloat16* const q = p.q[r] + (long long)(is ? s.row + token : 0) * p.ld_q + (h * p.group + head) * D;
       float mine = p.scale_log2;
@@ -306,7 +300,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
       }
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        const int mine_rho = (rg * NT + i) * 8 + 2 * c + a;
+        const int mine_rho = i * 8 + 2 * c + a;
         pos[i][a] = mine_rho < real ? s.base + mine_rho / p.group : -1;
         lo[i][a] = sight_of(max(pos[i][a], 0), p.window, p.sinks).lo;
         qscale[i][a] = __shfl_sync(0xffffffffu, mine, (2 * c + a) * 4);
@@ -320,11 +314,11 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
     }
-    const uint32_t scales = base + C::kOffScale + kg * kKeys * 4;
+    const uint32_t scales = base + C::kOffScale + warp * kKeys * 4;
     const int lo_last = sight_of(max(s.base + s.n - 1, 0), p.window, p.sinks).lo;
 
     for (int n = 0; n < here; ++n, cw.t += n < here ? 1 : 0) {
-      const int key = cw.first_key() + kg * kKeys;
+      const int key = cw.first_key() + warp * kKeys;
       if (!cw.any(key, kKeys)) {   // (other warps' keys)
         for (int value = 0; value < 2; ++value) {
           mbar_wait(full + cslot * 8, cround & 1, abort_flag, kWaitNs);
@@ -341,7 +335,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
         for (int t = 0; t < NT; ++t) sc[i][t][0] = sc[i][t][1] = sc[i][t][2] = sc[i][t][3] = 0.f;
       mbar_wait(full + cslot * 8, cround & 1, abort_flag, kWaitNs);
       {
-        const uint32_t at = base + cslot * C::kSlot + kg * kKeys * C::kWidth;
+        const uint32_t at = base + cslot * C::kSlot + warp * kKeys * C::kWidth;
         if constexpr (!E8) {
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
@@ -485,7 +479,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
           }
         }
       {
-        const uint32_t at = base + cslot * C::kSlot + kg * kKeys * C::kWidth;
+        const uint32_t at = base + cslot * C::kSlot + warp * kKeys * C::kWidth;
         // Places that no row sees may hold NaN: their values count as zeros.
         auto seen = [&](int k) { return k < s.end && (k >= cw.lo || k < cw.sinks_end); };
 #pragma unroll
@@ -562,44 +556,44 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
     meet();
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      if (t > 0 && RG == 1 && real <= 8 * t) break;   // (no rows)
+      if (t > 0 && real <= 8 * t) break;   // (no rows)
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < C::kGroups; ++k) top = fmaxf(top, stat[((k * RG + rg) * NT + t) * 8 + 2 * c + a].x);
+        for (int k = 0; k < 4; ++k) top = fmaxf(top, stat[(k * NT + t) * 8 + 2 * c + a].x);
 #pragma unroll
-        for (int k = 0; k < C::kGroups; ++k) {
-          const float2 v = stat[((k * RG + rg) * NT + t) * 8 + 2 * c + a];
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = stat[(k * NT + t) * 8 + 2 * c + a];
           sum += ex2_below(v.x, top) * v.y;
         }
         const float by = ex2_below(m[t][a], top) * (E8 ? sigma : 1.f);
         // Where this thread's values of D lie.
         auto d_of = [&](int j, int e) { return E8 ? (D / 8) * g + 2 * j + e : 16 * j + 8 * e + g; };
         float* const buf = reinterpret_cast<float*>(gbase + C::kOffJoin);
-        if (kg > 0) {
-          float* const to = buf + ((kg - 1) * RG + rg) * 4 * C::kApart + c * C::kApart;
+        if (warp > 0) {
+          float* const to = buf + (warp - 1) * 4 * C::kApart + c * C::kApart;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) to[d_of(j, e)] = o[j][t][2 * e + a] * by;
         }
-        if (C::kGroups > 1) meet();
-        if (kg == 0) {
-          float* const mine = buf + rg * 4 * C::kApart;   // the first other warp's, or (of its own) nobody else's
+        meet();
+        if (warp == 0) {
+          float* const mine = buf;   // (the first other warp's)
 #pragma unroll
           for (int j = 0; j < D / 16; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float v = o[j][t][2 * e + a] * by;
 #pragma unroll
-              for (int k = 1; k < C::kGroups; ++k) v += buf[((k - 1) * RG + rg) * 4 * C::kApart + c * C::kApart + d_of(j, e)];
+              for (int k = 1; k < 4; ++k) v += buf[(k - 1) * 4 * C::kApart + c * C::kApart + d_of(j, e)];
               mine[c * C::kApart + d_of(j, e)] = v;
             }
           __syncwarp();
           // Eight lanes a row.
           constexpr int kEach = D / 8;
-          const int mine_row = lane >> 3, rho = (rg * NT + t) * 8 + 2 * mine_row + a;
+          const int mine_row = lane >> 3, rho = t * 8 + 2 * mine_row + a;
           const float top_of = __shfl_sync(0xffffffffu, top, mine_row), sum_of = __shfl_sync(0xffffffffu, sum, mine_row);
           if (rho < real) {
             const float* const from = mine + mine_row * C::kApart + (lane & 7) * kEach;
@@ -712,10 +706,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
   if (tid == 0 && *abort_flag) fo::record_error(p.batch.status, FO_ERR_TIMEOUT, -1, -1, 0);
 }
 
-template <int D, bool E8, int NT, int RG>
+template <int D, bool E8, int NT>
 fo_status launch(FewParams& k, int sms, cudaStream_t s) {
-  using C = Few<D, E8, NT, RG>;
-  auto kern = few_kernel<D, E8, NT, RG>;
+  using C = Few<D, E8, NT>;
+  auto kern = few_kernel<D, E8, NT>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return launched(e, "paged attention", k.R, k.batch.rows, D, 0, kFewThreads);
   const int blocks = std::min(sms, FO_GB300_SMS) * kFewBlocks;
@@ -723,17 +717,15 @@ fo_status launch(FewParams& k, int sms, cudaStream_t s) {
                   kFewThreads);
 }
 template <int D>
-fo_status launch_for(FewParams& k, int eights, bool eight, int sms, cudaStream_t s) {
-  if (eight)
-    return eights == 1   ? launch<D, true, 1, 1>(k, sms, s)
-           : eights == 2 ? launch<D, true, 2, 1>(k, sms, s)
-           : eights == 4 ? launch<D, true, 2, 2>(k, sms, s)
-                         : launch<D, true, 2, 4>(k, sms, s);
-  return eights == 1   ? launch<D, false, 1, 1>(k, sms, s)
-         : eights == 2 ? launch<D, false, 2, 1>(k, sms, s)
-         : eights == 4 ? launch<D, false, 2, 2>(k, sms, s)
-                       : launch<D, false, 2, 4>(k, sms, s);
+fo_status launch_for(FewParams& k, bool wide, bool eight, int sms, cudaStream_t s) {
+  if (eight) return wide ? launch<D, true, 2>(k, sms, s) : launch<D, true, 1>(k, sms, s);
+  return wide ? launch<D, false, 2>(k, sms, s) : launch<D, false, 1>(k, sms, s);
 }
 
 }  // namespace
+
+fo_status attend_few(FewParams& k, int D, bool wide, bool eight, int sms, cudaStream_t s) {
+  return D == 128 ? launch_for<128>(k, wide, eight, sms, s) : launch_for<64>(k, wide, eight, sms, s);
+}
+
 }  // namespace fo_ops

@@ -24,7 +24,8 @@
 // that, 2^-11 of it at most.
 //
 // A first kernel of one block lists the items; blocks take them from a
-// counter, the last (under the causal mask the costliest) first.
+// counter, the last (under the causal mask the costliest) first. A third joins
+// the parts of pairs of tiles that were cut.
 #include <cudaTypedefs.h>
 #include <math.h>
 #include <string.h>
@@ -58,12 +59,11 @@ struct PromptParams {
   float scale_log2;
   int32_t sms;
   int64_t* before;        // [seqs + 1]: pairs of the sequences before
-  uint32_t* next;         // [0] items dealt, [1] items of a key head
+  uint32_t* next;         // [0] items dealt, [1] items of a key head, [2] parts of it, [3] cut pairs of it, [4] blocks of 32 rows of the largest
   struct Record* items;   // [most_items]
   long long most_items;
-  float* part;            // [most parts][slot_rows * (D + 2)]
-  uint32_t* arrived;      // [most parts][8], zero between calls
-  int32_t slot_rows;      // rows of a part: of one tile or two
+  float* part;            // [most parts][2 * kTile * (D + 2)]
+  struct Record* cut;     // [kMostParts]: the first part of each pair that is cut, of a key head
 };
 
 // An item: a pair of tiles, or some of its steps.
@@ -71,7 +71,8 @@ struct Record {
   int32_t b, row, n, base, token;   // token: the pair's first
   int32_t from, to;                 // steps
   int32_t slot, parts;              // the pair's first part, its parts (1: the item is the whole pair)
-  int32_t part, pad[2];
+  int32_t part;
+  int32_t at, pad;                  // of a cut pair, while it is planned: its first item
 };
 // As the warps get it.
 struct Item {
@@ -116,9 +117,8 @@ struct Steps {
 // ---- the plan: one block lists the items of a key head.
 //
 // A pair of more steps than an even share among twice the SMs is cut into
-// parts, which are joined by the last warp of a row's to end: without that a
-// few long pairs (chunks of prompts on long prefixes, drafted tokens) left most
-// of the GPU idle.
+// parts, which a third kernel joins: without that a few long pairs (chunks of
+// prompts on long prefixes, drafted tokens) left most of the GPU idle.
 constexpr int kLeastSteps = 4;
 constexpr int kSharesPerSm = 2;
 // Parts of pairs that are cut, at most: sum of ceil(n / L) over pairs of n > L
@@ -148,24 +148,37 @@ __device__ __forceinline__ long long block_scan(long long mine, long long* sums,
 
 __global__ void __launch_bounds__(1024) prompt_plan_kernel(const __grid_constant__ PromptParams p) {
   __shared__ long long sums[32];
+  __shared__ int largest;
+  __shared__ int few[1025];   // pairs before each of up to 1024 sequences: looked up here, not in global memory
+  if (threadIdx.x == 0) largest = 0;
   grid_release();
   grid_wait();
   const int tid = threadIdx.x, each = 2 * p.tokens;
-  long long pairs, steps, items, parts;
+  long long pairs, steps, items, parts, cuts;
+  const bool in_few = p.batch.seqs <= 1024 && p.batch.rows < 1 << 30;
   {
     const int run = (p.batch.seqs + 1023) / 1024, first = min(tid * run, p.batch.seqs), last = min(first + run, p.batch.seqs);
     long long mine = 0;
     for (int b = first; b < last; ++b) mine += (sequence(p.batch, b).n + each - 1) / each;
     long long at = block_scan(mine, sums, &pairs) - mine;
-    for (int b = first; b < last; ++b) {
-      p.before[b] = at;
-      at += (sequence(p.batch, b).n + each - 1) / each;
+    if (in_few) {
+      if (tid < p.batch.seqs) few[tid] = (int)at;
+      if (tid == 0) few[p.batch.seqs] = (int)pairs;
+    } else {
+      for (int b = first; b < last; ++b) {
+        p.before[b] = at;
+        at += (sequence(p.batch, b).n + each - 1) / each;
+      }
+      if (tid == 0) p.before[p.batch.seqs] = pairs;
     }
-    if (tid == 0) p.before[p.batch.seqs] = pairs;
     __syncthreads();
   }
+  // More rows than the call's: only starts that fall can say so.
+  const bool bad = pairs > p.most_items;
+  if (bad) pairs = 0;
+  auto before = [&](int b) { return in_few ? (long long)few[b] : p.before[b]; };
   // A thread's run of pairs, from the last on; a visit to each.
-  const long long run = (pairs + 1023) / 1024, first = min(tid * run, pairs), last = min(first + run, pairs);   // (of pairs)
+  const long long run = (pairs + 1023) / 1024, first = min(tid * run, pairs), last = min(first + run, pairs);
   Record own;
   int own_n = -1;   // of a run of one, which is looked at once
   auto visit = [&](auto&& f) {
@@ -174,11 +187,11 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const __grid_constant
       f(own, own_n);
       return;
     }
-    int lo = 0, hi = p.batch.seqs;   // before[lo] <= pair < before[hi]
+    int lo = 0, hi = p.batch.seqs;   // before(lo) <= pair < before(hi)
     const long long start = pairs - 1 - first;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (p.before[mid] <= start) lo = mid;
+      if (before(mid) <= start) lo = mid;
       else hi = mid;
     }
     Seq s = sequence(p.batch, lo);
@@ -186,9 +199,9 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const __grid_constant
     Steps st;
     for (long long e = first; e < last; ++e) {
       const long long pair = pairs - 1 - e;
-      while (pair < p.before[lo]) s = sequence(p.batch, --lo);
+      while (pair < before(lo)) s = sequence(p.batch, --lo);
       it.b = lo, it.row = s.row, it.n = s.n, it.base = s.base;
-      it.token = (int)(pair - p.before[lo]) * each;
+      it.token = (int)(pair - before(lo)) * each;
       st.of(it, p.tokens, p.window, p.sinks);
       if (run == 1) own = it, own_n = st.n;
       f(it, st.n);
@@ -199,31 +212,49 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const __grid_constant
   block_scan(mine, sums, &steps);
   const long long shares = (long long)kSharesPerSm * p.sms;
   const int most = (int)min((long long)INT32_MAX, max((steps * p.R * p.heads_k + shares - 1) / shares, (long long)kLeastSteps));
+  // Items, and in the upper half of the number parts; cut pairs by themselves.
   long long my_items = 0, my_parts = 0;
   visit([&](Record&, int n) {
     const int k = n > most ? (n + most - 1) / most : 1;
     my_items += k;
-    my_parts += k > 1 ? k : 0;
+    my_parts += k > 1 ? ((long long)k << 32) + 1 : 0;
   });
-  long long at = block_scan(my_items, sums, &items) - my_items, slot = block_scan(my_parts, sums, &parts) - my_parts;
+  long long at = block_scan(my_items, sums, &items) - my_items, both = block_scan(my_parts, sums, &parts) - my_parts;
+  cuts = parts & 0xffffffffll, parts >>= 32;
+  long long cut = both & 0xffffffffll, slot = both >> 32;
   visit([&](Record& it, int n) {
     const int k = n > most ? (n + most - 1) / most : 1;
-    it.parts = k;
+    it.parts = k, it.part = 0;
     it.slot = (int)slot;
-    for (int i = 0; i < k; ++i) {
-      it.part = i;
-      it.from = (int)((long long)n * i / k), it.to = (int)((long long)n * (i + 1) / k);
-      if (at < p.most_items) p.items[at] = it;
-      ++at;
+    it.from = 0, it.to = n;
+    if (k > 1) {
+      it.at = (int)at;
+      if (cut < kMostParts) p.cut[cut] = it;
+      ++cut, slot += k;
+      atomicMax(&largest, it.n - it.token <= p.tokens ? ((it.n - it.token) * p.group + 31) / 32 : 2 * kTile / 32);
+    } else if (at < p.most_items) {
+      p.items[at] = it;
     }
-    slot += k > 1 ? k : 0;
+    at += k;
   });
+  // A warp for a cut pair's items: one of many parts is as many items.
+  __syncthreads();
+  for (long long c = tid >> 5; c < (items <= p.most_items ? cuts : 0); c += 32) {
+    Record it = p.cut[c];
+    const int n = it.to, k = it.parts, q = (n + k - 1) / k;
+    for (int i = tid & 31; i < k; i += 32) {
+      it.part = i;
+      it.from = min(i * q, n), it.to = min((i + 1) * q, n);
+      p.items[it.at + i] = it;
+    }
+  }
   if (tid == 0) {
-    // More rows than the call's: only starts that fall can say so.
-    if (items > p.most_items) report(p.batch, 0, kBadStarts, p.batch.rows);
+    if (bad || items > p.most_items) report(p.batch, 0, kBadStarts, p.batch.rows);
     p.next[0] = 0;
     p.next[1] = items > p.most_items ? 0u : (uint32_t)items;
     p.next[2] = (uint32_t)parts;
+    p.next[3] = items > p.most_items ? 0u : (uint32_t)cuts;
+    p.next[4] = (uint32_t)largest;
   }
 }
 
@@ -382,8 +413,8 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
     for (; ok; ++n) {
       const int sl = n & 1;
       if (!mbar_wait(bar(kItemFree + sl), ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, kWaitNs)) break;
-      unsigned L32 = 0;
-      if (lane == 0) L32 = atomicAdd(p.next, 1u);
+      unsigned L32 = blockIdx.x;   // (the first without a look at the counter)
+      if (n > 0 && lane == 0) L32 = atomicAdd(p.next, 1u) + gridDim.x;
       const long long L = __shfl_sync(0xffffffffu, L32, 0);
       it.r = -1;
       if (L < total) {
@@ -731,11 +762,11 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
     for (int n = 0; ok; ++n) {
       if (!take(n, it)) break;
       st.of(it, p.tokens, p.window, p.sinks);
-      const int token = it.token + t * p.tokens + row / p.group;
+      const int tile_token = it.token + t * p.tokens, token = tile_token + row / p.group;
       const bool real = row < p.tokens * p.group && token < it.n;
       const int pos = real ? it.base + token : -1, lo = sight_of(max(pos, 0), p.window, p.sinks).lo;
       // Blocks all of whose keys all of the tile's rows see need no mask.
-      const int first_pos = it.base + it.token + t * p.tokens;
+      const int first_pos = it.base + tile_token;
       const int last_lo = sight_of(max(first_pos + p.tokens - 1, 0), p.window, p.sinks).lo;
       float m = -INFINITY, l = 0.f, row_factor = p.scale_log2, sigma = 0.f;
       bool any = false;
@@ -914,7 +945,8 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         continue;
       }
       // A part: four columns of all rows side by side, then maxima and sums.
-      const int place = t * kTile + row, rows = p.slot_rows;
+      constexpr int rows = 2 * kTile;
+      const int place = t * kTile + row;
       auto part_of = [&](int i) { return p.part + (int64_t)(it.slot + i) * rows * (D + 2); };
       const int stat = D * rows + place;
       if (any) {
@@ -937,47 +969,6 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         if (lane == 0) mbar_arrive(bar(kOFree + t));
       }
       if (real) part_of(it.part)[stat] = m, part_of(it.part)[stat + rows] = l;
-      __threadfence();
-      __syncwarp();
-      uint32_t* const counter = p.arrived + (int64_t)it.slot * 8 + (warp - 4);
-      uint32_t came = 0;
-      if (lane == 0) {
-        came = atom_add_acq_rel_u32(counter, 1u);
-        if (came == (uint32_t)it.parts - 1u) *counter = 0u;
-      }
-      if (__shfl_sync(0xffffffffu, came, 0) != (uint32_t)it.parts - 1u) continue;
-      __threadfence();
-      // The last of the parts' warps of these rows joins them, in their order.
-      float top = -INFINITY, total = 0.f;
-      if (real) {
-        for (int i = 0; i < it.parts; ++i) top = fmaxf(top, __ldcg(part_of(i) + stat));
-        for (int i = 0; i < it.parts; ++i) total += ex2_below(__ldcg(part_of(i) + stat), top) * __ldcg(part_of(i) + stat + rows);
-      }
-      const float inv = top == -INFINITY && total == 0.f ? 0.f : 1.f / total;
-#pragma unroll 1
-      for (int e = 0; e < D / 32; ++e) {
-        float acc[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) acc[k] = 0.f;
-        for (int i = 0; real && i < it.parts; ++i) {
-          const float mi = __ldcg(part_of(i) + stat), li = __ldcg(part_of(i) + stat + rows);
-          if (mi == -INFINITY && li == 0.f) continue;   // (nothing was written)
-          const float f = ex2_below(mi, top) * inv;
-          const float4* const from = reinterpret_cast<const float4*>(part_of(i)) + 8 * e * rows + place;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 u = __ldcg(from + k * rows);
-            acc[4 * k] = fmaf(f, u.x, acc[4 * k]), acc[4 * k + 1] = fmaf(f, u.y, acc[4 * k + 1]);
-            acc[4 * k + 2] = fmaf(f, u.z, acc[4 * k + 2]), acc[4 * k + 3] = fmaf(f, u.w, acc[4 * k + 3]);
-          }
-        }
-        __syncwarp();
-        uint32_t w[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) w[k] = bf16x2(acc[2 * k], acc[2 * k + 1]);
-        store(e, w);
-      }
-      if (real && p.lse[it.r]) p.lse[it.r][out * p.heads_q + head] = lse_of(top, total);
     }
   }
 
@@ -991,6 +982,121 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
   if (threadIdx.x == 0 && *abort_flag) record_error(p.batch.status, FO_ERR_TIMEOUT, -1, -1, 0);
 }
 
+// Parts of a cut pair together, in an order of their own. A lane has a row's 32
+// columns. Up to eight parts are one warp's, and a block has the pair's eight
+// blocks of rows; more are dealt to a block's eight warps, whose sums meet in
+// shared memory. (With eight warps to a row's parts always, chunks of prompts,
+// of two or three parts a pair, took 36 us here, not 16; with one warp, the
+// parts of 17 contexts of 4100 tokens and 40 rows 18 us, not 9.) Few rows are
+// dealt to all warps too: their blocks would be too few.
+constexpr int kJoinWays = 8;
+static_assert(kJoinWays * 32 == 2 * kTile, "a warp for a block of rows");
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWays) prompt_join_kernel(const __grid_constant__ PromptParams p) {
+  __shared__ float4 sums[kJoinWays][32][9];
+  __shared__ float tops[kJoinWays][32], totals[kJoinWays][32];
+  grid_release();
+  grid_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int rows = 2 * kTile, E = D / 32;
+  // (All of them are fewer than kMostParts.)
+  const int parts = (int)p.next[2], units = p.R * p.heads_k, all = units * (int)p.next[3], most = all * E * (int)p.next[4];
+  const long long step = (long long)rows * (D + 2);
+  for (int x = blockIdx.x; x < most; x += gridDim.x) {
+    const int y = x % all, z = x / all, e = z % E, u = y % units;
+    const Record it = p.cut[y / units];
+    const bool split = it.parts > kJoinWays || (it.n - it.token) * p.group <= 2 * 32;
+    if (!split && z >= E) continue;
+    const int first_row = (split ? z / E : warp) * 32, r = u / p.heads_k, h = u - r * p.heads_k;
+    auto token_of = [&](int place) { return it.token + place / kTile * p.tokens + place % kTile / p.group; };
+    auto real = [&](int place) { return place % kTile < p.tokens * p.group && token_of(place) < it.n; };
+    auto write = [&](int place, int column, const float4& o, float inv) {
+      *reinterpret_cast<uint2*>(p.o[r] + ((long long)it.row + token_of(place)) * p.ld_o + (h * p.group + place % kTile % p.group) * D + column) =
+          make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
+    };
+    auto write_lse = [&](int place, float top, float total) {
+      if (p.lse[r] && e == 0)
+        p.lse[r][((long long)it.row + token_of(place)) * p.heads_q + h * p.group + place % kTile % p.group] = lse_of(top, total);
+    };
+    if (!real(first_row)) continue;   // (nor any after it)
+    const int place = first_row + lane, by = split ? kJoinWays : 1;
+    const float* const first = p.part + (int64_t)(u * parts + it.slot) * step;
+    float top = -INFINITY, total = 0.f;
+    float4 acc[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (real(place)) {
+      const float* const stat = first + D * rows + place;
+#pragma unroll 8
+      for (int i = split ? warp : 0; i < it.parts; i += by) top = fmaxf(top, stat[i * step]);
+#pragma unroll 1
+      for (int i0 = split ? warp : 0; i0 < it.parts; i0 += 2 * by) {
+        float m[2], l[2];
+        float4 v[2][8];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const bool there = i0 + j * by < it.parts;
+          const float* const at = stat + (i0 + j * by) * step;
+          m[j] = there ? at[0] : -INFINITY, l[j] = there ? at[rows] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          // (A part that was not written is read all the same: the columns are on
+          // their way with the sums, not after them.)
+          const bool there = i0 + j * by < it.parts;
+          const float4* const from = reinterpret_cast<const float4*>(first + (i0 + j * by) * step) + 8 * e * rows + place;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[j][k] = there ? from[k * rows] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float f = ex2_below(m[j], top);
+          if (m[j] == -INFINITY && l[j] == 0.f) continue;
+          total = fmaf(f, l[j], total);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            acc[k].x = fmaf(f, v[j][k].x, acc[k].x), acc[k].y = fmaf(f, v[j][k].y, acc[k].y);
+            acc[k].z = fmaf(f, v[j][k].z, acc[k].z), acc[k].w = fmaf(f, v[j][k].w, acc[k].w);
+          }
+        }
+      }
+    }
+    if (!split) {
+      if (real(place)) {
+        const float inv = top == -INFINITY && total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) write(place, 32 * e + 4 * k, acc[k], inv);
+        write_lse(place, top, total);
+      }
+      continue;
+    }
+    __syncthreads();
+    tops[warp][lane] = top, totals[warp][lane] = total;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sums[warp][lane][k] = acc[k];
+    __syncthreads();
+    // A thread for four of a row's columns.
+    const int mine = threadIdx.x >> 3, quad = threadIdx.x & 7;
+    if (real(first_row + mine)) {
+      top = -INFINITY, total = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kJoinWays; ++w) top = fmaxf(top, tops[w][mine]);
+#pragma unroll
+      for (int w = 0; w < kJoinWays; ++w) {
+        const float m = tops[w][mine], l = totals[w][mine];
+        if (m == -INFINITY && l == 0.f) continue;
+        const float f = ex2_below(m, top);
+        const float4 v = sums[w][mine][quad];
+        total = fmaf(f, l, total);
+        o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+      }
+      write(first_row + mine, 32 * e + 4 * quad, o, top == -INFINITY && total == 0.f ? 0.f : 1.f / total);
+      if (quad == 0) write_lse(first_row + mine, top, total);
+    }
+  }
+}
+
 template <int D, bool E8>
 fo_status launch_prompt(PromptParams& k, int sms, cudaStream_t s) {
   using C = Prompt<D, E8>;
@@ -999,8 +1105,8 @@ fo_status launch_prompt(PromptParams& k, int sms, cudaStream_t s) {
   fo_status st = launched(e, "paged prompt", k.R, k.batch.rows, D, 0, C::kThreads);
   if (st || (st = launched(launch_after(prompt_plan_kernel, dim3(1), 1024, 0, 0, s, k), "paged prompt plan", k.R, k.batch.rows, D, 1, 1024)))
     return st;
-  const int blocks = sms;
-  return launched(launch_after(kern, dim3(blocks), C::kThreads, C::kSmem, 0, s, k), "paged prompt", k.R, k.batch.rows, D, blocks, C::kThreads);
+  if ((st = launched(launch_after(kern, dim3(sms), C::kThreads, C::kSmem, 0, s, k), "paged prompt", k.R, k.batch.rows, D, sms, C::kThreads))) return st;
+  return launched(launch_after(prompt_join_kernel<D>, dim3(4 * sms), 32 * kJoinWays, 0, 0, s, k), "paged prompt join", k.R, k.batch.rows, D, 4 * sms, 32 * kJoinWays);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -1041,27 +1147,26 @@ bool encode_rows(CUtensorMap* m, const void* p, int64_t rows, int64_t ld, int he
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Workspace: header, deal, arrivals, pairs before each sequence, items, parts.
+// Workspace: header, deal, (the other kernel's counters,) pairs before each
+// sequence, items, cut pairs, parts.
 namespace {
 struct PromptPlaces {
-  size_t arrived, before, items, part, bytes;
+  size_t before, items, cut, part, bytes;
   int64_t most_items;
-  int32_t slot_rows;
-  PromptPlaces(const fo_paged_desc* d, int64_t seqs, int64_t rows, int64_t max_new) {
+  PromptPlaces(const fo_paged_desc* d, int64_t seqs, int64_t rows) {
     const int tokens = kTile / (d->heads_q / d->heads_k);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-    slot_rows = max_new > tokens ? 2 * kTile : kTile;
     most_items = rows / (2 * tokens) + seqs + kMostParts;
-    arrived = 256 + kFewCountBytes;
     before = kScratchAt;
     items = before + up((size_t)(seqs + 1) * 8);
-    part = items + up((size_t)most_items * sizeof(Record));
-    bytes = part + (size_t)kMostParts * slot_rows * (d->head_dim + 2) * 4;
+    cut = items + up((size_t)most_items * sizeof(Record));
+    part = cut + up((size_t)kMostParts * sizeof(Record));
+    bytes = part + (size_t)kMostParts * 2 * kTile * (d->head_dim + 2) * 4;
   }
 };
 }  // namespace
-size_t prompt_bytes(const fo_paged_desc* d, int32_t seqs, int64_t rows, int32_t max_new) {
-  return PromptPlaces(d, seqs, rows, max_new).bytes;
+size_t prompt_bytes(const fo_paged_desc* d, int32_t seqs, int64_t rows) {
+  return PromptPlaces(d, seqs, rows).bytes;
 }
 
 fo_status attend_prompts(const PagedCall& c, cudaStream_t s) {
@@ -1090,15 +1195,14 @@ fo_status attend_prompts(const PagedCall& c, cudaStream_t s) {
   k.window = d->window;
   k.sinks = d->sinks;
   k.scale_log2 = c.scale_log2;
-  const PromptPlaces at(d, c.b->seqs, c.rows, c.b->max_new);
+  const PromptPlaces at(d, c.b->seqs, c.rows);
   k.sms = std::min(c.sms, FO_GB300_SMS);
   k.next = reinterpret_cast<uint32_t*>(c.ws + 128);
-  k.arrived = reinterpret_cast<uint32_t*>(c.ws + at.arrived);
+  k.cut = reinterpret_cast<Record*>(c.ws + at.cut);
   k.before = reinterpret_cast<int64_t*>(c.ws + at.before);
   k.items = reinterpret_cast<Record*>(c.ws + at.items);
   k.most_items = at.most_items;
   k.part = reinterpret_cast<float*>(c.ws + at.part);
-  k.slot_rows = at.slot_rows;
   if (d->head_dim == 128) return eight ? launch_prompt<128, true>(k, c.sms, s) : launch_prompt<128, false>(k, c.sms, s);
   return eight ? launch_prompt<64, true>(k, c.sms, s) : launch_prompt<64, false>(k, c.sms, s);
 }

@@ -656,7 +656,8 @@ typedef struct {
  * found: 1 a needed entry of the table that names no page (nothing is read or
  * written through it), 2 more new tokens than max_new (those beyond it are
  * left out), 3 starts that fall or leave the call's rows (the sequence is left
- * out), 4 a length that the table has no entries for (the sequence is left
+ * out; where sequences then overlap in more rows than the call has, others may
+ * be too), 4 a length that the table has no entries for (the sequence is left
  * out). Results of the sequence are then undefined, of the others not. */
 typedef struct {
   int32_t seqs;               /* >= 0 */
@@ -696,23 +697,31 @@ fo_status fo_kv_append(const fo_paged_desc* desc, const fo_rope_desc* rope, cons
  *     s_j = scale q . k_j,   m = max s_j,   l = sum exp(s_j - m)
  *     o = sum exp(s_j - m) v_j / l,   lse = m + ln l
  * over them. Weights are rounded to bf16 for the tensor cores' sum (by at most
- * 2^-8 of each), o once to bf16. A row that sees nothing (a sequence that is not
- * there, a token before its beginning) gets o = 0 and lse = -infinity. Rows
+ * 2^-8 of each), o once to bf16. With an 8-bit cache and max_new * heads_q /
+ * heads_k above 16, weights, queries and the elements times their scales are
+ * rounded to f16 instead (by at most 2^-11 of each; values whose scale is below
+ * 2^-87 may count as zero). A row that sees nothing (a sequence that is not
+ * there, a token before its beginning), or whose scores are all -infinity, gets
+ * o = 0 and lse = -infinity. Rows
  * that no sequence has are left as they were. Neither places behind a
  * sequence's length nor pages that hold nothing any new token of it sees are
  * looked at: their entries of the table may be anything, their places may hold
- * NaN. q, o: rows ld[0..1] elements apart (a multiple of 8; 16-byte aligned),
+ * NaN. (An infinity or NaN among the values that one new token of a sequence
+ * sees may reach the sequence's others, which see less.) q, o: rows ld[0..1] elements apart (a multiple of 8; 16-byte aligned),
  * head h at h * head_dim; caches and scales 16-byte aligned; lse (may be NULL)
  * [rows x heads_q] fp32. o must not overlap q. ws: fo_paged_attention_workspace
  * bytes, 16-byte aligned, zeroed once by fo_ops_workspace_init; one call per
- * workspace may be in flight. Results repeat bit for bit. */
+ * workspace may be in flight. Results repeat bit for bit. One launch where
+ * max_new * heads_q / heads_k is at most 16, else three: the cache's length is
+ * split in the one, prompts are cut into tiles in the others. */
 fo_status fo_paged_attention(const fo_paged_desc* desc, const fo_paged_batch* batch, int64_t rows,
                              const void* const* q, const int64_t ld[2], const void* const* k_cache,
                              const void* const* v_cache, const float* const* k_scale, const float* const* v_scale,
                              void* const* o, float* const* lse, void* ws, fo_stream_t stream);
 
 /* Bytes of workspace for calls of up to `seqs` sequences, `rows` rows and
- * `max_new` new tokens a sequence. */
+ * `max_new` new tokens a sequence: at head_dim 128 some 5 MB for few new tokens,
+ * 81 MB for more. */
 fo_status fo_paged_attention_workspace(const fo_paged_desc* desc, int32_t seqs, int64_t rows, int32_t max_new,
                                        size_t* bytes);
 

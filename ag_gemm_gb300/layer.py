@@ -309,3 +309,114 @@ class Fp8AttentionBlock:
     def status(self, stream=None) -> List[int]:
         """The status words once the stream's work so far is done (0: no device wait has run out)."""
         return [B.fo_status_query(self.plan, self.ws_attn, stream)[0], B.fo_ops_status_query(self.ws, stream)[0]]
+
+
+class PagedAttentionBlock:
+    """The attention half of a TP-SP layer when it answers: the new tokens of a batch of sequences, their keys and values
+    in a paged cache, all products in 8 bits:
+
+        norm      s = x + residual, n = rmsnorm(s); n in 8 bits with a scale for 128 columns   fo_rmsnorm
+        QKV       Y_r = n . Wqkv_r^T, every rank in one launch                                fo_gemm_fp8
+        append    Y_r's Q and K turned by their tokens' positions, K and V into the cache     fo_kv_append
+        attention O_r over the cache                                                          fo_paged_attention
+        o         O_r in 8 bits, y = sum_r O_r . Wo_r^T, the ranks' shards of its rows        fo_quant_fp8, fo_gemm_fp8,
+                                                                                              fo_reduce_scatter_f32
+
+    A call has `rows` rows (a multiple of R) and up to `seqs` sequences; what they are is read from the device when it
+    runs, from the block's own tensors: `lengths` [seqs] (new tokens included, 0: not there), `starts` [seqs + 1] (with
+    max_new = 1 there are none: sequence b's new token is row b) and `table` [seqs, cols] of page numbers. So a captured
+    call may be replayed with other ones. Rows that no sequence has hold results of no meaning.
+
+    `like`: a block with the same heads, H, R and cache, whose weights and cache this one shares; one for prompts and one
+    for single tokens serve the same sequences so. Weights are given in bf16 (a rank's Wqkv [(heads_q + 2 heads_k) *
+    head_dim x H], rows Q | K | V, and Wo [H x heads_q * head_dim]) and quantised by set_weights, once for each version
+    of them. All of a call's work is on its stream, and what it returns are the block's own buffers."""
+
+    def __init__(self, H, heads_q, heads_k, *, rows, seqs, pages, cols, max_new=1, R=1, head_dim=128, page=64, cache="e4m3",
+                 window=0, sinks=0, eps=1e-6, rope_base=10000.0, device="cuda", like=None, **rope):
+        if rows % R or H % 64:
+            raise ValueError("rows must be divisible by R, and H by 64")
+        if max_new == 1 and rows < seqs:
+            raise ValueError("a row for each sequence")
+        self.H, self.R, self.rows, self.heads_q, self.heads_k, self.head_dim = H, R, rows, heads_q, heads_k, head_dim
+        q, k = heads_q * head_dim, heads_k * head_dim
+        self.width, self.widths = q, (q, k, k)
+        dev = torch.device(device)
+        bf, f32, e4m3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+        def zeros(*shp, dtype=bf):
+            return torch.zeros(shp, dtype=dtype, device=dev)
+
+        def each(*shp, dtype=bf):
+            return [zeros(*shp, dtype=dtype) for _ in range(R)]
+
+        def blocks(n):
+            return -(-n // 128)
+
+        self.norm = B.fo_norm_desc(H, eps=eps)
+        self.qkv = B.fo_gemm_fp8_desc(q + 2 * k, H, R=R)
+        self.out = B.fo_gemm_fp8_desc(H, q, R=R, out_dtype="f32")
+        self.rope = B.fo_rope_desc(head_dim, heads_q, heads_k, heads_k, R=R, base=rope_base, **rope)
+        self.paged = B.fo_paged_desc(heads_q, heads_k, head_dim=head_dim, R=R, page=page, cache=cache, window=window,
+                                     sinks=sinks)
+        self.sum_plan = B.fo_plan("gemm_rs", R, rows, H, H)
+        if like is None:
+            eight = cache == "e4m3"
+            self.Wq, self.Wq_scale = each(q + 2 * k, H, dtype=e4m3), each(blocks(q + 2 * k), blocks(H), dtype=f32)
+            self.Wo, self.Wo_scale = each(H, q, dtype=e4m3), each(blocks(H), blocks(q), dtype=f32)
+            self.weight = zeros(H)
+            kept = (pages, heads_k, page)
+            self.k, self.v = (each(*kept, head_dim, dtype=e4m3 if eight else bf) for _ in range(2))
+            self.k_scale, self.v_scale = (each(*kept, dtype=f32) if eight else None for _ in range(2))
+        else:
+            mine = (H, R, heads_q, heads_k, head_dim, page, pages, cache)
+            its = (like.H, like.R, like.heads_q, like.heads_k, like.head_dim, like.paged.page, like.pages, like.cache)
+            if mine != its:
+                raise ValueError(f"blocks that share weights and cache have the same H, R, heads and cache: {mine}, {its}")
+            for name in ("Wq", "Wq_scale", "Wo", "Wo_scale", "weight", "k", "v", "k_scale", "v_scale"):
+                setattr(self, name, getattr(like, name))
+        self.pages, self.cache = pages, cache
+        self.lengths, self.table = zeros(seqs, dtype=torch.int32), zeros(seqs, cols, dtype=torch.int32)
+        self.starts = zeros(seqs + 1, dtype=torch.int32) if max_new > 1 else None
+        self.batch = B.fo_paged_batch(self.lengths, self.table, pages, starts=self.starts, max_new=max_new)
+        self.h, self.n8, self.n_scale = zeros(rows, H), zeros(rows, H, dtype=e4m3), zeros(rows, blocks(H), dtype=f32)
+        self.y_qkv = each(rows, q + 2 * k)
+        self.Q, self.O = each(rows, q), each(rows, q)
+        self.o8, self.o_scale = each(rows, q, dtype=e4m3), each(rows, blocks(q), dtype=f32)
+        self.parts, self.y_whole = each(rows, H, dtype=f32), zeros(rows, H, dtype=f32)
+        self.y = list(self.y_whole.split(rows // R))
+        self.ws = zeros(max(B.fo_gemm_fp8_workspace(self.qkv, rows), B.fo_gemm_fp8_workspace(self.out, rows)),
+                        dtype=torch.uint8)
+        self.ws_paged = zeros(B.fo_paged_attention_workspace(self.paged, seqs, rows, max_new), dtype=torch.uint8)
+        for ws in (self.ws, self.ws_paged):
+            B.fo_ops_workspace_init(ws)
+        torch.cuda.current_stream(dev).synchronize()   # all is zeroed before a call on any other stream
+
+    def set_weights(self, weight, Wqkv, Wo, stream=None):
+        """The norm's weight [H], each rank's Wqkv and Wo, bf16; of blocks that share them too."""
+        with _on(stream):
+            self.weight.copy_(weight)
+        B.fo_quant_fp8(sum(self.widths), self.H, Wqkv, self.Wq, self.Wq_scale, block_rows=128, stream=stream)
+        B.fo_quant_fp8(self.H, self.width, Wo, self.Wo, self.Wo_scale, block_rows=128, stream=stream)
+
+    def forward(self, x, residual=None, positions=None, stream=None):
+        """x, residual [rows x H] bf16; positions [rows] (None: the tokens' places in their sequences). Returns the R shards
+        [rows / R x H] of y, fp32; h is the new residual. Seven launches, with more than 16 rows for a key head nine."""
+        T, R = self.rows, self.R
+        B.fo_rmsnorm(self.norm, T, [x], None if residual is None else [residual], self.weight, [self.h], None,
+                     [self.n8], [self.n_scale], None, stream)
+        B.fo_gemm_fp8(self.qkv, T, [self.n8] * R, [self.n_scale] * R, self.Wq, self.Wq_scale, self.y_qkv, self.ws, stream)
+        q, k, v = map(list, zip(*(y.split(self.widths, dim=1) for y in self.y_qkv)))
+        B.fo_kv_append(self.paged, self.rope, self.batch, T, q, k, v, self.Q, self.k, self.v, self.k_scale, self.v_scale,
+                       positions, self.ws_paged, stream)
+        B.fo_paged_attention(self.paged, self.batch, T, self.Q, self.k, self.v, self.O, self.ws_paged, self.k_scale,
+                             self.v_scale, None, stream)
+        B.fo_quant_fp8(T, self.width, self.O, self.o8, self.o_scale, stream=stream)
+        B.fo_gemm_fp8(self.out, T, self.o8, self.o_scale, self.Wo, self.Wo_scale, self.parts, self.ws, stream)
+        B.fo_reduce_scatter_f32(self.sum_plan, self.parts, self.y, stream)
+        return self.y
+
+    def status(self, stream=None) -> List[int]:
+        """The status words once the stream's work so far is done (0: no device wait has run out, nothing wrong was found
+        in lengths, starts and table)."""
+        return [B.fo_ops_status_query(ws, stream)[0] for ws in (self.ws, self.ws_paged)]

@@ -18,10 +18,12 @@
 // issuer for both fell behind: a wait for a barrier that is ready takes it 150
 // cycles), 3 puts zeros in the place of values that nobody sees, 4-7 and 8-11
 // are the tiles' softmax. With an 8-bit cache 12-15 turn its bytes into f16,
-// times their scales over a power of two for each 32 keys: queries and weights
-// are f16 then. (The scales' columns in the softmax, an earlier form, took it
-// twice the time.) A key's or value's element is rounded to f16's 11 bits by
-// that, 2^-11 of it at most.
+// and queries and weights are f16 too. Keys stay exact, and the softmax
+// multiplies scores with their scales: with the scales in the keys, each
+// rounded to 2^-11 of it, lse was off by 1e-4 where fp32's 1e-7 could be had,
+// for 84 us in place of 92 (8-bit chunks). Values are turned times their scale
+// over a power of two for each 32, which the softmax puts on their weights; what
+// that rounds, 2^-11 of a value, is less than the result's own 2^-8.
 //
 // A first kernel of one block lists the items; blocks take them from a
 // counter, the last (under the causal mask the costliest) first. A third joins
@@ -41,7 +43,6 @@ namespace {
 using namespace fo;
 
 constexpr int kTile = 128;           // rows of a tile, keys of a step
-constexpr int kScaleSlots = 4;       // steps whose scales are in shared memory
 constexpr int kHeadsTogether = 8;    // key heads whose pairs are dealt together: their keys and values stay in L2
 
 struct PromptParams {
@@ -267,11 +268,16 @@ struct Prompt {
   static constexpr int kCuts = D / 64;               // 128-byte columns of a 16-bit tile
   static constexpr int kStages = E8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
   static constexpr int kRaws = E8 ? (D == 128 ? 3 : 4) : 0;
+  // Steps whose scales are in shared memory. Keys of step i + kScaleSlots are
+  // turned once the last reader has released their stage, which was a product's
+  // that followed the softmax of step i.
+  static constexpr int kScaleSlots = kStages / 2 + 1;
+  static constexpr int kScaleBytes = (kTile + 4) * 4;   // the keys', the values' powers of two
   static constexpr int kOffRing = 2 * kTileBytes;    // after the two tiles of queries
   static constexpr int kOffRaw = kOffRing + kStages * kTileBytes;
   static constexpr int kOffScale = kOffRaw + kRaws * kRawBytes;
-  static constexpr int kOffRow = kOffScale + (E8 ? kScaleSlots * 8 * 4 : 0);   // the rows' factors (bf16: powers of two), two items
-  static constexpr int kOffItem = kOffRow + (E8 ? 2 * 2 * kTile * 2 : 0);
+  static constexpr int kOffRow = kOffScale + (E8 ? kScaleSlots * kScaleBytes : 0);   // the rows' factors (exponents of two), two items
+  static constexpr int kOffItem = kOffRow + (E8 ? 2 * 2 * kTile : 0);
   static constexpr int kOffOut = (kOffItem + 2 * 48 + 127) / 128 * 128;   // results on their way out: a warp's 32 rows x 64 bytes
   static constexpr int kOffBar = kOffOut + 8 * 2048;
   static constexpr int kBars = 3 * kStages + 2 * kRaws + 26;
@@ -316,21 +322,11 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// Two f16 times two others (plus two).
+// Two f16 times two others.
 __device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
-}
-__device__ __forceinline__ uint32_t fma_f16(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ float half_of(uint32_t two) {   // the first of two f16
-  float f;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(two));
-  return f;
 }
 // The lowest n bits (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
@@ -668,7 +664,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
           }
           const uint32_t exponent = min(max(__float_as_uint(top) >> 23, 8u), 254u);
           const float by = top <= 3.4e38f ? __uint_as_float((261u - exponent) << 23) : 1.f;
-          reinterpret_cast<__nv_bfloat16*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + row] = __float2bfloat16_rn(1.f / by);
+          gbase[C::kOffRow + ((n & 1) * 2 + t) * kTile + row] = (uint8_t)(top <= 3.4e38f ? exponent - 7u : 127u);   // of 1 / by
 #pragma unroll 8
           for (int k = 0; k < D / 8; ++k) {
             const uint32_t a = at + (k >> 3) * (kTile * 128) + (((k & 7) ^ (row & 7)) << 4);
@@ -708,21 +704,21 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
               break;
             }
             if (value) k_next = scale_of(p.ks[it.r], next), v_next = scale_of(p.vs[it.r], next);
-            // A power of two not below the warp's 32 scales: they are divided
-            // by it, and the softmax knows it.
-            const float scale = value ? v_scale : k_scale;
-            const uint32_t top = __reduce_max_sync(0xffffffffu, seen ? __float_as_uint(scale) & 0x7fffffffu : 0u);
-            const uint32_t exponent = min(max((top + 0x7fffffu) >> 23, 40u), 253u);
-            if (lane == 0)
-              reinterpret_cast<float*>(gbase + C::kOffScale)[((n_step + i - it.from) % kScaleSlots) * 8 + value * 4 + (tid >> 5)] =
-                  __uint_as_float(exponent << 23);
-            const float by = scale * __uint_as_float((254u - exponent) << 23);
-            // The multiplier in two f16 parts for keys: a rounding of a key's
-            // scale would move all of its score, those of its values do not
-            // add up. For values one part.
-            const uint32_t hi = f16x2(by, by);
-            const float rest = by - half_of(hi);
-            const uint32_t lo = value ? 0u : f16x2(rest, rest);
+            // Keys stay as they are (f16 holds them), and the softmax multiplies
+            // with their scales. Values are multiplied here, with their scale
+            // over a power of two not below the warp's 32, which the softmax
+            // puts on their weights.
+            float* const scales = reinterpret_cast<float*>(gbase + C::kOffScale + ((n_step + i - it.from) % C::kScaleSlots) * C::kScaleBytes);
+            uint32_t by = 0;
+            if (value) {
+              const uint32_t top = __reduce_max_sync(0xffffffffu, seen ? __float_as_uint(v_scale) & 0x7fffffffu : 0u);
+              const uint32_t exponent = min(max((top + 0x7fffffu) >> 23, 40u), 253u);
+              if (lane == 0) scales[kTile + (tid >> 5)] = __uint_as_float(exponent << 23);
+              const float scale = v_scale * __uint_as_float((254u - exponent) << 23);
+              by = f16x2(scale, scale);
+            } else {
+              scales[tid] = seen ? k_scale : 0.f;
+            }
             // A thread's key, sixteen bytes a time (the swizzle has neighbours'
             // in other banks).
             const uint32_t from = base + C::kOffRaw + rs * C::kRawBytes, to = base + C::kOffRing + ss * C::kTileBytes;
@@ -733,7 +729,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
               uint32_t w[8] = {f16x2_of_e4m3(u.x), f16x2_of_e4m3_high(u.x), f16x2_of_e4m3(u.y), f16x2_of_e4m3_high(u.y),
                                f16x2_of_e4m3(u.z), f16x2_of_e4m3_high(u.z), f16x2_of_e4m3(u.w), f16x2_of_e4m3_high(u.w)};
 #pragma unroll
-              for (int e = 0; e < 8; ++e) w[e] = value ? mul_f16(w[e], hi) : fma_f16(w[e], hi, mul_f16(w[e], lo));
+              for (int e = 0; e < 8; ++e) w[e] = value ? mul_f16(w[e], by) : w[e];
               const uint32_t at = row_at + (k >> 2) * (value ? 8192 : kTile * 128);
               const int c16 = (k & 3) * 2;
               sts128(at + ((c16 ^ (tid & 7)) << 4), seen ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0));
@@ -779,17 +775,27 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         uint32_t v[4][32];   // the row's scores
 #pragma unroll
         for (int e = 0; e < 4; ++e) tmem_ld32(s_at + 32 * e, v[e]);
-        // In 8 bits, of each 32 keys: the power of two that their scores, and
-        // that their values, are still to be multiplied with.
-        const float* const pow2 = reinterpret_cast<const float*>(gbase + C::kOffScale) + ((n_step + i - it.from) % kScaleSlots) * 8;
+        // In 8 bits: the keys' scales, and of each 32 values the power of two
+        // that they are still to be multiplied with.
+        const uint32_t scales = base + C::kOffScale + (E8 ? (n_step + i - it.from) % C::kScaleSlots * C::kScaleBytes : 0);
         if constexpr (E8)
-          if (!any) row_factor = p.scale_log2 * to_f(reinterpret_cast<const __nv_bfloat16*>(gbase + C::kOffRow)[((n & 1) * 2 + t) * kTile + row]);
-        float factor[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) factor[e] = E8 ? row_factor * pow2[e] : row_factor;
+          if (!any) row_factor = p.scale_log2 * __uint_as_float((uint32_t)gbase[C::kOffRow + ((n & 1) * 2 + t) * kTile + row] << 23);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 4; ++e) reg_fence(v[e]);
+        if constexpr (E8) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const uint4 by = lds128(scales + (32 * e + k) * 4);
+              float a[4];
+              halves(mul2(pair_of(v[e][k], v[e][k + 1]), pair_of(by.x, by.y)), a[0], a[1]);
+              halves(mul2(pair_of(v[e][k + 2], v[e][k + 3]), pair_of(by.z, by.w)), a[2], a[3]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[e][k + j] = __float_as_uint(a[j]);
+            }
+        }
         if (key + kTile - 1 > first_pos || !(key >= last_lo || key + kTile <= p.sinks)) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -811,13 +817,9 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               tops[2 * e + (k >> 1 & 1)] = max3(tops[2 * e + (k >> 1 & 1)], __uint_as_float(v[e][k]), __uint_as_float(v[e][k + 1]));
-          if constexpr (E8) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(tops[2 * e], tops[2 * e + 1]) * factor[e]);
-          } else {
-            top = max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]), fmaxf(tops[6], tops[7])) * row_factor;
-          }
+          top = max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]), fmaxf(tops[6], tops[7])) * row_factor;
         }
+        float pow2[4];
         float by = 1.f;   // what O is rescaled with
         if (top > m + kLazy || (m == -INFINITY && top > m)) {
           by = ex2_below(m, top);
@@ -828,7 +830,9 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
           // Weights are kept over sigma, 2^-7 times the largest power of two of
           // the values so far (so they stay below 2^15 in f16); it is one for
           // all rows.
-          const float mx = fmaxf(fmaxf(pow2[4], pow2[5]), fmaxf(pow2[6], pow2[7])) * 0.0078125f;
+          const uint4 u = lds128(scales + kTile * 4);
+          pow2[0] = __uint_as_float(u.x), pow2[1] = __uint_as_float(u.y), pow2[2] = __uint_as_float(u.z), pow2[3] = __uint_as_float(u.w);
+          const float mx = fmaxf(fmaxf(pow2[0], pow2[1]), fmaxf(pow2[2], pow2[3])) * 0.0078125f;
           if (mx > sigma) {
             by *= sigma == 0.f ? 0.f : sigma / mx;
             sigma = mx;
@@ -843,8 +847,8 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
           // In 8 bits what multiplies a value is its weight times its 32's
           // power of two over sigma, which goes into the exponent; the sum is
           // of the weights alone. (Below 2^-60 nothing is left of them in f16.)
-          const int lift = E8 ? max((int)(__float_as_uint(pow2[4 + e]) >> 23) - (int)(__float_as_uint(sigma) >> 23), -60) : 0;
-          const f32x2 factor2 = pair_of(factor[e], factor[e]), down2 = pair_of(down + (float)lift, down + (float)lift);
+          const int lift = E8 ? max((int)(__float_as_uint(pow2[e]) >> 23) - (int)(__float_as_uint(sigma) >> 23), -60) : 0;
+          const f32x2 factor2 = pair_of(row_factor, row_factor), down2 = pair_of(down + (float)lift, down + (float)lift);
           f32x2 sums[2] = {0ull, 0ull};
           uint32_t w[16];
 #pragma unroll

@@ -7,9 +7,9 @@ Attention: a score is a sum of D products in fp32, off by at most (D + 8) u of t
 the 8 for the scale, the change to base 2 and the difference from the maximum), and 2^x by 2^-22 of itself; both change a
 weight and the weights' sum, so a result by twice that of `size` (the weights' sum over |v|). Sums over n keys add n u to
 each of numerator and denominator. A weight is rounded to bf16 (2^-8 of it, so 2^-8 of `size`), the result once (2^-8 of it).
-A column's 8-bit scale adds one more rounding of fp32. With more than 16 rows for a key head, an 8-bit cache's elements times
-their scales over a power of two become f16: each off by 2^-11 of it (a key's scale itself by 2^-22, a value's by 2^-11), so a
-score by 2^-11 of `far`, a result by 2^-10 of `size`. lse: the scores' and the sum's errors, and 4 u of itself.
+A column's 8-bit scale adds one more rounding of fp32. With more than 16 rows for a key head, an 8-bit cache's values times
+their scales over a power of two become f16, and so do weights: two roundings of 2^-11 in place of the
+one of 2^-8. lse: the scores' and the sum's errors, and 4 u of itself.
 """
 import numpy as np
 import pytest
@@ -120,9 +120,8 @@ def held_to_the_oracle(cache, q, o, lse, first=0):
             want, wl, size, far = P.attention(q[r][rows].reshape(m - gone, d.heads_q, d.head_dim), cache.k[r][b], cache.v[r][b], m - gone,
                                               d.window, d.sinks, d.scale or None)
             got = o[r][rows].reshape(want.shape)
-            f16 = d.cache_dtype == 1 and max(cache.new) * (d.heads_q // d.heads_k) > 16
-            score = ((d.head_dim + 8) * U + f16 * 1.01 * 2.0 ** -11) * far + 2.0 ** -22
-            bound = (2.0 ** -8 + f16 * 1.01 * 2.0 ** -10 + 2 * score[..., None] + (2 * n + 8) * U) * size + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7)
+            score = (d.head_dim + 8) * U * far + 2.0 ** -22
+            bound = (2.0 ** -8 + 2 * score[..., None] + (2 * n + 8) * U) * size + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7)
             assert np.all(np.abs(got - want) <= bound), (b, r, np.max(np.abs(got - want) / np.maximum(bound, 1e-300)))
             if lse is not None:
                 off = score + (n + 8) * U + 4 * U * np.abs(wl)

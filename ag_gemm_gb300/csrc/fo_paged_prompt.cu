@@ -117,9 +117,13 @@ struct Steps {
 
 // ---- the plan: one block lists the items of a key head.
 //
-// A pair of more steps than an even share among twice the SMs is cut into
-// parts, which a third kernel joins: without that a few long pairs (chunks of
-// prompts on long prefixes, drafted tokens) left most of the GPU idle.
+// A pair of more steps than an SM's share of one and a half times what is still
+// to be dealt (but never of fewer than an even share among twice the SMs) is cut
+// into parts, which a third kernel joins: without that a few long pairs (chunks of
+// prompts on long prefixes, drafted tokens) left most of the GPU idle. What is
+// dealt early may be long, so few pairs are cut: with twice the SMs' even share
+// as the limit of all, 8-bit chunks took 92 us, not 84, and 40 rows over 65536
+// tokens 42, not 36 (64 contexts of up to 8192, on the other hand, 105, not 110).
 constexpr int kLeastSteps = 4;
 constexpr int kSharesPerSm = 2;
 // Parts of pairs that are cut, at most: sum of ceil(n / L) over pairs of n > L
@@ -210,21 +214,28 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const __grid_constant
   };
   long long mine = 0;
   visit([&](Record&, int n) { mine += max(n, 1); });
-  block_scan(mine, sums, &steps);
-  const long long shares = (long long)kSharesPerSm * p.sms;
-  const int most = (int)min((long long)INT32_MAX, max((steps * p.R * p.heads_k + shares - 1) / shares, (long long)kLeastSteps));
+  const long long dealt = block_scan(mine, sums, &steps) - mine, shares = (long long)kSharesPerSm * p.sms;
+  const long long least = max((steps * p.R * p.heads_k + shares - 1) / shares, (long long)kLeastSteps);
+  long long left;   // steps from a pair on
+  auto parts_of = [&](int n) {
+    const long long most = max(3 * left * p.R * p.heads_k / (2 * p.sms), least);
+    left -= max(n, 1);
+    return n > most ? (int)((n + most - 1) / most) : 1;
+  };
   // Items, and in the upper half of the number parts; cut pairs by themselves.
   long long my_items = 0, my_parts = 0;
+  left = steps - dealt;
   visit([&](Record&, int n) {
-    const int k = n > most ? (n + most - 1) / most : 1;
+    const int k = parts_of(n);
     my_items += k;
     my_parts += k > 1 ? ((long long)k << 32) + 1 : 0;
   });
   long long at = block_scan(my_items, sums, &items) - my_items, both = block_scan(my_parts, sums, &parts) - my_parts;
   cuts = parts & 0xffffffffll, parts >>= 32;
   long long cut = both & 0xffffffffll, slot = both >> 32;
+  left = steps - dealt;
   visit([&](Record& it, int n) {
-    const int k = n > most ? (n + most - 1) / most : 1;
+    const int k = parts_of(n);
     it.parts = k, it.part = 0;
     it.slot = (int)slot;
     it.from = 0, it.to = n;
@@ -242,10 +253,10 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const __grid_constant
   __syncthreads();
   for (long long c = tid >> 5; c < (items <= p.most_items ? cuts : 0); c += 32) {
     Record it = p.cut[c];
-    const int n = it.to, k = it.parts, q = (n + k - 1) / k;
+    const int n = it.to, k = it.parts, q = n / k, more = n - q * k;   // the first `more` have a step more
     for (int i = tid & 31; i < k; i += 32) {
       it.part = i;
-      it.from = min(i * q, n), it.to = min((i + 1) * q, n);
+      it.from = i * q + min(i, more), it.to = it.from + q + (i < more);
       p.items[it.at + i] = it;
     }
   }

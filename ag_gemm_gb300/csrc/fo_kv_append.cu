@@ -263,8 +263,8 @@ fo_status check_paged(const fo_paged_desc* d) {
 fo_status check_batch(const fo_paged_desc* d, const fo_paged_batch* b, int64_t rows) {
   if (!b) return FO_ERR_INVALID_ARG;
   if (rows < 0 || rows > INT32_MAX || b->seqs < 0 || b->max_new < 1) return FO_ERR_SHAPE;
-  if (b->pages < 1 || b->pages > INT32_MAX / d->heads_k || b->table_cols < 1 || b->table_cols > INT32_MAX / d->page)
-    return FO_ERR_SHAPE;
+  if (b->pages < 1 || b->pages > INT32_MAX / d->heads_k || b->table_cols < 1 || b->table_cols > (1 << 30) / d->page)
+    return FO_ERR_SHAPE;   // (positions, and a tile beyond them, are 32-bit numbers)
   if (!b->starts && (b->max_new != 1 || b->seqs > rows)) return FO_ERR_SHAPE;
   if ((int64_t)b->seqs * d->R * d->heads_k > INT32_MAX) return FO_ERR_SHAPE;
   if (b->seqs && rows) {

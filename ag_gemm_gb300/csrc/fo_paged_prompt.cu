@@ -28,6 +28,14 @@
 // A first kernel of one block lists the items; blocks take them from a
 // counter, the last (under the causal mask the costliest) first. A third joins
 // the parts of pairs of tiles that were cut.
+//
+// 8 ranks of 8192 tokens with 4 heads, causal, take 398 us, 1.38 PFLOP/s of the
+// products that are seen (tensor pipe 65% of its cycles); 8192 tokens with a
+// window of 1024 + 4 and 32 + 8 heads 142 us, 0.91 PFLOP/s: a step's two tiles
+// are bound by the tensor core (2100 cycles of 2048), an item's end and start
+// (some 5500 cycles, ten steps apart) are not hidden, since two tiles' scores and
+// outputs fill TMEM. Chunks of up to 1030 tokens of 8 bits, D = 64, take 84 us:
+// at D = 64 the exponentials are as long as both products.
 #include <cudaTypedefs.h>
 #include <math.h>
 #include <string.h>

@@ -663,7 +663,7 @@ typedef struct {
   int32_t seqs;               /* >= 0 */
   int32_t max_new;            /* the most new tokens of a sequence; 1 without starts */
   int64_t pages;              /* pages of a cache; pages * heads_k below 2^31 */
-  int64_t table_cols;         /* entries of a sequence's row of the table; table_cols * page below 2^31 */
+  int64_t table_cols;         /* entries of a sequence's row of the table; table_cols * page at most 2^30 */
   const int32_t* lengths;     /* [seqs]; 0 (or less): a sequence that is not there */
   const int32_t* starts;      /* [seqs + 1], or NULL */
   const int32_t* table;       /* [seqs x table_cols] */
@@ -702,16 +702,17 @@ fo_status fo_kv_append(const fo_paged_desc* desc, const fo_rope_desc* rope, cons
  * f16 instead (by at most 2^-11 of each; values whose scale is below 2^-87 may
  * count as zero). A row that sees nothing (a sequence that is not
  * there, a token before its beginning), or whose scores are all -infinity, gets
- * o = 0 and lse = -infinity. Rows
- * that no sequence has are left as they were. Neither places behind a
- * sequence's length nor pages that hold nothing any new token of it sees are
- * looked at: their entries of the table may be anything, their places may hold
- * NaN. (An infinity or NaN among the values that one new token of a sequence
- * sees may reach the sequence's others, which see less.) q, o: rows ld[0..1] elements apart (a multiple of 8; 16-byte aligned),
- * head h at h * head_dim; caches and scales 16-byte aligned; lse (may be NULL)
+ * o = 0 and lse = -infinity. Rows that no sequence has are left as they were.
+ * Neither places behind a sequence's length nor pages that hold nothing any new
+ * token of it sees are looked at: their entries of the table may be anything,
+ * their places may hold NaN. (An infinity or NaN among the values that one new
+ * token of a sequence sees may reach the sequence's others, which see less.)
+ * q, o: rows ld[0..1] elements apart (a multiple of 8; 16-byte aligned), head h
+ * at h * head_dim; caches and scales 16-byte aligned; lse (may be NULL)
  * [rows x heads_q] fp32. o must not overlap q. ws: fo_paged_attention_workspace
  * bytes, 16-byte aligned, zeroed once by fo_ops_workspace_init; one call per
- * workspace may be in flight. Results repeat bit for bit. One launch where
+ * workspace may be in flight, and one whose waits ran out (FO_ERR_TIMEOUT) is
+ * zeroed anew. Results repeat bit for bit. One launch where
  * max_new * heads_q / heads_k is at most 16, else three: the cache's length is
  * split in the one, prompts are cut into tiles in the others. */
 fo_status fo_paged_attention(const fo_paged_desc* desc, const fo_paged_batch* batch, int64_t rows,

@@ -119,6 +119,14 @@ def test_bad_batches_are_refused(kw, code):
     assert append(b=batch(**kw)) == attention(b=batch(**kw)) == code
 
 
+def test_as_many_entries_as_positions_have_numbers_for():
+    for page in (16, 64, 256):
+        most = 2 ** 30 // page
+        for call in (append, attention):
+            assert call(desc(page=page), batch(table_cols=most), q=[257]) == B.FO_ERR_ALIGN     # (what is checked next)
+            assert call(desc(page=page), batch(table_cols=most + 1), q=[257]) == B.FO_ERR_SHAPE
+
+
 def test_bad_arguments_are_refused():
     for call, names in ((append, ("q", "k", "v", "q_out", "k_cache", "v_cache")), (attention, ("q", "k_cache", "v_cache", "o"))):
         assert call(rows=-1) == call(rows=2 ** 31) == call(rows=2) == B.FO_ERR_SHAPE

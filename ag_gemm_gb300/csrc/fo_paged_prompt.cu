@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const __grid_constant
   visit([&](Record&, int n) { mine += max(n, 1); });
   const long long dealt = block_scan(mine, sums, &steps) - mine, shares = (long long)kSharesPerSm * p.sms;
   const long long least = max((steps * p.R * p.heads_k + shares - 1) / shares, (long long)kLeastSteps);
-  long long left;   // steps from a pair on
+  long long left = 0;   // steps from a pair on
   auto parts_of = [&](int n) {
     const long long most = max(3 * left * p.R * p.heads_k / (2 * p.sms), least);
     left -= max(n, 1);

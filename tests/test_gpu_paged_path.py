@@ -370,3 +370,60 @@ def test_calls_without_the_native_marshalling_are_the_same(dev, monkeypatch):
             got.append(kc + vc + (ks or []) + (vs or []) + out)
         assert all(torch.equal(bits(a), bits(b)) for a, b in zip(*got))
         monkeypatch.undo()
+
+
+MANY_SEQUENCES = [  # seqs, new, longest, heads_q, heads_k, D, page: more than a block of the plan has threads, and pairs than that
+    (400, 1, 150, 4, 2, 64, 16),
+    (1800, 3, 60, 8, 1, 64, 16),
+    (1024, 5, 40, 4, 1, 128, 32),
+    (1100, 1, 90, 2, 2, 128, 16),
+]
+
+
+@pytest.mark.parametrize("kept", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", MANY_SEQUENCES)
+def test_many_sequences(dev, case, kept):
+    seqs, most, longest, hq, hk, D, page = case
+    g = np.random.default_rng(seqs)
+    lengths = [int(n) for n in g.integers(0, longest + 1, seqs)]
+    new = [int(m) for m in g.integers(0, most + 1, seqs)] if most > 1 else [1] * seqs
+    new = [min(m, n) if most > 1 else m for m, n in zip(new, lengths)]
+    new[-1] = max(new[-1], 1)
+    cache, q, o, ws, call = problem(dev, kept, lengths, new, seed=5, hq=hq, hk=hk, D=D, R=1, page=page)
+    call()
+    assert B.fo_ops_status_query(ws) == (0, [0, 0, 0, 0])
+    held_to_the_oracle(cache, [f64(x) for x in q], [f64(x) for x in o], None)
+
+
+@pytest.mark.parametrize("kept", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (5, 2 ** 31 - 1), (0, 2 ** 31 - 1), (1, 1)])
+@pytest.mark.parametrize("new", [[1, 1], [90, 33]])
+def test_the_largest_windows_and_sinks(dev, kept, window, sinks, new):
+    cache, q, o, ws, call = problem(dev, kept, [200, 33], new, hq=4, hk=2, D=64, R=1, window=window, sinks=sinks)
+    call()
+    assert B.fo_ops_status_query(ws)[0] == 0
+    held_to_the_oracle(cache, [f64(x) for x in q], [f64(x) for x in o], None)
+
+
+@pytest.mark.parametrize("kept", ["bf16", "e4m3"])
+def test_sixteen_ranks_prompts(dev, kept):
+    cache, q, o, ws, call = problem(dev, kept, [150, 0, 20], [40, 0, 20], hq=3, hk=1, D=64, R=16)
+    call()
+    assert B.fo_ops_status_query(ws)[0] == 0
+    held_to_the_oracle(cache, [f64(x) for x in q], [f64(x) for x in o], None)
+
+
+def test_a_batch_in_which_nothing_is_new_touches_nothing(dev):
+    d = B.fo_paged_desc(32, 2, page=16)
+    cache = Cache(dev, d, [40, 0, 7], [1, 0, 1])
+    for starts, lengths in (([0, 0, 0, 0], [40, 0, 7]), ([0, 0, 0, 0], [0, 0, 0]), ([3, 3, 3, 3], [0, 5, 0])):
+        batch = B.fo_paged_batch(whole(lengths, dev), cache.table, cache.pages, starts=whole(starts, dev), max_new=8)
+        o = [torch.full((6, 32 * 128), NAN, dtype=BF, device=dev)]
+        ws = workspace(dev, d, batch, 6)
+        B.fo_paged_attention(d, batch, 6, [torch.ones_like(o[0])], cache.kc, cache.vc, o, ws)
+        assert B.fo_ops_status_query(ws)[0] == 0 and torch.isnan(o[0].float()).all()
+        kept = [x.clone() for x in cache.kc + cache.vc]
+        part = [torch.ones(6, 256, dtype=BF, device=dev)]
+        B.fo_kv_append(d, None, batch, 6, [torch.ones_like(o[0])], part, part, o, cache.kc, cache.vc, ws=ws)
+        assert B.fo_ops_status_query(ws)[0] == 0 and torch.isnan(o[0].float()).all()
+        assert all(torch.equal(bits(a), bits(b)) for a, b in zip(kept, cache.kc + cache.vc))

@@ -427,3 +427,24 @@ def test_a_batch_in_which_nothing_is_new_touches_nothing(dev):
         B.fo_kv_append(d, None, batch, 6, [torch.ones_like(o[0])], part, part, o, cache.kc, cache.vc, ws=ws)
         assert B.fo_ops_status_query(ws)[0] == 0 and torch.isnan(o[0].float()).all()
         assert all(torch.equal(bits(a), bits(b)) for a, b in zip(kept, cache.kc + cache.vc))
+
+
+@pytest.mark.parametrize("spread", [4, 20, 30])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_values_of_all_magnitudes_in_8_bits(dev, spread, new):
+    """Scales of tokens 2^spread above and below one: weights times scales, and values in the prompts' kernel, are f16, each
+    off by 2^-11 of it, or, below 2^-14 with the largest magnitude at 2^8 (values) and 2^15 (weights times scales), by
+    2^-25: 2^-31 of the largest value at most, both together."""
+    hq, D, n = 8, 128, 300
+    cache, q, o, ws, call = problem(dev, "e4m3", [n], [new], seed=1, hq=hq, hk=1, D=D, R=1, page=16)
+    g = torch.Generator().manual_seed(2)
+    mult = torch.exp2(torch.randint(-spread, spread + 1, (n,), generator=g).float())
+    pg, slot = P.places(cache.table_all[0], n, 16)
+    pg, slot = torch.from_numpy(pg.astype(np.int64)).to(dev), torch.from_numpy(slot).to(dev)
+    cache.vs[0][pg, :, slot] *= mult.to(dev)[:, None]
+    values = cache.v[0][0] * mult.double().numpy()[:, None, None]
+    call()
+    want, _, size, far = P.attention(f64(q[0]).reshape(new, hq, D), cache.k[0][0], values, new, 0, 0)
+    score = (D + 8) * U * far + 2.0 ** -22
+    bound = (2.0 ** -10 + 2 * score[..., None] + (2 * n + 8) * U) * size + 2.0 ** -31 * np.abs(values).max() + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7)
+    assert np.all(np.abs(f64(o[0]).reshape(want.shape) - want) <= bound)

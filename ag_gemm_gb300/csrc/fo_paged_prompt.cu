@@ -30,11 +30,13 @@
 // the parts of pairs of tiles that were cut.
 //
 // 8 ranks of 8192 tokens with 4 heads, causal, take 398 us, 1.38 PFLOP/s of the
-// products that are seen (tensor pipe 65% of its cycles); 8192 tokens with a
-// window of 1024 + 4 and 32 + 8 heads 142 us, 0.91 PFLOP/s: a step's two tiles
-// are bound by the tensor core (2100 cycles of 2048), an item's end and start
-// (some 5500 cycles, ten steps apart) are not hidden, since two tiles' scores and
-// outputs fill TMEM. Chunks of up to 1030 tokens of 8 bits, D = 64, take 84 us:
+// products that are seen: a step of two tiles takes some 3000 cycles, 2048 of
+// them the tensor core's, since a tile's softmax with what it waits for is longer
+// than the other tile's products. 8192 tokens with a window of 1024 + 4 and 32 +
+// 8 heads take 142 us, 0.91 PFLOP/s: items of ten or eleven steps, whose ends and
+// starts are not hidden (two tiles' scores and outputs fill TMEM), and a fifth of
+// the products masked. Begun with the first 64 keys' weights, the weighted sum
+// made the one 392 us and the other 146. Chunks of up to 1030 tokens of 8 bits, D = 64, take 84 us:
 // at D = 64 the exponentials are as long as both products.
 #include <cudaTypedefs.h>
 #include <math.h>

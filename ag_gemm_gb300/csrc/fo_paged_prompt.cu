@@ -29,14 +29,16 @@
 // counter, the last (under the causal mask the costliest) first. A third joins
 // the parts of pairs of tiles that were cut.
 //
-// 8 ranks of 8192 tokens with 4 heads, causal, take 398 us, 1.38 PFLOP/s of the
+// 8 ranks of 8192 tokens with 4 heads, causal, take 395 us, 1.39 PFLOP/s of the
 // products that are seen: a step of two tiles takes some 3000 cycles, 2048 of
 // them the tensor core's, since a tile's softmax with what it waits for is longer
 // than the other tile's products. 8192 tokens with a window of 1024 + 4 and 32 +
-// 8 heads take 142 us, 0.91 PFLOP/s: items of ten or eleven steps, whose ends and
+// 8 heads take 141 us, 0.92 PFLOP/s: items of ten or eleven steps, whose ends and
 // starts are not hidden (two tiles' scores and outputs fill TMEM), and a fifth of
 // the products masked. Begun with the first 64 keys' weights, the weighted sum
-// made the one 392 us and the other 146. Chunks of up to 1030 tokens of 8 bits, D = 64, take 84 us:
+// made the one 392 us and the other 146. The loop's length counts: rescaling
+// written out for all columns, which seldom runs, cost the one 4 us, and a branch
+// around weights of 32 keys that no row sees 10. Chunks of up to 1030 tokens of 8 bits, D = 64, take 84 us:
 // at D = 64 the exponentials are as long as both products.
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -891,9 +893,9 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         }
         if (any && __any_sync(0xffffffffu, by != 1.f)) {
           // (These scores come after the sums before them in the issuer's
-          // order: those are done.)
+          // order: those are done.) Seldom, so in a loop: see above.
           const f32x2 by2 = pair_of(by, by);
-#pragma unroll
+#pragma unroll 1
           for (int e = 0; e < D / 32; ++e) {
             uint32_t o[32];
             tmem_ld32(o_at + 32 * e, o);

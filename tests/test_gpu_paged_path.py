@@ -448,3 +448,12 @@ def test_values_of_all_magnitudes_in_8_bits(dev, spread, new):
     score = (D + 8) * U * far + 2.0 ** -22
     bound = (2.0 ** -10 + 2 * score[..., None] + (2 * n + 8) * U) * size + 2.0 ** -31 * np.abs(values).max() + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7)
     assert np.all(np.abs(f64(o[0]).reshape(want.shape) - want) <= bound)
+
+
+@pytest.mark.parametrize("batch", [FEW, MANY])
+def test_a_workspace_that_is_too_small_is_refused(dev, batch):
+    cache, q, o, ws, call = problem(dev, "bf16", *batch)
+    with pytest.raises(ValueError, match="smaller"):
+        call(ws=ws[:-1])
+    call()
+    assert B.fo_ops_status_query(ws)[0] == 0

@@ -714,6 +714,11 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         float k_scale = scale_of(p.ks[it.r], next), v_scale = scale_of(p.vs[it.r], next);
         for (int i = it.from; i < it.to && ok; ++i) {
           const bool seen = st.any(st.block(i) * kTile + tid);
+          // A power of two not below the scales of the warp's 32 values. It goes
+          // out with the keys: the softmax reads it when it has the step's scores,
+          // which wait for the keys alone.
+          const uint32_t top = __reduce_max_sync(0xffffffffu, seen ? __float_as_uint(v_scale) & 0x7fffffffu : 0u);
+          const uint32_t exponent = min(max((top + 0x7fffffu) >> 23, 40u), 253u);
           next = place_of(i + 1);
           float k_next = 0.f, v_next = 0.f;
 #pragma unroll 1
@@ -729,18 +734,15 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
             if (value) k_next = scale_of(p.ks[it.r], next), v_next = scale_of(p.vs[it.r], next);
             // Keys stay as they are (f16 holds them), and the softmax multiplies
             // with their scales. Values are multiplied here, with their scale
-            // over a power of two not below the warp's 32, which the softmax
-            // puts on their weights.
-            float* const scales = reinterpret_cast<float*>(gbase + C::kOffScale + ((n_step + i - it.from) % C::kScaleSlots) * C::kScaleBytes);
+            // over the power of two, which the softmax puts on their weights.
             uint32_t by = 0;
             if (value) {
-              const uint32_t top = __reduce_max_sync(0xffffffffu, seen ? __float_as_uint(v_scale) & 0x7fffffffu : 0u);
-              const uint32_t exponent = min(max((top + 0x7fffffu) >> 23, 40u), 253u);
-              if (lane == 0) scales[kTile + (tid >> 5)] = __uint_as_float(exponent << 23);
               const float scale = v_scale * __uint_as_float((254u - exponent) << 23);
               by = f16x2(scale, scale);
             } else {
+              float* const scales = reinterpret_cast<float*>(gbase + C::kOffScale + ((n_step + i - it.from) % C::kScaleSlots) * C::kScaleBytes);
               scales[tid] = seen ? k_scale : 0.f;
+              if (lane == 0) scales[kTile + (tid >> 5)] = __uint_as_float(exponent << 23);
             }
             // A thread's key, sixteen bytes a time (the swizzle has neighbours'
             // in other banks).

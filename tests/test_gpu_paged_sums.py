@@ -1,0 +1,144 @@
+"""What the attention over a paged cache carries from one tile of keys to the next: running maxima and sums, the powers of two
+of an 8-bit cache's values, outputs that are rescaled; in single tiles, in items of many steps and in blocks with many
+tiles, against the fp64 oracle.
+
+Tolerances are the ones of the operator's own tests (test_gpu_paged.py), and of an 8-bit cache what its roundings leave:
+weights become f16 (2^-11 of each), with more than 16 rows for a key head the values too, times their scale over a power of
+two: the scale's share once and the product once (2^-11 each). Below f16's least normal number a weight, or a
+value's scale, is off by 2^-25 of a range whose top is 2^15 (or 2^7) times a power of two not below the largest scale of the
+values seen: with an e4m3 value of up to 448, 2^-31 of the largest value at most, for each value that the row sees. A
+query's row becomes f16 with its largest magnitude in [128, 256): 2^-32 of that.
+"""
+import numpy as np
+import pytest
+import torch
+
+from ag_gemm_gb300 import binding as B
+from oracle import paged as P
+from test_gpu_paged import BF, E4M3, NAN, U, f64, first_rows, whole, workspace
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    import __graft_entry__
+    __graft_entry__.build()
+    assert torch.cuda.is_available(), "GPU tests need a GB300"
+    return torch.device("cuda:0")
+
+
+class Kept:
+    """R ranks' caches of keys(r, b) and values(r, b), [length, heads_k, D]; self.k, self.v: what they stand for in fp64."""
+
+    def __init__(self, dev, d, lengths, keys, values, seed=0):
+        self.d, self.lengths, page = d, lengths, d.page
+        cols = max(-(-n // page) for n in lengths)
+        need = sum(-(-n // page) for n in lengths)
+        self.pages = need + 2
+        order = torch.randperm(self.pages, generator=torch.Generator().manual_seed(seed))[:need].tolist()
+        table = np.full((len(lengths), cols), -7, dtype=np.int32)
+        for b, n in enumerate(lengths):
+            held = -(-n // page)
+            table[b, :held], order = order[:held], order[held:]
+        eight = d.cache_dtype == 1
+        shape = (self.pages, d.heads_k, page, d.head_dim)
+        fresh = (lambda: torch.full(shape, 0x7F, dtype=torch.uint8, device=dev).view(E4M3)) if eight else \
+            (lambda: torch.full(shape, NAN, dtype=BF, device=dev))
+        self.kc, self.vc = ([fresh() for _ in range(d.R)] for _ in range(2))
+        scales = lambda: [torch.full(shape[:3], NAN, device=dev) for _ in range(d.R)] if eight else None  # noqa: E731
+        self.ks, self.vs = scales(), scales()
+        self.k, self.v = ([[] for _ in range(d.R)] for _ in range(2))
+        for b, n in enumerate(lengths):
+            pg, slot = (torch.from_numpy(x.astype(np.int64)).to(dev) for x in P.places(table[b], n, page))
+            for r in range(d.R):
+                for c, s, held, x in ((self.kc, self.ks, self.k, keys(r, b)), (self.vc, self.vs, self.v, values(r, b))):
+                    if eight:
+                        scale = (x.abs().amax(dim=2) / 448.0).clamp(min=2.0 ** -126)
+                        q = (x / scale[..., None]).to(E4M3)
+                        c[r].view(torch.uint8)[pg, :, slot] = q.view(torch.uint8).to(dev)
+                        s[r][pg, :, slot] = scale.to(dev)
+                        x = q.double() * scale[..., None].double()
+                    else:
+                        x = x.to(BF)
+                        c[r][pg, :, slot] = x.to(dev)
+                    held[r].append(x.double().numpy())
+        self.table = torch.from_numpy(table).to(dev)
+
+
+def attend(dev, cache, new, q):
+    """Results [r] of o [rows, heads * D] and lse [rows, heads]; two calls give the same bits."""
+    d, rows = cache.d, sum(new)
+    batch = B.fo_paged_batch(whole(cache.lengths, dev), cache.table, cache.pages, starts=whole(first_rows(new), dev), max_new=max(new))
+    q = [x.to(dev) for x in q]
+    o = [torch.full((rows, d.heads_q * d.head_dim), NAN, dtype=BF, device=dev) for _ in range(d.R)]
+    lse = [torch.full((rows, d.heads_q), NAN, device=dev) for _ in range(d.R)]
+    ws = workspace(dev, d, batch, rows)
+    got = []
+    for _ in range(2):
+        B.fo_paged_attention(d, batch, rows, q, cache.kc, cache.vc, o, ws, cache.ks, cache.vs, lse)
+        assert B.fo_ops_status_query(ws) == (0, [0, 0, 0, 0])
+        got.append([x.clone() for x in o + lse])
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*got))
+    return [f64(x) for x in o], [f64(x) for x in lse]
+
+
+def held_to_the_oracle(cache, new, q, o, lse, rows_each=None, seed=0):
+    """All rows against the oracle, or `rows_each` of each sequence, the first and the last among them."""
+    d, at = cache.d, 0
+    prompts = max(new) * (d.heads_q // d.heads_k) > 16
+    g = np.random.default_rng(seed)
+    for b, (n, m) in enumerate(zip(cache.lengths, new)):
+        some = np.arange(m) if rows_each is None or rows_each >= m else \
+            np.unique(np.concatenate([[0, m - 1], g.integers(0, m, rows_each - 2)]))
+        seen = P.sees(n, m, d.window, d.sinks).any(axis=0)
+        for r in range(d.R):
+            k, v = cache.k[r][b], cache.v[r][b]
+            group = d.heads_q // d.heads_k
+            top = np.repeat(np.abs(v[seen]).max(axis=(0, 2)), group)[:, None]     # of a key head's values that are seen
+            for i in some:
+                p = n - m + i
+                mine = f64(q[r][at + i]).reshape(1, d.heads_q, d.head_dim)
+                want, wl, size, far = (x[0] for x in P.attention(mine, k[:p + 1], v[:p + 1], 1, d.window, d.sinks, d.scale or None))
+                count = int(P.sees(p + 1, 1, d.window, d.sinks).sum())
+                score, weights, least = (d.head_dim + 8) * U * far + 2.0 ** -22, 2.0 ** -8, 0.0
+                if d.cache_dtype == 1:
+                    key = np.repeat(np.abs(k[:p + 1]).sum(axis=2).max(axis=0), group)
+                    score = score + 2.0 ** -32 * np.abs(mine[0]).max(axis=1) * key * (d.scale or d.head_dim ** -0.5)
+                    weights, least = (3 if prompts else 1) * 2.0 ** -11 * (1 + 2.0 ** -9), count * 2.0 ** -31
+                bound = (weights + 2 * score[:, None] + (2 * n + 8) * U) * size + least * top + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7)
+                got = o[r][at + i].reshape(want.shape)
+                assert np.all(np.abs(got - want) <= bound), (b, r, i, np.max(np.abs(got - want) / np.maximum(bound, 1e-300)))
+                off = score + (n + 8) * U + 4 * U * np.abs(wl)
+                assert np.all(np.abs(lse[r][at + i] - wl) <= off), (b, r, i, np.max(np.abs(lse[r][at + i] - wl) / off))
+        at += m
+
+
+def draws(seed, hk, D, lengths):
+    """A function of (rank, sequence) with standard normal keys or values [length, hk, D]."""
+    def one(r, b):
+        return torch.randn(lengths[b], hk, D, generator=torch.Generator().manual_seed(seed * 1000 + r * 100 + b))
+    return one
+
+
+def queries(seed, d, rows):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(rows, d.heads_q * d.head_dim, generator=g).to(BF) for _ in range(d.R)]
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 0), (200, 33)])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64)])
+def test_each_32_values_of_an_8_bit_cache_have_a_power_of_two_of_their_own(dev, D, page, window, sinks):
+    """It is the step's own, and there when the step's weights are made, whatever the steps before had in its place."""
+    lengths, new, hq, hk, R = [1500, 700, 90], [900, 64, 90], 8, 2, 2
+    d = B.fo_paged_desc(hq, hk, head_dim=D, R=R, page=page, cache="e4m3", window=window, sinks=sinks)
+    normal = draws(3, hk, D, lengths)
+    g = torch.Generator().manual_seed(4)
+    powers = torch.randint(-8, 9, (max(lengths) // 32 + 1, R), generator=g).float()
+
+    def values(r, b):
+        return normal(r, b) * torch.exp2(powers[:, r].repeat_interleave(32)[:lengths[b]])[:, None, None]
+    cache = Kept(dev, d, lengths, draws(5, hk, D, lengths), values)
+    q = queries(6, d, sum(new))
+    o, lse = attend(dev, cache, new, q)
+    held_to_the_oracle(cache, new, q, o, lse, rows_each=60)

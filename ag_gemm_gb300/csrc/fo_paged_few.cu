@@ -315,10 +315,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
       }
     }
     float o[D / 16][NT][4], m[NT][2], l[NT][2];
+    float factor[NT][2], down[NT][2];     // a weight is 2^(score factor + down)
     float sigma = 0.f, sigma_inv = 0.f;   // what the values' scales are divided by (a power of two), and its reciprocal
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
+      factor[i][0] = qscale[i][0], factor[i][1] = qscale[i][1], down[i][0] = down[i][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
     }
@@ -431,6 +433,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
           if (mx > m[t][a] + kLazy || (m[t][a] == -INFINITY && mx > m[t][a])) {
             by[t][a] = ex2_below(m[t][a], mx);
             m[t][a] = mx;
+            const float less = held_back<E8>(mx);
+            factor[t][a] = qscale[t][a] * less, down[t][a] = -mx * less;
             l[t][a] *= by[t][a];
             grown = true;
           }
@@ -474,8 +478,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
           if constexpr (E8) v_scale = lds_f(scales + cslot * (C::kStep * 4) + (16 * i + 8 * e + g) * 4) * sigma_inv;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const float down0 = m[t][0] == -INFINITY ? 0.f : -m[t][0], down1 = m[t][1] == -INFINITY ? 0.f : -m[t][1];
-            float w0 = ex2(fmaf(sc[i][t][2 * e], qscale[t][0], down0)), w1 = ex2(fmaf(sc[i][t][2 * e + 1], qscale[t][1], down1));
+            float w0 = ex2(fmaf(sc[i][t][2 * e], factor[t][0], down[t][0])), w1 = ex2(fmaf(sc[i][t][2 * e + 1], factor[t][1], down[t][1]));
             l[t][0] += w0, l[t][1] += w1;
             if constexpr (E8) {
               w0 = part && w0 == 0.f ? 0.f : w0 * v_scale;

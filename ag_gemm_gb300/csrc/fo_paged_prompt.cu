@@ -865,7 +865,9 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         }
         // Weights, over the scores' first 64 columns (the row's scores are in
         // registers), and their sum.
-        const float down = m == -INFINITY ? 0.f : -m;
+        // (Held back anew each step, which costs 1%; kept from when m moves, 2%.)
+        const float less = held_back<E8>(m);
+        const float factor = m == -INFINITY ? row_factor : row_factor * less, down = m == -INFINITY ? 0.f : -m * less;
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -873,7 +875,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
           // power of two over sigma, which goes into the exponent; the sum is
           // of the weights alone. (Below 2^-60 nothing is left of them in f16.)
           const int lift = E8 ? max((int)(__float_as_uint(pow2[e]) >> 23) - (int)(__float_as_uint(sigma) >> 23), -60) : 0;
-          const f32x2 factor2 = pair_of(row_factor, row_factor), down2 = pair_of(down + (float)lift, down + (float)lift);
+          const f32x2 factor2 = pair_of(factor, factor), down2 = pair_of(down + (float)lift, down + (float)lift);
           f32x2 sums[2] = {0ull, 0ull};
           uint32_t w[16];
 #pragma unroll

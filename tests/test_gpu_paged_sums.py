@@ -142,3 +142,50 @@ def test_each_32_values_of_an_8_bit_cache_have_a_power_of_two_of_their_own(dev, 
     q = queries(6, d, sum(new))
     o, lse = attend(dev, cache, new, q)
     held_to_the_oracle(cache, new, q, o, lse, rows_each=60)
+
+
+@pytest.mark.parametrize("power", [20, 24, 27, 31, 40, 100])
+@pytest.mark.parametrize("kept", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_scores_of_any_magnitude_have_weights_that_are_numbers(dev, kept, new, power):
+    """Queries 2^power times ordinary ones, some rows of them, beside ordinary rows."""
+    hq, D, lengths = 8, 64, [900, 70]
+    d = B.fo_paged_desc(hq, 1, head_dim=D, page=16, cache=kept)
+    cache = Kept(dev, d, lengths, draws(1, 1, D, lengths), draws(2, 1, D, lengths))
+    q = queries(3, d, 2 * new)
+    for x in q:
+        x[::2] *= 2.0 ** power
+    o, lse = attend(dev, cache, [new, new], q)
+    held_to_the_oracle(cache, [new, new], q, o, lse)
+
+
+@pytest.mark.parametrize("power", [10, 20, 30, 40, 60])
+@pytest.mark.parametrize("kept", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_of_large_scores_without_roundings_the_largest_takes_all(dev, kept, new, power):
+    """Queries and keys that are powers of two at one place each: scores are exact, and 2^power apart at least."""
+    hq, D, n = 8, 64, 500
+    d = B.fo_paged_desc(hq, 1, head_dim=D, page=16, cache=kept, scale=1.0)
+    place = torch.randint(0, D, (n,), generator=torch.Generator().manual_seed(1))
+
+    def keys(r, b):
+        x = torch.zeros(n, 1, D)
+        x[torch.arange(n), 0, place] = -448.0 * 2.0 ** (torch.arange(n) % 5 - 8)
+        return x
+    cache = Kept(dev, d, [n], keys, draws(2, 1, D, [n]))
+    q = torch.zeros(new, hq, D)
+    for i in range(new):
+        for h in range(hq):
+            q[i, h] = 2.0 ** power / 1.75
+            q[i, h, place[(7 * i + 13 * h) % (n - new)]] = 0
+    q = q.to(BF)
+    o, lse = attend(dev, cache, [new], [q.view(new, -1)])
+    for i in range(new):
+        for h in range(hq):
+            s = f64(q[i, h]) @ cache.k[0][0][:n - new + i + 1, 0].T
+            top = np.flatnonzero(s == s.max())
+            want = cache.v[0][0][top, 0].mean(axis=0)
+            size = np.abs(cache.v[0][0][top, 0]).mean(axis=0)
+            got = o[0][i].reshape(hq, D)[h]
+            assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + (2 * n + 8) * U) * size + 2.0 ** -25)
+            assert abs(lse[0][i, h] - s.max() - np.log(len(top))) <= (n + 8) * U + 4 * U * abs(s.max() + np.log(len(top)))

@@ -2,6 +2,10 @@
 // a batch, and who sees whom.
 #pragma once
 
+#include <math.h>
+
+#include <algorithm>
+
 #include "fo_device.cuh"
 #include "fo_ops.h"
 
@@ -84,6 +88,14 @@ constexpr int kMostParts = 4 * FO_GB300_SMS;       // of the prompts' kernel
 constexpr size_t kFewCountBytes = (kFewBlocks * FO_GB300_SMS * 3 * 4 + 255) / 256 * 256;
 constexpr size_t kScratchAt = 256 + kFewCountBytes;
 
+// With an 8-bit cache a query's row is multiplied by 2^(134 - e), e the exponent
+// of its largest magnitude, and its scores by scale_log2 over that. The least e,
+// taken for rows of smaller ones (zeros, say): it leaves that factor a normal
+// number. Were it zero, a hidden key's -infinity would become NaN. Elements that
+// f16 then rounds, by up to 2^-25, change a score of keys below 2^25 by less
+// than 2^-110.
+inline uint32_t least_exponent(float scale_log2) { return (uint32_t)std::max(8, 8 - ilogbf(scale_log2)); }
+
 // A checked call of fo_paged_attention.
 struct PagedCall {
   const fo_paged_desc* d;
@@ -115,6 +127,7 @@ struct FewParams {
   int32_t boxes_log2;     // of a tile
   int32_t least;          // tiles of a piece, at least
   float scale_log2;
+  uint32_t least_exponent;
   float* part;            // [blocks][2][8 or 16 * (D + 2)]
   uint32_t* count;        // [blocks][3], zero between calls
 };

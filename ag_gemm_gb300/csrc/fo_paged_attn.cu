@@ -90,6 +90,7 @@ extern "C" fo_status fo_paged_attention(const fo_paged_desc* d, const fo_paged_b
     f.sinks = d->sinks;
     f.least = 1;
     f.scale_log2 = scale * 1.4426950408889634f;
+    f.least_exponent = least_exponent(f.scale_log2);
     f.count = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + 256);
     f.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kScratchAt);
     return attend_few(f, d->head_dim, unit_rows > 8, eight, sms, (cudaStream_t)stream);

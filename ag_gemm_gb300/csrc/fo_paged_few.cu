@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
         }
       } else {
         // The row times a power of two that brings its largest magnitude to
-        // [128, 256). What that makes smaller than f16's least normal number
-        // is 2^-21 of the largest.
+        // [128, 256) (or less: see least_exponent). What that makes smaller
+        // than f16's least normal number is 2^-21 of the largest.
         constexpr int kEach = D / 4;   // elements of a thread
         uint4 v[kEach / 8];
         float top = 0.f;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
           top = max_nan(top, amax_of(f));
         }
         top = lanes_max<4>(top);
-        const uint32_t exponent = min(max(__float_as_uint(top) >> 23, 8u), 254u);
+        const uint32_t exponent = min(max(__float_as_uint(top) >> 23, p.least_exponent), 254u);
         const float by = top <= 3.4e38f ? __uint_as_float((261u - exponent) << 23) : 1.f;
         mine *= 1.f / by;
 #pragma unroll

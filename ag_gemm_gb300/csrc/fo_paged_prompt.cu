@@ -70,6 +70,7 @@ struct PromptParams {
   int32_t R, heads_q, heads_k, group, tokens;   // tokens: of a tile
   int32_t window, sinks, box;
   float scale_log2;
+  uint32_t least_exponent;
   int32_t sms;
   int64_t* before;        // [seqs + 1]: pairs of the sequences before
   uint32_t* next;         // [0] items dealt, [1] items of a key head, [2] parts of it, [3] cut pairs of it, [4] blocks of 32 rows of the largest
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         st.of(it, p.tokens, p.window, p.sinks);
         if (!mbar_wait(bar(kQFull), (uint32_t)n & 1u, abort_flag, kWaitNs)) break;
         // The queries, each row times a power of two that brings its largest
-        // magnitude to [128, 256); in place.
+        // magnitude to [128, 256) (or less: see least_exponent); in place.
 #pragma unroll 1
         for (int t = 0; t < 2; ++t) {
           const int row = tid;
@@ -685,7 +686,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
             Vec16<__nv_bfloat16>::unpack(lds128(at + (k >> 3) * (kTile * 128) + (((k & 7) ^ (row & 7)) << 4)), f);
             top = max_nan(top, amax_of(f));
           }
-          const uint32_t exponent = min(max(__float_as_uint(top) >> 23, 8u), 254u);
+          const uint32_t exponent = min(max(__float_as_uint(top) >> 23, p.least_exponent), 254u);
           const float by = top <= 3.4e38f ? __uint_as_float((261u - exponent) << 23) : 1.f;
           gbase[C::kOffRow + ((n & 1) * 2 + t) * kTile + row] = (uint8_t)(top <= 3.4e38f ? exponent - 7u : 127u);   // of 1 / by
 #pragma unroll 8
@@ -1226,6 +1227,7 @@ fo_status attend_prompts(const PagedCall& c, cudaStream_t s) {
   k.window = d->window;
   k.sinks = d->sinks;
   k.scale_log2 = c.scale_log2;
+  k.least_exponent = least_exponent(c.scale_log2);
   const PromptPlaces at(d, c.b->seqs, c.rows);
   k.sms = std::min(c.sms, FO_GB300_SMS);
   k.next = reinterpret_cast<uint32_t*>(c.ws + 128);

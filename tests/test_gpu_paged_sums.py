@@ -189,3 +189,21 @@ def test_of_large_scores_without_roundings_the_largest_takes_all(dev, kept, new,
             got = o[0][i].reshape(hq, D)[h]
             assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + (2 * n + 8) * U) * size + 2.0 ** -25)
             assert abs(lse[0][i, h] - s.max() - np.log(len(top))) <= (n + 8) * U + 4 * U * abs(s.max() + np.log(len(top)))
+
+
+@pytest.mark.parametrize("scale", [1e-6, 4.0e-8, 1e-20, 1.2e-38, 1e-44])
+@pytest.mark.parametrize("kept", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_scores_of_a_scale_near_zero_are_numbers(dev, kept, new, scale):
+    """Queries that are zero, ordinary and large: a hidden key's weight is none, and the seen ones' are alike."""
+    hq, D, lengths = 4, 128, [200, 70]
+    d = B.fo_paged_desc(hq, 1, head_dim=D, page=16, cache=kept, scale=scale, window=50, sinks=3)
+    cache = Kept(dev, d, lengths, draws(1, 1, D, lengths), draws(2, 1, D, lengths))
+    q = queries(3, d, 2 * new)
+    for x in q:
+        x[0] = 0
+        x[-1, :D] *= 2.0 ** -120
+        x[-1, D:2 * D] *= 2.0 ** 60
+        x[-1, 2 * D:3 * D] *= 2.0 ** -128
+    o, lse = attend(dev, cache, [new, new], q)
+    held_to_the_oracle(cache, [new, new], q, o, lse)

@@ -256,7 +256,7 @@ fo_status check_paged(const fo_paged_desc* d) {
   if (d->page < 16 || d->page > 256 || (d->page & (d->page - 1))) return FO_ERR_SHAPE;
   if (d->cache_dtype != FO_CACHE_BF16 && d->cache_dtype != FO_CACHE_E4M3) return FO_ERR_DTYPE;
   if (d->window < 0 || d->sinks < 0) return FO_ERR_INVALID_ARG;
-  if (!(d->scale >= 0.f) || !isfinite(d->scale)) return FO_ERR_INVALID_ARG;
+  if (!(d->scale >= 0.f) || !isfinite(d->scale * 1.4426950408889634f)) return FO_ERR_INVALID_ARG;   // (in base 2, as it is used)
   return FO_OK;
 }
 

@@ -641,7 +641,7 @@ typedef struct {
   int32_t cache_dtype;        /* fo_cache_dtype */
   int32_t window;             /* 0: none; else how many tokens a query sees, its own the last */
   int32_t sinks;              /* the first tokens, which stay visible beyond the window */
-  float scale;                /* of the scores; 0: 1 / sqrt(head_dim) */
+  float scale;                /* of the scores, at most 2^127; 0: 1 / sqrt(head_dim) */
   int32_t reserved[3];        /* must be zero */
 } fo_paged_desc;
 

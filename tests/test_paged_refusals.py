@@ -1,0 +1,17 @@
+"""CPU tests of what the operators on a paged cache refuse, beside test_paged_oracle_abi.py."""
+import pytest
+
+from ag_gemm_gb300 import binding as B
+from test_paged_oracle_abi import append, attention, desc
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def test_a_scale_that_is_no_number_in_base_2_is_refused():
+    assert append(desc(scale=2.0 ** 127), q=[257]) == attention(desc(scale=2.0 ** 127), q=[257]) == B.FO_ERR_ALIGN   # (what is checked next)
+    for scale in (2.4e38, 3.4e38):
+        assert append(desc(scale=scale)) == attention(desc(scale=scale)) == B.FO_ERR_INVALID_ARG

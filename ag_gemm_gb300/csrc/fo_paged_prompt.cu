@@ -715,11 +715,13 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         float k_scale = scale_of(p.ks[it.r], next), v_scale = scale_of(p.vs[it.r], next);
         for (int i = it.from; i < it.to && ok; ++i) {
           const bool seen = st.any(st.block(i) * kTile + tid);
-          // A power of two not below the scales of the warp's 32 values. It goes
-          // out with the keys: the softmax reads it when it has the step's scores,
-          // which wait for the keys alone.
+          // 2^-7 times a power of two not below the scales of the warp's 32 values:
+          // scales over it are at most 128, values at most 57344, and where f16's
+          // least steps begin, 2^-31 of the largest value is lost. It goes out with
+          // the keys: the softmax reads it when it has the step's scores, which
+          // wait for the keys alone.
           const uint32_t top = __reduce_max_sync(0xffffffffu, seen ? __float_as_uint(v_scale) & 0x7fffffffu : 0u);
-          const uint32_t exponent = min(max((top + 0x7fffffu) >> 23, 40u), 253u);
+          const uint32_t exponent = max((top + 0x7fffffu) >> 23, 40u) - 7u;
           next = place_of(i + 1);
           float k_next = 0.f, v_next = 0.f;
 #pragma unroll 1

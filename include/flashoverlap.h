@@ -699,9 +699,9 @@ fo_status fo_kv_append(const fo_paged_desc* desc, const fo_rope_desc* rope, cons
  * over them. Weights are rounded to bf16 for the tensor cores' sum (by at most
  * 2^-8 of each), o once to bf16. With an 8-bit cache weights and values times
  * their scales are rounded to f16 instead: each value's part of o is off by at
- * most 2^-10 of it, or 2^-31 of the largest value that the sequence's new
- * tokens see where that is more; values whose scale is below 2^-87 may count as
- * zero. A row that sees nothing (a sequence that is not
+ * most 3 * 2^-11 of it (its weight's rounding, its scale's and the product's), or 2^-31
+ * of the largest value that the sequence's new tokens see where that is more;
+ * values whose scale is below 2^-87 may count as zero. A row that sees nothing (a sequence that is not
  * there, a token before its beginning), or whose scores are all -infinity, gets
  * o = 0 and lse = -infinity. Rows that no sequence has are left as they were.
  * Neither places behind a sequence's length nor pages that hold nothing any new

@@ -207,3 +207,17 @@ def test_scores_of_a_scale_near_zero_are_numbers(dev, kept, new, scale):
         x[-1, 2 * D:3 * D] *= 2.0 ** -128
     o, lse = attend(dev, cache, [new, new], q)
     held_to_the_oracle(cache, [new, new], q, o, lse)
+
+
+@pytest.mark.parametrize("spread", [6, 12, 20, 30])
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_values_beside_hidden_large_ones_in_8_bits(dev, D, spread):
+    """Prompts without a prefix: rows see few values, whose scales are 2^-spread to 2^spread of the ones they do not see."""
+    lengths = [300, 33, 90]
+    d = B.fo_paged_desc(8, 1, head_dim=D, page=32, cache="e4m3", window=60)
+    normal = draws(1, 1, D, lengths)
+    powers = torch.randint(-spread, spread + 1, (300,), generator=torch.Generator().manual_seed(3)).float()
+    cache = Kept(dev, d, lengths, draws(2, 1, D, lengths), lambda r, b: normal(r, b) * torch.exp2(powers[:lengths[b]])[:, None, None])
+    q = queries(4, d, sum(lengths))
+    o, lse = attend(dev, cache, lengths, q)
+    held_to_the_oracle(cache, lengths, q, o, lse)

@@ -37,6 +37,7 @@ CACHE_DTYPES = {"bf16": 0, "e4m3": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "wavelength": 2, "parts": 3}
 FO_ROPE_MAX_DIM = 256
 FO_NORM_MAX_H = 32768
+FO_OPS_HEADER = 64                # bytes of a workspace that hold its status
 FO_FP8_BLOCK = 128
 
 # Every symbol include/flashoverlap.h declares.
@@ -773,7 +774,8 @@ def fo_kv_append(desc: PagedDesc, rope: Optional[RopeDesc], batch: PagedBatch, r
     """Append the batch's new tokens to each rank's cache, turned by `rope` (None: as they are) at their positions in
     their sequences (or at positions [rows], int32 or int64), and turn their queries. q, q_out [rows, heads_q *
     head_dim], k, v [rows, heads_k * head_dim]: one matrix for each rank, whose rows may be parts of packed ones;
-    k_cache, v_cache [pages, heads_k, page, head_dim], k_scale, v_scale [pages, heads_k, page] (8 bits only)."""
+    k_cache, v_cache [pages, heads_k, page, head_dim], k_scale, v_scale [pages, heads_k, page] (8 bits only); ws: a
+    workspace that takes the status of what the device finds wrong, or None."""
     code = (_marshal or _native()).kv_append(desc, rope, batch, rows, q, k, v, q_out, k_cache, v_cache, k_scale, v_scale,
                                              positions, ws, stream)
     if code == FO_OK:
@@ -788,6 +790,8 @@ def fo_kv_append(desc: PagedDesc, rope: Optional[RopeDesc], batch: PagedBatch, r
         a, ld[j] = _rows_of(x, R, rows, heads * D, types[0], what)
         rows_of.append(a)
     at, size = _positions(positions, rows)
+    if ws is not None and not isinstance(ws, int) and ws.numel() * ws.element_size() < FO_OPS_HEADER:
+        raise ValueError(f"fo_kv_append: the workspace is smaller than its status, {FO_OPS_HEADER} bytes")
     _check(load().fo_kv_append(desc, rope, batch, rows, at, size, *rows_of, ld,
                                _addresses(k_cache, R, values, kept, "k_cache"), _addresses(v_cache, R, values, kept, "v_cache"),
                                _addresses(k_scale, R, slots, types[1], "k_scale"),

@@ -125,7 +125,6 @@ struct FewParams {
   int32_t R, heads_q, heads_k, group, window, sinks;
   int32_t box;            // tokens of a box: a page's, or a tile's
   int32_t boxes_log2;     // of a tile
-  int32_t least;          // tiles of a piece, at least
   float scale_log2;
   uint32_t least_exponent;
   float* part;            // [blocks][2][8 or 16 * (D + 2)]

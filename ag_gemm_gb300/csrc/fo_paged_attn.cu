@@ -88,7 +88,6 @@ extern "C" fo_status fo_paged_attention(const fo_paged_desc* d, const fo_paged_b
     f.group = d->heads_q / d->heads_k;
     f.window = d->window;
     f.sinks = d->sinks;
-    f.least = 1;
     f.scale_log2 = scale * 1.4426950408889634f;
     f.least_exponent = least_exponent(f.scale_log2);
     f.count = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + 256);

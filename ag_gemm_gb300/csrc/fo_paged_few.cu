@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
       if (w < warp) upto += sums[w];   // (warp 4 adds up none)
       total += sums[w];
     }
-    piece = max((total + gridDim.x - 1) / gridDim.x, (long long)p.least);
+    piece = (total + gridDim.x - 1) / gridDim.x;   // (none has work where the line is empty)
     x0 = blockIdx.x * piece;
     x1 = min(x0 + piece, total);
     long long at = upto - mine;

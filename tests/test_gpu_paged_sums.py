@@ -8,6 +8,10 @@ two: the scale's share once and the product once (2^-11 each). Below f16's least
 value's scale, is off by 2^-25 of a range whose top is 2^15 (or 2^7) times a power of two not below the largest scale of the
 values seen: with an e4m3 value of up to 448, 2^-31 of the largest value at most, for each value that the row sees. A
 query's row becomes f16 with its largest magnitude in [128, 256): 2^-32 of that.
+fp32 itself ends: a weight below 2^-126 is zero, and so is such a factor when tiles or parts are joined. Weights are at most
+2^8 (the maximum moves late) and their sum is at least 1, so each of n values loses at most 2^8 * 2^-126 of the largest of
+them: n 2^-118 max |v|. (Values that fall by 2^9 for each of 24 tiles whose weights grow as fast differ by 2^216: no fp32
+weight reaches the first of them, whatever the order of the sums.)
 """
 import numpy as np
 import pytest
@@ -106,7 +110,7 @@ def held_to_the_oracle(cache, new, q, o, lse, rows_each=None, seed=0):
                     key = np.repeat(np.abs(k[:p + 1]).sum(axis=2).max(axis=0), group)
                     score = score + 2.0 ** -32 * np.abs(mine[0]).max(axis=1) * key * (d.scale or d.head_dim ** -0.5)
                     weights, least = (3 if prompts else 1) * 2.0 ** -11 * (1 + 2.0 ** -9), count * 2.0 ** -31
-                bound = (weights + 2 * score[:, None] + (2 * n + 8) * U) * size + least * top + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7)
+                bound = (weights + 2 * score[:, None] + (2 * n + 8) * U) * size + (least + count * 2.0 ** -118) * top + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7)
                 got = o[r][at + i].reshape(want.shape)
                 assert np.all(np.abs(got - want) <= bound), (b, r, i, np.max(np.abs(got - want) / np.maximum(bound, 1e-300)))
                 off = score + (n + 8) * U + 4 * U * np.abs(wl)
@@ -221,3 +225,139 @@ def test_small_values_beside_hidden_large_ones_in_8_bits(dev, D, spread):
     q = queries(4, d, sum(lengths))
     o, lse = attend(dev, cache, lengths, q)
     held_to_the_oracle(cache, lengths, q, o, lse)
+
+
+@pytest.mark.parametrize("spread", [6, 12, 20, 30])
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_values_beside_hidden_large_ones_among_few_tokens(dev, D, spread):
+    lengths, new = [4, 3, 2, 70, 1], [4, 3, 2, 2, 1]
+    d = B.fo_paged_desc(4, 1, head_dim=D, page=16, cache="e4m3", window=3)
+    normal = draws(1, 1, D, lengths)
+    powers = torch.randint(-spread, spread + 1, (70,), generator=torch.Generator().manual_seed(3)).float()
+    cache = Kept(dev, d, lengths, draws(2, 1, D, lengths), lambda r, b: normal(r, b) * torch.exp2(powers[:lengths[b]])[:, None, None])
+    q = queries(4, d, sum(new))
+    o, lse = attend(dev, cache, new, q)
+    held_to_the_oracle(cache, new, q, o, lse)
+
+
+# ------------------------------------------------------------------ an 8-bit cache's own bound
+
+def shapes():
+    """The operator's own shapes, of sequences whose new tokens all are in the cache."""
+    from test_gpu_paged import DECODE, PROMPTS
+    for R, hq, hk, D, page, lengths, new in DECODE + PROMPTS:
+        kept = [(n, m) for n, m in zip(lengths, new) if n >= m > 0]
+        yield R, hq, hk, D, page, [n for n, _ in kept], [m for _, m in kept]
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (16, 4), (64, 130), (33, 1)])
+@pytest.mark.parametrize("case", list(shapes()))
+def test_an_8_bit_cache_costs_what_its_roundings_cost(dev, case, window, sinks):
+    R, hq, hk, D, page, lengths, new = case
+    d = B.fo_paged_desc(hq, hk, head_dim=D, R=R, page=page, cache="e4m3", window=window, sinks=sinks)
+    cache = Kept(dev, d, lengths, draws(hq, hk, D, lengths), draws(hq + 1, hk, D, lengths))
+    q = queries(2, d, sum(new))
+    o, lse = attend(dev, cache, new, q)
+    held_to_the_oracle(cache, new, q, o, lse, rows_each=40)
+
+
+# ------------------------------------------------------------------ maxima that grow, outputs that are rescaled
+
+def steps_of(by, each, lengths, hk, D, seed):
+    """Keys whose first place alone counts: with queries of 4 there and a scale of 1/4 the score of token j is by * (j //
+    each) / log2 e, plus what the other places, a tenth of normal ones, add."""
+    def one(r, b):
+        n = lengths[b]
+        x = 0.1 * torch.randn(n, hk, D, generator=torch.Generator().manual_seed(seed + 10 * r + b))
+        x[:, :, 0] = by / 1.4426950408889634 * (torch.arange(n) // each).float()[:, None]
+        return x
+    return one
+
+
+def aligned_queries(seed, d, rows):
+    q = queries(seed, d, rows)
+    for x in q:
+        x.view(rows, d.heads_q, d.head_dim)[:, :, 0] = 4
+    return q
+
+
+GROWTH = [  # lengths, new, heads_q, heads_k, R: blocks with several tiles, items with many steps
+    ([6000, 4100, 5300, 4900] * 4, [1] * 16, 8, 4, 1),
+    ([3000, 2100] * 3, [3] * 6, 10, 2, 2),
+    ([1500, 700], [40, 700], 8, 2, 2),
+    ([6000, 300], [1000, 300], 8, 2, 3),
+]
+
+
+@pytest.mark.parametrize("by", [9.0, 3.0, 7.9])
+@pytest.mark.parametrize("kept,shrink", [("bf16", 0), ("bf16", 1), ("e4m3", 0)])
+@pytest.mark.parametrize("case", GROWTH)
+def test_scores_that_grow_from_tile_to_tile(dev, case, kept, shrink, by):
+    """By 2^9 for each 128 keys (the maximum moves), 2^3 and just below 2^8 (it moves late); values that shrink as fast
+    (`shrink`) leave the first tiles' share as large as the last's."""
+    lengths, new, hq, hk, R = case
+    D, each = 64, 128
+    d = B.fo_paged_desc(hq, hk, head_dim=D, R=R, page=32, cache=kept, scale=0.25)
+    normal = draws(7, hk, D, lengths)
+
+    def values(r, b):
+        t = (torch.arange(lengths[b]) // each).float()
+        return normal(r, b) * torch.exp2(-by * shrink * (t - t.max() / 2)).clamp(2.0 ** -100, 2.0 ** 100)[:, None, None]
+    cache = Kept(dev, d, lengths, steps_of(by, each, lengths, hk, D, 3), values)
+    q = aligned_queries(8, d, sum(new))
+    o, lse = attend(dev, cache, new, q)
+    held_to_the_oracle(cache, new, q, o, lse, rows_each=12)
+
+
+@pytest.mark.parametrize("each,by", [(256, 9.0), (128, 8.0), (512, 20.0)])
+@pytest.mark.parametrize("case", GROWTH)
+def test_values_of_an_8_bit_cache_that_grow_from_tile_to_tile(dev, case, each, by):
+    """By 2^by for each block of keys, whose scores fall as fast: all blocks' shares are alike, and the power of two that the
+    weights are kept over moves with each."""
+    lengths, new, hq, hk, R = case
+    D = 64
+    lengths = [min(n, int(110 / by) * each) for n in lengths]
+    new = [min(m, n) for m, n in zip(new, lengths)]
+    d = B.fo_paged_desc(hq, hk, head_dim=D, R=R, page=32, cache="e4m3", scale=0.25)
+    normal = draws(7, hk, D, lengths)
+
+    def values(r, b):
+        t = (torch.arange(lengths[b]) // each).float()
+        return normal(r, b) * torch.exp2(by * (t - t.max() / 2)).clamp(2.0 ** -60, 2.0 ** 60)[:, None, None]
+    cache = Kept(dev, d, lengths, steps_of(-by, each, lengths, hk, D, 3), values)
+    q = aligned_queries(8, d, sum(new))
+    o, lse = attend(dev, cache, new, q)
+    held_to_the_oracle(cache, new, q, o, lse, rows_each=12)
+
+
+@pytest.mark.parametrize("kept", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", GROWTH)
+def test_peaked_rows(dev, case, kept):
+    """Scores of a standard deviation of 12: most of a row's weight is one key's, wherever it lies."""
+    lengths, new, hq, hk, R = case
+    d = B.fo_paged_desc(hq, hk, head_dim=128, R=R, page=64, cache=kept)
+    cache = Kept(dev, d, lengths, lambda r, b: 12 * draws(1, hk, 128, lengths)(r, b), draws(2, hk, 128, lengths))
+    q = queries(3, d, sum(new))
+    o, lse = attend(dev, cache, new, q)
+    held_to_the_oracle(cache, new, q, o, lse, rows_each=12)
+
+
+# ------------------------------------------------------------------ items of many steps
+
+LONG_ITEMS = [  # D, window, sinks: pairs that are not cut, of 33 and more steps, and of 65 and more
+    (64, 0, 0), (128, 0, 0), (64, 4500, 300), (128, 4500, 300), (128, 8200, 0),
+]
+
+
+@pytest.mark.parametrize("kept", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", LONG_ITEMS)
+def test_items_of_many_steps(dev, case, kept):
+    """8400 tokens of 3 ranks with 8 query heads to a key head: 263 pairs of tiles for each rank, of up to 66 steps, and with
+    so many to deal none of them is cut."""
+    D, window, sinks = case
+    lengths, R = [8400], 3
+    d = B.fo_paged_desc(8, 1, head_dim=D, R=R, page=64, cache=kept, window=window, sinks=sinks)
+    cache = Kept(dev, d, lengths, draws(1, 1, D, lengths), draws(2, 1, D, lengths))
+    q = queries(3, d, 8400)
+    o, lse = attend(dev, cache, lengths, q)
+    held_to_the_oracle(cache, lengths, q, o, lse, rows_each=80)

@@ -74,6 +74,11 @@ __device__ __forceinline__ float2 turn_of(const AppendParams& p, int row, int po
   return make_float2(c * p.factor, s * p.factor);
 }
 
+// A pair turned, with fo_rope's roundings.
+__device__ __forceinline__ float2 turn_pair(float u, float w, float c, float s) {
+  return make_float2(fmaf(u, c, -(w * s)), fmaf(w, c, u * s));
+}
+
 // Rows, heads and halves on the 16-byte grid. A thread has a token and two
 // pieces of eight elements in every head: in the half layout those that are
 // turned together, else neighbours' (the threads beyond the turned pieces copy
@@ -147,18 +152,16 @@ __global__ void __launch_bounds__(256, 3) append_wide_kernel(const __grid_consta
                   if (turn_a) {
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
-                      const float v = u[j];
-                      u[j] = v * c[j] - w[j] * s[j];
-                      w[j] = w[j] * c[j] + v * s[j];
+                      const float2 z = turn_pair(u[j], w[j], c[j], s[j]);
+                      u[j] = z.x, w[j] = z.y;
                     }
                   }
                 } else {
                   auto turn = [&](float (&z)[V], int at) {
 #pragma unroll
                     for (int j = 0; j < V / 2; ++j) {
-                      const float v = z[2 * j];
-                      z[2 * j] = v * c[at + j] - z[2 * j + 1] * s[at + j];
-                      z[2 * j + 1] = z[2 * j + 1] * c[at + j] + v * s[at + j];
+                      const float2 y = turn_pair(z[2 * j], z[2 * j + 1], c[at + j], s[at + j]);
+                      z[2 * j] = y.x, z[2 * j + 1] = y.y;
                     }
                   };
                   if (turn_a) turn(u, 0);
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
         const bool second = p.half ? e >= pairs : e & 1;
         const int other = p.half ? (second ? e - pairs : e + pairs) : e ^ 1;
         const float w = to_f(x[other]);
-        v[k] = second ? v[k] * cs[pair].x + w * cs[pair].y : v[k] * cs[pair].x - w * cs[pair].y;
+        v[k] = second ? turn_pair(w, v[k], cs[pair].x, cs[pair].y).y : turn_pair(v[k], w, cs[pair].x, cs[pair].y).x;
       }
       top = max_nan(top, fabsf(v[k]));
     }

@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
         qscale[i][a] = __shfl_sync(0xffffffffu, mine, (2 * c + a) * 4);
       }
     }
-    float o[D / 16][NT][4], m[NT][2], l[NT][2];
+    float o[D / 16][NT][4], m[NT][2], l[NT][2];   // m: of the scores as they are, before their factor
     float sigma = 0.f, sigma_inv = 0.f;   // what the values' scales are divided by (a power of two), and its reciprocal
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -426,10 +426,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
           for (int i = 1; i < kM; ++i) mx = max3(mx, sc[i][t][a], sc[i][t][2 + a]);
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-          mx *= qscale[t][a];
           by[t][a] = 1.f;
-          if (mx > m[t][a] + kLazy || (m[t][a] == -INFINITY && mx > m[t][a])) {
-            by[t][a] = ex2_below(m[t][a], mx);
+          if ((mx - m[t][a]) * qscale[t][a] > kLazy) {   // (false for -infinity less itself)
+            by[t][a] = ex2((m[t][a] - mx) * qscale[t][a]);
             m[t][a] = mx;
             l[t][a] *= by[t][a];
             grown = true;
@@ -465,17 +464,6 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
           sigma_inv = 1.f / to;
         }
       }
-      // A weight is 2^(score factor + down). (Made anew for each tile: kept from
-      // when a maximum moves, they cost 16 rows 11%, in registers.)
-      float factor[NT][2], down[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          const bool none = m[t][a] == -INFINITY;
-          const float less = none ? 1.f : held_back<E8>(m[t][a]);
-          factor[t][a] = qscale[t][a] * less, down[t][a] = none ? 0.f : -m[t][a] * less;
-        }
       uint32_t pf[kM][NT][2];
 #pragma unroll
       for (int i = 0; i < kM; ++i)
@@ -485,7 +473,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
           if constexpr (E8) v_scale = lds_f(scales + cslot * (C::kStep * 4) + (16 * i + 8 * e + g) * 4) * sigma_inv;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            float w0 = ex2(fmaf(sc[i][t][2 * e], factor[t][0], down[t][0])), w1 = ex2(fmaf(sc[i][t][2 * e + 1], factor[t][1], down[t][1]));
+            // (The difference first: a score's product with its factor, unrounded, less
+            // the maximum's, rounded, is no small number where scores are huge.)
+            const float down0 = m[t][0] == -INFINITY ? 0.f : m[t][0], down1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+            float w0 = ex2((sc[i][t][2 * e] - down0) * qscale[t][0]), w1 = ex2((sc[i][t][2 * e + 1] - down1) * qscale[t][1]);
             l[t][0] += w0, l[t][1] += w1;
             if constexpr (E8) {
               w0 = part && w0 == 0.f ? 0.f : w0 * v_scale;
@@ -569,6 +560,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
       for (int a = 0; a < 2; ++a) {
 #pragma unroll
         for (int d = 4; d < 32; d *= 2) l[t][a] += __shfl_xor_sync(0xffffffffu, l[t][a], d);
+        m[t][a] *= qscale[t][a];
         if (g == 0) stat[(warp * NT + t) * 8 + 2 * c + a] = make_float2(m[t][a], l[t][a]);
       }
     meet();

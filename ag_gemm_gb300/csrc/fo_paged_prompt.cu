@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       // Blocks all of whose keys all of the tile's rows see need no mask.
       const int first_pos = it.base + tile_token;
       const int last_lo = sight_of(max(first_pos + p.tokens - 1, 0), p.window, p.sinks).lo;
-      float m = -INFINITY, l = 0.f, row_factor = p.scale_log2, sigma = 0.f;   // m: of the scores as they are, before their factor
+      float m = -INFINITY, l = 0.f, row_factor = p.scale_log2, sigma = 0.f;
       bool any = false;
       for (int i = it.from; i < it.to; ++i) {
         if (!st.active(t, i)) continue;
@@ -845,12 +845,12 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               tops[2 * e + (k >> 1 & 1)] = max3(tops[2 * e + (k >> 1 & 1)], __uint_as_float(v[e][k]), __uint_as_float(v[e][k + 1]));
-          top = max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]), fmaxf(tops[6], tops[7]));
+          top = max3(max3(tops[0], tops[1], tops[2]), max3(tops[3], tops[4], tops[5]), fmaxf(tops[6], tops[7])) * row_factor;
         }
         float pow2[4];
         float by = 1.f;   // what O is rescaled with
-        if ((top - m) * row_factor > kLazy) {   // (false for -infinity less itself)
-          by = ex2((m - top) * row_factor);
+        if (top > m + kLazy || (m == -INFINITY && top > m)) {
+          by = ex2_below(m, top);
           l *= by;
           m = top;
         }
@@ -867,10 +867,10 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
           }
         }
         // Weights, over the scores' first 64 columns (the row's scores are in
-        // registers), and their sum. Each from the difference of scores: a score's
-        // product with the factor, unrounded, less the maximum's, rounded, is no
-        // small number where scores are huge.
-        const float down = m == -INFINITY ? 0.f : -m;
+        // registers), and their sum.
+        // (Held back anew each step, which costs 1%; kept from when m moves, 2%.)
+        const float less = held_back<E8>(m);
+        const float factor = m == -INFINITY ? row_factor : row_factor * less, down = m == -INFINITY ? 0.f : -m * less;
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -878,15 +878,14 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
           // power of two over sigma, which goes into the exponent; the sum is
           // of the weights alone. (Below 2^-60 nothing is left of them in f16.)
           const int lift = E8 ? max((int)(__float_as_uint(pow2[e]) >> 23) - (int)(__float_as_uint(sigma) >> 23), -60) : 0;
-          const f32x2 factor2 = pair_of(row_factor, row_factor), down2 = pair_of(down, down), lift2 = pair_of((float)lift, (float)lift);
+          const f32x2 factor2 = pair_of(factor, factor), down2 = pair_of(down + (float)lift, down + (float)lift);
           f32x2 sums[2] = {0ull, 0ull};
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
             float f[4];
-            const f32x2 x0 = add2(pair_of(v[e][k], v[e][k + 1]), down2), x1 = add2(pair_of(v[e][k + 2], v[e][k + 3]), down2);
-            halves(E8 ? fma2(x0, factor2, lift2) : mul2(x0, factor2), f[0], f[1]);
-            halves(E8 ? fma2(x1, factor2, lift2) : mul2(x1, factor2), f[2], f[3]);
+            halves(fma2(pair_of(v[e][k], v[e][k + 1]), factor2, down2), f[0], f[1]);
+            halves(fma2(pair_of(v[e][k + 2], v[e][k + 3]), factor2, down2), f[2], f[3]);
 #pragma unroll
             for (int a = 0; a < 4; ++a) f[a] = ex2(f[a]);
             sums[0] = add2(sums[0], pair_of(f[0], f[1]));
@@ -927,7 +926,6 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
       }
       if (!ok) break;
       n_step += it.to - it.from;
-      m *= row_factor;
       // ---- the rows' results
       if (any) {
         if (!mbar_wait(bar(kOFull + t), outs & 1u, abort_flag, kWaitNs)) break;

@@ -85,6 +85,18 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3_high(uint32_t two) {
   return r;
 }
 
+// A weight is 2^(s f - m), with the product unrounded and m the rounded product of
+// the largest score. Past 2^31 that rounding alone is more than a power of two in
+// fp32 holds, and for f16 weights (of up to 2^15 without it) from 2^24 on. With
+// this power of two on f and m, m stays below 2^30 (2^23). Scores so large then
+// differ by more than a weight's range, or (from 2^23 on) by less than what their
+// sums' roundings leave open.
+template <bool F16>
+__device__ __forceinline__ float held_back(float m) {
+  const int over = (int)(__float_as_uint(m) >> 23 & 0xffu) - (127 + (F16 ? 22 : 29));
+  return over > 0 ? __uint_as_float((uint32_t)(127 - over) << 23) : 1.f;
+}
+
 // ln of the sum, from a maximum in base 2.
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l > 0.f || l != l ? m * 0.69314718055994531f + logf(l) : -INFINITY; 

@@ -87,7 +87,7 @@ __device__ __forceinline__ float2 turn_pair(float u, float w, float c, float s) 
 // so its largest magnitude takes two or three shuffles.
 // Bandwidth-bound: 8192 tokens of 8 ranks with 4 + 4 + 4 heads (403 MB) take
 // 63 us, 6.4 TB/s, element by element (below) 321; 5015 tokens of 32 + 8 + 8
-// heads into 8 bits (113 MB) 26 us, element by element 80.
+// heads into 8 bits (113 MB) 26.5 us, element by element 80.
 template <bool HALF, bool E8, bool RANKS>
 __global__ void __launch_bounds__(256, 3) append_wide_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kHeads = 4, V = 8;

@@ -14,8 +14,9 @@ namespace {
 // takes. More are the prompts' kernel's, whose tiles have 128: 17 contexts of
 // up to 4100 on two ranks with 24, 40 and 64 rows take it 40, 43 and 44 us, and
 // took the split kernel (with two and four warps to a warp's keys) 53, 73 and
-// 89. With 16 rows the split kernel takes 37 us, the prompts' 45; over 64
-// contexts of up to 8192, 79 and 112.
+// 89. With 16 rows the split kernel takes 41 to 45 us, the prompts' 40, from an 8-bit
+// cache 44 and 49; over 64 contexts of up to 8192, with two key heads 80 and 107,
+// with four 128 and 147.
 constexpr int kFewRows = 16;
 size_t few_bytes(const fo_paged_desc* d) {
   return kScratchAt + (size_t)kFewBlocks * FO_GB300_SMS * 2 * kFewRows * (d->head_dim + 2) * 4;

@@ -31,12 +31,12 @@
 // times their values' scales over a running power of two.
 //
 // Bound by bandwidth: 64 contexts of up to 8192 with 32 + 8 heads (1.34 GB of
-// keys and values) take 208 us, 6.5 TB/s or 95% of a copy's; one of 131072 95
-// us (83%: the join of 38 parts a head, and the start); 32 of up to 16384 in 8
-// bits 123 us (84%). Eight of up to 512 take 11 us: the launch and look-ups,
+// keys and values) take 203 us, 6.6 TB/s or 97% of a copy's; one of 131072 91
+// us (87%: the join of 38 parts a head, and the start); 32 of up to 16384 in 8
+// bits 123 us (84%). Eight of up to 512 take 10 us: the launch and look-ups,
 // a tile, the join, each waiting for the one before (pieces of at least two or
-// four tiles, with fewer blocks and joins, 15.4 and 16.3 us). A third block an
-// SM spilled (407 us for the 64 contexts).
+// four tiles, with fewer blocks and joins, took 15.4 and 16.3 us, not 11.0). A
+// third block an SM spilled (407 us for the 64 contexts).
 #include <math.h>
 
 #include <algorithm>

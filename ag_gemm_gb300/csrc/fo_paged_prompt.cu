@@ -29,17 +29,19 @@
 // counter, the last (under the causal mask the costliest) first. A third joins
 // the parts of pairs of tiles that were cut.
 //
-// 8 ranks of 8192 tokens with 4 heads, causal, take 395 us, 1.39 PFLOP/s of the
-// products that are seen: a step of two tiles takes some 3000 cycles, 2048 of
-// them the tensor core's, since a tile's softmax with what it waits for is longer
-// than the other tile's products. 8192 tokens with a window of 1024 + 4 and 32 +
-// 8 heads take 141 us, 0.92 PFLOP/s: items of ten or eleven steps, whose ends and
-// starts are not hidden (two tiles' scores and outputs fill TMEM), and a fifth of
-// the products masked. Begun with the first 64 keys' weights, the weighted sum
-// made the one 392 us and the other 146. The loop's length counts: rescaling
-// written out for all columns, which seldom runs, cost the one 4 us, and a branch
-// around weights of 32 keys that no row sees 10. Chunks of up to 1030 tokens of 8 bits, D = 64, take 84 us:
-// at D = 64 the exponentials are as long as both products.
+// 8 ranks of 8192 tokens with 4 heads, causal, take 395 us (393 to 402 from box
+// to box), 1.39 PFLOP/s of the products that are seen: a step of two tiles takes
+// some 3000 cycles, 2048 of them the tensor core's, since a tile's softmax with
+// what it waits for is longer than the other tile's products. 8192 tokens with a
+// window of 1024 + 4 and 32 + 8 heads take 141 us (to 148), 0.92 PFLOP/s: items of
+// ten or eleven steps, whose ends and starts are not hidden (two tiles' scores
+// and outputs fill TMEM), and a fifth of the products masked. Begun with the first
+// 64 keys' weights, the weighted sum made the one 392 us and the other 146. The
+// loop's length counts: rescaling written out for all columns, which seldom runs,
+// cost the one 4 us, and a branch around weights of 32 keys that no row sees 10.
+// Chunks of up to 1030 tokens of 8 bits, D = 64, take 84 us, D = 128 108: at D =
+// 64 the exponentials are as long as both products. The first case from an 8-bit
+// cache takes 547 us, the second 208; in bf16 with D = 64, 317 and 119.
 #include <cudaTypedefs.h>
 #include <math.h>
 #include <string.h>
@@ -868,7 +870,8 @@ __global__ void __launch_bounds__(Prompt<D, E8>::kThreads, 1) prompt_kernel(cons
         }
         // Weights, over the scores' first 64 columns (the row's scores are in
         // registers), and their sum.
-        // (Held back anew each step, which costs 1%; kept from when m moves, 2%.)
+        // (Held back anew each step, which costs up to 1%; kept from when m moves
+        // 2%; the difference of scores first, as for few tokens, 4% at D = 64.)
         const float less = held_back<E8>(m);
         const float factor = m == -INFINITY ? row_factor : row_factor * less, down = m == -INFINITY ? 0.f : -m * less;
         float sum = 0.f;

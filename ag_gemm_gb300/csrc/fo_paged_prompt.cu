@@ -29,8 +29,8 @@
 // counter, the last (under the causal mask the costliest) first. A third joins
 // the parts of pairs of tiles that were cut.
 //
-// 8 ranks of 8192 tokens with 4 heads, causal, take 395 us (393 to 402 from box
-// to box), 1.39 PFLOP/s of the products that are seen: a step of two tiles takes
+// 8 ranks of 8192 tokens with 4 heads, causal, take 395 us (393 to 402 from one
+// GB300 to another), 1.39 PFLOP/s of the products that are seen: a step of two tiles takes
 // some 3000 cycles, 2048 of them the tensor core's, since a tile's softmax with
 // what it waits for is longer than the other tile's products. 8192 tokens with a
 // window of 1024 + 4 and 32 + 8 heads take 141 us (to 148), 0.92 PFLOP/s: items of

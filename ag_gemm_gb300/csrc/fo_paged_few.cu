@@ -442,6 +442,60 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
             o[j][t][0] *= by[t][0], o[j][t][1] *= by[t][1], o[j][t][2] *= by[t][0], o[j][t][3] *= by[t][1];
       }
       mbar_wait(full + cslot * 8, cround & 1, abort_flag, kWaitNs);
+      // Where some rows see a value and others do not, a weight of zero times an
+      // infinity or a NaN would be NaN: such elements are added to the rows that
+      // see them (weights are positive) and zeros in the product.
+      if (part && s.n > 1) {
+        const uint32_t at = base + cslot * C::kSlot + warp * kKeys * C::kWidth;
+        const uint32_t by_key = scales + cslot * (C::kStep * 4);
+        auto seen = [&](int k) { return k < s.end && (k >= cw.lo || k < cw.sinks_end); };
+        constexpr int kPieces = C::kRow / 16;
+        auto piece_at = [&](int x) {   // of 16 bytes; x / kPieces is the key
+          const int row = x / kPieces, piece = x % kPieces;
+          return at + (piece >> 3) * (C::kStep * 128) + row * C::kWidth + (piece & 7) * 16;
+        };
+        uint32_t odd = 0;
+#pragma unroll 4
+        for (int x = lane; x < kKeys * kPieces; x += 32)
+          if (seen(key + x / kPieces)) odd |= odd_of<E8>(lds128(piece_at(x)));
+        if constexpr (E8)
+          for (int k = lane; k < kKeys; k += 32) odd |= seen(key + k) && odd_of(lds_f(by_key + k * 4));
+        if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+          for (int k = 0; k < kKeys; ++k) {
+            if (!seen(key + k)) continue;
+            float scale = 1.f;
+            if constexpr (E8) scale = lds_f(by_key + k * 4);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float v;
+                if constexpr (E8) {
+                  const int d = (D / 8) * g + 2 * j + e, piece = D == 128 ? (d >> 4) ^ (k & 7) : (d >> 4) ^ ((k >> 1) & 3);
+                  const uint32_t two = f16x2_of_e4m3(lds_u8(at + k * C::kWidth + piece * 16 + (d & 15)));
+                  v = __half2float(__ushort_as_half((unsigned short)two)) * scale;
+                } else {
+                  const int d = 16 * j + 8 * e + g;
+                  v = __uint_as_float(lds_u16(at + (d >> 6) * (C::kStep * 128) + k * 128 + ((((d >> 3) & 7) ^ (k & 7)) << 4) + (d & 7) * 2) << 16);
+                }
+                if (odd_of(v))
+#pragma unroll
+                  for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int a = 0; a < 2; ++a)
+                      if (key + k <= pos[t][a] && (key + k >= lo[t][a] || key + k < p.sinks)) o[j][t][2 * e + a] += v;
+              }
+          }
+          __syncwarp();
+          for (int x = lane; x < kKeys * kPieces; x += 32) sts128(piece_at(x), even_of<E8>(lds128(piece_at(x))));
+          if constexpr (E8)
+            for (int k = lane; k < kKeys; k += 32)
+              if (odd_of(lds_f(by_key + k * 4))) sts_f(by_key + k * 4, 0.f);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      }
       if constexpr (E8) {
         // Weights times the values' scales over sigma, the largest scale so
         // far: at most 2^(kLazy + 7) in f16.
@@ -455,7 +509,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) few_kernel(const __gr
         top = __reduce_max_sync(0xffffffffu, top);
         if (__uint_as_float(top) > sigma * 128.f || sigma == 0.f) {
           const uint32_t exponent = min(max((top + 0x7fffffu) >> 23, 9u), 253u);
-          const float to = __uint_as_float((exponent - 7u) << 23), less = sigma == 0.f ? 0.f : sigma / to;
+          const float to = __uint_as_float((exponent - 7u) << 23), less = sigma == 0.f ? 1.f : sigma / to;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j)
 #pragma unroll

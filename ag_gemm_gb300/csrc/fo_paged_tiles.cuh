@@ -36,6 +36,17 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts_f(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
 __device__ __forceinline__ float lds_f(uint32_t a) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
@@ -96,6 +107,23 @@ __device__ __forceinline__ float held_back(float m) {
   const int over = (int)(__float_as_uint(m) >> 23 & 0xffu) - (127 + (F16 ? 22 : 29));
   return over > 0 ? __uint_as_float((uint32_t)(127 - over) << 23) : 1.f;
 }
+
+// The sign bits of the halves (or, of e4m3, bytes) that are no finite numbers.
+template <bool E8>
+__device__ __forceinline__ uint32_t odd_of(uint32_t w) {
+  return E8 ? ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+template <bool E8>
+__device__ __forceinline__ uint32_t odd_of(const uint4& v) { return odd_of<E8>(v.x) | odd_of<E8>(v.y) | odd_of<E8>(v.z) | odd_of<E8>(v.w); }
+// Zeros in their places.
+template <bool E8>
+__device__ __forceinline__ uint32_t even_of(uint32_t w) {
+  const uint32_t odd = odd_of<E8>(w);
+  return w & ~((odd >> (E8 ? 7 : 15)) * (E8 ? 0xffu : 0xffffu));
+}
+template <bool E8>
+__device__ __forceinline__ uint4 even_of(const uint4& v) { return make_uint4(even_of<E8>(v.x), even_of<E8>(v.y), even_of<E8>(v.z), even_of<E8>(v.w)); }
+__device__ __forceinline__ bool odd_of(float v) { return !(fabsf(v) <= 3.402823466e38f); }
 
 // ln of the sum, from a maximum in base 2.
 __device__ __forceinline__ float lse_of(float m, float l) {

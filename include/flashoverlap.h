@@ -706,8 +706,10 @@ fo_status fo_kv_append(const fo_paged_desc* desc, const fo_rope_desc* rope, cons
  * o = 0 and lse = -infinity. Rows that no sequence has are left as they were.
  * Neither places behind a sequence's length nor pages that hold nothing any new
  * token of it sees are looked at: their entries of the table may be anything,
- * their places may hold NaN. (An infinity or NaN among the values that one new
- * token of a sequence sees may reach the sequence's others, which see less.)
+ * their places may hold NaN. An infinity or NaN among the values that one new
+ * token of a sequence sees does not reach the sequence's others, which see less,
+ * where max_new * heads_q / heads_k is at most 16 (drafted tokens, say); in
+ * prompts it may.
  * q, o: rows ld[0..1] elements apart (a multiple of 8; 16-byte aligned), head h
  * at h * head_dim; caches and scales 16-byte aligned; lse (may be NULL)
  * [rows x heads_q] fp32. o must not overlap q. ws: fo_paged_attention_workspace

@@ -361,3 +361,74 @@ def test_items_of_many_steps(dev, case, kept):
     q = queries(3, d, 8400)
     o, lse = attend(dev, cache, lengths, q)
     held_to_the_oracle(cache, lengths, q, o, lse, rows_each=80)
+
+
+# ------------------------------------------------------------------ infinities and NaN
+
+ODD = [  # lengths, new, heads_q, heads_k, D, page, window, sinks: up to 16 rows a key head
+    ([40, 9, 300, 129], [4, 3, 4, 2], 8, 2, 128, 16, 0, 0),
+    ([40, 9, 300, 700], [4, 3, 4, 2], 4, 1, 64, 32, 33, 3),
+    ([200, 70], [2, 2], 5, 1, 128, 64, 5, 0),
+    ([300, 33, 140, 2], [16, 9, 11, 2], 2, 2, 128, 16, 0, 0),
+    ([600, 140], [8, 7], 2, 1, 64, 64, 100, 4),
+    ([20000, 15000], [5, 16], 3, 3, 128, 256, 0, 0),
+    ([5, 16], [5, 16], 1, 1, 64, 32, 3, 1),
+]
+
+
+@pytest.mark.parametrize("where", ["new", "anywhere"])
+@pytest.mark.parametrize("kept", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", ODD)
+def test_values_that_are_no_numbers_reach_the_rows_that_see_them_alone(dev, case, kept, where):
+    """Single elements of values (NaN; with bf16 infinities), an 8-bit token's scale, and keys: of new tokens, which the ones
+    before them do not see, or of any."""
+    lengths, new, hq, hk, D, page, window, sinks = case
+    R = 2
+    d = B.fo_paged_desc(hq, hk, head_dim=D, R=R, page=page, cache=kept, window=window, sinks=sinks)
+    cache = Kept(dev, d, lengths, draws(1, hk, D, lengths), draws(2, hk, D, lengths))
+    g = np.random.default_rng(5)
+    table = cache.table.cpu().numpy()
+    for b, (n, m) in enumerate(zip(lengths, new)):
+        pg, slot = P.places(table[b], n, page)
+        for r in range(R):
+            for what in ["nan", "inf", "-inf", "scale", "key"] * 2:
+                j, h, e = int(g.integers(n - m if where == "new" else 0, n)), int(g.integers(hk)), int(g.integers(D))
+                if what in ("scale", "key"):               # (of the last token, so that other rows stay clean)
+                    j = n - 1
+                if what == "key":
+                    cache.kc[r][int(pg[j]), h, int(slot[j]), e] = NAN
+                    cache.k[r][b][j, h, e] = NAN
+                elif what == "scale":
+                    if kept == "e4m3":
+                        cache.vs[r][int(pg[j]), h, int(slot[j])] = float("inf")
+                        with np.errstate(invalid="ignore"):
+                            cache.v[r][b][j, h] = cache.v[r][b][j, h] * np.inf
+                else:
+                    value = NAN if kept == "e4m3" else float(what)
+                    cache.vc[r][int(pg[j]), h, int(slot[j]), e] = value
+                    cache.v[r][b][j, h, e] = value
+    q = queries(3, d, sum(new))
+    o, lse = attend(dev, cache, new, q)
+    at, clean = 0, 0
+    for b, (n, m) in enumerate(zip(lengths, new)):
+        seen = P.sees(n, m, window, sinks)
+        for r in range(R):
+            k, v = cache.k[r][b], cache.v[r][b]
+            for i in range(m):
+                mine, p = f64(q[r][at + i]).reshape(1, hq, D), n - m + i
+                with np.errstate(invalid="ignore", over="ignore"):
+                    want, wl, size, far = (x[0] for x in P.attention(mine, k[:p + 1], v[:p + 1], 1, window, sinks))
+                got, gl = o[r][at + i].reshape(hq, D), lse[r][at + i]
+                fine = np.isfinite(want)
+                assert np.array_equal(got[~fine], want[~fine], equal_nan=True), (b, r, i)
+                assert np.all(np.isfinite(got[fine])) and np.array_equal(np.isfinite(gl), np.isfinite(wl)), (b, r, i)
+                rows = np.isfinite(wl)
+                top = np.where(np.isfinite(v), np.abs(v), 0)[seen.any(axis=0)].max()
+                score = (D + 8) * U * np.where(rows, far, 0)[:, None] + 2.0 ** -22
+                bound = (2.0 ** -8 + 2 * score + (2 * n + 8) * U) * np.where(fine, size, 0) + n * 2.0 ** -31 * top + \
+                    2.0 ** -8 * np.where(fine, np.abs(want), 0) * (1 + 2.0 ** -7)
+                assert np.all(np.abs(np.where(fine, got, 0) - np.where(fine, want, 0)) <= bound), (b, r, i)
+                clean += int(fine.sum())
+        at += m
+    assert 0 < clean < R * sum(new) * hq * D                # (rows see some of them, and others none)
+
